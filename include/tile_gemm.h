@@ -46,7 +46,8 @@ typedef enum {
   TILE_GEMM_ERR_DTYPE = 6,      /* unknown tile_gemm_dtype_t */
   TILE_GEMM_ERR_DEVICE = 7,     /* no such device, not gfx950, or not the current device */
   TILE_GEMM_ERR_HIP = 8,        /* the HIP runtime refused a call or a launch */
-  TILE_GEMM_ERR_EPILOGUE = 9    /* unknown activation in a fused epilogue */
+  TILE_GEMM_ERR_EPILOGUE = 9,   /* unknown activation in a fused epilogue */
+  TILE_GEMM_ERR_WORKSPACE = 10  /* workspace NULL, not 256-byte aligned or too small */
 } tile_gemm_status_t;
 
 /* Input is always bf16 with fp32 accumulation; the enum picks the output. */
@@ -222,6 +223,118 @@ tile_gemm_status_t tile_gemm_run_mx(tile_gemm_t h, const void* A, const void* B,
                                     const float* bias, tile_gemm_act_t act, void* stream);
 
 /*
+ * Gated block: C = act(A . B_gate + bias_gate) * (A . B_up + bias_up) over a
+ * merged gate+up B, the product of TILE_GEMM_ACT_SWIGLU with a choice of the
+ * gate's activation (TILE_GEMM_GATE_SILU is that act). One kernel: both
+ * projections, the activation and the product; shapes, layouts, types, bias,
+ * errors and ownership as for tile_gemm_run_epilogue with that act.
+ */
+typedef enum {
+  TILE_GEMM_GATE_SILU = 0,      /* x / (1 + e^-x) */
+  TILE_GEMM_GATE_GELU = 1,      /* x Phi(x), Phi the normal distribution function */
+  TILE_GEMM_GATE_GELU_TANH = 2, /* x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+  TILE_GEMM_GATE_RELU = 3,      /* max(x, 0); derivative 0 at 0 */
+  TILE_GEMM_GATE_SIGMOID = 4    /* 1 / (1 + e^-x) */
+} tile_gemm_gate_t;
+
+tile_gemm_status_t tile_gemm_run_glu(tile_gemm_t h, const void* A, const void* B, void* C,
+                                     int64_t M, int64_t N, int64_t K,
+                                     const tile_gemm_strides_t* strides, tile_gemm_dtype_t dtype,
+                                     const float* bias, tile_gemm_gate_t gate, void* stream);
+
+/*
+ * Backward pass of tile_gemm_run_glu. With z = A . B + bias, its gate half zg
+ * and its up half zu,
+ *   dzg = dC * zu * act'(zg),  dzu = dC * act(zg),
+ *   dA = dz . B^T,  dB = A^T . dz,  dbias = sum over rows of dz.
+ * A (M x K), dC (M x N/2) and dA (M x K) are bf16 and row-major, B and dB
+ * (K x N) bf16 and column-major (b_k = 1: the usual storage of weights, N rows
+ * of K), bias and dbias N fp32 values. N counts gate and up columns (a
+ * multiple of 16). z is computed again from A and B, so nothing has to be
+ * kept from the forward pass. dz is held in bf16 between the products; sums
+ * run in fp32 in a fixed order (results are bit-identical run to run).
+ * `strides` gives a_m, a_k of A and b_k, b_n of B (c_* are ignored);
+ * `grad_strides` the a_* of dA, b_* of dB and c_* of dC. dA, dB and dbias may
+ * each be NULL (not all three); bias may be NULL and dbias still be asked for.
+ * With M = 0 or N = 0 the gradients are zero.
+ *
+ * `workspace` is device memory of at least tile_gemm_glu_backward_workspace
+ * bytes, 256-byte aligned, this call's own until the stream has passed it:
+ * calls that may run at the same time need one each. Enqueue-only, allocates
+ * nothing, may be captured.
+ * Limits: M, N and K below 2^22, b_n below 2^22, A, B, dC, dA and dB each
+ * below 4 GiB. Errors as for tile_gemm_run_epilogue, plus
+ * TILE_GEMM_ERR_WORKSPACE; written arguments may overlap no other argument.
+ */
+tile_gemm_status_t tile_gemm_run_glu_backward(tile_gemm_t h, const void* A, const void* B,
+                                              const void* dC, void* dA, void* dB, int64_t M,
+                                              int64_t N, int64_t K,
+                                              const tile_gemm_strides_t* strides,
+                                              const tile_gemm_strides_t* grad_strides,
+                                              const float* bias, float* dbias,
+                                              tile_gemm_gate_t gate, void* workspace,
+                                              int64_t workspace_bytes, void* stream);
+
+/*
+ * Cross entropy of the projection l = A . B onto a vocabulary of N columns,
+ * without storing the logits l. Per row i with target t = target[i]:
+ *   lse[i]  = log sum_j e^(l_ij)
+ *   loss[i] = lse[i] - (1 - s) l_it - (s / N) sum_j l_ij + z lse[i]^2
+ * with s = label_smoothing and z = z_loss. A row whose target is ignore_index
+ * has loss 0 (its lse is still given); any other target outside [0, N) gives
+ * loss NaN. Every tile of l is turned into per-row maxima and sums by the
+ * workgroup that owns it and the pieces are joined in a fixed order: results
+ * are bit-identical run to run. A few rows stream B once.
+ *
+ * A is M x K, bf16, row-major; B K x N, bf16, column-major (b_k = 1; the usual
+ * storage of weights, N rows of K); target M int32 or int64 values; loss and
+ * lse M fp32 values each (either may be NULL). B may span 4 GiB or more.
+ * M = 0 is a no-op; N and K must be at least 1.
+ */
+typedef enum { TILE_GEMM_INDEX_I32 = 0, TILE_GEMM_INDEX_I64 = 1 } tile_gemm_index_t;
+
+typedef struct {
+  int64_t ignore_index;
+  float label_smoothing; /* in [0, 1] */
+  float z_loss;          /* >= 0 */
+  int64_t piece;         /* backward: at most this many vocabulary columns at a time; 0: chosen */
+  int32_t target_type;   /* tile_gemm_index_t */
+} tile_gemm_xent_t;
+
+tile_gemm_status_t tile_gemm_run_xent(tile_gemm_t h, const void* A, const void* B,
+                                      const void* target, float* loss, float* lse, int64_t M,
+                                      int64_t N, int64_t K, const tile_gemm_strides_t* strides,
+                                      const tile_gemm_xent_t* options, void* workspace,
+                                      int64_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of sum_i dloss[i] loss[i] for that loss, from the lse that
+ * tile_gemm_run_xent gave for the same A, B and options:
+ *   G_ij = dloss[i] ((1 + 2 z lse[i]) e^(l_ij - lse[i]) - (1 - s) [j = t] - s / N)
+ *   dA = G . B^T,  dB = A^T . G
+ * (a zero row of G where the target is ignore_index). The logits are computed
+ * again, `piece` columns of the vocabulary at a time, and never stored; G is
+ * held in bf16 for one piece, scaled by the largest |dloss|, which is
+ * multiplied onto the fp32 sums at the end. dloss is M fp32 values (a mean over n
+ * rows: 1 / n each). dA (M x K) and dB (K x N, column-major) are bf16; either
+ * may be NULL. M = 0 makes dB zero. A row of A that holds infinities or NaN
+ * makes dB NaN even where the row is ignored (0 * NaN).
+ *
+ * Limits of both: M, K and b_n below 2^22, A and dA below 4 GiB. Workspaces,
+ * errors and ownership as for tile_gemm_run_glu_backward; the workspace sizes
+ * are those of tile_gemm_xent_workspace and tile_gemm_xent_backward_workspace
+ * for the same shape, strides and options.
+ */
+tile_gemm_status_t tile_gemm_run_xent_backward(tile_gemm_t h, const void* A, const void* B,
+                                               const void* target, const float* lse,
+                                               const float* dloss, void* dA, void* dB, int64_t M,
+                                               int64_t N, int64_t K,
+                                               const tile_gemm_strides_t* strides,
+                                               const tile_gemm_strides_t* grad_strides,
+                                               const tile_gemm_xent_t* options, void* workspace,
+                                               int64_t workspace_bytes, void* stream);
+
+/*
  * Release a handle (host memory only). NULL is accepted and returns OK.
  * Source: the counterpart of the one-time preparation ("Rust Compute
  * Kernels", section "Quick example"); it touches no device memory, since the
@@ -278,6 +391,43 @@ tile_gemm_status_t tile_gemm_check_mx(const void* A, const void* B, const void* 
                                       int64_t scale_stride, tile_gemm_mx_format_t fmt,
                                       tile_gemm_dtype_t dtype, const float* bias,
                                       tile_gemm_act_t act);
+
+/*
+ * Workspace bytes of the calls above on the handle's device (h == NULL: an
+ * MI355X). A call that leaves out some gradients needs no more than these.
+ */
+tile_gemm_status_t tile_gemm_glu_backward_workspace(tile_gemm_t h, int64_t M, int64_t N, int64_t K,
+                                                    int64_t* bytes);
+tile_gemm_status_t tile_gemm_xent_workspace(tile_gemm_t h, int64_t M, int64_t N, int64_t K,
+                                            const tile_gemm_xent_t* options, int64_t* bytes);
+tile_gemm_status_t tile_gemm_xent_backward_workspace(tile_gemm_t h, int64_t M, int64_t N, int64_t K,
+                                                     const tile_gemm_strides_t* strides,
+                                                     const tile_gemm_xent_t* options,
+                                                     int64_t* bytes);
+
+/* The checks those calls perform before any launch (with an MI355X's
+ * workspace sizes), with the same results. */
+tile_gemm_status_t tile_gemm_check_glu_backward(const void* A, const void* B, const void* dC,
+                                                const void* dA, const void* dB, int64_t M,
+                                                int64_t N, int64_t K,
+                                                const tile_gemm_strides_t* strides,
+                                                const tile_gemm_strides_t* grad_strides,
+                                                const float* bias, const float* dbias,
+                                                tile_gemm_gate_t gate, const void* workspace,
+                                                int64_t workspace_bytes);
+tile_gemm_status_t tile_gemm_check_xent(const void* A, const void* B, const void* target,
+                                        const float* loss, const float* lse, int64_t M, int64_t N,
+                                        int64_t K, const tile_gemm_strides_t* strides,
+                                        const tile_gemm_xent_t* options, const void* workspace,
+                                        int64_t workspace_bytes);
+tile_gemm_status_t tile_gemm_check_xent_backward(const void* A, const void* B, const void* target,
+                                                 const float* lse, const float* dloss,
+                                                 const void* dA, const void* dB, int64_t M,
+                                                 int64_t N, int64_t K,
+                                                 const tile_gemm_strides_t* strides,
+                                                 const tile_gemm_strides_t* grad_strides,
+                                                 const tile_gemm_xent_t* options,
+                                                 const void* workspace, int64_t workspace_bytes);
 
 /* Kernel variants the planner chooses between. */
 typedef enum {

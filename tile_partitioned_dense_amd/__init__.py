@@ -17,6 +17,10 @@ fallback path.
 __all__ = ["tile_gemm_create", "tile_gemm_run", "tile_gemm_run_debug", "tile_gemm_run_epilogue",
            "tile_gemm_check_epilogue", "Act", "tile_gemm_destroy", "tile_gemm_run_mx",
            "tile_gemm_check_mx", "tile_gemm_plan_mx", "N_MX_CONFIGS", "MX_E4M3", "MX_E2M1", "VARIANT_MX",
+           "tile_gemm_run_glu", "tile_gemm_run_glu_backward", "tile_gemm_glu_backward_workspace",
+           "tile_gemm_check_glu_backward", "Gate", "tile_gemm_run_xent", "tile_gemm_xent_workspace",
+           "tile_gemm_check_xent", "tile_gemm_run_xent_backward", "tile_gemm_xent_backward_workspace",
+           "tile_gemm_check_xent_backward", "XentOptions", "IndexType",
            "tile_gemm_status_str", "tile_gemm_check_args", "tile_gemm_plan",
            "tile_gemm_tile_of", "TileGemm", "TileGemmError", "Status", "Dtype",
            "Strides", "Plan", "library_path", "load_library", "last_error_detail",

@@ -27,6 +27,7 @@ class Status(enum.IntEnum):
     ERR_DEVICE = 7
     ERR_HIP = 8
     ERR_EPILOGUE = 9
+    ERR_WORKSPACE = 10
 
 
 class Dtype(enum.IntEnum):
@@ -41,6 +42,20 @@ class Act(enum.IntEnum):
     TANH = 3
     SILU = 4
     SWIGLU = 5
+
+
+class Gate(enum.IntEnum):
+    """Activation of a gated block's gate half (tile_gemm_gate_t)."""
+    SILU = 0
+    GELU = 1
+    GELU_TANH = 2
+    RELU = 3
+    SIGMOID = 4
+
+
+class IndexType(enum.IntEnum):
+    I32 = 0
+    I64 = 1
 
 
 DEBUG_COUNT_WRITES = 1
@@ -92,6 +107,12 @@ class Plan(ctypes.Structure):
 
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class XentOptions(ctypes.Structure):
+    """Options of the cross entropy (tile_gemm_xent_t)."""
+    _fields_ = [("ignore_index", ctypes.c_int64), ("label_smoothing", ctypes.c_float),
+                ("z_loss", ctypes.c_float), ("piece", ctypes.c_int64), ("target_type", ctypes.c_int32)]
 
 
 class TileGemmError(RuntimeError):
@@ -151,6 +172,26 @@ def load_library():
     lib.tile_gemm_check_mx.argtypes = [vp, vp, vp, i64, i64, i64, P(Strides), vp, vp, i64, i32, i32,
                                        vp, i32]
     lib.tile_gemm_check_mx.restype = i32
+    PX = P(XentOptions)
+    lib.tile_gemm_run_glu.argtypes = [vp, vp, vp, vp, i64, i64, i64, P(Strides), i32, vp, i32, vp]
+    lib.tile_gemm_run_glu_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, P(Strides),
+                                               P(Strides), vp, vp, i32, vp, i64, vp]
+    lib.tile_gemm_check_glu_backward.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, P(Strides),
+                                                 P(Strides), vp, vp, i32, vp, i64]
+    lib.tile_gemm_glu_backward_workspace.argtypes = [vp, i64, i64, i64, P(i64)]
+    lib.tile_gemm_run_xent.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, P(Strides), PX, vp,
+                                       i64, vp]
+    lib.tile_gemm_check_xent.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, P(Strides), PX, vp, i64]
+    lib.tile_gemm_xent_workspace.argtypes = [vp, i64, i64, i64, PX, P(i64)]
+    lib.tile_gemm_run_xent_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64,
+                                                P(Strides), P(Strides), PX, vp, i64, vp]
+    lib.tile_gemm_check_xent_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64,
+                                                  P(Strides), P(Strides), PX, vp, i64]
+    lib.tile_gemm_xent_backward_workspace.argtypes = [vp, i64, i64, i64, P(Strides), PX, P(i64)]
+    for name in ("run_glu", "run_glu_backward", "check_glu_backward", "glu_backward_workspace",
+                 "run_xent", "check_xent", "xent_workspace", "run_xent_backward",
+                 "check_xent_backward", "xent_backward_workspace"):
+        getattr(lib, "tile_gemm_" + name).restype = i32
     lib.tile_gemm_tile_of.argtypes = [P(Plan), i64, i64, i64, P(i64), P(i64), P(i64), P(i64)]
     lib.tile_gemm_tile_of.restype = i32
     _lib = lib
@@ -383,6 +424,252 @@ def tile_gemm_run_mx(h, A, Bt, C, a_scale, b_scale, bias=None, act=Act.NONE, str
     return Status(st)
 
 
+# ------------------------------------------------ gated block, cross entropy
+
+def _ptr(x):
+    return x.data_ptr() if _is_tensor(x) else x
+
+
+def _matrix(name, t, shape):
+    """A 2-D bf16 tensor of the given shape (sizes None: any); its strides."""
+    import torch
+    if not _is_tensor(t):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.dim() != 2 or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, "
+                         f"got {tuple(t.shape)}")
+    return t.stride()
+
+
+def _vector(name, t, n, dtypes):
+    if not _is_tensor(t):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} values, got shape "
+                         f"{tuple(t.shape)} strides {tuple(t.stride())}")
+
+
+def _col_major_strides(K, b):
+    """(b_k, b_n) of a column-major K x N operand; a unit axis has no stride of
+    its own, so torch may report any value for it."""
+    b_k, b_n = b.stride()
+    if K == 1:
+        b_k = 1
+    if b.shape[1] <= 1:
+        b_n = max(b_n, K)
+    return b_k, b_n
+
+
+def _unit(t):
+    """The column stride of a row-major matrix (1 where there is one column)."""
+    return 1 if t.shape[1] <= 1 else t.stride(1)
+
+
+class _Workspace:
+    """The caller's workspace (any contiguous tensor on the device), or one
+    allocated for the call and kept by torch until the stream has passed it."""
+
+    def __init__(self, given, nbytes, device, stream):
+        import torch
+        if given is not None:
+            if not _is_tensor(given) or not given.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor")
+            _check_devices((("workspace", given),))
+            self.tensor, self.nbytes = given, given.numel() * given.element_size()
+        else:
+            self.tensor = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+            self.nbytes = nbytes
+            if stream is not None:
+                raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+                if raw != torch.cuda.current_stream(device).cuda_stream:
+                    if not hasattr(stream, "cuda_stream"):
+                        stream = torch.cuda.ExternalStream(raw, device=device)
+                    self.tensor.record_stream(stream)
+                    # the block may have been freed on the current stream
+                    # while work queued there still uses it
+                    stream.wait_stream(torch.cuda.current_stream(device))
+        self.ptr = self.tensor.data_ptr()
+
+
+def tile_gemm_run_glu(h, A, B, C, gate=Gate.SILU, bias=None, stream=None, check: bool = True):
+    """Enqueue the gated block C := act(A.B_gate + b_gate) * (A.B_up + b_up)
+    (torch tensors; B is K x N with the N/2 gate columns first, either layout;
+    C is M x N/2, float32 or bfloat16)."""
+    a, b, c, M, N, K, s, dt = _operands(A, B, C, None, None, None, None, None, 2)
+    _check_bias(bias, N)
+    _check_devices((("A", A), ("B", B), ("C", C), ("bias", bias)))
+    if M == 1:  # the stride of a single row is never used
+        s.a_m, s.c_m = (K + 7) // 8 * 8, (N // 2 + 7) // 8 * 8
+    st = load_library().tile_gemm_run_glu(h, a, b, c, M, N, K, ctypes.byref(s), dt, _ptr(bias),
+                                          int(gate), _stream_ptr(stream, C))
+    if check:
+        _raise_if(st)
+    return Status(st)
+
+
+def tile_gemm_glu_backward_workspace(h, M, N, K) -> int:
+    """Workspace bytes of tile_gemm_run_glu_backward (h None: an MI355X)."""
+    n = ctypes.c_int64()
+    _raise_if(load_library().tile_gemm_glu_backward_workspace(h, int(M), int(N), int(K),
+                                                              ctypes.byref(n)))
+    return n.value
+
+
+def tile_gemm_run_glu_backward(h, A, B, dC, dA=None, dB=None, gate=Gate.SILU, bias=None, dbias=None,
+                               workspace=None, stream=None, check: bool = True):
+    """Enqueue the backward pass of the gated block (torch tensors): dA (M x K),
+    dB (K x N, column-major like B) and dbias (N float32) from dC (M x N/2);
+    any of the three may be left out. Without `workspace` one is allocated for
+    the call."""
+    import torch
+    a_m, _ = _matrix("A", A, (None, None))
+    M, K = A.shape
+    _matrix("B", B, (K, None))
+    N = B.shape[1]
+    c_m, _ = _matrix("dC", dC, (M, N // 2))
+    s = Strides(a_m, _unit(A), *_col_major_strides(K, B), 0, 0)
+    g = Strides(0, 1, 1, 0, c_m, _unit(dC))
+    if dA is not None:
+        g.a_m, _ = _matrix("dA", dA, (M, K))
+        g.a_k = _unit(dA)
+    if dB is not None:
+        _matrix("dB", dB, (K, N))
+        g.b_k, g.b_n = _col_major_strides(K, dB)
+    _check_bias(bias, N)
+    if dbias is not None:
+        _vector("dbias", dbias, N, (torch.float32,))
+    _check_devices((("A", A), ("B", B), ("dC", dC), ("dA", dA), ("dB", dB), ("bias", bias),
+                    ("dbias", dbias)))
+    need = 0 if workspace is not None else tile_gemm_glu_backward_workspace(h, M, N, K)
+    ws = _Workspace(workspace, need, A.device, stream)
+    st = load_library().tile_gemm_run_glu_backward(
+        h, _ptr(A), _ptr(B), _ptr(dC), _ptr(dA), _ptr(dB), M, N, K, ctypes.byref(s), ctypes.byref(g),
+        _ptr(bias), _ptr(dbias), int(gate), ws.ptr, ws.nbytes, _stream_ptr(stream, A))
+    if check:
+        _raise_if(st)
+    return Status(st)
+
+
+def _xent_operands(A, B, target, ignore_index, label_smoothing, z_loss, piece):
+    import torch
+    a_m, _ = _matrix("A", A, (None, None))
+    M, K = A.shape
+    _matrix("B", B, (K, None))
+    _vector("target", target, M, (torch.int64, torch.int32))
+    s = Strides(a_m, _unit(A), *_col_major_strides(K, B), 0, 0)
+    o = XentOptions(int(ignore_index), float(label_smoothing), float(z_loss), int(piece),
+                    IndexType.I64 if target.dtype == torch.int64 else IndexType.I32)
+    return M, B.shape[1], K, s, o
+
+
+def tile_gemm_xent_workspace(h, M, N, K, label_smoothing=0.0) -> int:
+    """Workspace bytes of tile_gemm_run_xent (h None: an MI355X)."""
+    n = ctypes.c_int64()
+    o = XentOptions(0, float(label_smoothing), 0.0, 0, 0)
+    _raise_if(load_library().tile_gemm_xent_workspace(h, int(M), int(N), int(K), ctypes.byref(o),
+                                                      ctypes.byref(n)))
+    return n.value
+
+
+def tile_gemm_run_xent(h, A, B, target, loss=None, lse=None, ignore_index=-100, label_smoothing=0.0,
+                       z_loss=0.0, workspace=None, stream=None, check: bool = True):
+    """Enqueue the per-row cross entropy of the projection A.B onto B's N
+    columns (torch tensors; B K x N column-major): loss and lse, M float32
+    values each, without storing the logits."""
+    import torch
+    M, N, K, s, o = _xent_operands(A, B, target, ignore_index, label_smoothing, z_loss, 0)
+    for name, t in (("loss", loss), ("lse", lse)):
+        if t is not None:
+            _vector(name, t, M, (torch.float32,))
+    _check_devices((("A", A), ("B", B), ("target", target), ("loss", loss), ("lse", lse)))
+    need = 0 if workspace is not None else tile_gemm_xent_workspace(h, M, N, K, label_smoothing)
+    ws = _Workspace(workspace, need, A.device, stream)
+    st = load_library().tile_gemm_run_xent(h, _ptr(A), _ptr(B), _ptr(target), _ptr(loss), _ptr(lse), M,
+                                           N, K, ctypes.byref(s), ctypes.byref(o), ws.ptr, ws.nbytes,
+                                           _stream_ptr(stream, A))
+    if check:
+        _raise_if(st)
+    return Status(st)
+
+
+def tile_gemm_xent_backward_workspace(h, M, N, K, b_n=None, piece=0) -> int:
+    """Workspace bytes of tile_gemm_run_xent_backward (h None: an MI355X) for a
+    B whose columns are b_n elements apart (None: K)."""
+    n = ctypes.c_int64()
+    s = Strides(0, 1, 1, int(K if b_n is None else b_n), 0, 0)
+    o = XentOptions(0, 0.0, 0.0, int(piece), 0)
+    _raise_if(load_library().tile_gemm_xent_backward_workspace(h, int(M), int(N), int(K), ctypes.byref(s),
+                                                               ctypes.byref(o), ctypes.byref(n)))
+    return n.value
+
+
+def tile_gemm_run_xent_backward(h, A, B, target, lse, dloss, dA=None, dB=None, ignore_index=-100,
+                                label_smoothing=0.0, z_loss=0.0, piece=0, workspace=None, stream=None,
+                                check: bool = True):
+    """Enqueue the gradients dA (M x K) and dB (K x N, column-major like B) of
+    sum(dloss * loss) from tile_gemm_run_xent's lse; either may be left out.
+    `piece`: at most this many vocabulary columns at a time (0: chosen)."""
+    import torch
+    M, N, K, s, o = _xent_operands(A, B, target, ignore_index, label_smoothing, z_loss, piece)
+    _vector("lse", lse, M, (torch.float32,))
+    _vector("dloss", dloss, M, (torch.float32,))
+    g = Strides(0, 1, 1, 0, 0, 1)
+    if dA is not None:
+        g.a_m, _ = _matrix("dA", dA, (M, K))
+        g.a_k = _unit(dA)
+    if dB is not None:
+        _matrix("dB", dB, (K, N))
+        g.b_k, g.b_n = _col_major_strides(K, dB)
+    _check_devices((("A", A), ("B", B), ("target", target), ("lse", lse), ("dloss", dloss), ("dA", dA),
+                    ("dB", dB)))
+    need = 0
+    if workspace is None:
+        need = tile_gemm_xent_backward_workspace(h, M, N, K, s.b_n, piece)
+    ws = _Workspace(workspace, need, A.device, stream)
+    st = load_library().tile_gemm_run_xent_backward(
+        h, _ptr(A), _ptr(B), _ptr(target), _ptr(lse), _ptr(dloss), _ptr(dA), _ptr(dB), M, N, K,
+        ctypes.byref(s), ctypes.byref(g), ctypes.byref(o), ws.ptr, ws.nbytes, _stream_ptr(stream, A))
+    if check:
+        _raise_if(st)
+    return Status(st)
+
+
+def _strides(s):
+    return s if s is None or isinstance(s, Strides) else Strides(*s)
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def tile_gemm_check_glu_backward(A, B, dC, dA, dB, M, N, K, strides, grad_strides, bias=None, dbias=None,
+                                 gate=Gate.SILU, workspace=None, workspace_bytes=0) -> Status:
+    """Host-only checks of tile_gemm_run_glu_backward's arguments (pointers are integers)."""
+    return Status(load_library().tile_gemm_check_glu_backward(
+        A, B, dC, dA, dB, int(M), int(N), int(K), _ref(_strides(strides)), _ref(_strides(grad_strides)), bias,
+        dbias, int(gate), workspace, int(workspace_bytes)))
+
+
+def tile_gemm_check_xent(A, B, target, loss, lse, M, N, K, strides, options, workspace=None,
+                         workspace_bytes=0) -> Status:
+    """Host-only checks of tile_gemm_run_xent's arguments (pointers are integers)."""
+    return Status(load_library().tile_gemm_check_xent(
+        A, B, target, loss, lse, int(M), int(N), int(K), _ref(_strides(strides)), _ref(options), workspace,
+        int(workspace_bytes)))
+
+
+def tile_gemm_check_xent_backward(A, B, target, lse, dloss, dA, dB, M, N, K, strides, grad_strides, options,
+                                  workspace=None, workspace_bytes=0) -> Status:
+    """Host-only checks of tile_gemm_run_xent_backward's arguments (pointers are integers)."""
+    return Status(load_library().tile_gemm_check_xent_backward(
+        A, B, target, lse, dloss, dA, dB, int(M), int(N), int(K), _ref(_strides(strides)),
+        _ref(_strides(grad_strides)), _ref(options), workspace, int(workspace_bytes)))
+
+
 def tile_gemm_check_mx(A, B, C, M, N, K, strides, a_scale, b_scale, scale_stride, dtype,
                        bias=None, act=Act.NONE, fmt=MX_E4M3) -> Status:
     """Host-only checks of tile_gemm_run_mx's arguments (pointers are integers)."""
@@ -450,6 +737,30 @@ class TileGemm:
         return tile_gemm_run_mx(self.handle, A, Bt, C, a_scale, b_scale, bias=bias,
                                 act=Act.NONE if act is None else act, stream=stream,
                                 counts=counts, flags=flags, fmt=fmt)
+
+    def glu(self, A, B, C, gate=Gate.SILU, bias=None, stream=None):
+        """Gated block (tile_gemm_run_glu) into C."""
+        return tile_gemm_run_glu(self.handle, A, B, C, gate=gate, bias=bias, stream=stream)
+
+    def glu_backward(self, A, B, dC, dA=None, dB=None, gate=Gate.SILU, bias=None, dbias=None,
+                     workspace=None, stream=None):
+        """Backward pass of the gated block (tile_gemm_run_glu_backward)."""
+        return tile_gemm_run_glu_backward(self.handle, A, B, dC, dA=dA, dB=dB, gate=gate, bias=bias,
+                                          dbias=dbias, workspace=workspace, stream=stream)
+
+    def xent(self, A, B, target, loss=None, lse=None, ignore_index=-100, label_smoothing=0.0,
+             z_loss=0.0, workspace=None, stream=None):
+        """Cross entropy of the projection A.B (tile_gemm_run_xent)."""
+        return tile_gemm_run_xent(self.handle, A, B, target, loss=loss, lse=lse,
+                                  ignore_index=ignore_index, label_smoothing=label_smoothing,
+                                  z_loss=z_loss, workspace=workspace, stream=stream)
+
+    def xent_backward(self, A, B, target, lse, dloss, dA=None, dB=None, ignore_index=-100,
+                      label_smoothing=0.0, z_loss=0.0, piece=0, workspace=None, stream=None):
+        """Gradients of the cross entropy (tile_gemm_run_xent_backward)."""
+        return tile_gemm_run_xent_backward(self.handle, A, B, target, lse, dloss, dA=dA, dB=dB,
+                                           ignore_index=ignore_index, label_smoothing=label_smoothing,
+                                           z_loss=z_loss, piece=piece, workspace=workspace, stream=stream)
 
     def close(self):
         if self.handle is not None:

@@ -29,6 +29,7 @@ ARCH = "gfx950"
 N_TILE_CONFIGS = 29
 N_SKINNY_CONFIGS = 6
 N_MX_CONFIGS = 8
+N_TRAIN_KERNELS = 46  # kernels_train.hip: products with the stores of train_epilogue.hpp
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
@@ -50,6 +51,10 @@ def _units():
     for i in range(N_MX_CONFIGS):
         units.append((f"kernels_mx_{i}", os.path.join(CSRC, "kernels_mx.hip"),
                       [f"-DTG_MX_CONFIG={i}"]))
+    for i in range(N_TRAIN_KERNELS):
+        units.append((f"kernels_train_{i}", os.path.join(CSRC, "kernels_train.hip"),
+                      [f"-DTG_TRAIN_KERNEL={i}"]))
+    units.append(("kernels_train_rows", os.path.join(CSRC, "kernels_train_rows.hip"), []))
     return units
 
 

@@ -297,6 +297,7 @@ const char* tile_gemm_status_str(tile_gemm_status_t s) {
     case TILE_GEMM_ERR_DEVICE: return "device unavailable, not gfx950, or not current";
     case TILE_GEMM_ERR_HIP: return "HIP runtime error";
     case TILE_GEMM_ERR_EPILOGUE: return "activation unknown or not available here";
+    case TILE_GEMM_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
   }
   return "unknown status";
 }

@@ -52,7 +52,7 @@
 // strip and all threads form silu(gate) * up for the BN / 2 output columns.
 #pragma once
 
-#include "tile_kernel.hpp"
+#include "train_epilogue.hpp"
 
 namespace tg {
 
@@ -70,8 +70,8 @@ __device__ __forceinline__ bf16x8 keep_first(const bf16x8& v, int valid) {
   return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-template <int BM, int BN, int SB, int NST, int KS, bool OUT_BF16, bool DEBUG>
-__global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(TileArgs p) {
+template <int BM, int BN, int SB, int NST, int KS, bool OUT_BF16, bool DEBUG, int EPI = kEpiNone>
+__global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(EpiArgs<EPI> p) {
   static_assert(BM == 16 || BM == 32 || BM == 64, "half a 32-row block, or one or two blocks");
   static_assert(BN % 64 == 0 && BN <= 256, "whole waves, even gate and up halves");
   static_assert(SB == 128 || SB == 256 || SB == 512, "stage rows of whole 128-byte lines");
@@ -113,7 +113,7 @@ __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(TileA
   const int64_t lda = p.lda, ldb = p.ldb;
   const int nss = (K + KST - 1) / KST;      // stages
   const int nfull = K / KST;                // stages wholly inside K
-  const int glu = p.glu_half;
+  const int glu = (EPI == kEpiNone || EPI == kEpiGlu) ? p.glu_half : 0;
   const int gshift = glu ? glu - BN / 2 : 0;
 
   auto swz = [](int r) { return SB >= 256 ? (r & 15) : ((r >> 1) & 7); };
@@ -281,7 +281,26 @@ __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(TileA
       wait_lgkmcnt0();
       block_barrier();
     }
-    if (glu) {
+    if constexpr (EPI == kEpiGlu) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if (kh == 0) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            lds_store_f4(ebuf + (uint32_t)(lrow * OPG + (32 * cb + 8 * q + 4 * lgrp) * 4),
+                         floatx4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]});
+        }
+        wait_lgkmcnt0();
+        block_barrier();
+        glu_strip<OUT_BF16, BR, BN / 2>(ebuf, OPG, m0 + 32 * i, n0, tid, NT, p);
+        wait_lgkmcnt0();
+        block_barrier();
+      }
+    } else if constexpr (EPI != kEpiNone) {
+      if (kh == 0)
+        train_store_32<EPI, FM>(acc, ebuf + (uint32_t)(cb * 32 * kStrip32), lane, m0, n0 + 32 * cb,
+                                (int64_t)tn * NCB + cb, p);
+    } else if (glu) {
       const EpiOut eo{p.C, p.ldc, M, glu, p.bias, p.act, p.counts, p.flags};
 #pragma unroll
       for (int i = 0; i < FM; ++i) {

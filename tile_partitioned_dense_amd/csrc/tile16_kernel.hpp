@@ -39,7 +39,7 @@
 // within the 256 registers a wave has at two waves per SIMD.
 #pragma once
 
-#include "tile_kernel.hpp"
+#include "train_epilogue.hpp"
 
 namespace tg {
 
@@ -119,8 +119,9 @@ __device__ __forceinline__ void pin_row(floatx4 (&row)[FN]) {
   for (int j = 0; j < FN; ++j) asm volatile("" : "+a"(row[j]));
 }
 
-template <int BM, int BN, int WM, int WN, int NST, bool BCOL, bool OUT_BF16, bool DEBUG>
-__global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(TileArgs p) {
+template <int BM, int BN, int WM, int WN, int NST, bool BCOL, bool OUT_BF16, bool DEBUG,
+          int EPI = kEpiNone>
+__global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(EpiArgs<EPI> p) {
   constexpr int kStages = NST;
   static_assert(NST >= 3 && NST <= 6, "ring depth");
   constexpr int NW = WM * WN;
@@ -162,8 +163,15 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(TileArgs p
   const int tG = lane >> 4, tj = (lane >> 2) & 3, tq = lane & 3;
 
   const int n_tiles = p.map.tiles_m * p.map.tiles_n;
-  for (int wg_it = blockIdx.x; wg_it < n_tiles; wg_it += gridDim.x) {
+  int n_work = n_tiles;
+  if constexpr (EPI == kEpiPartial) n_work *= p.splits;  // every tile once for each part of K
+  for (int wg_it = blockIdx.x; wg_it < n_work; wg_it += gridDim.x) {
     int wg = wg_it;
+    [[maybe_unused]] int part = 0;
+    if constexpr (EPI == kEpiPartial) {
+      part = wg_it / n_tiles;
+      wg = wg_it - part * n_tiles;
+    }
     if constexpr (DEBUG) {
       if ((p.flags & kDbgCollide) && wg == 1) wg = 0;  // negative control only
     }
@@ -174,16 +182,36 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(TileArgs p
     // it drains every load at the loop's head; settled here, once per tile,
     // the loop keeps only its own waits.
     if constexpr (TIED) wait_vmcnt<0>();
-    const int M = p.M, N = p.N, K = p.K;
+    const int M = p.M, N = p.N;
     const int64_t lda = p.lda, ldb = p.ldb;
-    const int glu = p.glu_half;
+    const int glu = (EPI == kEpiNone || epi_gated(EPI)) ? p.glu_half : 0;
     const int gshift = glu ? glu - BN / 2 : 0;
     const int m0 = tm * BM, n0 = tn * (glu ? BN / 2 : BN);
+    // this part of K (kEpiPartial: a whole number of slabs but for the last part)
+    int K = p.K;
+    const uint16_t *pA = p.A, *pB = p.B;
+    if constexpr (EPI == kEpiPartial) {
+      const int k_lo = part * p.k_per;
+      pA += k_lo;
+      pB += BCOL ? (int64_t)k_lo : (int64_t)k_lo * ldb;
+      K = tg_min(p.k_per, K - k_lo);
+    }
+    // B column of tile column r: gate columns in the first half of the tile
+    // and up columns in the second, or (gated stores) in the two halves of
+    // every wave's columns, so that one lane holds both pre-activations
+    auto b_col = [&](int r) {
+      if constexpr (epi_gated(EPI)) {
+        const int w = r / WTN, c = r - (r / WTN) * WTN;
+        return w * (WTN / 2) + (c >= WTN / 2 ? c - WTN / 2 + glu : c);
+      } else {
+        return r + (r >= BN / 2 ? gshift : 0);
+      }
+    };
 
     // ---- panels, their valid extents (to the operand's last element), steps
-    const char* a_panel = reinterpret_cast<const char*>(p.A + (int64_t)m0 * lda);
+    const char* a_panel = reinterpret_cast<const char*>(pA + (int64_t)m0 * lda);
     const int64_t a_bytes = K > 0 ? (((int64_t)(M - 1) * lda + K) - (int64_t)m0 * lda) * 2 : 0;
-    const char* b_panel = reinterpret_cast<const char*>(BCOL ? p.B + (int64_t)n0 * ldb : p.B + n0);
+    const char* b_panel = reinterpret_cast<const char*>(BCOL ? pB + (int64_t)n0 * ldb : pB + n0);
     const int64_t b_bytes = K <= 0 ? 0
                             : BCOL ? (((int64_t)(N - 1) * ldb + K) - (int64_t)n0 * ldb) * 2
                                    : (((int64_t)(K - 1) * ldb + N) - n0) * 2;
@@ -207,12 +235,15 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(TileArgs p
       if constexpr (BCOL) {
         const int r = 16 * ins + (lane >> 2);
         const int c = (lane & 3) ^ swz16(r);
-        voB[t] = (uint32_t)((r + (r >= BN / 2 ? gshift : 0)) * ldb * 2) + c * 16;
+        voB[t] = (uint32_t)(b_col(r) * ldb * 2) + c * 16;
       } else {
         const int q = 64 * ins + lane;
         const int row = q / CPR, pc = q - (q / CPR) * CPR;
         const int lc = swzB<CPR>(pc, row);  // the chunk that belongs at position pc
-        voB[t] = (uint32_t)(row * ldb * 2) + lc * 16 + (lc >= CPR / 2 ? 2 * gshift : 0);
+        if constexpr (epi_gated(EPI))
+          voB[t] = (uint32_t)(row * ldb * 2) + (uint32_t)(b_col(8 * lc) * 2);
+        else
+          voB[t] = (uint32_t)(row * ldb * 2) + lc * 16 + (lc >= CPR / 2 ? 2 * gshift : 0);
       }
     }
 
@@ -241,15 +272,15 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(TileArgs p
         uint4* dB = reinterpret_cast<uint4*>(reinterpret_cast<char*>(smem) + st * STAGE + A_BYTES);
         for (int q = tid; q < BM * 4; q += NT) {
           const int r = q >> 2, c = q & 3;
-          const uint4 v = (m0 + r < M) ? load8_masked(p.A + (int64_t)(m0 + r) * lda, k0 + 8 * c, K)
+          const uint4 v = (m0 + r < M) ? load8_masked(pA + (int64_t)(m0 + r) * lda, k0 + 8 * c, K)
                                        : make_uint4(0, 0, 0, 0);
           dA[r * 4 + (c ^ swz16(r))] = v;
         }
         if constexpr (BCOL) {
           for (int q = tid; q < BN * 4; q += NT) {
             const int r = q >> 2, c = q & 3;
-            const int col = n0 + r + (r >= BN / 2 ? gshift : 0);
-            const uint4 v = (col < N) ? load8_masked(p.B + (int64_t)col * ldb, k0 + 8 * c, K)
+            const int col = n0 + b_col(r);
+            const uint4 v = (col < N) ? load8_masked(pB + (int64_t)col * ldb, k0 + 8 * c, K)
                                       : make_uint4(0, 0, 0, 0);
             dB[r * 4 + (c ^ swz16(r))] = v;
           }
@@ -258,8 +289,8 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(TileArgs p
             const int row = q / CPR, pc = q - (q / CPR) * CPR;
             const int lc = swzB<CPR>(pc, row);
             const int gk = k0 + row;
-            const int col = n0 + 8 * lc + (lc >= CPR / 2 ? gshift : 0);
-            const uint4 v = (gk < K) ? load8_masked(p.B + (int64_t)gk * ldb, col, N)
+            const int col = n0 + (epi_gated(EPI) ? b_col(8 * lc) : 8 * lc + (lc >= CPR / 2 ? gshift : 0));
+            const uint4 v = (gk < K) ? load8_masked(pB + (int64_t)gk * ldb, col, N)
                                      : make_uint4(0, 0, 0, 0);
             dB[row * CPR + pc] = v;
           }
@@ -563,43 +594,67 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(TileArgs p
     constexpr int CH = WTN * ESZ / 16;  // 16-byte chunks per staged row
     constexpr int EPC = 16 / ESZ;       // elements per chunk
     __syncthreads();  // every wave is done reading the ring
-    if (glu) {
-      constexpr int OPG = BN * 4 + 16;
-      static_assert(WM * SH * OPG <= RING, "a block-wide fp32 strip fits the ring");
-      static_assert(BN / 2 % 8 == 0 && BN / 2 / 4 <= NT, "whole output chunks per block row");
-      const EpiOut eo{p.C, p.ldc, M, glu, p.bias, p.act, p.counts, p.flags};
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          lds_store_f4(lds0 + (uint32_t)((wm * SH + l16) * OPG + (wn * WTN + 16 * j + 4 * lg) * 4),
-                       acc[i][j]);
-        __syncthreads();
-        store_staged_glu<OUT_BF16, DEBUG>(lds0, OPG, WM * SH, BN / 2, SH, WTM, m0 + 16 * i, n0, tid,
-                                          NT, eo);
-        __syncthreads();
-      }
-      continue;
-    }
-    if (p.bias != nullptr || p.act != kActNone) {
-      constexpr int OPF = WTN * 4 + 16;
-      static_assert(NW * SH * OPF <= RING, "an fp32 strip of every wave fits the ring");
-      static_assert(WTN / 4 <= 64, "one wave covers a staged row in 16-byte chunks");
-      const uint32_t stf = lds0 + (uint32_t)(wave * SH * OPF);
-      const EpiOut eo{p.C, p.ldc, M, N, p.bias, p.act, p.counts, p.flags};
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          lds_store_f4(stf + (uint32_t)(l16 * OPF + (16 * j + 4 * lg) * 4), acc[i][j]);
-        wait_lgkmcnt0();
-        store_staged_fused<OUT_BF16, DEBUG>(stf, OPF, SH, WTN, m0 + wm * WTM + 16 * i, n0 + wn * WTN,
-                                            lane, 64, eo);
-        wait_lgkmcnt0();
-      }
+    if constexpr (EPI != kEpiNone && EPI != kEpiPartial) {
+      // strip of 16 rows, private to the wave: bf16 values, or fp32 values of
+      // half as many columns
+      constexpr int TP = FN * 32 + 16;
+      static_assert(NW * SH * TP <= RING, "a strip of every wave fits the ring");
+      constexpr int WC = epi_gated(EPI) ? WTN / 2 : WTN;  // columns of C a wave covers
+      train_store<EPI, OUT_BF16>(acc, lds0 + (uint32_t)(wave * SH * TP), lane, m0 + wm * WTM, n0 + wn * WC,
+                       (int64_t)tn * WN + wn, tm * WM + wm, p, [](floatx4(&row)[FN]) {
+                         if constexpr (TIED) pin_row(row);
+                       });
       wait_lgkmcnt0();
       block_barrier();
       continue;
+    }
+    if constexpr (EPI == kEpiNone) {
+      if (glu) {
+        constexpr int OPG = BN * 4 + 16;
+        static_assert(WM * SH * OPG <= RING, "a block-wide fp32 strip fits the ring");
+        static_assert(BN / 2 % 8 == 0 && BN / 2 / 4 <= NT, "whole output chunks per block row");
+        const EpiOut eo{p.C, p.ldc, M, glu, p.bias, p.act, p.counts, p.flags};
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            lds_store_f4(lds0 + (uint32_t)((wm * SH + l16) * OPG + (wn * WTN + 16 * j + 4 * lg) * 4),
+                         acc[i][j]);
+          __syncthreads();
+          store_staged_glu<OUT_BF16, DEBUG>(lds0, OPG, WM * SH, BN / 2, SH, WTM, m0 + 16 * i, n0, tid,
+                                            NT, eo);
+          __syncthreads();
+        }
+        continue;
+      }
+      if (p.bias != nullptr || p.act != kActNone) {
+        constexpr int OPF = WTN * 4 + 16;
+        static_assert(NW * SH * OPF <= RING, "an fp32 strip of every wave fits the ring");
+        static_assert(WTN / 4 <= 64, "one wave covers a staged row in 16-byte chunks");
+        const uint32_t stf = lds0 + (uint32_t)(wave * SH * OPF);
+        const EpiOut eo{p.C, p.ldc, M, N, p.bias, p.act, p.counts, p.flags};
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            lds_store_f4(stf + (uint32_t)(l16 * OPF + (16 * j + 4 * lg) * 4), acc[i][j]);
+          wait_lgkmcnt0();
+          store_staged_fused<OUT_BF16, DEBUG>(stf, OPF, SH, WTN, m0 + wm * WTM + 16 * i, n0 + wn * WTN,
+                                              lane, 64, eo);
+          wait_lgkmcnt0();
+        }
+        wait_lgkmcnt0();
+        block_barrier();
+        continue;
+      }
+    }
+    // kEpiPartial: the bf16 result is scaled, a part's fp32 result goes to its
+    // own slice of C
+    float scale = 1.0f;
+    char* c_out = static_cast<char*>(p.C);
+    if constexpr (EPI == kEpiPartial) {
+      if (OUT_BF16 && p.scale) scale = *p.scale;
+      c_out += (int64_t)part * p.part_stride * ESZ;
     }
     const uint32_t stg = lds0 + (uint32_t)(wave * SH * OPITCH);
     const bool full_mn = (m0 + BM <= M) && (n0 + BN <= N);
@@ -608,7 +663,8 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(TileArgs p
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const uint32_t a = stg + (uint32_t)(l16 * OPITCH + (16 * j + 4 * lg) * ESZ);
-        const floatx4 v = acc[i][j];
+        floatx4 v = acc[i][j];
+        if constexpr (EPI == kEpiPartial && OUT_BF16) v *= scale;
         if constexpr (OUT_BF16) {
           const u32x2v w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
           *(__attribute__((address_space(3))) u32x2v*)(uintptr_t)a = w;
@@ -630,7 +686,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(TileArgs p
         const uint4 v = make_uint4(lv.x, lv.y, lv.z, lv.w);
         const int row = grow0 + r, col = gcol0 + ch * EPC;
         const int64_t off = (int64_t)row * p.ldc + col;
-        char* cbase = static_cast<char*>(p.C) + off * ESZ;
+        char* cbase = c_out + off * ESZ;
         if (full_mn || (row < M && col + EPC <= N)) {
           *reinterpret_cast<uint4*>(cbase) = v;
           if constexpr (DEBUG) {

@@ -369,3 +369,5 @@ tile_gemm_status_t tile_gemm_run_mx_debug(tile_gemm_t h, const void* A, const vo
 }
 
 }  // extern "C"
+
+#include "train_run.hpp"

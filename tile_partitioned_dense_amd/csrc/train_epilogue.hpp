@@ -1,0 +1,577 @@
+// train_epilogue.hpp -- the stores of the tile and stream kernels that belong
+// to the gated block's backward pass and to the cross entropy of a projection.
+//
+// Each is a dense product whose owned tile is not written as C but turned, in
+// the owning workgroup, into what the operator needs of it:
+//
+//   kEpiStats     logits l = x W^T of a large vocabulary: per row and segment
+//                 of columns the running maximum m and sum of e^(l - m), the
+//                 logit of the row's target, and (label smoothing) the sum of
+//                 the logits. The logits themselves are never written.
+//   kEpiXentGrad  the same logits computed again, turned into
+//                 G = a e^(l - lse) - u - b [column is the target]
+//                 (a, b, u: per row, see xent_rows_kernel).
+//   kEpiGluGrad   gate and up pre-activations z = x W^T + bias turned, with
+//                 the output gradient dh, into dz_gate = dh z_up act'(z_gate)
+//                 and dz_up = dh act(z_gate).
+//   kEpiGlu       the gated block's forward result act(z_gate) z_up, for the
+//                 gates that the plain kernels' store does not know.
+//   kEpiPartial   a gradient's product with K cut into `splits` parts: fp32
+//                 partial results of each part, or (one part) the bf16 result
+//                 times a device scalar.
+//
+// G and dz feed two products each: dx contracts their columns, dW their rows.
+// Both want the contracted axis contiguous, so they are written twice, as
+// rows and transposed: one more write of 2 bytes a value, where a transposing
+// product would need a second LDS layout and twice the LDS reads for A. Both
+// copies are the round-to-nearest-even bf16 of the same fp32 value, the form
+// the MFMA takes; the two gradients therefore carry one rounding of G besides
+// their own (both about 2^-9 of a value, independent).
+//
+// Everything is formed from the accumulator registers of one wave: lane l of
+// a 16-row block holds row l % 16, columns 16 j + 4 (l / 16) .. + 3 of block
+// j, so a row's maximum and sum are a loop over registers and two exchanges
+// across the lanes. No LDS traffic for kEpiStats; the gradients stage 16 (or
+// 32) rows of bf16 in a strip of LDS that is private to the wave.
+#pragma once
+
+#include <type_traits>
+
+#include "tile_kernel.hpp"
+
+namespace tg {
+
+constexpr int kEpiNone = 0, kEpiStats = 1, kEpiXentGrad = 2, kEpiGluGrad = 3, kEpiPartial = 4, kEpiGlu = 5;
+
+// A gated store can have its gate compiled in, EPI = kind + 16 (gate + 1): the
+// one-wave-per-SIMD kernel's 256 accumulators stay where the MFMAs left them
+// only if a single code path reads them (five of them made the compiler move
+// accumulators inside the K loop). The others take it from the arguments.
+constexpr int epi_kind(int epi) { return epi & 15; }
+constexpr int epi_gate(int epi) { return (epi >> 4) - 1; }
+constexpr int with_gate(int kind, int gate) { return kind + 16 * (gate + 1); }
+constexpr bool epi_gated(int epi) { return epi_kind(epi) == kEpiGluGrad || epi_kind(epi) == kEpiGlu; }
+
+// Per-row constants of kEpiXentGrad (xent_rows_kernel): lse * log2 e, a, b and
+// the target's column (-1: none).
+struct XentRow {
+  float lse2, a, b;
+  int32_t target;
+};
+
+struct TrainArgs : TileArgs {
+  // kEpiStats
+  const void* target;  // M targets, int32 or int64
+  int32_t target64;
+  float2* part;     // [segment][M]: maximum, sum
+  float* part_sum;  // [segment][M]: sum of the logits, or NULL
+  float* hit;       // [M]: the target's logit (rows without one are not written)
+  // kEpiXentGrad
+  const XentRow* rows;
+  int32_t first;  // vocabulary column of this piece's column 0
+  float smooth;   // u = b * smooth (label smoothing over the vocabulary size)
+  float keep;     // the target's share: b * keep is subtracted there
+  // kEpiXentGrad, kEpiGluGrad: the result as rows and transposed (either NULL)
+  uint16_t* Z;
+  int64_t ldz;
+  uint16_t* Zt;
+  int64_t ldzt;
+  // kEpiGluGrad
+  const uint16_t* dC;
+  int64_t lddc;
+  float* dbias_part;  // [tile row, wave row][2 F] column sums, or NULL
+  int32_t gate;
+  // kEpiPartial
+  int32_t splits, k_per;
+  int64_t part_stride;  // elements between the partial results
+  const float* scale;   // bf16 result: one fp32 value, or NULL
+};
+
+template <int EPI>
+using EpiArgs = std::conditional_t<EPI == kEpiNone, TileArgs, TrainArgs>;
+
+constexpr float kLog2e = 1.44269504088896341f;
+
+__device__ __forceinline__ float lane_xor(float v, int m) { return __shfl_xor(v, m, 64); }
+
+// Column of row `row`'s target, relative to `first`; a value no column has
+// where the row or its target is outside.
+__device__ __forceinline__ int target_col(const TrainArgs& p, int row, int first) {
+  if (row >= p.M) return -1;
+  const int64_t t = p.target64 ? static_cast<const int64_t*>(p.target)[row]
+                               : (int64_t) static_cast<const int32_t*>(p.target)[row];
+  return (t < first || t >= p.N) ? -1 : (int)(t - first);
+}
+
+// Maximum, sum of exponentials, (sum) and target of one row held as NJ groups
+// of four consecutive columns, group j at column step * j + 4 lg of a segment
+// that starts at column col0 (col0 < N); the lanes of a row differ in lg and
+// are joined by the given exchanges.
+template <int NJ, int X0, int X1>
+__device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, int col0, int row,
+                                          int64_t seg, const TrainArgs& p) {
+  const int left = p.N - col0 - 4 * lg;  // columns of this lane's groups inside the vocabulary
+  float sum = 0.0f;
+  if (p.part_sum) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += (step * j + e < left) ? v[j][e] : 0.0f;
+  }
+  float m = -INFINITY;
+  if (left >= step * (NJ - 1) + 4) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = fmaxf(m, v[j][e]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[j][e] = (step * j + e < left) ? v[j][e] : -INFINITY;
+        m = fmaxf(m, v[j][e]);
+      }
+  }
+  if constexpr (X0 > 0) m = fmaxf(m, lane_xor(m, X0));
+  m = fmaxf(m, lane_xor(m, X1));
+  const float m2 = m * kLog2e;
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(v[j][e], kLog2e, -m2));
+  if constexpr (X0 > 0) s += lane_xor(s, X0);
+  s += lane_xor(s, X1);
+  const int c = target_col(p, row, col0);
+  if (c >= 0 && c < step * NJ) {
+    // few rows have their target in this segment: the search is skipped by
+    // every other wave
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c == step * j + 4 * lg + e) p.hit[row] = v[j][e];
+  }
+  if (p.part_sum) {
+    if constexpr (X0 > 0) sum += lane_xor(sum, X0);
+    sum += lane_xor(sum, X1);
+  }
+  if (lg == 0 && row < p.M) {
+    p.part[seg * p.M + row] = make_float2(m, s);
+    if (p.part_sum) p.part_sum[seg * p.M + row] = sum;
+  }
+}
+
+// G of one logit (XentRow's constants). Rows that count for nothing (b = 0)
+// give an exact zero whatever their logits are.
+__device__ __forceinline__ float xent_grad(float l, int col, const XentRow& r, float u, float hit) {
+  const float g = fmaf(r.a, __builtin_amdgcn_exp2f(fmaf(l, kLog2e, -r.lse2)), -u) -
+                  (col == r.target ? hit : 0.0f);
+  return r.b == 0.0f ? 0.0f : g;
+}
+
+// act(z) and act'(z).
+//   silu     z s, s (1 + z (1 - s)) with s = 1 / (1 + e^-z)
+//   gelu     z P, P + z p with P the normal distribution function, p its
+//            density; P from the rational approximation of erfc(x) e^(x^2) by
+//            Hastings (Abramowitz and Stegun 7.1.26, error of erfc at most
+//            1.5e-7), which shares its exponential with p
+//   gelu_tanh  z (1 + t) / 2, t = tanh(y), y = c (z + 0.044715 z^3), written
+//            with s = 1 / (1 + e^-2y) = (1 + t) / 2: z s and
+//            s + z s (1 - s) 2 c (1 + 0.134145 z^2); in both this and silu
+//            the rounding of 1 - s near s = 1 is small against the slope of
+//            about 1 there
+//   relu     z, 1 for z > 0, else 0 (NaN stays)
+//   sigmoid  s, s (1 - s), 1 - s from its own exponential (it is the value)
+constexpr int kGateSilu = 0, kGateGelu = 1, kGateGeluTanh = 2, kGateRelu = 3, kGateSigmoid = 4;
+
+template <int GATE>
+__device__ __forceinline__ void gate_both(float z, float& act, float& slope) {
+  if constexpr (GATE == kGateSilu) {
+    const float s = sigmoid_hw(z);
+    act = z * s;
+    slope = s * fmaf(z, 1.0f - s, 1.0f);
+  } else if constexpr (GATE == kGateGelu) {
+    const float x = fabsf(z) * 0.70710678118654752f, ex = exp_hw(-x * x);
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    q *= 0.5f * t * ex;  // erfc(x) / 2
+    const float P = z < 0.0f ? q : 1.0f - q;
+    act = z * P;
+    slope = fmaf(z * 0.39894228040143268f, ex, P);
+  } else if constexpr (GATE == kGateGeluTanh) {
+    const float y2 = 1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f);
+    const float s = sigmoid_hw(y2);
+    act = z * s;
+    slope = fmaf(z * s, (1.0f - s) * (1.5957691216057308f * fmaf(0.134145f * z, z, 1.0f)), s);
+  } else if constexpr (GATE == kGateRelu) {
+    slope = z > 0.0f ? 1.0f : 0.0f;
+    act = z * slope;
+  } else {
+    const float s = sigmoid_hw(z);
+    act = s;
+    slope = s * sigmoid_hw(-z);
+  }
+}
+
+typedef uint32_t u32x2s __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void lds_store_u32x2(uint32_t addr, uint32_t a, uint32_t b) {
+  *(__attribute__((address_space(3))) u32x2s*)(uintptr_t)addr = u32x2s{a, b};
+}
+__device__ __forceinline__ uint32_t lds_load_u32(uint32_t addr) {
+  return *(const __attribute__((address_space(3))) uint32_t*)(uintptr_t)addr;
+}
+
+// Write a wave's strip of ROWS x COLS bf16 values (LDS address `strip`, row
+// pitch COLS * 2 + 16 bytes; rows grow0 ..) as rows of p.Z and transposed into
+// p.Zt. col_of(c) gives the output column of strip column c (a multiple of
+// 8's worth of columns stays together), or -1 where it is outside. Both
+// leading dimensions are padded (ldz to 8 columns, ldzt to 16 rows), so whole
+// chunks are written wherever their first value is inside; the padding is
+// never read. Rows: 16-byte chunks. Transposed: a lane takes two columns and
+// RPL consecutive rows, pairing rows of each column into dwords.
+template <int ROWS, int COLS, class ColOf>
+__device__ __forceinline__ void store_both(uint32_t strip, int lane, int grow0, const TrainArgs& p,
+                                           ColOf col_of) {
+  constexpr int PITCH = COLS * 2 + 16;
+  if (p.Z) {
+    constexpr int CH = COLS / 8;
+#pragma unroll
+    for (int c0 = 0; c0 < ROWS * CH; c0 += 64) {
+      const int c = c0 + lane;
+      if (ROWS * CH % 64 != 0 && c >= ROWS * CH) break;
+      const int r = c / CH, ch = c - (c / CH) * CH;
+      const u32x4s v =
+          *(const __attribute__((address_space(3))) u32x4s*)(uintptr_t)(strip + (uint32_t)(r * PITCH + ch * 16));
+      const int col = col_of(ch * 8), row = grow0 + r;
+      if (row < p.M && col >= 0) *reinterpret_cast<u32x4s*>(p.Z + (int64_t)row * p.ldz + col) = v;
+    }
+  }
+  if (p.Zt) {
+    constexpr int P = COLS / 2 < 64 ? COLS / 2 : 64;  // column pairs covered at once
+    constexpr int RG = 64 / P;                        // lanes sharing a pair
+    constexpr int RPL = ROWS / RG;                    // rows of each
+    static_assert(RPL == 4 || RPL == 8 || RPL == 16, "whole vector stores");
+    static_assert(COLS / 2 <= 64, "one pass over the columns");
+    const int pr = lane % P, rg = lane / P;
+    const int col = col_of((2 * pr) & ~7);
+    uint32_t d[RPL];
+#pragma unroll
+    for (int r = 0; r < RPL; ++r) d[r] = lds_load_u32(strip + (uint32_t)((rg * RPL + r) * PITCH + pr * 4));
+    const int row = grow0 + rg * RPL;
+    if (row < p.M && col >= 0) {
+      const int c = col + ((2 * pr) & 7);
+      uint32_t lo[RPL / 2], hi[RPL / 2];
+#pragma unroll
+      for (int r = 0; r < RPL / 2; ++r) {
+        lo[r] = pack_halves(d[2 * r], d[2 * r + 1], false);
+        hi[r] = pack_halves(d[2 * r], d[2 * r + 1], true);
+      }
+      uint16_t* z0 = p.Zt + (int64_t)c * p.ldzt + row;
+      uint16_t* z1 = z0 + p.ldzt;
+      if constexpr (RPL == 4) {
+        if (c < p.N) *reinterpret_cast<u32x2s*>(z0) = u32x2s{lo[0], lo[1]};
+        if (c + 1 < p.N) *reinterpret_cast<u32x2s*>(z1) = u32x2s{hi[0], hi[1]};
+      } else {
+#pragma unroll
+        for (int h = 0; h < RPL / 8; ++h) {
+          if (c < p.N)
+            reinterpret_cast<u32x4s*>(z0)[h] = u32x4s{lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]};
+          if (c + 1 < p.N)
+            reinterpret_cast<u32x4s*>(z1)[h] = u32x4s{hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]};
+        }
+      }
+    }
+  }
+}
+
+// kEpiGluGrad for one gate; see train_store.
+template <int GATE, int FM, int FN, class Pin>
+__device__ __forceinline__ void glu_grad_store(floatx4 (&acc)[FM][FN], uint32_t strip, int lane, int row0,
+                                               int col0, int wave_row, const TrainArgs& p, Pin pin) {
+  constexpr int H = FN / 2;
+  constexpr int PITCH = FN * 32 + 16;
+  const int l16 = lane & 15, lg = lane >> 4;
+  const int F = p.glu_half;
+  float db[FN][4];
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) db[j][e] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    pin(acc[i]);
+    const int row = row0 + 16 * i + l16;
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+      const int c = col0 + 16 * j + 4 * lg;
+      float dg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, du[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (row < p.M && c < F) {
+        const u32x2s dv = *reinterpret_cast<const u32x2s*>(p.dC + (int64_t)row * p.lddc + c);
+        const float dh[4] = {__uint_as_float(dv.x << 16), __uint_as_float(dv.x & 0xffff0000u),
+                             __uint_as_float(dv.y << 16), __uint_as_float(dv.y & 0xffff0000u)};
+        float bg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, bu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (p.bias) {
+          const float4 x = *reinterpret_cast<const float4*>(p.bias + c);
+          const float4 y = *reinterpret_cast<const float4*>(p.bias + F + c);
+          bg[0] = x.x; bg[1] = x.y; bg[2] = x.z; bg[3] = x.w;
+          bu[0] = y.x; bu[1] = y.y; bu[2] = y.z; bu[3] = y.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float act, slope;
+          gate_both<GATE>(acc[i][j][e] + bg[e], act, slope);
+          dg[e] = dh[e] * (acc[i][j + H][e] + bu[e]) * slope;
+          du[e] = dh[e] * act;
+          db[j][e] += dg[e];
+          db[j + H][e] += du[e];
+        }
+      }
+      const uint32_t a = strip + (uint32_t)(l16 * PITCH + (16 * j + 4 * lg) * 2);
+      lds_store_u32x2(a, pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
+      lds_store_u32x2(a + H * 32, pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]));
+    }
+    wait_lgkmcnt0();
+    store_both<16, FN * 16>(strip, lane, row0 + 16 * i, p, [&](int c) {
+      const int h = c >= FN * 8, g = col0 + c - h * FN * 8;
+      return g < F ? g + h * F : -1;
+    });
+    wait_lgkmcnt0();
+  }
+  if (!p.dbias_part) return;
+  // column sums of the wave's rows, in fp32 before the rounding of dz
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int h = j >= H;
+    const int c = col0 + 16 * (j - h * H) + 4 * lg;
+    float t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      t[e] = db[j][e];
+      t[e] += lane_xor(t[e], 1);
+      t[e] += lane_xor(t[e], 2);
+      t[e] += lane_xor(t[e], 4);
+      t[e] += lane_xor(t[e], 8);
+    }
+    if (l16 == 0 && c < F)
+      *reinterpret_cast<float4*>(p.dbias_part + (int64_t)wave_row * (2 * F) + h * F + c) =
+          make_float4(t[0], t[1], t[2], t[3]);
+  }
+}
+
+// kEpiGlu for one gate: gate and up pre-activations of the same output column
+// are in the same lane (the two halves of the wave's columns); the results are
+// staged 16 rows at a time and stored as 16-byte row chunks.
+template <int GATE, bool OUT_BF16, int FM, int FN, class Pin>
+__device__ __forceinline__ void glu_store(floatx4 (&acc)[FM][FN], uint32_t strip, int lane, int row0,
+                                          int col0, const TrainArgs& p, Pin pin) {
+  constexpr int H = FN / 2;
+  constexpr int ESZ = OUT_BF16 ? 2 : 4;
+  constexpr int PITCH = H * 16 * ESZ + 16;
+  constexpr int CH = H * 16 * ESZ / 16, EPC = 16 / ESZ;
+  const int l16 = lane & 15, lg = lane >> 4;
+  const int F = p.glu_half;
+  floatx4 bg[H], bu[H];
+#pragma unroll
+  for (int j = 0; j < H; ++j) {
+    const int c = col0 + 16 * j + 4 * lg;
+    bg[j] = bu[j] = floatx4{};
+    if (p.bias && c < F) {
+      bg[j] = *reinterpret_cast<const floatx4*>(p.bias + c);
+      bu[j] = *reinterpret_cast<const floatx4*>(p.bias + F + c);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    pin(acc[i]);
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+      floatx4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float act, slope;
+        gate_both<GATE>(acc[i][j][e] + bg[j][e], act, slope);
+        v[e] = act * (acc[i][j + H][e] + bu[j][e]);
+      }
+      const uint32_t a = strip + (uint32_t)(l16 * PITCH + (16 * j + 4 * lg) * ESZ);
+      if constexpr (OUT_BF16)
+        lds_store_u32x2(a, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      else
+        lds_store_f4(a, v);
+    }
+    wait_lgkmcnt0();
+#pragma unroll
+    for (int c0 = 0; c0 < 16 * CH; c0 += 64) {
+      const int c = c0 + lane;
+      if (16 * CH % 64 != 0 && c >= 16 * CH) break;
+      const int r = c / CH, ch = c - (c / CH) * CH;
+      const u32x4s v =
+          *(const __attribute__((address_space(3))) u32x4s*)(uintptr_t)(strip + (uint32_t)(r * PITCH + ch * 16));
+      const int row = row0 + 16 * i + r, col = col0 + ch * EPC;
+      // F is a multiple of 8: a chunk is inside or outside as a whole
+      if (row < p.M && col < F)
+        *reinterpret_cast<u32x4s*>(static_cast<char*>(p.C) + ((int64_t)row * p.ldc + col) * ESZ) = v;
+    }
+    wait_lgkmcnt0();
+  }
+}
+
+// Calls f(integral_constant<int, gate>) for a gate known only at run time.
+template <class F>
+__device__ __forceinline__ void for_gate(int gate, F f) {
+  switch (gate) {
+    case kGateGelu: f(std::integral_constant<int, kGateGelu>{}); break;
+    case kGateGeluTanh: f(std::integral_constant<int, kGateGeluTanh>{}); break;
+    case kGateRelu: f(std::integral_constant<int, kGateRelu>{}); break;
+    case kGateSigmoid: f(std::integral_constant<int, kGateSigmoid>{}); break;
+    default: f(std::integral_constant<int, kGateSilu>{});
+  }
+}
+
+// The store of a wave's FM x FN blocks (16 x 16 each) of its tile, rows
+// row0 .. and columns col0 .. (gated: FN / 2 blocks of gate columns from
+// gcol0, then the matching up columns). `strip` is LDS private to the wave;
+// `pin` ties block row i's accumulators to this point of the program.
+template <int EPI, bool OUT_BF16, int FM, int FN, class Pin>
+__device__ __forceinline__ void train_store(floatx4 (&acc)[FM][FN], uint32_t strip, int lane, int row0,
+                                            int col0, int64_t seg, int wave_row, const TrainArgs& p,
+                                            Pin pin) {
+  const int l16 = lane & 15, lg = lane >> 4;
+  constexpr int KIND = epi_kind(EPI);
+  if constexpr (KIND == kEpiStats) {
+    if (col0 >= p.N) return;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      pin(acc[i]);
+      stats_row<FN, 16, 32>(acc[i], 16, lg, col0, row0 + 16 * i + l16, seg, p);
+    }
+  } else if constexpr (KIND == kEpiXentGrad) {
+    constexpr int PITCH = FN * 32 + 16;
+    if (col0 >= p.N) return;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      pin(acc[i]);
+      const int row = row0 + 16 * i + l16;
+      XentRow r{0.0f, 0.0f, 0.0f, -1};
+      if (row < p.M) r = p.rows[row];
+      r.target -= p.first + col0 + 4 * lg;
+      const float u = r.b * p.smooth, hit = r.b * p.keep;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        float g[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = xent_grad(acc[i][j][e], 16 * j + e, r, u, hit);
+        lds_store_u32x2(strip + (uint32_t)(l16 * PITCH + (16 * j + 4 * lg) * 2), pack_bf16x2(g[0], g[1]),
+                        pack_bf16x2(g[2], g[3]));
+      }
+      wait_lgkmcnt0();
+      store_both<16, FN * 16>(strip, lane, row0 + 16 * i, p,
+                              [&](int c) { return col0 + c < p.N ? col0 + c : -1; });
+      wait_lgkmcnt0();
+    }
+  } else {
+    if (col0 >= p.glu_half) return;
+    auto run = [&](auto gate) {
+      constexpr int GATE = decltype(gate)::value;
+      if constexpr (KIND == kEpiGluGrad)
+        glu_grad_store<GATE>(acc, strip, lane, row0, col0, wave_row, p, pin);
+      else
+        glu_store<GATE, OUT_BF16>(acc, strip, lane, row0, col0, p, pin);
+    };
+    if constexpr (epi_gate(EPI) >= 0)
+      run(std::integral_constant<int, epi_gate(EPI)>{});
+    else
+      for_gate(p.gate, run);
+  }
+}
+
+// The same stores for the stream kernel's 32 x 32 blocks, FM of them down one
+// 32-column block: lane l holds row l % 32, columns 8 q + 4 (l / 32) .. + 3 in
+// elements 4 q .. + 3.
+constexpr int kStrip32 = 32 * 2 + 16;  // bytes of a strip row
+
+template <int EPI, int FM>
+__device__ __forceinline__ void train_store_32(floatx16 (&acc)[FM], uint32_t strip, int lane, int row0,
+                                               int col0, int64_t seg, const TrainArgs& p) {
+  static_assert(EPI == kEpiStats || EPI == kEpiXentGrad, "logits only; kEpiGlu has its own");
+  const int lrow = lane & 31, lgrp = lane >> 5;
+  if (col0 >= p.N) return;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int row = row0 + 32 * i + lrow;
+    if constexpr (EPI == kEpiStats) {
+      floatx4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[q] = floatx4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
+      stats_row<4, 0, 32>(v, 8, lgrp, col0, row, seg, p);
+    } else {
+      XentRow r{0.0f, 0.0f, 0.0f, -1};
+      if (row < p.M) r = p.rows[row];
+      r.target -= p.first + col0 + 4 * lgrp;
+      const float u = r.b * p.smooth, hit = r.b * p.keep;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float g[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = xent_grad(acc[i][4 * q + e], 8 * q + e, r, u, hit);
+        lds_store_u32x2(strip + (uint32_t)(lrow * kStrip32 + (8 * q + 4 * lgrp) * 2),
+                        pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]));
+      }
+      wait_lgkmcnt0();
+      store_both<32, 32>(strip, lane, row0 + 32 * i, p,
+                         [&](int c) { return col0 + c < p.N ? col0 + c : -1; });
+      wait_lgkmcnt0();
+    }
+  }
+}
+
+// kEpiGlu of the stream kernel. The gate and up columns of an output are in
+// different 32-column blocks, so a block-wide strip holds ROWS x (COLS gate,
+// COLS up) fp32 pre-activations (row pitch in bytes) and all threads form one
+// 16-byte output chunk each at a time.
+template <bool OUT_BF16, int ROWS, int COLS>
+__device__ __forceinline__ void glu_strip(uint32_t src, int pitch, int row0, int col0, int tid, int nthr,
+                                          const TrainArgs& p) {
+  constexpr int EPC = OUT_BF16 ? 8 : 4;
+  constexpr int ESZ = OUT_BF16 ? 2 : 4;
+  constexpr int CH = COLS / EPC;
+  const int F = p.glu_half;
+  for_gate(p.gate, [&](auto gate) {
+    for (int c = tid; c < ROWS * CH; c += nthr) {
+      const int r = c / CH, ch = c - (c / CH) * CH;
+      const int row = row0 + r, col = col0 + ch * EPC;
+      if (row >= p.M || col >= F) continue;
+      float v[EPC];
+#pragma unroll
+      for (int h = 0; h < EPC / 4; ++h) {
+        const uint32_t a = src + (uint32_t)(r * pitch + (ch * EPC + 4 * h) * 4);
+        floatx4 g = lds_load_f4(a), u = lds_load_f4(a + (uint32_t)(COLS * 4));
+        if (p.bias) {
+          g += *reinterpret_cast<const floatx4*>(p.bias + col + 4 * h);
+          u += *reinterpret_cast<const floatx4*>(p.bias + F + col + 4 * h);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float act, slope;
+          gate_both<decltype(gate)::value>(g[e], act, slope);
+          v[4 * h + e] = act * u[e];
+        }
+      }
+      char* out = static_cast<char*>(p.C) + ((int64_t)row * p.ldc + col) * ESZ;
+      if constexpr (OUT_BF16)
+        *reinterpret_cast<u32x4s*>(out) = u32x4s{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+      else
+        *reinterpret_cast<floatx4*>(out) = floatx4{v[0], v[1], v[2], v[3]};
+    }
+  });
+}
+
+}  // namespace tg

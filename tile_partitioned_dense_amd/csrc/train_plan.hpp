@@ -1,0 +1,299 @@
+// train_plan.hpp -- launch geometry and workspace layout of the gated block's
+// backward pass and of the cross entropy of a projection. Host only, no HIP
+// dependency, pure functions of the shape and the compute-unit count.
+#pragma once
+
+#include "plan.hpp"
+
+namespace tg {
+
+// The tile kernels these operators are compiled for: 256 x 256 tiles of the
+// 64-deep one-wave-per-SIMD kernel (tile configuration 26's geometry) and
+// 128 x 128 tiles of the 32-deep eight-wave kernel, two of which share a
+// compute unit, for shapes with few tiles. `eff` is the rate of a compute
+// unit relative to 256 x 256 tiles, `eff1` with a single tile on it.
+struct TrainTile {
+  int bm, bn, wm, wn;
+  double eff, eff1;
+  int occ;
+};
+constexpr int kNumTrainTiles = 2;
+constexpr TrainTile kTrainTiles[kNumTrainTiles] = {
+    {256, 256, 2, 2, 1.0, 1.0, 1},
+    {128, 128, 2, 4, 0.75, 0.50, 2},
+};
+// What a product is turned into (train_epilogue.hpp; a gradient's bf16 result
+// or the fp32 partial results of its parts are both kEpiPartial there).
+enum TrainStore { kStoreStats = 0, kStoreXentGrad, kStoreBf16, kStoreParts, kStoreGluGrad, kStoreGlu };
+
+// The compiled kernels: on the tiles above (tile 0, 1) or the stream kernel's
+// configurations (tile 2 + configuration), gate < 0 where it is an argument.
+// Logits and pre-activations take W as it is stored (column-major B) and the
+// gated forward product either layout; gradients contract over W's rows (dx)
+// or over the tokens (dW), where the second operand is row-major.
+struct TrainKernel {
+  int store, tile, gate;
+  bool bcol, bf16;
+};
+constexpr int kNumTrainKernels = 46;
+struct TrainKernels {
+  TrainKernel k[kNumTrainKernels] = {};
+  int n = 0;
+  constexpr void add(int store, int tile, int gate, bool bcol, bool bf16) {
+    k[n].store = store;
+    k[n].tile = tile;
+    k[n].gate = gate;
+    k[n].bcol = bcol;
+    k[n].bf16 = bf16;
+    ++n;
+  }
+  constexpr TrainKernels() {
+    for (int t = 0; t < kNumTrainTiles; ++t) {
+      add(kStoreStats, t, -1, true, true);
+      add(kStoreXentGrad, t, -1, true, true);
+      add(kStoreBf16, t, -1, false, true);
+      add(kStoreParts, t, -1, false, false);
+    }
+    for (int c = 0; c < 3; ++c) {
+      add(kStoreStats, 2 + c, -1, true, true);
+      add(kStoreXentGrad, 2 + c, -1, true, true);
+      add(kStoreGlu, 2 + c, -1, true, true);
+      add(kStoreGlu, 2 + c, -1, true, false);
+    }
+    for (int g = 0; g < 5; ++g) add(kStoreGluGrad, 0, g, true, true);
+    add(kStoreGluGrad, 1, -1, true, true);
+    for (int l = 0; l < 4; ++l) {
+      for (int g = 1; g < 5; ++g) add(kStoreGlu, 0, g, l & 1, l & 2);
+      add(kStoreGlu, 1, -1, l & 1, l & 2);
+    }
+  }
+};
+constexpr TrainKernels kTrainKernels{};
+static_assert(kTrainKernels.n == kNumTrainKernels, "the table is as long as it says");
+
+// Index of a compiled kernel, -1 if there is none.
+inline int train_kernel(int store, int tile, int gate, bool bcol, bool bf16) {
+  for (int i = 0; i < kNumTrainKernels; ++i) {
+    const TrainKernel& k = kTrainKernels.k[i];
+    if (k.store == store && k.tile == tile && (k.gate < 0 || k.gate == gate) && k.bcol == bcol &&
+        k.bf16 == bf16)
+      return i;
+  }
+  return -1;
+}
+
+// A product cut into tiles and, for gradients whose output has few tiles but
+// a long contraction (dx over the vocabulary, dW over the tokens), into
+// `splits` parts of k_per along K whose fp32 results are added in a fixed
+// order afterwards.
+struct TrainProduct {
+  int tile;
+  int splits;
+  int64_t k_per;
+  TileMap map;
+  int64_t grid;
+};
+
+// Microseconds a product takes, roughly: tiles on the busiest compute unit,
+// each a fixed cost plus its K loop at the rate measured on full grids
+// (1.15 PFLOP/s over 256 compute units for 256 x 256 tiles), and the pass
+// that adds the parts (its bytes at 4 TB/s and a launch).
+inline double product_us(const TrainTile& t, int64_t M, int64_t N, int64_t k_per, int splits, int cu) {
+  const int64_t work = ceil_div(M, t.bm) * ceil_div(N, t.bn) * splits;
+  const int64_t per_cu = ceil_div(work, cu);
+  const double rate = 4.5e6 * (per_cu >= t.occ ? t.eff : t.eff1);  // flop per us and compute unit
+  double us = (double)per_cu * (2.0 * t.bm * t.bn * (double)k_per / rate + 2.5);
+  if (splits > 1) us += 4.0 + (double)M * (double)N * (8.0 * splits + 2.0) / 4.0e6;
+  return us;
+}
+
+inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits, int cu) {
+  TrainProduct best{};
+  double best_us = 0.0;
+  for (int c = 0; c < kNumTrainTiles; ++c) {
+    const TrainTile& t = kTrainTiles[c];
+    for (int s = 1; s <= max_splits; s *= 2) {
+      const int64_t k_per = ceil_div(ceil_div(K, s), 64) * 64;
+      // parts of at least 256 keep the load pipeline longer than its ramp
+      if (s > 1 && (k_per < 256 || ceil_div(K, k_per) != s)) continue;
+      const double us = product_us(t, M, N, s == 1 ? K : k_per, s, cu);
+      if (best_us == 0.0 || us < best_us * 0.999) {
+        best_us = us;
+        best.tile = c;
+        best.splits = s;
+        best.k_per = k_per;
+      }
+    }
+  }
+  const TrainTile& t = kTrainTiles[best.tile];
+  best.map.tiles_m = (int32_t)ceil_div(M, t.bm);
+  best.map.tiles_n = (int32_t)ceil_div(N, t.bn);
+  best.map.group_m = pick_group_m(best.map.tiles_m, best.map.tiles_n);
+  best.map.xcds = kXcds;
+  best.grid = persistent_grid((int64_t)best.map.tiles_m * best.map.tiles_n * best.splits, cu * t.occ);
+  return best;
+}
+constexpr int kMaxSplits = 64;
+
+// A gradient's product with its workspace: `slots` fp32 partial results of
+// M x N (0: the product writes its bf16 result itself).
+inline int64_t slot_bytes(int64_t M, int64_t N) { return M * ceil_div(N, 4) * 16; }
+
+// Bytes of one workspace region, and the running offset past it: regions
+// start at multiples of 256 bytes.
+inline int64_t region(int64_t& at, int64_t bytes) {
+  const int64_t p = at;
+  at += ceil_div(bytes, 256) * 256;
+  return p;
+}
+
+// The product over W as it is stored (logits, the gated forward result): up
+// to kStreamMaxM rows (and an even K) it is the stream kernel's, as in
+// make_plan. `seg_cols`: the columns whose logits one wave joins.
+struct ForwardPlan {
+  TrainProduct z;
+  int seg_cols;
+};
+
+inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu) {
+  ForwardPlan f{};
+  if (M <= kStreamMaxM && K % 2 == 0) {
+    const Plan p = make_plan(M, N, K, true, cu);
+    f.z.tile = 2 + p.config - kStreamConfig;
+    f.z.map = p.map;
+    f.z.grid = p.grid;
+    f.z.splits = 1;
+    f.seg_cols = 32;
+  } else {
+    f.z = plan_product(M, N, K, 1, cu);
+    const TrainTile& t = kTrainTiles[f.z.tile];
+    f.seg_cols = t.bn / t.wn;
+  }
+  return f;
+}
+
+// ------------------------------------------------------------ gated block
+
+struct GluGradPlan {
+  TrainProduct z, dx, dw;
+  int64_t ldz, ldzt;
+  int64_t off_z, off_zt, off_part, off_bias;
+  int64_t bias_rows;
+  int64_t bytes;
+};
+
+// z is M x N (N = 2 F columns, tiled F columns of gate and up at a time), dx
+// M x K over N, dW N x K over M.
+inline GluGradPlan plan_glu_grad(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw,
+                                 bool want_bias, int cu) {
+  GluGradPlan p{};
+  if (M <= 0 || N <= 0) return p;
+  p.z = plan_product(M, N, K, 1, cu);
+  p.dx = plan_product(M, K, N, kMaxSplits, cu);
+  p.dw = plan_product(N, K, M, kMaxSplits, cu);
+  p.ldz = ceil_div(N, 8) * 8;
+  p.ldzt = ceil_div(M, 16) * 16;
+  int64_t at = 0;
+  if (want_dx) p.off_z = region(at, M * p.ldz * 2);
+  if (want_dw) p.off_zt = region(at, N * p.ldzt * 2);
+  int64_t part = 0;
+  if (want_dx && p.dx.splits > 1) part = p.dx.splits * slot_bytes(M, K);
+  if (want_dw && p.dw.splits > 1) {
+    const int64_t b = p.dw.splits * slot_bytes(N, K);
+    if (b > part) part = b;  // the two products run one after the other
+  }
+  p.off_part = region(at, part);
+  p.bias_rows = (int64_t)p.z.map.tiles_m * kTrainTiles[p.z.tile].wm;
+  p.off_bias = region(at, want_bias ? p.bias_rows * N * 4 : 0);
+  p.bytes = at;
+  return p;
+}
+
+// ----------------------------------------------- cross entropy of a product
+
+struct XentPlan {
+  ForwardPlan l;
+  int64_t segs;
+  int64_t off_part, off_sum, off_hit;
+  int64_t bytes;
+};
+
+inline XentPlan plan_xent(int64_t M, int64_t N, int64_t K, bool smooth, int cu) {
+  XentPlan p{};
+  if (M <= 0) return p;
+  p.l = plan_forward(M, N, K, cu);
+  p.segs = ceil_div(N, p.l.seg_cols);
+  int64_t at = 0;
+  p.off_part = region(at, p.segs * M * 8);
+  p.off_sum = region(at, smooth ? p.segs * M * 4 : 0);
+  p.off_hit = region(at, M * 4);
+  p.bytes = at;
+  return p;
+}
+
+struct XentGradPlan {
+  int64_t piece, n_pieces;
+  int64_t ldz, ldzt;
+  int slots;  // fp32 partial results of dx over all pieces (0: written at once)
+  int64_t off_rows, off_scale, off_z, off_zt, off_dx, off_dw;
+  int64_t bytes;
+};
+
+// Columns of a vocabulary piece: both copies of its G (2 bytes a value) stay
+// within 1 GiB. Fewer, larger pieces need fewer partial results of dx and
+// leave fewer ragged rounds of tiles.
+constexpr int64_t kXentPieceBytes = (int64_t)1 << 30;
+
+inline TrainProduct plan_xent_dx(int64_t M, int64_t K, int64_t cols, int cu) {
+  return plan_product(M, K, cols, kMaxSplits, cu);
+}
+inline TrainProduct plan_xent_dw(int64_t M, int64_t K, int64_t cols, int cu) {
+  return plan_product(cols, K, M, kMaxSplits, cu);
+}
+
+inline XentGradPlan plan_xent_grad(int64_t M, int64_t N, int64_t K, int64_t ldw, int64_t piece,
+                                   bool want_dx, bool want_dw, int cu) {
+  XentGradPlan p{};
+  if (M <= 0 || N <= 0) return p;
+  p.ldzt = ceil_div(M, 16) * 16;
+  // the dx product reads a piece of W through 32-bit offsets
+  const int64_t rows = ((int64_t)1 << 31) / (2 * ldw);
+  if (piece <= 0) {
+    piece = kXentPieceBytes / (4 * p.ldzt) / 256 * 256;
+    if (piece < 256) piece = 256;
+    if (piece > rows) piece = rows;
+    const int64_t n = ceil_div(N, piece);
+    const int64_t even = ceil_div(ceil_div(N, n), 256) * 256;  // pieces of equal size
+    if (even < piece) piece = even;
+  }
+  if (piece > rows) piece = rows;
+  if (piece > N) piece = N;
+  p.piece = piece;
+  p.n_pieces = ceil_div(N, piece);
+  p.ldz = ceil_div(piece, 8) * 8;
+  int64_t at = 0;
+  p.off_rows = region(at, M * 16);
+  p.off_scale = region(at, 4);
+  if (want_dx) {
+    p.off_z = region(at, M * p.ldz * 2);
+    for (int64_t v = 0; v < N; v += piece)
+      p.slots += plan_xent_dx(M, K, N - v < piece ? N - v : piece, cu).splits;
+    if (p.slots == 1) p.slots = 0;
+    p.off_dx = region(at, p.slots * slot_bytes(M, K));
+  }
+  if (want_dw) {
+    p.off_zt = region(at, piece * p.ldzt * 2);
+    int64_t part = 0;
+    for (int64_t v = 0; v < N; v += piece) {
+      const int64_t cols = N - v < piece ? N - v : piece;
+      const TrainProduct q = plan_xent_dw(M, K, cols, cu);
+      const int64_t b = q.splits > 1 ? q.splits * slot_bytes(cols, K) : 0;
+      if (b > part) part = b;
+    }
+    p.off_dw = region(at, part);
+  }
+  p.bytes = at;
+  return p;
+}
+
+}  // namespace tg
