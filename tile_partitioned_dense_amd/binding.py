@@ -425,97 +425,133 @@ def tile_gemm_run_mx(h, A, Bt, C, a_scale, b_scale, bias=None, act=Act.NONE, str
 
 
 # ------------------------------------------------ gated block, cross entropy
+# A call on few rows takes the GPU a few microseconds, so these bindings keep
+# what they do for each call short: one comparison per argument, and the long
+# form of a check only to word its error.
 
-def _ptr(x):
-    return x.data_ptr() if _is_tensor(x) else x
-
-
-def _matrix(name, t, shape):
-    """A 2-D bf16 tensor of the given shape (sizes None: any); its strides."""
+def _matrix(name, t, rows, cols):
+    """Checks a 2-D bf16 tensor (rows, cols None: any)."""
     import torch
     if not _is_tensor(t):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
-    if t.dim() != 2 or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, "
-                         f"got {tuple(t.shape)}")
-    return t.stride()
+    s = t.shape
+    if len(s) != 2 or (rows is not None and s[0] != rows) or (cols is not None and s[1] != cols):
+        raise ValueError(f"{name} must have shape ({'any' if rows is None else rows}, "
+                         f"{'any' if cols is None else cols}), got {tuple(s)}")
 
 
 def _vector(name, t, n, dtypes):
+    """Checks a contiguous vector of n values."""
     if not _is_tensor(t):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
-    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+    s = t.shape
+    if len(s) != 1 or s[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} values, got shape "
-                         f"{tuple(t.shape)} strides {tuple(t.stride())}")
+                         f"{tuple(s)} strides {tuple(t.stride())}")
 
 
-def _col_major_strides(K, b):
-    """(b_k, b_n) of a column-major K x N operand; a unit axis has no stride of
-    its own, so torch may report any value for it."""
+def _current_device(names, tensors):
+    """The current device, on which every tensor has to be."""
+    import torch
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and t.get_device() != cur:
+            _check_devices(zip(names, tensors))
+    return cur
+
+
+def _col_major_strides(b):
+    """(b_k, b_n) of a column-major K x N operand; an axis of one element has
+    no stride of its own (torch may report any value for it)."""
     b_k, b_n = b.stride()
+    K, N = b.shape
     if K == 1:
         b_k = 1
-    if b.shape[1] <= 1:
+    if N <= 1:
         b_n = max(b_n, K)
     return b_k, b_n
 
 
-def _unit(t):
-    """The column stride of a row-major matrix (1 where there is one column)."""
-    return 1 if t.shape[1] <= 1 else t.stride(1)
+def _row_major_strides(t):
+    """(row, column) strides of a row-major matrix; see _col_major_strides."""
+    return t.stride(0), (1 if t.shape[1] <= 1 else t.stride(1))
 
 
-class _Workspace:
-    """The caller's workspace (any contiguous tensor on the device), or one
-    allocated for the call and kept by torch until the stream has passed it."""
+def _launch_stream(stream, device):
+    """The raw stream of a call on the current device, and the stream a
+    workspace allocated for it has to be handed over to (None: the current)."""
+    import torch
+    cur = torch._C._cuda_getCurrentRawStream(device)
+    if stream is None:
+        return cur, None
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if raw == cur:
+        return cur, None
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(raw, device=torch.device("cuda", device))
+    return raw, stream
 
-    def __init__(self, given, nbytes, device, stream):
-        import torch
-        if given is not None:
-            if not _is_tensor(given) or not given.is_contiguous():
-                raise ValueError("workspace must be a contiguous tensor")
-            _check_devices((("workspace", given),))
-            self.tensor, self.nbytes = given, given.numel() * given.element_size()
-        else:
-            self.tensor = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-            self.nbytes = nbytes
-            if stream is not None:
-                raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-                if raw != torch.cuda.current_stream(device).cuda_stream:
-                    if not hasattr(stream, "cuda_stream"):
-                        stream = torch.cuda.ExternalStream(raw, device=device)
-                    self.tensor.record_stream(stream)
-                    # the block may have been freed on the current stream
-                    # while work queued there still uses it
-                    stream.wait_stream(torch.cuda.current_stream(device))
-        self.ptr = self.tensor.data_ptr()
+
+def _own_workspace(nbytes, device, other):
+    """A workspace for one call; torch keeps its memory until the stream has
+    passed the call."""
+    import torch
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=f"cuda:{device}")
+    if other is not None:
+        ws.record_stream(other)
+        # the block may have been freed on the current stream while work
+        # queued there still uses it
+        other.wait_stream(torch.cuda.current_stream(device))
+    return ws
+
+
+def _workspace_bytes(ws):
+    if not _is_tensor(ws) or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor")
+    return ws.numel() * ws.element_size()
+
+
+def _result(st, check):
+    if st:
+        if check:
+            _raise_if(st)
+        return Status(st)
+    return Status.OK
 
 
 def tile_gemm_run_glu(h, A, B, C, gate=Gate.SILU, bias=None, stream=None, check: bool = True):
     """Enqueue the gated block C := act(A.B_gate + b_gate) * (A.B_up + b_up)
     (torch tensors; B is K x N with the N/2 gate columns first, either layout;
     C is M x N/2, float32 or bfloat16)."""
-    a, b, c, M, N, K, s, dt = _operands(A, B, C, None, None, None, None, None, 2)
-    _check_bias(bias, N)
-    _check_devices((("A", A), ("B", B), ("C", C), ("bias", bias)))
+    _matrix("A", A, None, None)
+    M, K = A.shape
+    _matrix("B", B, K, None)
+    N = B.shape[1]
+    if not _is_tensor(C) or C.dim() != 2 or N % 2 or tuple(C.shape) != (M, N // 2):
+        raise ValueError(f"C must be a tensor of shape {(M, N // 2)} for B{tuple(B.shape)}")
+    dt = _c_dtype(C)
+    if bias is not None:
+        _check_bias(bias, N)
+    dev = _current_device(("A", "B", "C", "bias"), (A, B, C, bias if _is_tensor(bias) else None))
     if M == 1:  # the stride of a single row is never used
-        s.a_m, s.c_m = (K + 7) // 8 * 8, (N // 2 + 7) // 8 * 8
-    st = load_library().tile_gemm_run_glu(h, a, b, c, M, N, K, ctypes.byref(s), dt, _ptr(bias),
-                                          int(gate), _stream_ptr(stream, C))
-    if check:
-        _raise_if(st)
-    return Status(st)
+        s = Strides((K + 7) // 8 * 8, 1, *B.stride(), (N // 2 + 7) // 8 * 8, 1)
+    else:
+        s = Strides(*A.stride(), *B.stride(), *C.stride())
+    raw, _ = _launch_stream(stream, dev)
+    st = load_library().tile_gemm_run_glu(h, A.data_ptr(), B.data_ptr(), C.data_ptr(), M, N, K,
+                                          ctypes.byref(s), dt,
+                                          bias.data_ptr() if _is_tensor(bias) else bias, gate, raw)
+    return _result(st, check)
 
 
 def tile_gemm_glu_backward_workspace(h, M, N, K) -> int:
     """Workspace bytes of tile_gemm_run_glu_backward (h None: an MI355X)."""
     n = ctypes.c_int64()
-    _raise_if(load_library().tile_gemm_glu_backward_workspace(h, int(M), int(N), int(K),
-                                                              ctypes.byref(n)))
+    _raise_if(load_library().tile_gemm_glu_backward_workspace(h, M, N, K, ctypes.byref(n)))
     return n.value
 
 
@@ -526,52 +562,58 @@ def tile_gemm_run_glu_backward(h, A, B, dC, dA=None, dB=None, gate=Gate.SILU, bi
     any of the three may be left out. Without `workspace` one is allocated for
     the call."""
     import torch
-    a_m, _ = _matrix("A", A, (None, None))
+    _matrix("A", A, None, None)
     M, K = A.shape
-    _matrix("B", B, (K, None))
+    _matrix("B", B, K, None)
     N = B.shape[1]
-    c_m, _ = _matrix("dC", dC, (M, N // 2))
-    s = Strides(a_m, _unit(A), *_col_major_strides(K, B), 0, 0)
-    g = Strides(0, 1, 1, 0, c_m, _unit(dC))
+    _matrix("dC", dC, M, N // 2)
+    s = Strides(*_row_major_strides(A), *_col_major_strides(B), 0, 0)
+    g = Strides(0, 1, 1, 0, *_row_major_strides(dC))
+    p_dA = p_dB = p_bias = p_dbias = None
     if dA is not None:
-        g.a_m, _ = _matrix("dA", dA, (M, K))
-        g.a_k = _unit(dA)
+        _matrix("dA", dA, M, K)
+        g.a_m, g.a_k = _row_major_strides(dA)
+        p_dA = dA.data_ptr()
     if dB is not None:
-        _matrix("dB", dB, (K, N))
-        g.b_k, g.b_n = _col_major_strides(K, dB)
-    _check_bias(bias, N)
+        _matrix("dB", dB, K, N)
+        g.b_k, g.b_n = _col_major_strides(dB)
+        p_dB = dB.data_ptr()
+    if bias is not None:
+        _vector("bias", bias, N, (torch.float32,))
+        p_bias = bias.data_ptr()
     if dbias is not None:
         _vector("dbias", dbias, N, (torch.float32,))
-    _check_devices((("A", A), ("B", B), ("dC", dC), ("dA", dA), ("dB", dB), ("bias", bias),
-                    ("dbias", dbias)))
-    need = 0 if workspace is not None else tile_gemm_glu_backward_workspace(h, M, N, K)
-    ws = _Workspace(workspace, need, A.device, stream)
+        p_dbias = dbias.data_ptr()
+    dev = _current_device(("A", "B", "dC", "dA", "dB", "bias", "dbias", "workspace"),
+                          (A, B, dC, dA, dB, bias, dbias, workspace))
+    raw, other = _launch_stream(stream, dev)
+    if workspace is None:
+        nbytes = tile_gemm_glu_backward_workspace(h, M, N, K)
+        workspace = _own_workspace(nbytes, dev, other)
+    else:
+        nbytes = _workspace_bytes(workspace)
     st = load_library().tile_gemm_run_glu_backward(
-        h, _ptr(A), _ptr(B), _ptr(dC), _ptr(dA), _ptr(dB), M, N, K, ctypes.byref(s), ctypes.byref(g),
-        _ptr(bias), _ptr(dbias), int(gate), ws.ptr, ws.nbytes, _stream_ptr(stream, A))
-    if check:
-        _raise_if(st)
-    return Status(st)
+        h, A.data_ptr(), B.data_ptr(), dC.data_ptr(), p_dA, p_dB, M, N, K, ctypes.byref(s),
+        ctypes.byref(g), p_bias, p_dbias, gate, workspace.data_ptr(), nbytes, raw)
+    return _result(st, check)
 
 
 def _xent_operands(A, B, target, ignore_index, label_smoothing, z_loss, piece):
     import torch
-    a_m, _ = _matrix("A", A, (None, None))
+    _matrix("A", A, None, None)
     M, K = A.shape
-    _matrix("B", B, (K, None))
+    _matrix("B", B, K, None)
     _vector("target", target, M, (torch.int64, torch.int32))
-    s = Strides(a_m, _unit(A), *_col_major_strides(K, B), 0, 0)
-    o = XentOptions(int(ignore_index), float(label_smoothing), float(z_loss), int(piece),
-                    IndexType.I64 if target.dtype == torch.int64 else IndexType.I32)
+    s = Strides(*_row_major_strides(A), *_col_major_strides(B), 0, 0)
+    o = XentOptions(ignore_index, label_smoothing, z_loss, piece, target.dtype is torch.int64)
     return M, B.shape[1], K, s, o
 
 
 def tile_gemm_xent_workspace(h, M, N, K, label_smoothing=0.0) -> int:
     """Workspace bytes of tile_gemm_run_xent (h None: an MI355X)."""
     n = ctypes.c_int64()
-    o = XentOptions(0, float(label_smoothing), 0.0, 0, 0)
-    _raise_if(load_library().tile_gemm_xent_workspace(h, int(M), int(N), int(K), ctypes.byref(o),
-                                                      ctypes.byref(n)))
+    o = XentOptions(0, label_smoothing, 0.0, 0, 0)
+    _raise_if(load_library().tile_gemm_xent_workspace(h, M, N, K, ctypes.byref(o), ctypes.byref(n)))
     return n.value
 
 
@@ -582,28 +624,35 @@ def tile_gemm_run_xent(h, A, B, target, loss=None, lse=None, ignore_index=-100, 
     values each, without storing the logits."""
     import torch
     M, N, K, s, o = _xent_operands(A, B, target, ignore_index, label_smoothing, z_loss, 0)
-    for name, t in (("loss", loss), ("lse", lse)):
-        if t is not None:
-            _vector(name, t, M, (torch.float32,))
-    _check_devices((("A", A), ("B", B), ("target", target), ("loss", loss), ("lse", lse)))
-    need = 0 if workspace is not None else tile_gemm_xent_workspace(h, M, N, K, label_smoothing)
-    ws = _Workspace(workspace, need, A.device, stream)
-    st = load_library().tile_gemm_run_xent(h, _ptr(A), _ptr(B), _ptr(target), _ptr(loss), _ptr(lse), M,
-                                           N, K, ctypes.byref(s), ctypes.byref(o), ws.ptr, ws.nbytes,
-                                           _stream_ptr(stream, A))
-    if check:
-        _raise_if(st)
-    return Status(st)
+    p_loss = p_lse = None
+    if loss is not None:
+        _vector("loss", loss, M, (torch.float32,))
+        p_loss = loss.data_ptr()
+    if lse is not None:
+        _vector("lse", lse, M, (torch.float32,))
+        p_lse = lse.data_ptr()
+    dev = _current_device(("A", "B", "target", "loss", "lse", "workspace"),
+                          (A, B, target, loss, lse, workspace))
+    raw, other = _launch_stream(stream, dev)
+    if workspace is None:
+        nbytes = tile_gemm_xent_workspace(h, M, N, K, label_smoothing)
+        workspace = _own_workspace(nbytes, dev, other)
+    else:
+        nbytes = _workspace_bytes(workspace)
+    st = load_library().tile_gemm_run_xent(h, A.data_ptr(), B.data_ptr(), target.data_ptr(), p_loss, p_lse,
+                                           M, N, K, ctypes.byref(s), ctypes.byref(o),
+                                           workspace.data_ptr(), nbytes, raw)
+    return _result(st, check)
 
 
 def tile_gemm_xent_backward_workspace(h, M, N, K, b_n=None, piece=0) -> int:
     """Workspace bytes of tile_gemm_run_xent_backward (h None: an MI355X) for a
     B whose columns are b_n elements apart (None: K)."""
     n = ctypes.c_int64()
-    s = Strides(0, 1, 1, int(K if b_n is None else b_n), 0, 0)
-    o = XentOptions(0, 0.0, 0.0, int(piece), 0)
-    _raise_if(load_library().tile_gemm_xent_backward_workspace(h, int(M), int(N), int(K), ctypes.byref(s),
-                                                               ctypes.byref(o), ctypes.byref(n)))
+    s = Strides(0, 1, 1, K if b_n is None else b_n, 0, 0)
+    o = XentOptions(0, 0.0, 0.0, piece, 0)
+    _raise_if(load_library().tile_gemm_xent_backward_workspace(h, M, N, K, ctypes.byref(s), ctypes.byref(o),
+                                                               ctypes.byref(n)))
     return n.value
 
 
@@ -618,24 +667,27 @@ def tile_gemm_run_xent_backward(h, A, B, target, lse, dloss, dA=None, dB=None, i
     _vector("lse", lse, M, (torch.float32,))
     _vector("dloss", dloss, M, (torch.float32,))
     g = Strides(0, 1, 1, 0, 0, 1)
+    p_dA = p_dB = None
     if dA is not None:
-        g.a_m, _ = _matrix("dA", dA, (M, K))
-        g.a_k = _unit(dA)
+        _matrix("dA", dA, M, K)
+        g.a_m, g.a_k = _row_major_strides(dA)
+        p_dA = dA.data_ptr()
     if dB is not None:
-        _matrix("dB", dB, (K, N))
-        g.b_k, g.b_n = _col_major_strides(K, dB)
-    _check_devices((("A", A), ("B", B), ("target", target), ("lse", lse), ("dloss", dloss), ("dA", dA),
-                    ("dB", dB)))
-    need = 0
+        _matrix("dB", dB, K, N)
+        g.b_k, g.b_n = _col_major_strides(dB)
+        p_dB = dB.data_ptr()
+    dev = _current_device(("A", "B", "target", "lse", "dloss", "dA", "dB", "workspace"),
+                          (A, B, target, lse, dloss, dA, dB, workspace))
+    raw, other = _launch_stream(stream, dev)
     if workspace is None:
-        need = tile_gemm_xent_backward_workspace(h, M, N, K, s.b_n, piece)
-    ws = _Workspace(workspace, need, A.device, stream)
+        nbytes = tile_gemm_xent_backward_workspace(h, M, N, K, s.b_n, piece)
+        workspace = _own_workspace(nbytes, dev, other)
+    else:
+        nbytes = _workspace_bytes(workspace)
     st = load_library().tile_gemm_run_xent_backward(
-        h, _ptr(A), _ptr(B), _ptr(target), _ptr(lse), _ptr(dloss), _ptr(dA), _ptr(dB), M, N, K,
-        ctypes.byref(s), ctypes.byref(g), ctypes.byref(o), ws.ptr, ws.nbytes, _stream_ptr(stream, A))
-    if check:
-        _raise_if(st)
-    return Status(st)
+        h, A.data_ptr(), B.data_ptr(), target.data_ptr(), lse.data_ptr(), dloss.data_ptr(), p_dA, p_dB, M,
+        N, K, ctypes.byref(s), ctypes.byref(g), ctypes.byref(o), workspace.data_ptr(), nbytes, raw)
+    return _result(st, check)
 
 
 def _strides(s):
