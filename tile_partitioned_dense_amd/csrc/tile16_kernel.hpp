@@ -121,7 +121,8 @@ __device__ __forceinline__ void pin_row(floatx4 (&row)[FN]) {
 
 template <int BM, int BN, int WM, int WN, int NST, bool BCOL, bool OUT_BF16, bool DEBUG,
           int EPI = kEpiNone>
-__global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(EpiArgs<EPI> p) {
+__global__ __launch_bounds__(WM * WN * 64, EPI != kEpiNone && BM * BN <= 128 * 128 ? 2 : 1)
+void tile16_gemm_kernel(EpiArgs<EPI> p) {
   constexpr int kStages = NST;
   static_assert(NST >= 3 && NST <= 6, "ring depth");
   constexpr int NW = WM * WN;
@@ -135,7 +136,8 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(EpiArgs<EP
   static_assert(WTM % (32 * FQ) == 0 && WTN % 16 == 0,
                 "wave tile: an even number of steps of FQ 16-row blocks, whole 16-column blocks");
   static_assert(NW == 4 || NW == 8, "one or two waves per SIMD");
-  constexpr bool TIED = NW == 4;  // accumulators tied in place (see mma16)
+  // accumulators tied in place (see mma16): the one-wave-per-SIMD tiles
+  constexpr bool TIED = NW == 4 && WTM * WTN > 64 * 64;
   constexpr int BK = kTileBK;
   constexpr int A_BYTES = BM * BK * 2;  // per stage
   constexpr int B_BYTES = BN * BK * 2;
@@ -197,15 +199,13 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile16_gemm_kernel(EpiArgs<EP
       K = tg_min(p.k_per, K - k_lo);
     }
     // B column of tile column r: gate columns in the first half of the tile
-    // and up columns in the second, or (gated stores) in the two halves of
-    // every wave's columns, so that one lane holds both pre-activations
+    // and up columns in the second, or (gated stores) 8 gate columns and the
+    // matching 8 up columns in every 16, so that a wave holds both
     auto b_col = [&](int r) {
-      if constexpr (epi_gated(EPI)) {
-        const int w = r / WTN, c = r - (r / WTN) * WTN;
-        return w * (WTN / 2) + (c >= WTN / 2 ? c - WTN / 2 + glu : c);
-      } else {
+      if constexpr (epi_gated(EPI))
+        return (r >> 4) * 8 + (r & 7) + ((r & 8) ? glu : 0);
+      else
         return r + (r >= BN / 2 ? gshift : 0);
-      }
     };
 
     // ---- panels, their valid extents (to the operand's last element), steps

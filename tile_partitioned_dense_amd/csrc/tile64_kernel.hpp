@@ -111,15 +111,13 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
       K = tg_min(p.k_per, K - k_lo);
     }
     // B column of tile column r: gate columns in the first half of the tile
-    // and up columns in the second, or (gated stores) in the two halves of
-    // every wave's columns, so that one lane holds both pre-activations
+    // and up columns in the second, or (gated stores) 8 gate columns and the
+    // matching 8 up columns in every 16, so that a wave holds both
     auto b_col = [&](int r) {
-      if constexpr (epi_gated(EPI)) {
-        const int w = r / WTN, c = r - (r / WTN) * WTN;
-        return w * (WTN / 2) + (c >= WTN / 2 ? c - WTN / 2 + glu : c);
-      } else {
+      if constexpr (epi_gated(EPI))
+        return (r >> 4) * 8 + (r & 7) + ((r & 8) ? glu : 0);
+      else
         return r + (r >= BN / 2 ? gshift : 0);
-      }
     };
 
     const char* a_panel = reinterpret_cast<const char*>(pA + (int64_t)m0 * lda);

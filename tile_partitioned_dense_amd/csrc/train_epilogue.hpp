@@ -255,7 +255,7 @@ __device__ __forceinline__ void store_both(uint32_t strip, int lane, int grow0, 
   }
   if (p.Zt) {
     constexpr int P = COLS / 2 < 64 ? COLS / 2 : 64;  // column pairs covered at once
-    constexpr int RG = 64 / P;                        // lanes sharing a pair
+    constexpr int RG = 64 / P;                        // lanes sharing a pair (any past RG * P idle)
     constexpr int RPL = ROWS / RG;                    // rows of each
     static_assert(RPL == 4 || RPL == 8 || RPL == 16, "whole vector stores");
     static_assert(COLS / 2 <= 64, "one pass over the columns");
@@ -263,9 +263,10 @@ __device__ __forceinline__ void store_both(uint32_t strip, int lane, int grow0, 
     const int col = col_of((2 * pr) & ~7);
     uint32_t d[RPL];
 #pragma unroll
-    for (int r = 0; r < RPL; ++r) d[r] = lds_load_u32(strip + (uint32_t)((rg * RPL + r) * PITCH + pr * 4));
+    for (int r = 0; r < RPL; ++r)  // (idle lanes read row group 0)
+      d[r] = lds_load_u32(strip + (uint32_t)(((rg < RG ? rg : 0) * RPL + r) * PITCH + pr * 4));
     const int row = grow0 + rg * RPL;
-    if (row < p.M && col >= 0) {
+    if (rg < RG && row < p.M && col >= 0) {
       const int c = col + ((2 * pr) & 7);
       uint32_t lo[RPL / 2], hi[RPL / 2];
 #pragma unroll
@@ -291,120 +292,157 @@ __device__ __forceinline__ void store_both(uint32_t strip, int lane, int grow0, 
   }
 }
 
+// Gated stores: every 16-column block of the tile is 8 gate columns and the
+// matching 8 up columns (b_col of the kernels), so lanes 0-31 hold gate and
+// lanes 32-63 up pre-activations. Exchanging the upper half of block j with
+// the lower half of block j + 1 leaves each lane with the gate (g) and up (u)
+// values of four consecutive outputs, lanes 0-31 of block j and lanes 32-63 of
+// block j + 1; the last block of an odd number is paired with itself, its
+// upper lanes then count for nothing (glu_live). Any width of 16 columns works.
+template <int J, int FN>
+__device__ __forceinline__ void glu_pair(const floatx4 (&row)[FN], float (&g)[4], float (&u)[4]) {
+  constexpr int J1 = 2 * J + 1 < FN ? 2 * J + 1 : 2 * J;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(row[2 * J][e]), __float_as_uint(row[J1][e]),
+                                                    false, false);
+    g[e] = __uint_as_float(r[0]);
+    u[e] = __uint_as_float(r[1]);
+  }
+}
+// First output column (relative to the wave's first) of a lane's pair J, and
+// whether the pair is there at all.
+template <int J>
+__device__ __forceinline__ int glu_col(int lg) {
+  return 8 * (2 * J + (lg >> 1)) + 4 * (lg & 1);
+}
+template <int J, int FN>
+__device__ __forceinline__ bool glu_live(int lg) {
+  return 2 * J + 1 < FN || lg < 2;
+}
+
 // kEpiGluGrad for one gate; see train_store.
 template <int GATE, int FM, int FN, class Pin>
 __device__ __forceinline__ void glu_grad_store(floatx4 (&acc)[FM][FN], uint32_t strip, int lane, int row0,
                                                int col0, int wave_row, const TrainArgs& p, Pin pin) {
-  constexpr int H = FN / 2;
+  constexpr int NP = (FN + 1) / 2;
   constexpr int PITCH = FN * 32 + 16;
   const int l16 = lane & 15, lg = lane >> 4;
   const int F = p.glu_half;
-  float db[FN][4];
+  float db[NP][2][4];
 #pragma unroll
-  for (int j = 0; j < FN; ++j)
+  for (int j = 0; j < NP; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) db[j][e] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
+    for (int e = 0; e < 4; ++e) db[j][0][e] = db[j][1][e] = 0.0f;
+  static_for<0, FM>([&](auto i_c) {
+    constexpr int i = decltype(i_c)::value;
     pin(acc[i]);
     const int row = row0 + 16 * i + l16;
-#pragma unroll
-    for (int j = 0; j < H; ++j) {
-      const int c = col0 + 16 * j + 4 * lg;
+    static_for<0, NP>([&](auto j_c) {
+      constexpr int j = decltype(j_c)::value;
+      float g[4], u[4];
+      glu_pair<j>(acc[i], g, u);
+      const int cw = glu_col<j>(lg), c = col0 + cw;
       float dg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, du[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (row < p.M && c < F) {
-        const u32x2s dv = *reinterpret_cast<const u32x2s*>(p.dC + (int64_t)row * p.lddc + c);
-        const float dh[4] = {__uint_as_float(dv.x << 16), __uint_as_float(dv.x & 0xffff0000u),
-                             __uint_as_float(dv.y << 16), __uint_as_float(dv.y & 0xffff0000u)};
-        float bg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, bu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (p.bias) {
-          const float4 x = *reinterpret_cast<const float4*>(p.bias + c);
-          const float4 y = *reinterpret_cast<const float4*>(p.bias + F + c);
-          bg[0] = x.x; bg[1] = x.y; bg[2] = x.z; bg[3] = x.w;
-          bu[0] = y.x; bu[1] = y.y; bu[2] = y.z; bu[3] = y.w;
-        }
+      if (glu_live<j, FN>(lg)) {
+        if (row < p.M && c < F) {
+          const u32x2s dv = *reinterpret_cast<const u32x2s*>(p.dC + (int64_t)row * p.lddc + c);
+          const float dh[4] = {__uint_as_float(dv.x << 16), __uint_as_float(dv.x & 0xffff0000u),
+                               __uint_as_float(dv.y << 16), __uint_as_float(dv.y & 0xffff0000u)};
+          if (p.bias) {
+            const float4 x = *reinterpret_cast<const float4*>(p.bias + c);
+            const float4 y = *reinterpret_cast<const float4*>(p.bias + F + c);
+            g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
+            u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+          }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float act, slope;
-          gate_both<GATE>(acc[i][j][e] + bg[e], act, slope);
-          dg[e] = dh[e] * (acc[i][j + H][e] + bu[e]) * slope;
-          du[e] = dh[e] * act;
-          db[j][e] += dg[e];
-          db[j + H][e] += du[e];
+          for (int e = 0; e < 4; ++e) {
+            float act, slope;
+            gate_both<GATE>(g[e], act, slope);
+            dg[e] = dh[e] * u[e] * slope;
+            du[e] = dh[e] * act;
+            db[j][0][e] += dg[e];
+            db[j][1][e] += du[e];
+          }
         }
+        const uint32_t a = strip + (uint32_t)(l16 * PITCH + cw * 2);
+        lds_store_u32x2(a, pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
+        lds_store_u32x2(a + FN * 16, pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]));
       }
-      const uint32_t a = strip + (uint32_t)(l16 * PITCH + (16 * j + 4 * lg) * 2);
-      lds_store_u32x2(a, pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
-      lds_store_u32x2(a + H * 32, pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]));
-    }
-    wait_lgkmcnt0();
-    store_both<16, FN * 16>(strip, lane, row0 + 16 * i, p, [&](int c) {
-      const int h = c >= FN * 8, g = col0 + c - h * FN * 8;
-      return g < F ? g + h * F : -1;
     });
     wait_lgkmcnt0();
-  }
+    store_both<16, FN * 16>(strip, lane, row0 + 16 * i, p, [&](int c) {
+      const int h = c >= FN * 8, k = col0 + c - h * FN * 8;
+      return k < F ? k + h * F : -1;
+    });
+    wait_lgkmcnt0();
+  });
   if (!p.dbias_part) return;
   // column sums of the wave's rows, in fp32 before the rounding of dz
+  static_for<0, NP>([&](auto j_c) {
+    constexpr int j = decltype(j_c)::value;
+    const int c = col0 + glu_col<j>(lg);
 #pragma unroll
-  for (int j = 0; j < FN; ++j) {
-    const int h = j >= H;
-    const int c = col0 + 16 * (j - h * H) + 4 * lg;
-    float t[4];
+    for (int h = 0; h < 2; ++h) {
+      float t[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      t[e] = db[j][e];
-      t[e] += lane_xor(t[e], 1);
-      t[e] += lane_xor(t[e], 2);
-      t[e] += lane_xor(t[e], 4);
-      t[e] += lane_xor(t[e], 8);
+      for (int e = 0; e < 4; ++e) {
+        t[e] = db[j][h][e];
+        t[e] += lane_xor(t[e], 1);
+        t[e] += lane_xor(t[e], 2);
+        t[e] += lane_xor(t[e], 4);
+        t[e] += lane_xor(t[e], 8);
+      }
+      if (l16 == 0 && glu_live<j, FN>(lg) && c < F)
+        *reinterpret_cast<float4*>(p.dbias_part + (int64_t)wave_row * (2 * F) + h * F + c) =
+            make_float4(t[0], t[1], t[2], t[3]);
     }
-    if (l16 == 0 && c < F)
-      *reinterpret_cast<float4*>(p.dbias_part + (int64_t)wave_row * (2 * F) + h * F + c) =
-          make_float4(t[0], t[1], t[2], t[3]);
-  }
+  });
 }
 
-// kEpiGlu for one gate: gate and up pre-activations of the same output column
-// are in the same lane (the two halves of the wave's columns); the results are
-// staged 16 rows at a time and stored as 16-byte row chunks.
+// kEpiGlu for one gate: the results of 16 rows at a time are staged and stored
+// as 16-byte row chunks.
 template <int GATE, bool OUT_BF16, int FM, int FN, class Pin>
 __device__ __forceinline__ void glu_store(floatx4 (&acc)[FM][FN], uint32_t strip, int lane, int row0,
                                           int col0, const TrainArgs& p, Pin pin) {
-  constexpr int H = FN / 2;
+  constexpr int NP = (FN + 1) / 2;
   constexpr int ESZ = OUT_BF16 ? 2 : 4;
-  constexpr int PITCH = H * 16 * ESZ + 16;
-  constexpr int CH = H * 16 * ESZ / 16, EPC = 16 / ESZ;
+  constexpr int PITCH = FN * 8 * ESZ + 16;
+  constexpr int CH = FN * 8 * ESZ / 16, EPC = 16 / ESZ;
   const int l16 = lane & 15, lg = lane >> 4;
   const int F = p.glu_half;
-  floatx4 bg[H], bu[H];
-#pragma unroll
-  for (int j = 0; j < H; ++j) {
-    const int c = col0 + 16 * j + 4 * lg;
+  floatx4 bg[NP], bu[NP];
+  static_for<0, NP>([&](auto j_c) {
+    constexpr int j = decltype(j_c)::value;
+    const int c = col0 + glu_col<j>(lg);
     bg[j] = bu[j] = floatx4{};
     if (p.bias && c < F) {
       bg[j] = *reinterpret_cast<const floatx4*>(p.bias + c);
       bu[j] = *reinterpret_cast<const floatx4*>(p.bias + F + c);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
+  });
+  static_for<0, FM>([&](auto i_c) {
+    constexpr int i = decltype(i_c)::value;
     pin(acc[i]);
-#pragma unroll
-    for (int j = 0; j < H; ++j) {
+    static_for<0, NP>([&](auto j_c) {
+      constexpr int j = decltype(j_c)::value;
+      float g[4], u[4];
+      glu_pair<j>(acc[i], g, u);
       floatx4 v;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float act, slope;
-        gate_both<GATE>(acc[i][j][e] + bg[j][e], act, slope);
-        v[e] = act * (acc[i][j + H][e] + bu[j][e]);
+        gate_both<GATE>(g[e] + bg[j][e], act, slope);
+        v[e] = act * (u[e] + bu[j][e]);
       }
-      const uint32_t a = strip + (uint32_t)(l16 * PITCH + (16 * j + 4 * lg) * ESZ);
-      if constexpr (OUT_BF16)
-        lds_store_u32x2(a, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-      else
-        lds_store_f4(a, v);
-    }
+      if (glu_live<j, FN>(lg)) {
+        const uint32_t a = strip + (uint32_t)(l16 * PITCH + glu_col<j>(lg) * ESZ);
+        if constexpr (OUT_BF16)
+          lds_store_u32x2(a, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        else
+          lds_store_f4(a, v);
+      }
+    });
     wait_lgkmcnt0();
 #pragma unroll
     for (int c0 = 0; c0 < 16 * CH; c0 += 64) {
@@ -419,7 +457,7 @@ __device__ __forceinline__ void glu_store(floatx4 (&acc)[FM][FN], uint32_t strip
         *reinterpret_cast<u32x4s*>(static_cast<char*>(p.C) + ((int64_t)row * p.ldc + col) * ESZ) = v;
     }
     wait_lgkmcnt0();
-  }
+  });
 }
 
 // Calls f(integral_constant<int, gate>) for a gate known only at run time.
@@ -435,8 +473,8 @@ __device__ __forceinline__ void for_gate(int gate, F f) {
 }
 
 // The store of a wave's FM x FN blocks (16 x 16 each) of its tile, rows
-// row0 .. and columns col0 .. (gated: FN / 2 blocks of gate columns from
-// gcol0, then the matching up columns). `strip` is LDS private to the wave;
+// row0 .. and columns col0 .. (gated: 8 FN output columns from col0). `strip`
+// is LDS private to the wave;
 // `pin` ties block row i's accumulators to this point of the program.
 template <int EPI, bool OUT_BF16, int FM, int FN, class Pin>
 __device__ __forceinline__ void train_store(floatx4 (&acc)[FM][FN], uint32_t strip, int lane, int row0,
@@ -446,16 +484,16 @@ __device__ __forceinline__ void train_store(floatx4 (&acc)[FM][FN], uint32_t str
   constexpr int KIND = epi_kind(EPI);
   if constexpr (KIND == kEpiStats) {
     if (col0 >= p.N) return;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
+    static_for<0, FM>([&](auto i_c) {
+      constexpr int i = decltype(i_c)::value;
       pin(acc[i]);
       stats_row<FN, 16, 32>(acc[i], 16, lg, col0, row0 + 16 * i + l16, seg, p);
-    }
+    });
   } else if constexpr (KIND == kEpiXentGrad) {
     constexpr int PITCH = FN * 32 + 16;
     if (col0 >= p.N) return;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
+    static_for<0, FM>([&](auto i_c) {
+      constexpr int i = decltype(i_c)::value;
       pin(acc[i]);
       const int row = row0 + 16 * i + l16;
       XentRow r{0.0f, 0.0f, 0.0f, -1};
@@ -474,7 +512,7 @@ __device__ __forceinline__ void train_store(floatx4 (&acc)[FM][FN], uint32_t str
       store_both<16, FN * 16>(strip, lane, row0 + 16 * i, p,
                               [&](int c) { return col0 + c < p.N ? col0 + c : -1; });
       wait_lgkmcnt0();
-    }
+    });
   } else {
     if (col0 >= p.glu_half) return;
     auto run = [&](auto gate) {

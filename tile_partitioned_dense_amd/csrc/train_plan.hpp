@@ -7,27 +7,31 @@
 
 namespace tg {
 
-// The tile kernels these operators are compiled for: 256 x 256 tiles of the
-// 64-deep one-wave-per-SIMD kernel (tile configuration 26's geometry) and
-// 128 x 128 tiles of the 32-deep eight-wave kernel, two of which share a
-// compute unit, for shapes with few tiles. `eff` is the rate of a compute
-// unit relative to 256 x 256 tiles, `eff1` with a single tile on it.
+// The tile kernels these operators are compiled for: 256-row tiles of the
+// 64-deep one-wave-per-SIMD kernel in four widths (which one leaves the fewest
+// compute units idle depends on the output) and 128 x 128 tiles of the 32-deep
+// kernel, two of which share a compute unit, for shapes with few tiles. `eff`
+// is the rate of a compute unit relative to 256 x 256 tiles, `eff1` with a
+// single tile on it. `gated`: compiled with the gated block's stores too.
 struct TrainTile {
   int bm, bn, wm, wn;
   double eff, eff1;
   int occ;
+  bool gated;
 };
-constexpr int kNumTrainTiles = 2;
+constexpr int kNumTrainTiles = 5;
+constexpr int kSmallTile = 4;
 constexpr TrainTile kTrainTiles[kNumTrainTiles] = {
-    {256, 256, 2, 2, 1.0, 1.0, 1},
-    {128, 128, 2, 4, 0.75, 0.50, 2},
+    {256, 256, 2, 2, 1.0, 1.0, 1, true},   {256, 224, 2, 2, 0.97, 0.97, 1, true},
+    {256, 192, 2, 2, 0.93, 0.93, 1, false}, {256, 160, 2, 2, 0.88, 0.88, 1, true},
+    {128, 128, 2, 2, 0.75, 0.50, 2, true},
 };
 // What a product is turned into (train_epilogue.hpp; a gradient's bf16 result
 // or the fp32 partial results of its parts are both kEpiPartial there).
 enum TrainStore { kStoreStats = 0, kStoreXentGrad, kStoreBf16, kStoreParts, kStoreGluGrad, kStoreGlu };
 
-// The compiled kernels: on the tiles above (tile 0, 1) or the stream kernel's
-// configurations (tile 2 + configuration), gate < 0 where it is an argument.
+// The compiled kernels: on the tiles above or the stream kernel's
+// configurations (tile kNumTrainTiles + configuration), gate < 0 where it is an argument.
 // Logits and pre-activations take W as it is stored (column-major B) and the
 // gated forward product either layout; gradients contract over W's rows (dx)
 // or over the tokens (dW), where the second operand is row-major.
@@ -35,7 +39,7 @@ struct TrainKernel {
   int store, tile, gate;
   bool bcol, bf16;
 };
-constexpr int kNumTrainKernels = 46;
+constexpr int kNumTrainKernels = 100;
 struct TrainKernels {
   TrainKernel k[kNumTrainKernels] = {};
   int n = 0;
@@ -54,18 +58,20 @@ struct TrainKernels {
       add(kStoreBf16, t, -1, false, true);
       add(kStoreParts, t, -1, false, false);
     }
-    for (int c = 0; c < 3; ++c) {
-      add(kStoreStats, 2 + c, -1, true, true);
-      add(kStoreXentGrad, 2 + c, -1, true, true);
-      add(kStoreGlu, 2 + c, -1, true, true);
-      add(kStoreGlu, 2 + c, -1, true, false);
+    for (int c = kNumTrainTiles; c < kNumTrainTiles + 3; ++c) {
+      add(kStoreStats, c, -1, true, true);
+      add(kStoreXentGrad, c, -1, true, true);
+      add(kStoreGlu, c, -1, true, true);
+      add(kStoreGlu, c, -1, true, false);
     }
-    for (int g = 0; g < 5; ++g) add(kStoreGluGrad, 0, g, true, true);
-    add(kStoreGluGrad, 1, -1, true, true);
-    for (int l = 0; l < 4; ++l) {
-      for (int g = 1; g < 5; ++g) add(kStoreGlu, 0, g, l & 1, l & 2);
-      add(kStoreGlu, 1, -1, l & 1, l & 2);
+    for (int t = 0; t < kSmallTile; ++t) {
+      if (!kTrainTiles[t].gated) continue;
+      for (int g = 0; g < 5; ++g) add(kStoreGluGrad, t, g, true, true);
+      for (int l = 0; l < 4; ++l)
+        for (int g = 1; g < 5; ++g) add(kStoreGlu, t, g, l & 1, l & 2);
     }
+    add(kStoreGluGrad, kSmallTile, -1, true, true);
+    for (int l = 0; l < 4; ++l) add(kStoreGlu, kSmallTile, -1, l & 1, l & 2);
   }
 };
 constexpr TrainKernels kTrainKernels{};
@@ -107,11 +113,13 @@ inline double product_us(const TrainTile& t, int64_t M, int64_t N, int64_t k_per
   return us;
 }
 
-inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits, int cu) {
+inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits, int cu,
+                                 bool gated = false) {
   TrainProduct best{};
   double best_us = 0.0;
   for (int c = 0; c < kNumTrainTiles; ++c) {
     const TrainTile& t = kTrainTiles[c];
+    if (gated && !t.gated) continue;
     for (int s = 1; s <= max_splits; s *= 2) {
       const int64_t k_per = ceil_div(ceil_div(K, s), 64) * 64;
       // parts of at least 256 keep the load pipeline longer than its ramp
@@ -155,17 +163,17 @@ struct ForwardPlan {
   int seg_cols;
 };
 
-inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu) {
+inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu, bool gated = false) {
   ForwardPlan f{};
   if (M <= kStreamMaxM && K % 2 == 0) {
     const Plan p = make_plan(M, N, K, true, cu);
-    f.z.tile = 2 + p.config - kStreamConfig;
+    f.z.tile = kNumTrainTiles + p.config - kStreamConfig;
     f.z.map = p.map;
     f.z.grid = p.grid;
     f.z.splits = 1;
     f.seg_cols = 32;
   } else {
-    f.z = plan_product(M, N, K, 1, cu);
+    f.z = plan_product(M, N, K, 1, cu, gated);
     const TrainTile& t = kTrainTiles[f.z.tile];
     f.seg_cols = t.bn / t.wn;
   }
@@ -188,7 +196,7 @@ inline GluGradPlan plan_glu_grad(int64_t M, int64_t N, int64_t K, bool want_dx, 
                                  bool want_bias, int cu) {
   GluGradPlan p{};
   if (M <= 0 || N <= 0) return p;
-  p.z = plan_product(M, N, K, 1, cu);
+  p.z = plan_product(M, N, K, 1, cu, true);
   p.dx = plan_product(M, K, N, kMaxSplits, cu);
   p.dw = plan_product(N, K, M, kMaxSplits, cu);
   p.ldz = ceil_div(N, 8) * 8;

@@ -106,7 +106,8 @@ tile_gemm_status_t run_glu(tile_gemm_t h, const void* A, const void* B, void* C,
   TG_TRY(check_device(h));
   const bool bcol = K > 0 && !b_is_row_major(s, N);
   const tg::TrainProduct q =
-      bcol ? tg::plan_forward(M, N, K, h->cu_count).z : tg::plan_product(M, N, K, 1, h->cu_count);
+      bcol ? tg::plan_forward(M, N, K, h->cu_count, true).z
+                                  : tg::plan_product(M, N, K, 1, h->cu_count, true);
   if (q.grid > 0x7fffffff) return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: too many workgroups");
   tg::TrainArgs a{};
   a.A = static_cast<const uint16_t*>(A);
