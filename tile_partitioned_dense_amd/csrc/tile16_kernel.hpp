@@ -157,12 +157,8 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
   const int tid = threadIdx.x;
-  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave - (wave / WN) * WN;
-  const int l16 = lane & 15, lg = lane >> 4;  // block row / column, k chunk
-  // row-major B transposed reads: lane = 16 G + 4 j + q
-  const int tG = lane >> 4, tj = (lane >> 2) & 3, tq = lane & 3;
 
   const int n_tiles = p.map.tiles_m * p.map.tiles_n;
   int n_work = n_tiles;
@@ -184,6 +180,13 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
     // it drains every load at the loop's head; settled here, once per tile,
     // the loop keeps only its own waits.
     if constexpr (TIED) wait_vmcnt<0>();
+    // With a training store, what depends on the lane is formed anew for every
+    // tile: held across the store, the K loop's offsets push it into spilling.
+    int lane = tid & 63;
+    if constexpr (EPI != kEpiNone) asm volatile("" : "+v"(lane));
+    const int l16 = lane & 15, lg = lane >> 4;  // block row / column, k chunk
+    // row-major B transposed reads: lane = 16 G + 4 j + q
+    const int tG = lane >> 4, tj = (lane >> 2) & 3, tq = lane & 3;
     const int M = p.M, N = p.N;
     const int64_t lda = p.lda, ldb = p.ldb;
     const int glu = (EPI == kEpiNone || epi_gated(EPI)) ? p.glu_half : 0;
@@ -253,6 +256,8 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
     // the resource and would read as zero) go through registers.
     const int nk_full = (!BCOL && (N & 1)) ? (K - 1) / BK : K / BK;
 
+    // (see tile64_kernel.hpp)
+    [[maybe_unused]] const bool dma_tail = EPI != kEpiNone && K % 8 == 0 && (BCOL || !(N & 1));
     auto issue_slab = [&](int s) {
       const int st = s % kStages;
       const uint32_t la = lds0 + st * STAGE;
@@ -265,6 +270,22 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
 #pragma unroll
         for (int t = 0; t < B_MAX; ++t)
           if (t < B_MIN || t < b_cnt) dma16(lb + 1024 * (wave + NW * t), rsB, voB[t], 0u);
+      } else if (EPI != kEpiNone && dma_tail) {
+        constexpr int64_t kReach = (int64_t)1 << 31;  // no panel is this long
+        const int64_t a_left = a_bytes - s * a_step, b_left = b_bytes - s * b_step;
+        const i32x4 rsA = make_rsrc(a_panel + s * a_step, a_left < kReach ? a_left : kReach);
+        const i32x4 rsB = make_rsrc(b_panel + s * b_step, b_left < kReach ? b_left : kReach);
+        auto past = [&](int r) { return s * BK + 8 * ((lane & 3) ^ swz16(r)) >= K; };
+#pragma unroll
+        for (int t = 0; t < A_PER; ++t)
+          dma16(la + 1024 * (wave + NW * t), rsA, past(16 * (wave + NW * t) + (lane >> 2)) ? 0x80000000u : voA[t], 0u);
+#pragma unroll
+        for (int t = 0; t < B_MAX; ++t)
+          if (t < B_MIN || t < b_cnt) {
+            bool out = false;  // a row-major B: rows past K are past its resource
+            if constexpr (BCOL) out = past(16 * (wave + NW * t) + (lane >> 2));
+            dma16(lb + 1024 * (wave + NW * t), rsB, out ? 0x80000000u : voB[t], 0u);
+          }
       } else {
         // exact zeros past K (and past M, N) in both operands, through registers
         const int k0 = s * BK;
@@ -600,7 +621,11 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
       constexpr int TP = FN * 32 + 16;
       static_assert(NW * SH * TP <= RING, "a strip of every wave fits the ring");
       constexpr int WC = epi_gated(EPI) ? WTN / 2 : WTN;  // columns of C a wave covers
-      train_store<EPI, OUT_BF16>(acc, lds0 + (uint32_t)(wave * SH * TP), lane, m0 + wm * WTM, n0 + wn * WC,
+      // the store's addresses must not be formed before the K loop (they would
+      // be held, or spilled, across it)
+      int lane_now = lane;
+      asm volatile("" : "+v"(lane_now));
+      train_store<EPI, OUT_BF16>(acc, lds0 + (uint32_t)(wave * SH * TP), lane_now, m0 + wm * WTM, n0 + wn * WC,
                        (int64_t)tn * WN + wn, tm * WM + wm, p, [](floatx4(&row)[FN]) {
                          if constexpr (TIED) pin_row(row);
                        });

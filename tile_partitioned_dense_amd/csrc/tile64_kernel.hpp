@@ -73,11 +73,8 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
   const int tid = threadIdx.x;
-  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave - (wave / WN) * WN;
-  const int l16 = lane & 15, lg = lane >> 4;
-  const int tG = lane >> 4, tj = (lane >> 2) & 3, tq = lane & 3;
 
   const int n_tiles = p.map.tiles_m * p.map.tiles_n;
   int n_work = n_tiles;
@@ -96,6 +93,10 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
     tile_of(p.map, wg, tm, tn);
     // (see tile16_kernel.hpp: the K loop keeps only its own waits)
     if constexpr (TIED) wait_vmcnt<0>();
+    int lane = tid & 63;  // (see tile16_kernel.hpp)
+    if constexpr (EPI != kEpiNone) asm volatile("" : "+v"(lane));
+    const int l16 = lane & 15, lg = lane >> 4;
+    const int tG = lane >> 4, tj = (lane >> 2) & 3, tq = lane & 3;
     const int M = p.M, N = p.N;
     const int64_t lda = p.lda, ldb = p.ldb;
     const int glu = (EPI == kEpiNone || epi_gated(EPI)) ? p.glu_half : 0;
@@ -164,6 +165,11 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
     // the resource and would read as zero) go through registers.
     const int nk_full = (!BCOL && (N & 1)) ? (K - 1) / BK : K / BK;
 
+    // A K tail of whole 16-byte chunks is loaded like any slab, with the chunks
+    // past K sent to an offset that no operand's resource covers (they arrive
+    // as zeros); measured 9 us less per tile than through registers. Only for
+    // the training products: the plain ones keep the path they were tuned on.
+    [[maybe_unused]] const bool dma_tail = EPI != kEpiNone && K % 8 == 0 && (BCOL || !(N & 1));
     // Whole slab s into stage s & 1 (DMA, or the register path past nk_full).
     auto issue_slab = [&](int s) {
       const int st = s & 1;
@@ -177,6 +183,22 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
 #pragma unroll
         for (int t = 0; t < B_MAX; ++t)
           if (t < B_MIN || t < b_cnt) dma16(lb + 1024 * (wave + NW * t), rsB, voB[t], 0u);
+      } else if (EPI != kEpiNone && dma_tail) {
+        constexpr int64_t kReach = (int64_t)1 << 31;  // no panel is this long
+        const int64_t a_left = a_bytes - s * a_step, b_left = b_bytes - s * b_step;
+        const i32x4 rsA = make_rsrc(a_panel + s * a_step, a_left < kReach ? a_left : kReach);
+        const i32x4 rsB = make_rsrc(b_panel + s * b_step, b_left < kReach ? b_left : kReach);
+        auto past = [&](int r) { return s * BK + 8 * ((lane & 7) ^ swz64(r)) >= K; };
+#pragma unroll
+        for (int t = 0; t < A_PER; ++t)
+          dma16(la + 1024 * (wave + NW * t), rsA, past(8 * (wave + NW * t) + (lane >> 3)) ? 0x80000000u : voA[t], 0u);
+#pragma unroll
+        for (int t = 0; t < B_MAX; ++t)
+          if (t < B_MIN || t < b_cnt) {
+            bool out = false;  // a row-major B: rows past K are past its resource
+            if constexpr (BCOL) out = past(8 * (wave + NW * t) + (lane >> 3));
+            dma16(lb + 1024 * (wave + NW * t), rsB, out ? 0x80000000u : voB[t], 0u);
+          }
       } else {
         const int k0 = s * BK;
         uint4* dA = reinterpret_cast<uint4*>(reinterpret_cast<char*>(smem) + st * STAGE);
@@ -599,7 +621,11 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
       constexpr int TP = FN * 32 + 16;
       static_assert(NW * SH * TP <= RING, "a strip of every wave fits the ring");
       constexpr int WC = epi_gated(EPI) ? WTN / 2 : WTN;  // columns of C a wave covers
-      train_store<EPI, OUT_BF16>(acc, lds0 + (uint32_t)(wave * SH * TP), lane, m0 + wm * WTM, n0 + wn * WC,
+      // the store's addresses must not be formed before the K loop (they would
+      // be held, or spilled, across it)
+      int lane_now = lane;
+      asm volatile("" : "+v"(lane_now));
+      train_store<EPI, OUT_BF16>(acc, lds0 + (uint32_t)(wave * SH * TP), lane_now, m0 + wm * WTM, n0 + wn * WC,
                        (int64_t)tn * WN + wn, tm * WM + wm, p, [](floatx4(&row)[FN]) {
                          if constexpr (TIED) pin_row(row);
                        });

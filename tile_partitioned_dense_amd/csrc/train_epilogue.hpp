@@ -94,6 +94,22 @@ constexpr float kLog2e = 1.44269504088896341f;
 
 __device__ __forceinline__ float lane_xor(float v, int m) { return __shfl_xor(v, m, 64); }
 
+// The value of the lane 16 (SPAN = 16) or 32 lanes away joined with the
+// lane's own: both halves of an exchange of a register with itself. These run
+// in the vector ALU, where a cross-lane move through LDS would cost its
+// latency with no other wave on the SIMD to fill it.
+template <int SPAN, class Op>
+__device__ __forceinline__ float join_lanes(float v, Op op) {
+  const uint32_t u = __float_as_uint(v);
+  if constexpr (SPAN == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+}
+
 // Column of row `row`'s target, relative to `first`; a value no column has
 // where the row or its target is outside.
 __device__ __forceinline__ int target_col(const TrainArgs& p, int row, int first) {
@@ -105,11 +121,17 @@ __device__ __forceinline__ int target_col(const TrainArgs& p, int row, int first
 
 // Maximum, sum of exponentials, (sum) and target of one row held as NJ groups
 // of four consecutive columns, group j at column step * j + 4 lg of a segment
-// that starts at column col0 (col0 < N); the lanes of a row differ in lg and
-// are joined by the given exchanges.
-template <int NJ, int X0, int X1>
-__device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, int col0, int row,
+// that starts at column col0 (col0 < N). The lanes of a row differ in lg (two
+// or, with FOUR, four of them). c: the target's column in the segment.
+template <int NJ, bool FOUR>
+__device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, int col0, int row, int c,
                                           int64_t seg, const TrainArgs& p) {
+  const auto add = [](float x, float y) { return x + y; };
+  const auto most = [](float x, float y) { return fmaxf(x, y); };
+  auto join = [&](float x, auto op) {
+    if constexpr (FOUR) x = join_lanes<16>(x, op);
+    return join_lanes<32>(x, op);
+  };
   const int left = p.N - col0 - 4 * lg;  // columns of this lane's groups inside the vocabulary
   float sum = 0.0f;
   if (p.part_sum) {
@@ -118,32 +140,25 @@ __device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, in
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum += (step * j + e < left) ? v[j][e] : 0.0f;
   }
-  float m = -INFINITY;
-  if (left >= step * (NJ - 1) + 4) {
+  if (p.N - col0 < step * NJ) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m = fmaxf(m, v[j][e]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[j][e] = (step * j + e < left) ? v[j][e] : -INFINITY;
-        m = fmaxf(m, v[j][e]);
-      }
+      for (int e = 0; e < 4; ++e) v[j][e] = (step * j + e < left) ? v[j][e] : -INFINITY;
   }
-  if constexpr (X0 > 0) m = fmaxf(m, lane_xor(m, X0));
-  m = fmaxf(m, lane_xor(m, X1));
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = fmaxf(m, v[j][e]);
+  m = join(m, most);
   const float m2 = m * kLog2e;
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(v[j][e], kLog2e, -m2));
-  if constexpr (X0 > 0) s += lane_xor(s, X0);
-  s += lane_xor(s, X1);
-  const int c = target_col(p, row, col0);
+  s = join(s, add);
   if (c >= 0 && c < step * NJ) {
     // few rows have their target in this segment: the search is skipped by
     // every other wave
@@ -153,10 +168,7 @@ __device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, in
       for (int e = 0; e < 4; ++e)
         if (c == step * j + 4 * lg + e) p.hit[row] = v[j][e];
   }
-  if (p.part_sum) {
-    if constexpr (X0 > 0) sum += lane_xor(sum, X0);
-    sum += lane_xor(sum, X1);
-  }
+  if (p.part_sum) sum = join(sum, add);
   if (lg == 0 && row < p.M) {
     p.part[seg * p.M + row] = make_float2(m, s);
     if (p.part_sum) p.part_sum[seg * p.M + row] = sum;
@@ -234,8 +246,8 @@ __device__ __forceinline__ uint32_t lds_load_u32(uint32_t addr) {
 // 8's worth of columns stays together), or -1 where it is outside. Both
 // leading dimensions are padded (ldz to 8 columns, ldzt to 16 rows), so whole
 // chunks are written wherever their first value is inside; the padding is
-// never read. Rows: 16-byte chunks. Transposed: a lane takes two columns and
-// RPL consecutive rows, pairing rows of each column into dwords.
+// never read. No waits are written between the strip's writes, its reads and
+// the next writes: a wave's LDS operations run in order.
 template <int ROWS, int COLS, class ColOf>
 __device__ __forceinline__ void store_both(uint32_t strip, int lane, int grow0, const TrainArgs& p,
                                            ColOf col_of) {
@@ -254,39 +266,52 @@ __device__ __forceinline__ void store_both(uint32_t strip, int lane, int grow0, 
     }
   }
   if (p.Zt) {
-    constexpr int P = COLS / 2 < 64 ? COLS / 2 : 64;  // column pairs covered at once
-    constexpr int RG = 64 / P;                        // lanes sharing a pair (any past RG * P idle)
-    constexpr int RPL = ROWS / RG;                    // rows of each
-    static_assert(RPL == 4 || RPL == 8 || RPL == 16, "whole vector stores");
-    static_assert(COLS / 2 <= 64, "one pass over the columns");
-    const int pr = lane % P, rg = lane / P;
-    const int col = col_of((2 * pr) & ~7);
-    uint32_t d[RPL];
+    if constexpr (ROWS == 16) {
+      // Transposing 8-byte reads: within 16 lanes, lane 4 j + q names row j,
+      // columns 4 q .. + 3 of a 4 x 16 block and receives the four rows of
+      // column lane % 16. Each 16 lanes take another 16-column block, four
+      // reads the sixteen rows: 32 consecutive bytes of one column per lane.
+      constexpr int NB = COLS / 16;
+      const int g = lane >> 4, l16 = lane & 15;
+      const uint32_t src = strip + (uint32_t)((l16 >> 2) * PITCH + (l16 & 3) * 8);
 #pragma unroll
-    for (int r = 0; r < RPL; ++r)  // (idle lanes read row group 0)
-      d[r] = lds_load_u32(strip + (uint32_t)(((rg < RG ? rg : 0) * RPL + r) * PITCH + pr * 4));
-    const int row = grow0 + rg * RPL;
-    if (rg < RG && row < p.M && col >= 0) {
-      const int c = col + ((2 * pr) & 7);
-      uint32_t lo[RPL / 2], hi[RPL / 2];
+      for (int b0 = 0; b0 < NB; b0 += 4) {
+        const int b = b0 + g < NB ? b0 + g : NB - 1;  // idle lanes repeat the last block
+        i16x4 t[4];
 #pragma unroll
-      for (int r = 0; r < RPL / 2; ++r) {
-        lo[r] = pack_halves(d[2 * r], d[2 * r + 1], false);
-        hi[r] = pack_halves(d[2 * r], d[2 * r + 1], true);
-      }
-      uint16_t* z0 = p.Zt + (int64_t)c * p.ldzt + row;
-      uint16_t* z1 = z0 + p.ldzt;
-      if constexpr (RPL == 4) {
-        if (c < p.N) *reinterpret_cast<u32x2s*>(z0) = u32x2s{lo[0], lo[1]};
-        if (c + 1 < p.N) *reinterpret_cast<u32x2s*>(z1) = u32x2s{hi[0], hi[1]};
-      } else {
-#pragma unroll
-        for (int h = 0; h < RPL / 8; ++h) {
-          if (c < p.N)
-            reinterpret_cast<u32x4s*>(z0)[h] = u32x4s{lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]};
-          if (c + 1 < p.N)
-            reinterpret_cast<u32x4s*>(z1)[h] = u32x4s{hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]};
+        for (int q = 0; q < 4; ++q)
+          t[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) i16x4*)(uintptr_t)(src + (uint32_t)(4 * q * PITCH + b * 32)));
+        const int cs = 16 * b + l16, col8 = col_of(cs & ~7);
+        const int c = col8 + (cs & 7);
+        if (b0 + g < NB && grow0 < p.M && col8 >= 0 && c < p.N) {
+          u32x4s* z = reinterpret_cast<u32x4s*>(p.Zt + (int64_t)c * p.ldzt + grow0);
+          const u32x2s w[4] = {__builtin_bit_cast(u32x2s, t[0]), __builtin_bit_cast(u32x2s, t[1]),
+                               __builtin_bit_cast(u32x2s, t[2]), __builtin_bit_cast(u32x2s, t[3])};
+          z[0] = u32x4s{w[0].x, w[0].y, w[1].x, w[1].y};
+          z[1] = u32x4s{w[2].x, w[2].y, w[3].x, w[3].y};
         }
+      }
+    } else {
+      // 32 x 32 (the stream kernel): a lane takes two columns and eight rows
+      static_assert(ROWS == 32 && COLS == 32, "one lane per column pair and eight rows");
+      const int pr = lane & 15, rg = lane >> 4;
+      const int col = col_of((2 * pr) & ~7);
+      uint32_t d[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) d[r] = lds_load_u32(strip + (uint32_t)((rg * 8 + r) * PITCH + pr * 4));
+      const int row = grow0 + rg * 8;
+      if (row < p.M && col >= 0) {
+        const int c = col + ((2 * pr) & 7);
+        u32x4s lo, hi;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          lo[r] = pack_halves(d[2 * r], d[2 * r + 1], false);
+          hi[r] = pack_halves(d[2 * r], d[2 * r + 1], true);
+        }
+        uint16_t* z0 = p.Zt + (int64_t)c * p.ldzt + row;
+        if (c < p.N) *reinterpret_cast<u32x4s*>(z0) = lo;
+        if (c + 1 < p.N) *reinterpret_cast<u32x4s*>(z0 + p.ldzt) = hi;
       }
     }
   }
@@ -321,6 +346,21 @@ __device__ __forceinline__ bool glu_live(int lg) {
   return 2 * J + 1 < FN || lg < 2;
 }
 
+// The bias of a lane's gate and up columns, one load for all block rows.
+template <int NP>
+__device__ __forceinline__ void glu_bias(floatx4 (&bg)[NP], floatx4 (&bu)[NP], int lg, int col0,
+                                         const TrainArgs& p) {
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    const int c = col0 + 8 * (2 * j + (lg >> 1)) + 4 * (lg & 1);
+    bg[j] = bu[j] = floatx4{};
+    if (p.bias && c < p.glu_half) {
+      bg[j] = *reinterpret_cast<const floatx4*>(p.bias + c);
+      bu[j] = *reinterpret_cast<const floatx4*>(p.bias + p.glu_half + c);
+    }
+  }
+}
+
 // kEpiGluGrad for one gate; see train_store.
 template <int GATE, int FM, int FN, class Pin>
 __device__ __forceinline__ void glu_grad_store(floatx4 (&acc)[FM][FN], uint32_t strip, int lane, int row0,
@@ -334,48 +374,59 @@ __device__ __forceinline__ void glu_grad_store(floatx4 (&acc)[FM][FN], uint32_t 
   for (int j = 0; j < NP; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) db[j][0][e] = db[j][1][e] = 0.0f;
+  floatx4 bg[NP], bu[NP];
+  glu_bias(bg, bu, lg, col0, p);
+  // dh of a block row is loaded one block row ahead
+  u32x2s dn[NP];
+  auto load_dh = [&](int i) {
+    const int row = row0 + 16 * i + l16;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int c = col0 + 8 * (2 * j + (lg >> 1)) + 4 * (lg & 1);
+      dn[j] = u32x2s{0u, 0u};
+      if (row < p.M && c < F) dn[j] = *reinterpret_cast<const u32x2s*>(p.dC + (int64_t)row * p.lddc + c);
+    }
+  };
+  load_dh(0);
   static_for<0, FM>([&](auto i_c) {
     constexpr int i = decltype(i_c)::value;
     pin(acc[i]);
-    const int row = row0 + 16 * i + l16;
+    u32x2s dc[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) dc[j] = dn[j];
+    if constexpr (i + 1 < FM) load_dh(i + 1);
     static_for<0, NP>([&](auto j_c) {
       constexpr int j = decltype(j_c)::value;
       float g[4], u[4];
       glu_pair<j>(acc[i], g, u);
-      const int cw = glu_col<j>(lg), c = col0 + cw;
-      float dg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, du[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const int cw = glu_col<j>(lg);
       if (glu_live<j, FN>(lg)) {
-        if (row < p.M && c < F) {
-          const u32x2s dv = *reinterpret_cast<const u32x2s*>(p.dC + (int64_t)row * p.lddc + c);
-          const float dh[4] = {__uint_as_float(dv.x << 16), __uint_as_float(dv.x & 0xffff0000u),
-                               __uint_as_float(dv.y << 16), __uint_as_float(dv.y & 0xffff0000u)};
-          if (p.bias) {
-            const float4 x = *reinterpret_cast<const float4*>(p.bias + c);
-            const float4 y = *reinterpret_cast<const float4*>(p.bias + F + c);
-            g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
-            u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
-          }
+        // rows and columns outside have dh = 0; what their pre-activations are
+        // (rows past M are zero, columns past F those of another half) must
+        // not matter, so their results are set, not multiplied
+        const bool live = row0 + 16 * i + l16 < p.M && col0 + cw < F;
+        const float dh[4] = {__uint_as_float(dc[j].x << 16), __uint_as_float(dc[j].x & 0xffff0000u),
+                             __uint_as_float(dc[j].y << 16), __uint_as_float(dc[j].y & 0xffff0000u)};
+        float dg[4], du[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float act, slope;
-            gate_both<GATE>(g[e], act, slope);
-            dg[e] = dh[e] * u[e] * slope;
-            du[e] = dh[e] * act;
-            db[j][0][e] += dg[e];
-            db[j][1][e] += du[e];
-          }
+        for (int e = 0; e < 4; ++e) {
+          float act, slope;
+          gate_both<GATE>(g[e] + bg[j][e], act, slope);
+          dg[e] = live ? dh[e] * (u[e] + bu[j][e]) * slope : 0.0f;
+          du[e] = live ? dh[e] * act : 0.0f;
+          db[j][0][e] += dg[e];
+          db[j][1][e] += du[e];
         }
         const uint32_t a = strip + (uint32_t)(l16 * PITCH + cw * 2);
         lds_store_u32x2(a, pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
         lds_store_u32x2(a + FN * 16, pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]));
       }
     });
-    wait_lgkmcnt0();
     store_both<16, FN * 16>(strip, lane, row0 + 16 * i, p, [&](int c) {
       const int h = c >= FN * 8, k = col0 + c - h * FN * 8;
       return k < F ? k + h * F : -1;
     });
-    wait_lgkmcnt0();
+    __builtin_amdgcn_sched_barrier(0);  // block rows in turn: interleaved, they spill
   });
   if (!p.dbias_part) return;
   // column sums of the wave's rows, in fp32 before the rounding of dz
@@ -412,15 +463,7 @@ __device__ __forceinline__ void glu_store(floatx4 (&acc)[FM][FN], uint32_t strip
   const int l16 = lane & 15, lg = lane >> 4;
   const int F = p.glu_half;
   floatx4 bg[NP], bu[NP];
-  static_for<0, NP>([&](auto j_c) {
-    constexpr int j = decltype(j_c)::value;
-    const int c = col0 + glu_col<j>(lg);
-    bg[j] = bu[j] = floatx4{};
-    if (p.bias && c < F) {
-      bg[j] = *reinterpret_cast<const floatx4*>(p.bias + c);
-      bu[j] = *reinterpret_cast<const floatx4*>(p.bias + F + c);
-    }
-  });
+  glu_bias(bg, bu, lg, col0, p);
   static_for<0, FM>([&](auto i_c) {
     constexpr int i = decltype(i_c)::value;
     pin(acc[i]);
@@ -443,7 +486,6 @@ __device__ __forceinline__ void glu_store(floatx4 (&acc)[FM][FN], uint32_t strip
           lds_store_f4(a, v);
       }
     });
-    wait_lgkmcnt0();
 #pragma unroll
     for (int c0 = 0; c0 < 16 * CH; c0 += 64) {
       const int c = c0 + lane;
@@ -456,7 +498,6 @@ __device__ __forceinline__ void glu_store(floatx4 (&acc)[FM][FN], uint32_t strip
       if (row < p.M && col < F)
         *reinterpret_cast<u32x4s*>(static_cast<char*>(p.C) + ((int64_t)row * p.ldc + col) * ESZ) = v;
     }
-    wait_lgkmcnt0();
   });
 }
 
@@ -484,34 +525,38 @@ __device__ __forceinline__ void train_store(floatx4 (&acc)[FM][FN], uint32_t str
   constexpr int KIND = epi_kind(EPI);
   if constexpr (KIND == kEpiStats) {
     if (col0 >= p.N) return;
+    int c[FM];  // loaded together: one latency, not one for each block row
+#pragma unroll
+    for (int i = 0; i < FM; ++i) c[i] = target_col(p, row0 + 16 * i + l16, col0);
     static_for<0, FM>([&](auto i_c) {
       constexpr int i = decltype(i_c)::value;
       pin(acc[i]);
-      stats_row<FN, 16, 32>(acc[i], 16, lg, col0, row0 + 16 * i + l16, seg, p);
+      stats_row<FN, true>(acc[i], 16, lg, col0, row0 + 16 * i + l16, c[i], seg, p);
     });
   } else if constexpr (KIND == kEpiXentGrad) {
     constexpr int PITCH = FN * 32 + 16;
     if (col0 >= p.N) return;
+    XentRow r[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int row = row0 + 16 * i + l16;
+      r[i] = row < p.M ? p.rows[row] : XentRow{0.0f, 0.0f, 0.0f, -1};
+      r[i].target -= p.first + col0 + 4 * lg;
+    }
     static_for<0, FM>([&](auto i_c) {
       constexpr int i = decltype(i_c)::value;
       pin(acc[i]);
-      const int row = row0 + 16 * i + l16;
-      XentRow r{0.0f, 0.0f, 0.0f, -1};
-      if (row < p.M) r = p.rows[row];
-      r.target -= p.first + col0 + 4 * lg;
-      const float u = r.b * p.smooth, hit = r.b * p.keep;
+      const float u = r[i].b * p.smooth, hit = r[i].b * p.keep;
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         float g[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] = xent_grad(acc[i][j][e], 16 * j + e, r, u, hit);
+        for (int e = 0; e < 4; ++e) g[e] = xent_grad(acc[i][j][e], 16 * j + e, r[i], u, hit);
         lds_store_u32x2(strip + (uint32_t)(l16 * PITCH + (16 * j + 4 * lg) * 2), pack_bf16x2(g[0], g[1]),
                         pack_bf16x2(g[2], g[3]));
       }
-      wait_lgkmcnt0();
       store_both<16, FN * 16>(strip, lane, row0 + 16 * i, p,
                               [&](int c) { return col0 + c < p.N ? col0 + c : -1; });
-      wait_lgkmcnt0();
     });
   } else {
     if (col0 >= p.glu_half) return;
@@ -548,7 +593,7 @@ __device__ __forceinline__ void train_store_32(floatx16 (&acc)[FM], uint32_t str
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         v[q] = floatx4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
-      stats_row<4, 0, 32>(v, 8, lgrp, col0, row, seg, p);
+      stats_row<4, false>(v, 8, lgrp, col0, row, target_col(p, row, col0), seg, p);
     } else {
       XentRow r{0.0f, 0.0f, 0.0f, -1};
       if (row < p.M) r = p.rows[row];
@@ -562,10 +607,8 @@ __device__ __forceinline__ void train_store_32(floatx16 (&acc)[FM], uint32_t str
         lds_store_u32x2(strip + (uint32_t)(lrow * kStrip32 + (8 * q + 4 * lgrp) * 2),
                         pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]));
       }
-      wait_lgkmcnt0();
       store_both<32, 32>(strip, lane, row0 + 32 * i, p,
                          [&](int c) { return col0 + c < p.N ? col0 + c : -1; });
-      wait_lgkmcnt0();
     }
   }
 }
