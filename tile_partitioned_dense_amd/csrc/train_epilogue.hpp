@@ -152,12 +152,20 @@ __device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, in
 #pragma unroll
     for (int e = 0; e < 4; ++e) m = fmaxf(m, v[j][e]);
   m = join(m, most);
+  // written as passes over independent values: the exponential's latency
+  // would otherwise be paid once per value, with no other wave to hide it
   const float m2 = m * kLog2e;
-  float s = 0.0f;
+  float x[4 * NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(v[j][e], kLog2e, -m2));
+    for (int e = 0; e < 4; ++e) x[4 * j + e] = fmaf(v[j][e], kLog2e, -m2);
+#pragma unroll
+  for (int k = 0; k < 4 * NJ; ++k) x[k] = __builtin_amdgcn_exp2f(x[k]);
+  float part4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int k = 4; k < 4 * NJ; ++k) part4[k & 3] += x[k];
+  float s = (part4[0] + part4[1]) + (part4[2] + part4[3]);
   s = join(s, add);
   if (c >= 0 && c < step * NJ) {
     // few rows have their target in this segment: the search is skipped by
@@ -175,12 +183,30 @@ __device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, in
   }
 }
 
-// G of one logit (XentRow's constants). Rows that count for nothing (b = 0)
-// give an exact zero whatever their logits are.
-__device__ __forceinline__ float xent_grad(float l, int col, const XentRow& r, float u, float hit) {
-  const float g = fmaf(r.a, __builtin_amdgcn_exp2f(fmaf(l, kLog2e, -r.lse2)), -u) -
-                  (col == r.target ? hit : 0.0f);
-  return r.b == 0.0f ? 0.0f : g;
+// G of NV logits of one row, value k being column col(k) of the wave's segment
+// (XentRow's constants, its target relative to the segment). Rows that count
+// for nothing (b = 0) give exact zeros whatever their logits are. `near`:
+// whether any row of the wave has its target in the segment; few do, and the
+// others skip the comparisons.
+template <int NV, class Get, class Col>
+__device__ __forceinline__ void xent_grad(float (&g)[NV], Get logit, Col col, const XentRow& r, bool near,
+                                          const TrainArgs& p) {
+#pragma unroll
+  for (int k = 0; k < NV; ++k) g[k] = fmaf(logit(k), kLog2e, -r.lse2);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) g[k] = __builtin_amdgcn_exp2f(g[k]);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) g[k] = r.b == 0.0f ? 0.0f : r.a * g[k];
+  if (p.smooth != 0.0f) {
+    const float u = r.b * p.smooth;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) g[k] -= u;
+  }
+  if (near) {
+    const float hit = r.b * p.keep;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) g[k] -= col(k) == r.target ? hit : 0.0f;
+  }
 }
 
 // act(z) and act'(z).
@@ -541,20 +567,19 @@ __device__ __forceinline__ void train_store(floatx4 (&acc)[FM][FN], uint32_t str
     for (int i = 0; i < FM; ++i) {
       const int row = row0 + 16 * i + l16;
       r[i] = row < p.M ? p.rows[row] : XentRow{0.0f, 0.0f, 0.0f, -1};
-      r[i].target -= p.first + col0 + 4 * lg;
+      r[i].target -= p.first + col0;
     }
     static_for<0, FM>([&](auto i_c) {
       constexpr int i = decltype(i_c)::value;
       pin(acc[i]);
-      const float u = r[i].b * p.smooth, hit = r[i].b * p.keep;
+      float g[4 * FN];
+      xent_grad(g, [&](int k) { return acc[i][k >> 2][k & 3]; },
+                [&](int k) { return 16 * (k >> 2) + 4 * lg + (k & 3); }, r[i],
+                __any(r[i].target >= 0 && r[i].target < 16 * FN), p);
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        float g[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] = xent_grad(acc[i][j][e], 16 * j + e, r[i], u, hit);
-        lds_store_u32x2(strip + (uint32_t)(l16 * PITCH + (16 * j + 4 * lg) * 2), pack_bf16x2(g[0], g[1]),
-                        pack_bf16x2(g[2], g[3]));
-      }
+      for (int j = 0; j < FN; ++j)
+        lds_store_u32x2(strip + (uint32_t)(l16 * PITCH + (16 * j + 4 * lg) * 2),
+                        pack_bf16x2(g[4 * j], g[4 * j + 1]), pack_bf16x2(g[4 * j + 2], g[4 * j + 3]));
       store_both<16, FN * 16>(strip, lane, row0 + 16 * i, p,
                               [&](int c) { return col0 + c < p.N ? col0 + c : -1; });
     });
@@ -597,16 +622,15 @@ __device__ __forceinline__ void train_store_32(floatx16 (&acc)[FM], uint32_t str
     } else {
       XentRow r{0.0f, 0.0f, 0.0f, -1};
       if (row < p.M) r = p.rows[row];
-      r.target -= p.first + col0 + 4 * lgrp;
-      const float u = r.b * p.smooth, hit = r.b * p.keep;
+      r.target -= p.first + col0;
+      float g[16];
+      xent_grad(g, [&](int k) { return acc[i][k]; },
+                [&](int k) { return 8 * (k >> 2) + 4 * lgrp + (k & 3); }, r,
+                __any(r.target >= 0 && r.target < 32), p);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float g[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] = xent_grad(acc[i][4 * q + e], 8 * q + e, r, u, hit);
+      for (int q = 0; q < 4; ++q)
         lds_store_u32x2(strip + (uint32_t)(lrow * kStrip32 + (8 * q + 4 * lgrp) * 2),
-                        pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]));
-      }
+                        pack_bf16x2(g[4 * q], g[4 * q + 1]), pack_bf16x2(g[4 * q + 2], g[4 * q + 3]));
       store_both<32, 32>(strip, lane, row0 + 32 * i, p,
                          [&](int c) { return col0 + c < p.N ? col0 + c : -1; });
     }
