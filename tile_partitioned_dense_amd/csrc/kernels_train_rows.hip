@@ -1,6 +1,7 @@
 // kernels_train_rows.hip -- the small kernels around the training products:
 // joining the segments of a softmax, per-row constants of its gradient, sums
 // of partial results. All sums run in a fixed order.
+#include "outer_kernel.hpp"
 #include "train_launch.hpp"
 
 namespace tg {
@@ -180,6 +181,20 @@ hipError_t launch_add_rows(const float* part, int64_t rows, int64_t cols, float*
   void* argv[] = {&part, &rows, &cols, &out};
   return hipLaunchKernel(reinterpret_cast<const void*>(&add_rows_kernel), dim3((unsigned)ceil_div(cols, 64)),
                          dim3(256), argv, 0, stream);
+}
+
+hipError_t launch_outer(OuterArgs a, int cu_count, hipStream_t stream) {
+  a.col_groups = (int32_t)ceil_div(a.K, kOuterCols);
+  // about eight workgroups per compute unit (their waves fill its SIMDs), but
+  // at least 64 rows each, so that the x fragments are read for several blocks
+  int64_t rows = ceil_div((int64_t)a.V * a.col_groups, 8 * cu_count);
+  rows = ceil_div(rows < 64 ? 64 : rows, 16) * 16;
+  a.rows_per_group = (int32_t)rows;
+  const dim3 grid((unsigned)(a.col_groups * ceil_div(a.V, rows)));
+  const void* fn = a.T <= 32   ? reinterpret_cast<const void*>(&outer_kernel<1>)
+                   : a.T <= 64 ? reinterpret_cast<const void*>(&outer_kernel<2>)
+                               : reinterpret_cast<const void*>(&outer_kernel<4>);
+  return launch_raw(fn, grid, dim3(256), a, stream);
 }
 
 hipError_t launch_zero(void* p, int64_t rows, int64_t bytes, int64_t pitch, hipStream_t stream) {

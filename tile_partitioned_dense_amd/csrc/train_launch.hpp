@@ -3,6 +3,7 @@
 #pragma once
 
 #include "launch.hpp"
+#include "outer_kernel.hpp"
 #include "train_plan.hpp"
 
 namespace tg {
@@ -51,6 +52,9 @@ struct AddArgs {
   int64_t ldo;
 };
 hipError_t launch_add_parts(const AddArgs& a, hipStream_t stream);
+
+// The weight gradient over at most kOuterMaxT tokens (outer_kernel.hpp).
+hipError_t launch_outer(OuterArgs a, int cu_count, hipStream_t stream);
 
 // out[c] = sum over rows of part[r][c], fp32.
 hipError_t launch_add_rows(const float* part, int64_t rows, int64_t cols, float* out, hipStream_t stream);

@@ -127,6 +127,19 @@ tile_gemm_status_t run_glu(tile_gemm_t h, const void* A, const void* B, void* C,
                                    dtype == TILE_GEMM_BF16_TO_BF16));
 }
 
+// The weight gradient dW = scale * left . right with left V x T (G or dz
+// transposed) and right the T x K activations.
+tile_gemm_status_t run_weight_gradient(const tg::TrainProduct& q, const uint16_t* left, int64_t ldl,
+                                       const uint16_t* right, int64_t ldr, int64_t rows, int64_t cols,
+                                       int64_t len, uint16_t* out, int64_t ldo, const float* scale, float* part,
+                                       int cu, hipStream_t st) {
+  if (len <= tg::kOuterMaxT)
+    return hip_status(tg::launch_outer(tg::OuterArgs{left, ldl, right, ldr, out, ldo, scale, (int32_t)len,
+                                                     (int32_t)rows, (int32_t)cols, 0, 0},
+                                       cu, st));
+  return run_gradient(q, left, ldl, right, ldr, rows, cols, len, out, ldo, scale, part, st);
+}
+
 tile_gemm_status_t run_glu_backward(tile_gemm_t h, const void* A, const void* B, const void* dC, void* dA,
                                     void* dB, int64_t M, int64_t N, int64_t K, const tile_gemm_strides_t* s,
                                     const tile_gemm_strides_t* g, const float* bias, float* dbias, int gate,
@@ -172,8 +185,8 @@ tile_gemm_status_t run_glu_backward(tile_gemm_t h, const void* A, const void* B,
     TG_TRY(run_gradient(p.dx, z, p.ldz, a.B, a.ldb, M, K, N, static_cast<uint16_t*>(dA), g->a_m, nullptr, part,
                         st));
   if (dB)
-    TG_TRY(run_gradient(p.dw, zt, p.ldzt, a.A, a.lda, N, K, M, static_cast<uint16_t*>(dB), g->b_n, nullptr, part,
-                        st));
+    TG_TRY(run_weight_gradient(p.dw, zt, p.ldzt, a.A, a.lda, N, K, M, static_cast<uint16_t*>(dB), g->b_n, nullptr,
+                               part, h->cu_count, st));
   return TILE_GEMM_OK;
 }
 
@@ -273,9 +286,9 @@ tile_gemm_status_t run_xent_backward(tile_gemm_t h, const void* A, const void* B
       }
     }
     if (dB)
-      TG_TRY(run_gradient(tg::plan_xent_dw(M, K, cols, cu), a.Zt, p.ldzt, a.A, a.lda, cols, K, M,
-                          static_cast<uint16_t*>(dB) + v * g->b_n, g->b_n, scale,
-                          reinterpret_cast<float*>(ws + p.off_dw), st));
+      TG_TRY(run_weight_gradient(tg::plan_xent_dw(M, K, cols, cu), a.Zt, p.ldzt, a.A, a.lda, cols, K, M,
+                                 static_cast<uint16_t*>(dB) + v * g->b_n, g->b_n, scale,
+                                 reinterpret_cast<float*>(ws + p.off_dw), cu, st));
   }
   if (dA && p.slots)
     TG_LAUNCH(tg::launch_add_parts(tg::AddArgs{dx_part, M * part_ld, p.slots, (int32_t)M, (int32_t)K, part_ld,
