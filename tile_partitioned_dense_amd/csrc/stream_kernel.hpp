@@ -113,7 +113,7 @@ __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(EpiAr
   const int64_t lda = p.lda, ldb = p.ldb;
   const int nss = (K + KST - 1) / KST;      // stages
   const int nfull = K / KST;                // stages wholly inside K
-  const int glu = (EPI == kEpiNone || EPI == kEpiGlu) ? p.glu_half : 0;
+  const int glu = (EPI == kEpiNone || epi_gated(EPI)) ? p.glu_half : 0;
   const int gshift = glu ? glu - BN / 2 : 0;
 
   auto swz = [](int r) { return SB >= 256 ? (r & 15) : ((r >> 1) & 7); };
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(EpiAr
       wait_lgkmcnt0();
       block_barrier();
     }
-    if constexpr (EPI == kEpiGlu) {
+    if constexpr (epi_gated(EPI)) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         if (kh == 0) {
@@ -292,7 +292,12 @@ __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(EpiAr
         }
         wait_lgkmcnt0();
         block_barrier();
-        glu_strip<OUT_BF16, BR, BN / 2>(ebuf, OPG, m0 + 32 * i, n0, tid, NT, p);
+        if constexpr (EPI == kEpiGlu) {
+          glu_strip<OUT_BF16, BR, BN / 2>(ebuf, OPG, m0 + 32 * i, n0, tid, NT, p);
+        } else {
+          static_assert(EPI != kEpiGluGrad || BR * OPG + BR / 8 * (BN / 2) * 8 <= STAGE, "strip and column sums");
+          glu_grad_strip<BR, BN / 2>(ebuf, OPG, ebuf + BR * OPG, m0 + 32 * i, n0, tm * FM + i, tid, NT, p);
+        }
         wait_lgkmcnt0();
         block_barrier();
       }

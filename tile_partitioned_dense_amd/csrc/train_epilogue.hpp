@@ -679,4 +679,89 @@ __device__ __forceinline__ void glu_strip(uint32_t src, int pitch, int row0, int
   });
 }
 
+// kEpiGluGrad of the stream kernel, from the same block-wide strip of ROWS x
+// (COLS gate, COLS up) fp32 pre-activations. A thread takes one output column
+// and eight rows of it: one 16-byte chunk of each transposed row, and single
+// values of the rows (consecutive lanes write consecutive columns). The
+// strips are small (outputs with few tiles), so the narrow stores do not
+// count. `sums` is LDS for the column sums of the row groups.
+template <int ROWS, int COLS>
+__device__ __forceinline__ void glu_grad_strip(uint32_t src, int pitch, uint32_t sums, int row0, int col0,
+                                               int strip_row, int tid, int nthr, const TrainArgs& p) {
+  constexpr int RG = ROWS / 8;
+  const int F = p.glu_half;
+  for_gate(p.gate, [&](auto gate) {
+    for (int k = tid; k < RG * COLS; k += nthr) {
+      const int rg = k / COLS, cc = k - (k / COLS) * COLS;
+      const int c = col0 + cc, r0 = row0 + 8 * rg;
+      float bg = 0.0f, bu = 0.0f, sg = 0.0f, su = 0.0f;
+      uint32_t wg[4], wu[4];
+      if (c < F && p.bias) {
+        bg = p.bias[c];
+        bu = p.bias[F + c];
+      }
+      float dh[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        dh[r] = (c < F && r0 + r < p.M)
+                    ? __uint_as_float((uint32_t)p.dC[(int64_t)(r0 + r) * p.lddc + c] << 16)
+                    : 0.0f;
+#pragma unroll
+      for (int r = 0; r < 8; r += 2) {
+        float dg[2], du[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a = src + (uint32_t)((8 * rg + r + h) * pitch + cc * 4);
+          const float g = __uint_as_float(lds_load_u32(a)) + bg;
+          const float u = __uint_as_float(lds_load_u32(a + (uint32_t)(COLS * 4))) + bu;
+          float act, slope;
+          gate_both<decltype(gate)::value>(g, act, slope);
+          const bool live = c < F && r0 + r + h < p.M;
+          dg[h] = live ? dh[r + h] * u * slope : 0.0f;
+          du[h] = live ? dh[r + h] * act : 0.0f;
+          sg += dg[h];
+          su += du[h];
+        }
+        wg[r / 2] = pack_bf16x2(dg[0], dg[1]);
+        wu[r / 2] = pack_bf16x2(du[0], du[1]);
+      }
+      if (c < F && r0 < p.M) {
+        if (p.Zt) {
+          *reinterpret_cast<u32x4s*>(p.Zt + (int64_t)c * p.ldzt + r0) = u32x4s{wg[0], wg[1], wg[2], wg[3]};
+          *reinterpret_cast<u32x4s*>(p.Zt + (int64_t)(F + c) * p.ldzt + r0) = u32x4s{wu[0], wu[1], wu[2], wu[3]};
+        }
+        if (p.Z) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            if (r0 + r < p.M) {
+              uint16_t* z = p.Z + (int64_t)(r0 + r) * p.ldz + c;
+              z[0] = (uint16_t)(wg[r / 2] >> (16 * (r & 1)));
+              z[F] = (uint16_t)(wu[r / 2] >> (16 * (r & 1)));
+            }
+          }
+        }
+      }
+      if (p.dbias_part) {
+        lds_store_u32x2(sums + (uint32_t)(k * 8), __float_as_uint(sg), __float_as_uint(su));
+      }
+    }
+  });
+  if (!p.dbias_part) return;
+  wait_lgkmcnt0();
+  block_barrier();
+  for (int cc = tid; cc < COLS; cc += nthr) {
+    const int c = col0 + cc;
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) s[h] += __uint_as_float(lds_load_u32(sums + (uint32_t)((rg * COLS + cc) * 8 + h * 4)));
+    if (c < F) {
+      float* d = p.dbias_part + (int64_t)strip_row * (2 * F) + c;
+      d[0] = s[0];
+      d[F] = s[1];
+    }
+  }
+}
+
 }  // namespace tg

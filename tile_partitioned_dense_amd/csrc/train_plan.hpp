@@ -10,22 +10,33 @@ namespace tg {
 // The tile kernels these operators are compiled for: 256-row tiles of the
 // 64-deep one-wave-per-SIMD kernel in four widths (which one leaves the fewest
 // compute units idle depends on the output) and 128 x 128 tiles of the 32-deep
-// kernel, two of which share a compute unit, for shapes with few tiles. `eff`
-// is the rate of a compute unit relative to 256 x 256 tiles, `eff1` with a
-// single tile on it. `gated`: compiled with the gated block's stores too.
+// kernel, two of which share a compute unit, for shapes with few tiles.
+//
+// A round of tiles, one on every compute unit (two of the small ones), was
+// measured to take us_k microseconds per 1000 values of K and us_tile for the
+// rest (first loads, last slabs, store); with few compute units busy the chip
+// clocks higher and us_k falls by about 15%. us_k1: a small tile alone on its
+// compute unit. `gated`: compiled with the gated block's stores too.
 struct TrainTile {
   int bm, bn, wm, wn;
-  double eff, eff1;
+  double us_k, us_tile, us_k1;
   int occ;
   bool gated;
 };
 constexpr int kNumTrainTiles = 5;
 constexpr int kSmallTile = 4;
 constexpr TrainTile kTrainTiles[kNumTrainTiles] = {
-    {256, 256, 2, 2, 1.0, 1.0, 1, true},   {256, 224, 2, 2, 0.97, 0.97, 1, true},
-    {256, 192, 2, 2, 0.93, 0.93, 1, false}, {256, 160, 2, 2, 0.88, 0.88, 1, true},
-    {128, 128, 2, 2, 0.75, 0.50, 2, true},
+    {256, 256, 2, 2, 19.5, 10.0, 19.5, 1, true}, {256, 224, 2, 2, 17.6, 9.5, 17.6, 1, true},
+    {256, 192, 2, 2, 15.6, 9.0, 15.6, 1, false}, {256, 160, 2, 2, 13.3, 8.5, 13.3, 1, true},
+    {128, 128, 2, 2, 17.5, 5.0, 12.0, 2, true},
 };
+// The stream kernel's configurations, in the same terms: few rows or few
+// tiles, where a tile's K loop is latency and shorter stages of more K win.
+struct TrainStream {
+  double us_k, us_tile;
+};
+constexpr TrainStream kTrainStreams[3] = {{3.9, 2.0}, {8.0, 2.5}, {7.2, 2.5}};
+
 // What a product is turned into (train_epilogue.hpp; a gradient's bf16 result
 // or the fp32 partial results of its parts are both kEpiPartial there).
 enum TrainStore { kStoreStats = 0, kStoreXentGrad, kStoreBf16, kStoreParts, kStoreGluGrad, kStoreGlu };
@@ -39,7 +50,7 @@ struct TrainKernel {
   int store, tile, gate;
   bool bcol, bf16;
 };
-constexpr int kNumTrainKernels = 100;
+constexpr int kNumTrainKernels = 103;
 struct TrainKernels {
   TrainKernel k[kNumTrainKernels] = {};
   int n = 0;
@@ -63,6 +74,7 @@ struct TrainKernels {
       add(kStoreXentGrad, c, -1, true, true);
       add(kStoreGlu, c, -1, true, true);
       add(kStoreGlu, c, -1, true, false);
+      add(kStoreGluGrad, c, -1, true, true);
     }
     for (int t = 0; t < kSmallTile; ++t) {
       if (!kTrainTiles[t].gated) continue;
@@ -100,21 +112,24 @@ struct TrainProduct {
   int64_t grid;
 };
 
-// Microseconds a product takes, roughly: tiles on the busiest compute unit,
-// each a fixed cost plus its K loop at the rate measured on full grids
-// (1.15 PFLOP/s over 256 compute units for 256 x 256 tiles), and the pass
-// that adds the parts (its bytes at 4 TB/s and a launch).
+// Microseconds a product takes, roughly: the rounds of its tiles, and the pass
+// that adds the parts of K (its bytes at 4 TB/s and a launch).
+inline double rounds_us(int64_t tiles, int occ, double us_k, double us_k1, double us_tile, double k, int cu) {
+  if (tiles <= cu) {
+    const double busy = (double)tiles / cu;
+    return k * 1e-3 * us_k1 * (0.85 + 0.15 * busy) + us_tile;
+  }
+  return (double)ceil_div(tiles, (int64_t)cu * occ) * (k * 1e-3 * us_k + us_tile);
+}
 inline double product_us(const TrainTile& t, int64_t M, int64_t N, int64_t k_per, int splits, int cu) {
-  const int64_t work = ceil_div(M, t.bm) * ceil_div(N, t.bn) * splits;
-  const int64_t per_cu = ceil_div(work, cu);
-  const double rate = 4.5e6 * (per_cu >= t.occ ? t.eff : t.eff1);  // flop per us and compute unit
-  double us = (double)per_cu * (2.0 * t.bm * t.bn * (double)k_per / rate + 2.5);
+  const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn) * splits;
+  double us = rounds_us(tiles, t.occ, t.us_k, t.us_k1, t.us_tile, (double)k_per, cu);
   if (splits > 1) us += 4.0 + (double)M * (double)N * (8.0 * splits + 2.0) / 4.0e6;
   return us;
 }
 
 inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits, int cu,
-                                 bool gated = false) {
+                                 bool gated = false, double* us_out = nullptr) {
   TrainProduct best{};
   double best_us = 0.0;
   for (int c = 0; c < kNumTrainTiles; ++c) {
@@ -133,6 +148,7 @@ inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits
       }
     }
   }
+  if (us_out) *us_out = best_us;
   const TrainTile& t = kTrainTiles[best.tile];
   best.map.tiles_m = (int32_t)ceil_div(M, t.bm);
   best.map.tiles_n = (int32_t)ceil_div(N, t.bn);
@@ -155,28 +171,48 @@ inline int64_t region(int64_t& at, int64_t bytes) {
   return p;
 }
 
-// The product over W as it is stored (logits, the gated forward result): up
-// to kStreamMaxM rows (and an even K) it is the stream kernel's, as in
-// make_plan. `seg_cols`: the columns whose logits one wave joins.
+// The product over W as it is stored (logits, gated pre-activations): a tile
+// kernel or, with an even K, a configuration of the stream kernel, whichever
+// is expected to be shorter; neither is shorter than the stream of W's bytes,
+// which decides between them for few rows. `seg_cols`: the columns whose
+// logits one wave joins; `row_groups`: the groups of a tile's rows whose
+// column sums are stored apart.
 struct ForwardPlan {
   TrainProduct z;
-  int seg_cols;
+  int seg_cols, row_groups;
 };
 
 inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu, bool gated = false) {
   ForwardPlan f{};
-  if (M <= kStreamMaxM && K % 2 == 0) {
-    const Plan p = make_plan(M, N, K, true, cu);
-    f.z.tile = kNumTrainTiles + p.config - kStreamConfig;
-    f.z.map = p.map;
-    f.z.grid = p.grid;
-    f.z.splits = 1;
-    f.seg_cols = 32;
-  } else {
-    f.z = plan_product(M, N, K, 1, cu, gated);
-    const TrainTile& t = kTrainTiles[f.z.tile];
-    f.seg_cols = t.bn / t.wn;
+  double us = 0.0;
+  f.z = plan_product(M, N, K, 1, cu, gated, &us);
+  const TrainTile& t = kTrainTiles[f.z.tile];
+  f.seg_cols = t.bn / t.wn;
+  f.row_groups = t.wm;
+  if (K % 2 != 0) return f;
+  const double bytes_us = (double)N * (double)K * 2.0 / 6.0e6;
+  if (us < bytes_us) us = bytes_us;
+  int best = -1;
+  for (int c = 0; c < 3; ++c) {
+    const TileConfig& sc = kTileConfigs[kStreamConfig + c];
+    const int64_t tiles = ceil_div(M, sc.bm) * ceil_div(N, sc.bn);
+    double s = rounds_us(tiles, 1, kTrainStreams[c].us_k, kTrainStreams[c].us_k, kTrainStreams[c].us_tile,
+                         (double)K, cu);
+    if (s < bytes_us) s = bytes_us;
+    // level with a tile kernel (both at the rate of W's bytes): the stream
+    if (s < us || (best < 0 && s <= us)) {
+      best = c;
+      us = s;
+    }
   }
+  if (best < 0) return f;
+  const Plan p = plan_for(1, kStreamConfig + best, M, N, cu);
+  f.z.tile = kNumTrainTiles + best;
+  f.z.map = p.map;
+  f.z.grid = p.grid;
+  f.z.splits = 1;
+  f.seg_cols = 32;
+  f.row_groups = p.bm / 32;
   return f;
 }
 
@@ -196,7 +232,8 @@ inline GluGradPlan plan_glu_grad(int64_t M, int64_t N, int64_t K, bool want_dx, 
                                  bool want_bias, int cu) {
   GluGradPlan p{};
   if (M <= 0 || N <= 0) return p;
-  p.z = plan_product(M, N, K, 1, cu, true);
+  const ForwardPlan f = plan_forward(M, N, K, cu, true);
+  p.z = f.z;
   p.dx = plan_product(M, K, N, kMaxSplits, cu);
   p.dw = plan_product(N, K, M, kMaxSplits, cu);
   p.ldz = ceil_div(N, 8) * 8;
@@ -211,7 +248,7 @@ inline GluGradPlan plan_glu_grad(int64_t M, int64_t N, int64_t K, bool want_dx, 
     if (b > part) part = b;  // the two products run one after the other
   }
   p.off_part = region(at, part);
-  p.bias_rows = (int64_t)p.z.map.tiles_m * kTrainTiles[p.z.tile].wm;
+  p.bias_rows = (int64_t)p.z.map.tiles_m * f.row_groups;
   p.off_bias = region(at, want_bias ? p.bias_rows * N * 4 : 0);
   p.bytes = at;
   return p;
