@@ -225,9 +225,10 @@ tile_gemm_status_t tile_gemm_run_mx(tile_gemm_t h, const void* A, const void* B,
 /*
  * Gated block: C = act(A . B_gate + bias_gate) * (A . B_up + bias_up) over a
  * merged gate+up B, the product of TILE_GEMM_ACT_SWIGLU with a choice of the
- * gate's activation (TILE_GEMM_GATE_SILU is that act). One kernel: both
- * projections, the activation and the product; shapes, layouts, types, bias,
- * errors and ownership as for tile_gemm_run_epilogue with that act.
+ * gate's activation (TILE_GEMM_GATE_SILU computes that act; with a
+ * column-major B its kernels, and so its last bits, may be others). One
+ * kernel: both projections, the activation and the product; shapes, layouts,
+ * types, bias, errors and ownership as for tile_gemm_run_epilogue with that act.
  */
 typedef enum {
   TILE_GEMM_GATE_SILU = 0,      /* x / (1 + e^-x) */

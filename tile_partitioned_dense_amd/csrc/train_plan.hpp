@@ -50,7 +50,7 @@ struct TrainKernel {
   int store, tile, gate;
   bool bcol, bf16;
 };
-constexpr int kNumTrainKernels = 103;
+constexpr int kNumTrainKernels = 109;
 struct TrainKernels {
   TrainKernel k[kNumTrainKernels] = {};
   int n = 0;
@@ -80,7 +80,7 @@ struct TrainKernels {
       if (!kTrainTiles[t].gated) continue;
       for (int g = 0; g < 5; ++g) add(kStoreGluGrad, t, g, true, true);
       for (int l = 0; l < 4; ++l)
-        for (int g = 1; g < 5; ++g) add(kStoreGlu, t, g, l & 1, l & 2);
+        for (int g = (l & 1) ? 0 : 1; g < 5; ++g) add(kStoreGlu, t, g, l & 1, l & 2);
     }
     add(kStoreGluGrad, kSmallTile, -1, true, true);
     for (int l = 0; l < 4; ++l) add(kStoreGlu, kSmallTile, -1, l & 1, l & 2);

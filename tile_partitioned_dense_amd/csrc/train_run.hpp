@@ -94,8 +94,8 @@ tile_gemm_status_t run_gradient(const tg::TrainProduct& q, const uint16_t* left,
                                          st));
 }
 
-// The gated forward product for the gates that the plain kernels do not know
-// (silu is their SwiGLU store).
+// The gated forward product. With a row-major B, silu is the plain kernels'
+// SwiGLU store (which have a few-row kernel for that layout).
 tile_gemm_status_t run_glu(tile_gemm_t h, const void* A, const void* B, void* C, int64_t M, int64_t N,
                            int64_t K, const tile_gemm_strides_t* s, int dtype, const float* bias, int gate,
                            void* stream) {
@@ -309,7 +309,7 @@ tile_gemm_status_t tile_gemm_run_glu(tile_gemm_t h, const void* A, const void* B
                                      void* stream) {
   g_detail[0] = '\0';
   TG_TRY(check_gate((int)gate));
-  if (gate == TILE_GEMM_GATE_SILU)
+  if (gate == TILE_GEMM_GATE_SILU && (!strides || K <= 0 || b_is_row_major(strides, N)))
     return run_impl(h, A, B, C, M, N, K, strides, dtype, stream, nullptr, 0, bias, TILE_GEMM_ACT_SWIGLU);
   return run_glu(h, A, B, C, M, N, K, strides, (int)dtype, bias, (int)gate, stream);
 }
