@@ -113,7 +113,9 @@ struct TrainProduct {
 };
 
 // Microseconds a product takes, roughly: the rounds of its tiles, and the pass
-// that adds the parts of K (its bytes at 4 TB/s and a launch).
+// that adds the parts of K (the bytes it reads and writes at 4 TB/s and a
+// launch). A row-major right operand (the gradients) takes two transposing
+// LDS reads per fragment, measured 12% longer per value of K.
 inline double rounds_us(int64_t tiles, int occ, double us_k, double us_k1, double us_tile, double k, int cu) {
   if (tiles <= cu) {
     const double busy = (double)tiles / cu;
@@ -121,13 +123,16 @@ inline double rounds_us(int64_t tiles, int occ, double us_k, double us_k1, doubl
   }
   return (double)ceil_div(tiles, (int64_t)cu * occ) * (k * 1e-3 * us_k + us_tile);
 }
-inline double product_us(const TrainTile& t, int64_t M, int64_t N, int64_t k_per, int splits, int cu) {
+inline double product_us(const TrainTile& t, int64_t M, int64_t N, int64_t k_per, int splits, bool row_major,
+                         int cu) {
   const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn) * splits;
-  double us = rounds_us(tiles, t.occ, t.us_k, t.us_k1, t.us_tile, (double)k_per, cu);
-  if (splits > 1) us += 4.0 + (double)M * (double)N * (8.0 * splits + 2.0) / 4.0e6;
+  const double f = row_major ? 1.12 : 1.0;
+  double us = rounds_us(tiles, t.occ, f * t.us_k, f * t.us_k1, t.us_tile, (double)k_per, cu);
+  if (splits > 1) us += 4.0 + (double)M * (double)N * (4.0 * splits + 2.0) / 4.0e6;
   return us;
 }
 
+// max_splits > 1: a gradient.
 inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits, int cu,
                                  bool gated = false, double* us_out = nullptr) {
   TrainProduct best{};
@@ -139,7 +144,7 @@ inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits
       const int64_t k_per = ceil_div(ceil_div(K, s), 64) * 64;
       // parts of at least 256 keep the load pipeline longer than its ramp
       if (s > 1 && (k_per < 256 || ceil_div(K, k_per) != s)) continue;
-      const double us = product_us(t, M, N, s == 1 ? K : k_per, s, cu);
+      const double us = product_us(t, M, N, s == 1 ? K : k_per, s, max_splits > 1, cu);
       if (best_us == 0.0 || us < best_us * 0.999) {
         best_us = us;
         best.tile = c;
