@@ -474,6 +474,25 @@ typedef struct {
 tile_gemm_status_t tile_gemm_plan(int64_t M, int64_t N, int64_t K, int b_col_major,
                                   int cu_count, tile_gemm_plan_t* out);
 
+/*
+ * The launch plan of the products of tile_gemm_run_glu, tile_gemm_run_xent and
+ * their backward passes (a pure function, as tile_gemm_plan):
+ * logits or gated pre-activations of an M x N output over K, or a gradient's
+ * M x N result contracted over K. config counts the compiled training tiles
+ * (256 rows x 256, 224, 192 or 160 columns, 128 x 128, then the stream
+ * configurations of 32 x 64, 64 x 128 and 64 x 64); k_split is the number of
+ * parts a gradient's contraction is cut into.
+ */
+typedef enum {
+  TILE_GEMM_TRAIN_LOGITS = 0,
+  TILE_GEMM_TRAIN_GATED = 1,
+  TILE_GEMM_TRAIN_GRADIENT = 2
+} tile_gemm_train_product_t;
+
+tile_gemm_status_t tile_gemm_plan_train(int64_t M, int64_t N, int64_t K,
+                                        tile_gemm_train_product_t product, int cu_count,
+                                        tile_gemm_plan_t* out);
+
 /* The plan of tile_gemm_run_mx for a shape and element format (variant
  * TILE_GEMM_VARIANT_MX; the configurations rank differently for E4M3 and
  * E2M1). An unknown fmt is TILE_GEMM_ERR_DTYPE. */

@@ -101,6 +101,36 @@ def test_backward(g, gate, T, K, F):
     assert bool(sx[:, K:].isnan().all()) and bool(sw[:, K:].isnan().all())
 
 
+def test_no_contraction(g):
+    """K = 0: the gated block of the biases."""
+    T, F = 5, 24
+    b = torch.randn(2 * F)
+    ref = Glu(torch.zeros(T, 8).bfloat16(), torch.zeros(2 * F, 8).bfloat16(), b, "GELU")
+    h = torch.empty(T, F, device=DEV)
+    none = torch.empty(T, 0, dtype=torch.bfloat16, device=DEV)
+    g.glu(none, torch.empty(2 * F, 0, dtype=torch.bfloat16, device=DEV).t(), h, gate=tg.Gate.GELU, bias=b.to(DEV))
+    close(h, ref.h, ref.h_err, False, "h")
+
+
+def test_masked_rows_stay_out(g):
+    """Columns and rows past the edges of a tile read the neighbours' memory or
+    zeros; not even infinities there reach a result."""
+    T, K, F = 70, 72, 40
+    x, w, b, dh = make(T, K, F, 22, True)
+    big_x = torch.full((T + 200, K), float("inf"), dtype=torch.bfloat16, device=DEV)
+    big_w = torch.full((2 * F + 200, K), float("inf"), dtype=torch.bfloat16, device=DEV)
+    big_d = torch.full((T + 200, F), float("inf"), dtype=torch.bfloat16, device=DEV)
+    big_x[:T], big_w[:2 * F], big_d[:T] = x.to(DEV), w.to(DEV), dh.to(DEV)
+    ref = Glu(x, w, b, "GELU_TANH", dh)
+    dx, dw = torch.empty(T, K, dtype=torch.bfloat16, device=DEV), torch.empty(2 * F, K, dtype=torch.bfloat16, device=DEV)
+    db = torch.empty(2 * F, device=DEV)
+    g.glu_backward(big_x[:T], big_w[:2 * F].t(), big_d[:T], dA=dx, dB=dw.t(), dbias=db, bias=b.to(DEV),
+                   gate=tg.Gate.GELU_TANH)
+    close(db, ref.dbias, ref.dbias_err, False, "dbias")
+    close(dx, ref.dx, ref.dx_err, True, "dx")
+    close(dw, ref.dw, ref.dw_err, True, "dw")
+
+
 def integers(T, K, F, seed):
     """Small integers for which every dz of a relu gate is exact in bf16: up to
     three non-zeros of +-1 in a row of x against w in -2..2, dh in -2..2."""

@@ -100,6 +100,73 @@ def test_backward_exact_targets(g, T, K, V, piece):
         assert torch.equal(dw.cpu().float(), want.bfloat16().float())
 
 
+@pytest.mark.parametrize("T,K,V", [(2048, 64, 300), (2500, 72, 1030)])
+def test_many_rows(g, T, K, V):
+    """From 2048 rows on, sixteen rows share a workgroup that joins segments."""
+    x, w, t, _ = make(T, K, V, 16, 0.3)
+    ref = Xent(x, w, t, smoothing=0.1, z_loss=1e-3)
+    loss, lse = forward(g, put(x), put(w), t.to(DEV), label_smoothing=0.1, z_loss=1e-3)
+    close(lse, ref.lse, ref.lse_err, False, "lse")
+    close(loss, ref.loss, ref.loss_err, False, "loss")
+
+
+@pytest.mark.parametrize("ignore", [0, 17, 2 ** 40, -(2 ** 63)])
+def test_any_ignore_index(g, ignore):
+    """The index to leave out may be a column of the vocabulary or no int32."""
+    T, K, V = 90, 64, 120
+    x, w, t, d = make(T, K, V, 17)
+    t[::3] = ignore if abs(ignore) < 2 ** 31 else 5
+    ref = Xent(x, w, t, ignore=ignore, dloss=d)
+    xd, wd = put(x), put(w)
+    for it in (torch.int64, torch.int32):
+        td = t.to(DEV, it)
+        loss, lse = forward(g, xd, wd, td, ignore_index=ignore)
+        close(loss, ref.loss, ref.loss_err, False, "loss")
+        dx = torch.empty_like(xd)
+        g.xent_backward(xd, wd.t(), td, lse, d.to(DEV), dA=dx, ignore_index=ignore)
+        close(dx, ref.dx, ref.dx_err, True, "dx")
+
+
+@pytest.mark.parametrize("T", [8, 300])
+def test_weights_past_four_gib(g, T):
+    """A vocabulary whose weights span more than 4 GiB: rows on both sides of
+    the 32-bit boundary, by the loss (targets there) and by single gradients."""
+    K, V = 8192, 270000  # 4.4 GB
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    gen = torch.Generator(device=DEV).manual_seed(18)
+    w = torch.empty(V, K, dtype=torch.bfloat16, device=DEV)
+    for a in range(0, V, 30000):
+        w[a:a + 30000] = torch.randn(min(30000, V - a), K, generator=gen, device=DEV) * K ** -0.5
+    x = torch.randn(T, K, generator=gen, device=DEV).bfloat16()
+    edge = 2 ** 32 // (2 * K)
+    t = torch.randint(0, V, (T,), generator=gen, device=DEV)
+    t[:4] = torch.tensor([edge - 1, edge, V - 1, 0], device=DEV)
+    loss, lse = forward(g, x, w, t)
+    want = torch.full((T,), -math.inf, device=DEV, dtype=torch.float64)
+    for a in range(0, V, 30000):
+        want = torch.logaddexp(want, torch.logsumexp((x.double() @ w[a:a + 30000].double().t()), 1))
+    hit = (x.double() * w[t].double()).sum(1)
+    # logits of about unit size over 8192 products: TAU * D is 1e-5 * 0.64 * 91
+    assert float((lse.double() - want).abs().max()) <= 1e-3
+    assert float((loss.double() - (want - hit)).abs().max()) <= 2e-3
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    d = torch.ones(T, device=DEV)
+    g.xent_backward(x, w.t(), t, lse, d, dA=dx, dB=dw.t())
+    rows = torch.tensor([0, edge - 1, edge, V - 1, V // 2], device=DEV)
+    G = torch.exp(x.double() @ w[rows].double().t() - want[:, None])
+    G -= (t[:, None] == rows[None]).double()
+    wdw = G.t() @ x.double()
+    # each of the T terms and the result rounded to bf16
+    err = 2.0 ** -8 * (G.abs().t() @ x.double().abs() + wdw.abs()) + 1e-4
+    assert bool(((dw[rows].double() - wdw).abs() <= err).all())
+    wdx = torch.zeros(T, K, device=DEV, dtype=torch.float64)
+    for a in range(0, V, 30000):
+        wdx += torch.exp(x.double() @ w[a:a + 30000].double().t() - want[:, None]) @ w[a:a + 30000].double()
+    wdx -= w[t].double()
+    assert float((dx.double() - wdx).norm() / wdx.norm()) <= 1.5 * 2.0 ** -8
+
+
 def test_large_and_tiny_logits(g):
     """Logits in the thousands of both signs: no exponential overflows."""
     T, K, V = 70, 64, 600

@@ -174,3 +174,26 @@ def test_workspaces(M, N, K):
                     strides=st, grad_strides=st, options=o, workspace=far[6])
         assert tg.tile_gemm_check_xent_backward(workspace_bytes=need, **args) == Status.OK
         assert tg.tile_gemm_check_xent_backward(workspace_bytes=need - 1, **args) == Status.ERR_WORKSPACE
+
+
+def test_plans():
+    """A training product's plan is a partition like a plain product's: tiles
+    that cover the output, no more workgroups than pieces of work."""
+    for product in tg.TrainProduct:
+        for M, N, K in ((1, 1, 1), (1, 131072, 4096), (45, 10928, 4096), (1501, 5488, 4104), (8192, 7168, 8192),
+                        (129, 129, 129), (5000, 64, 200000)):
+            p = tg.tile_gemm_plan_train(M, N, K, product)
+            assert p.tiles_m == -(-M // p.bm) and p.tiles_n == -(-N // p.bn) and p.tiles == p.tiles_m * p.tiles_n
+            assert 1 <= p.grid <= p.tiles * p.k_split
+            assert p.k_split == 1 or product == tg.TrainProduct.GRADIENT
+            cover = 0
+            for i in range(min(p.tiles, 4096)):
+                _, _, rows, cols = tg.tile_gemm_tile_of(p, M, N, i)
+                assert rows > 0 and cols > 0
+                cover += rows * cols
+            assert p.tiles > 4096 or cover == M * N
+    with pytest.raises(tg.TileGemmError):
+        tg.tile_gemm_plan_train(0, 1, 1, 0)
+    with pytest.raises(tg.TileGemmError):
+        tg.tile_gemm_plan_train(1, 1, 1, 3)
+    assert tg.tile_gemm_plan_train(101, 999, 77, 0).config < 5  # an odd K: no stream configuration

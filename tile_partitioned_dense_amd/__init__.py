@@ -21,6 +21,7 @@ __all__ = ["tile_gemm_create", "tile_gemm_run", "tile_gemm_run_debug", "tile_gem
            "tile_gemm_check_glu_backward", "Gate", "tile_gemm_run_xent", "tile_gemm_xent_workspace",
            "tile_gemm_check_xent", "tile_gemm_run_xent_backward", "tile_gemm_xent_backward_workspace",
            "tile_gemm_check_xent_backward", "XentOptions", "IndexType",
+           "TrainProduct", "tile_gemm_plan_train",
            "tile_gemm_status_str", "tile_gemm_check_args", "tile_gemm_plan",
            "tile_gemm_tile_of", "TileGemm", "TileGemmError", "Status", "Dtype",
            "Strides", "Plan", "library_path", "load_library", "last_error_detail",

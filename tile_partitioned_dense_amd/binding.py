@@ -53,6 +53,13 @@ class Gate(enum.IntEnum):
     SIGMOID = 4
 
 
+class TrainProduct(enum.IntEnum):
+    """Products of the gated block and the cross entropy (tile_gemm_plan_train)."""
+    LOGITS = 0
+    GATED = 1
+    GRADIENT = 2
+
+
 class IndexType(enum.IntEnum):
     I32 = 0
     I64 = 1
@@ -188,7 +195,8 @@ def load_library():
     lib.tile_gemm_check_xent_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64,
                                                   P(Strides), P(Strides), PX, vp, i64]
     lib.tile_gemm_xent_backward_workspace.argtypes = [vp, i64, i64, i64, P(Strides), PX, P(i64)]
-    for name in ("run_glu", "run_glu_backward", "check_glu_backward", "glu_backward_workspace",
+    lib.tile_gemm_plan_train.argtypes = [i64, i64, i64, i32, i32, P(Plan)]
+    for name in ("plan_train", "run_glu", "run_glu_backward", "check_glu_backward", "glu_backward_workspace",
                  "run_xent", "check_xent", "xent_workspace", "run_xent_backward",
                  "check_xent_backward", "xent_backward_workspace"):
         getattr(lib, "tile_gemm_" + name).restype = i32
@@ -688,6 +696,13 @@ def tile_gemm_run_xent_backward(h, A, B, target, lse, dloss, dA=None, dB=None, i
         h, A.data_ptr(), B.data_ptr(), target.data_ptr(), lse.data_ptr(), dloss.data_ptr(), p_dA, p_dB, M,
         N, K, ctypes.byref(s), ctypes.byref(g), ctypes.byref(o), workspace.data_ptr(), nbytes, raw)
     return _result(st, check)
+
+
+def tile_gemm_plan_train(M, N, K, product, cu_count=256) -> Plan:
+    p = Plan()
+    _raise_if(load_library().tile_gemm_plan_train(int(M), int(N), int(K), int(product), int(cu_count),
+                                                  ctypes.byref(p)))
+    return p
 
 
 def _strides(s):

@@ -221,6 +221,33 @@ inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu, bool ga
   return f;
 }
 
+// A training product as a launch plan (log lines, introspection).
+inline Plan train_plan(const TrainProduct& q) {
+  Plan p{};
+  p.variant = 1;
+  p.config = q.tile;
+  if (q.tile < kNumTrainTiles) {
+    const TrainTile& t = kTrainTiles[q.tile];
+    p.bm = t.bm;
+    p.bn = t.bn;
+    p.bk = t.bm == 256 ? 64 : 32;
+    p.threads = t.wm * t.wn * 64;
+    p.lds_bytes = (t.bm == 256 ? 2 : 4) * (t.bm + t.bn) * p.bk * 2;
+  } else {
+    const TileConfig& c = kTileConfigs[kStreamConfig + q.tile - kNumTrainTiles];
+    p.bm = c.bm;
+    p.bn = c.bn;
+    p.bk = c.sb / 2;
+    p.threads = c.bn / 32 * c.ks * 64;
+    p.lds_bytes = tile_lds_bytes(c);
+  }
+  p.map = q.map;
+  p.k_split = q.splits;
+  p.tiles = (int64_t)q.map.tiles_m * q.map.tiles_n;
+  p.grid = q.grid;
+  return p;
+}
+
 // ------------------------------------------------------------ gated block
 
 struct GluGradPlan {

@@ -41,28 +41,7 @@ tile_gemm_status_t check_device(tile_gemm_t h) {
 
 void log_product(tile_gemm_handle* h, const char* kind, int64_t M, int64_t N, int64_t K,
                  const tg::TrainProduct& q) {
-  if (!h->log) return;
-  tg::Plan p{};
-  p.variant = 1;
-  p.config = q.tile;
-  if (q.tile < tg::kNumTrainTiles) {
-    const tg::TrainTile& t = tg::kTrainTiles[q.tile];
-    p.bm = t.bm;
-    p.bn = t.bn;
-    p.bk = t.bm == 256 ? 64 : 32;
-    p.threads = t.wm * t.wn * 64;
-  } else {
-    const tg::TileConfig& c = tg::kTileConfigs[tg::kStreamConfig + q.tile - tg::kNumTrainTiles];
-    p.bm = c.bm;
-    p.bn = c.bn;
-    p.bk = c.sb / 2;
-    p.threads = c.bn / 32 * c.ks * 64;
-  }
-  p.tiles = (int64_t)q.map.tiles_m * q.map.tiles_n;
-  p.grid = q.grid;
-  p.k_split = q.splits;
-  p.map = q.map;
-  log_plan(h, kind, M, N, K, 1, 1, 0, p);
+  if (h->log) log_plan(h, kind, M, N, K, 1, 1, 0, tg::train_plan(q));
 }
 
 // One gradient: out (bf16) = scale * (left [rows x len]) . (right [len x cols],
@@ -340,6 +319,22 @@ tile_gemm_status_t tile_gemm_glu_backward_workspace(tile_gemm_t h, int64_t M, in
   if (!bytes) return fail(TILE_GEMM_ERR_NULL_ARG, "bytes: NULL");
   TG_TRY(check_train_shape(M, N, K, kTrainMaxRows));
   *bytes = tg::plan_glu_grad(M, N, K, true, true, true, handle_cus(h)).bytes;
+  return TILE_GEMM_OK;
+}
+
+tile_gemm_status_t tile_gemm_plan_train(int64_t M, int64_t N, int64_t K, tile_gemm_train_product_t product,
+                                        int cu_count, tile_gemm_plan_t* out) {
+  g_detail[0] = '\0';
+  if (!out) return fail(TILE_GEMM_ERR_NULL_ARG, "out: NULL");
+  if (M < 1 || N < 1 || K < 1 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+    return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: M, N and K must be in [1, 2^31)");
+  if (product < TILE_GEMM_TRAIN_LOGITS || product > TILE_GEMM_TRAIN_GRADIENT)
+    return fail(TILE_GEMM_ERR_BAD_SHAPE, "product: unknown value %d", (int)product);
+  if (cu_count <= 0) return fail(TILE_GEMM_ERR_DEVICE, "cu_count: %d", cu_count);
+  const tg::TrainProduct q = product == TILE_GEMM_TRAIN_GRADIENT
+                                 ? tg::plan_product(M, N, K, tg::kMaxSplits, cu_count)
+                                 : tg::plan_forward(M, N, K, cu_count, product == TILE_GEMM_TRAIN_GATED).z;
+  fill_plan(tg::train_plan(q), out);
   return TILE_GEMM_OK;
 }
 
