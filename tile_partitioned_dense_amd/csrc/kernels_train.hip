@@ -19,7 +19,7 @@ const void* train_fn(int& threads) {
                                                    : kEpiPartial;
   constexpr int epi = k.gate >= 0 ? with_gate(kind, k.gate) : kind;
   if constexpr (k.tile >= kNumTrainTiles) {
-    constexpr TileConfig c = kTileConfigs[kStreamConfig + k.tile - kNumTrainTiles];
+    constexpr TrainStream c = kTrainStreams[k.tile - kNumTrainTiles];
     threads = c.bn / 32 * c.ks * 64;
     return reinterpret_cast<const void*>(&stream_gemm_kernel<c.bm, c.bn, c.sb, c.stages, c.ks, k.bf16, false, epi>);
   } else {

@@ -18,15 +18,15 @@
 // fetches; the sixteen rows one MFMA operand read touches (same chunk,
 // consecutive rows) then sit in sixteen distinct bank groups.
 //
-// KS waves (one or two) work on each 32-column block of the tile, all its
+// KS waves (one, two or four) work on each 32-column block of the tile, all its
 // rows: wave w takes block w % (BN / 32) and, of every stage's MFMA steps,
 // the share (w / (BN / 32)) * NSTEP / KS ..; every wave issues a share of
-// the loads (two waves per SIMD hide each other's issue stalls). A wave holds
+// the loads (waves sharing a SIMD hide each other's stalls). A wave holds
 // one 32 x 32 accumulator block per 32 rows, transposed (the B fragment is
 // the MFMA's first operand, as in mma(), and is read once for all blocks),
 // fed by v_mfma_f32_32x32x16_bf16 over chunk pairs 2 t, 2 t + 1 of a stage.
-// With KS = 2 the second wave of a block adds its partial sums into the
-// first's after the K loop, always in that order, and the first stores. With
+// With KS > 1 the first wave of a block adds the others' partial sums to its
+// own after the K loop, always in that order, and stores. With
 // BM = 16 the lanes of rows 16..31 give zero A operands and are never
 // stored.
 //
@@ -38,7 +38,7 @@
 // and the next tile starts with its ring already filling; the store stages
 // the tile in the buffer of its last stage, the one buffer no load is
 // filling then. Each wave accumulates its share of K in
-// ascending order in fp32, and the two shares of a block meet in a fixed
+// ascending order in fp32, and the shares of a block meet in a fixed
 // order: results are bit-identical run to run. A last stage that ends
 // inside K zeroes, in both operands, every value at or past K (the bytes
 // loaded there belong to the next row, or read as zero past the operand).
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(EpiAr
   static_assert(BM == 16 || BM == 32 || BM == 64, "half a 32-row block, or one or two blocks");
   static_assert(BN % 64 == 0 && BN <= 256, "whole waves, even gate and up halves");
   static_assert(SB == 128 || SB == 256 || SB == 512, "stage rows of whole 128-byte lines");
-  static_assert(KS == 1 || KS == 2, "one or two waves per 32-column block");
+  static_assert(KS == 1 || KS == 2 || KS == 4, "one, two or four waves per 32-column block");
   constexpr int NCB = BN / 32;               // 32-column blocks
   constexpr int NW = NCB * KS;               // waves (all of them issue loads)
   constexpr int NT = NW * 64;
@@ -99,7 +99,7 @@ __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(EpiAr
   static_assert(RING <= 160 * 1024, "LDS");
   constexpr int OPF = 32 * 4 + 16;          // per-wave fp32 strip pitch
   constexpr int OPG = BN * 4 + 16;          // block-wide fp32 strip pitch (SiLU(gate) * up)
-  constexpr int PART = KS > 1 ? NCB * FM * 4096 : 0;  // second waves' partial sums
+  constexpr int PART = (KS - 1) * NCB * FM * 4096;  // the other waves' partial sums
   static_assert(NCB * 32 * OPF <= STAGE && 32 * OPG <= STAGE && PART <= STAGE,
                 "staged strips, and before them the partial sums, fit one stage buffer");
 
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(EpiAr
   }
   const uint32_t ldsw = __builtin_amdgcn_readfirstlane(lds0 + 1024 * wave);
 
-  // Wave w works on column block cb = w % NCB and, with two waves per block,
+  // Wave w works on column block cb = w % NCB and, with several waves per block,
   // on MFMA steps kh * KSTEP .. of every stage (kh = w / NCB).
   const int cb = wave % NCB, kh = wave / NCB;
   // Operand reads: A row 32 i + lrow of block i (rows >= BM give zeros), B
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(EpiAr
 
     // Store: the finished accumulators are staged as fp32 in the free ring
     // and written once per element (bias and activation applied there). With
-    // two waves per block the second passes its partial sums through LDS
+    // several waves per block the others pass their partial sums through LDS
     // (the top of the ring) and the first adds them, always in that order.
     wait_lgkmcnt0();
     block_barrier();
@@ -257,25 +257,28 @@ __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(EpiAr
     const uint32_t ebuf = lds0 + (uint32_t)(((gbase + nss + NST - 1) % NST) * STAGE);
     if constexpr (KS > 1) {
       const uint32_t pb = ebuf;
-      if (kh == 1) {
+      if (kh > 0) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            lds_store_f4(pb + (uint32_t)((cb * FM + i) * 4096 + q * 1024 + lane * 16),
+            lds_store_f4(pb + (uint32_t)((((kh - 1) * NCB + cb) * FM + i) * 4096 + q * 1024 + lane * 16),
                          floatx4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]});
       }
       wait_lgkmcnt0();
       block_barrier();
       if (kh == 0) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int h = 0; h < KS - 1; ++h)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const floatx4 v = lds_load_f4(pb + (uint32_t)((cb * FM + i) * 4096 + q * 1024 + lane * 16));
+          for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][4 * q + e] += v[e];
-          }
+            for (int q = 0; q < 4; ++q) {
+              const floatx4 v =
+                  lds_load_f4(pb + (uint32_t)(((h * NCB + cb) * FM + i) * 4096 + q * 1024 + lane * 16));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][4 * q + e] += v[e];
+            }
       }
       // the strips below reuse the partial sums' bytes
       wait_lgkmcnt0();

@@ -30,12 +30,21 @@ constexpr TrainTile kTrainTiles[kNumTrainTiles] = {
     {256, 192, 2, 2, 15.6, 9.0, 15.6, 1, false}, {256, 160, 2, 2, 13.3, 8.5, 13.3, 1, true},
     {128, 128, 2, 2, 17.5, 5.0, 12.0, 2, true},
 };
-// The stream kernel's configurations, in the same terms: few rows or few
-// tiles, where a tile's K loop is latency and shorter stages of more K win.
+// The stream kernel's configurations here, in the same terms: for few rows or
+// few tiles, where a tile's K loop is latency and long stages shared by many
+// waves win. (Four waves on each 32-column block instead of the two of the
+// plain configurations: 64 x 64 tiles 7.2 to 4.2 us per 1000 of K, 32 x 64
+// tiles 3.9 to 3.3.)
 struct TrainStream {
+  int bm, bn, sb, stages, ks;
   double us_k, us_tile;
 };
-constexpr TrainStream kTrainStreams[3] = {{3.9, 2.0}, {8.0, 2.5}, {7.2, 2.5}};
+constexpr int kNumTrainStreams = 3;
+constexpr TrainStream kTrainStreams[kNumTrainStreams] = {
+    {32, 64, 512, 3, 4, 3.3, 2.0},
+    {64, 128, 256, 3, 2, 8.0, 2.5},
+    {64, 64, 512, 2, 4, 4.2, 2.5},
+};
 
 // What a product is turned into (train_epilogue.hpp; a gradient's bf16 result
 // or the fp32 partial results of its parts are both kEpiPartial there).
@@ -69,7 +78,7 @@ struct TrainKernels {
       add(kStoreBf16, t, -1, false, true);
       add(kStoreParts, t, -1, false, false);
     }
-    for (int c = kNumTrainTiles; c < kNumTrainTiles + 3; ++c) {
+    for (int c = kNumTrainTiles; c < kNumTrainTiles + kNumTrainStreams; ++c) {
       add(kStoreStats, c, -1, true, true);
       add(kStoreXentGrad, c, -1, true, true);
       add(kStoreGlu, c, -1, true, true);
@@ -132,6 +141,15 @@ inline double product_us(const TrainTile& t, int64_t M, int64_t N, int64_t k_per
   return us;
 }
 
+inline TileMap tile_map(int64_t M, int64_t N, int bm, int bn) {
+  TileMap m{};
+  m.tiles_m = (int32_t)ceil_div(M, bm);
+  m.tiles_n = (int32_t)ceil_div(N, bn);
+  m.group_m = pick_group_m(m.tiles_m, m.tiles_n);
+  m.xcds = kXcds;
+  return m;
+}
+
 // max_splits > 1: a gradient.
 inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits, int cu,
                                  bool gated = false, double* us_out = nullptr) {
@@ -155,10 +173,7 @@ inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits
   }
   if (us_out) *us_out = best_us;
   const TrainTile& t = kTrainTiles[best.tile];
-  best.map.tiles_m = (int32_t)ceil_div(M, t.bm);
-  best.map.tiles_n = (int32_t)ceil_div(N, t.bn);
-  best.map.group_m = pick_group_m(best.map.tiles_m, best.map.tiles_n);
-  best.map.xcds = kXcds;
+  best.map = tile_map(M, N, t.bm, t.bn);
   best.grid = persistent_grid((int64_t)best.map.tiles_m * best.map.tiles_n * best.splits, cu * t.occ);
   return best;
 }
@@ -198,11 +213,10 @@ inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu, bool ga
   const double bytes_us = (double)N * (double)K * 2.0 / 6.0e6;
   if (us < bytes_us) us = bytes_us;
   int best = -1;
-  for (int c = 0; c < 3; ++c) {
-    const TileConfig& sc = kTileConfigs[kStreamConfig + c];
+  for (int c = 0; c < kNumTrainStreams; ++c) {
+    const TrainStream& sc = kTrainStreams[c];
     const int64_t tiles = ceil_div(M, sc.bm) * ceil_div(N, sc.bn);
-    double s = rounds_us(tiles, 1, kTrainStreams[c].us_k, kTrainStreams[c].us_k, kTrainStreams[c].us_tile,
-                         (double)K, cu);
+    double s = rounds_us(tiles, 1, sc.us_k, sc.us_k, sc.us_tile, (double)K, cu);
     if (s < bytes_us) s = bytes_us;
     // level with a tile kernel (both at the rate of W's bytes): the stream
     if (s < us || (best < 0 && s <= us)) {
@@ -211,13 +225,13 @@ inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu, bool ga
     }
   }
   if (best < 0) return f;
-  const Plan p = plan_for(1, kStreamConfig + best, M, N, cu);
+  const TrainStream& sc = kTrainStreams[best];
   f.z.tile = kNumTrainTiles + best;
-  f.z.map = p.map;
-  f.z.grid = p.grid;
+  f.z.map = tile_map(M, N, sc.bm, sc.bn);
+  f.z.grid = persistent_grid((int64_t)f.z.map.tiles_m * f.z.map.tiles_n, cu);
   f.z.splits = 1;
   f.seg_cols = 32;
-  f.row_groups = p.bm / 32;
+  f.row_groups = sc.bm / 32;
   return f;
 }
 
@@ -234,12 +248,12 @@ inline Plan train_plan(const TrainProduct& q) {
     p.threads = t.wm * t.wn * 64;
     p.lds_bytes = (t.bm == 256 ? 2 : 4) * (t.bm + t.bn) * p.bk * 2;
   } else {
-    const TileConfig& c = kTileConfigs[kStreamConfig + q.tile - kNumTrainTiles];
+    const TrainStream& c = kTrainStreams[q.tile - kNumTrainTiles];
     p.bm = c.bm;
     p.bn = c.bn;
     p.bk = c.sb / 2;
     p.threads = c.bn / 32 * c.ks * 64;
-    p.lds_bytes = tile_lds_bytes(c);
+    p.lds_bytes = c.stages * (c.bm + c.bn) * c.sb;
   }
   p.map = q.map;
   p.k_split = q.splits;
