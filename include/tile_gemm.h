@@ -321,8 +321,9 @@ tile_gemm_status_t tile_gemm_run_xent(tile_gemm_t h, const void* A, const void* 
  * may be NULL. M = 0 makes dB zero. A row of A that holds infinities or NaN
  * makes dB NaN even where the row is ignored (0 * NaN).
  *
- * Limits of both: M, K and b_n below 2^22, A and dA below 4 GiB. Workspaces,
- * errors and ownership as for tile_gemm_run_glu_backward; the workspace sizes
+ * Limits of both: M, K and b_n below 2^22; M / 32 times N / 64, and M / 32 and
+ * N / 32 times K / 64, below 2^31; A and dA below 4 GiB. Workspaces, errors and
+ * ownership as for tile_gemm_run_glu_backward; the workspace sizes
  * are those of tile_gemm_xent_workspace and tile_gemm_xent_backward_workspace
  * for the same shape, strides and options.
  */

@@ -92,6 +92,7 @@ def test_glu_backward(kw, status):
     (dict(N=0), Status.ERR_BAD_SHAPE),
     (dict(K=0), Status.ERR_BAD_SHAPE),
     (dict(N=1 << 31), Status.ERR_BAD_SHAPE),
+    (dict(M=1 << 21, N=(1 << 31) - 1, K=8, strides=(8, 1, 1, 8, 0, 0)), Status.ERR_BAD_SHAPE),  # 2^41 tiles
     (dict(target_type=2), Status.ERR_DTYPE),
     (dict(label_smoothing=-0.1), Status.ERR_BAD_SHAPE),
     (dict(label_smoothing=float("nan")), Status.ERR_BAD_SHAPE),

@@ -11,8 +11,7 @@
 // MFMA operands as in tile16_kernel.hpp: the x fragment is the row operand, so
 // lane l receives row l % 16 of a block, four consecutive columns 4 (l / 16) ..
 // of it. The wave's 16 x 64 results pass through a strip of LDS private to it
-// (no barrier), so that every store instruction writes whole 128-byte lines;
-// stores of half lines measured 4.2 TB/s.
+// (no barrier), so that every store instruction writes whole 128-byte lines.
 #pragma once
 
 #include "train_epilogue.hpp"

@@ -82,6 +82,13 @@ tile_gemm_status_t check_train_shape(int64_t M, int64_t N, int64_t K, int64_t ma
     return fail(TILE_GEMM_ERR_BAD_SHAPE,
                 "shape: M=%lld N=%lld K=%lld, need M and K < 2^22 and N < %lld", (long long)M,
                 (long long)N, (long long)K, (long long)max_n);
+  // the kernels number tiles (32 x 64 at the smallest) in 32 bits, those of
+  // the gradients M x K and N x K too
+  const int64_t cols = tg::ceil_div(K, 64) > 0 ? tg::ceil_div(K, 64) : 1;
+  if (tg::ceil_div(M, 32) * tg::ceil_div(N, 64) >= kMaxDim || tg::ceil_div(M, 32) * cols >= kMaxDim ||
+      tg::ceil_div(N, 32) * cols >= kMaxDim)
+    return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: M=%lld N=%lld K=%lld, too many tiles for one call",
+                (long long)M, (long long)N, (long long)K);
   return TILE_GEMM_OK;
 }
 
@@ -230,3 +237,57 @@ tile_gemm_status_t check_xent_backward(const void* A, const void* B, const void*
 }
 
 }  // namespace
+
+extern "C" {
+
+tile_gemm_status_t tile_gemm_check_glu_backward(const void* A, const void* B, const void* dC, const void* dA,
+                                                const void* dB, int64_t M, int64_t N, int64_t K,
+                                                const tile_gemm_strides_t* strides,
+                                                const tile_gemm_strides_t* grad_strides, const float* bias,
+                                                const float* dbias, tile_gemm_gate_t gate,
+                                                const void* workspace, int64_t workspace_bytes) {
+  tg::GluGradPlan p;
+  return check_glu_backward(A, B, dC, dA, dB, M, N, K, strides, grad_strides, bias, dbias, (int)gate, workspace,
+                            workspace_bytes, kDefaultCus, &p);
+}
+
+tile_gemm_status_t tile_gemm_check_xent(const void* A, const void* B, const void* target, const float* loss,
+                                        const float* lse, int64_t M, int64_t N, int64_t K,
+                                        const tile_gemm_strides_t* strides, const tile_gemm_xent_t* options,
+                                        const void* workspace, int64_t workspace_bytes) {
+  tg::XentPlan p;
+  return check_xent(A, B, target, loss, lse, M, N, K, strides, options, workspace, workspace_bytes, kDefaultCus,
+                    &p);
+}
+
+tile_gemm_status_t tile_gemm_check_xent_backward(const void* A, const void* B, const void* target,
+                                                 const float* lse, const float* dloss, const void* dA,
+                                                 const void* dB, int64_t M, int64_t N, int64_t K,
+                                                 const tile_gemm_strides_t* strides,
+                                                 const tile_gemm_strides_t* grad_strides,
+                                                 const tile_gemm_xent_t* options, const void* workspace,
+                                                 int64_t workspace_bytes) {
+  tg::XentGradPlan p;
+  return check_xent_backward(A, B, target, lse, dloss, dA, dB, M, N, K, strides, grad_strides, options, workspace,
+                             workspace_bytes, kDefaultCus, &p);
+}
+
+tile_gemm_status_t tile_gemm_plan_train(int64_t M, int64_t N, int64_t K, tile_gemm_train_product_t product,
+                                        int cu_count, tile_gemm_plan_t* out) {
+  g_detail[0] = '\0';
+  if (!out) return fail(TILE_GEMM_ERR_NULL_ARG, "out: NULL");
+  if (M < 1 || N < 1 || K < 1 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+    return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: M, N and K must be in [1, 2^31)");
+  if (product < TILE_GEMM_TRAIN_LOGITS || product > TILE_GEMM_TRAIN_GRADIENT)
+    return fail(TILE_GEMM_ERR_BAD_SHAPE, "product: unknown value %d", (int)product);
+  if (tg::ceil_div(M, 32) * tg::ceil_div(N, 64) >= kMaxDim)
+    return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: too many tiles");
+  if (cu_count <= 0) return fail(TILE_GEMM_ERR_DEVICE, "cu_count: %d", cu_count);
+  const tg::TrainProduct q = product == TILE_GEMM_TRAIN_GRADIENT
+                                 ? tg::plan_product(M, N, K, tg::kMaxSplits, cu_count)
+                                 : tg::plan_forward(M, N, K, cu_count, product == TILE_GEMM_TRAIN_GATED).z;
+  fill_plan(tg::train_plan(q), out);
+  return TILE_GEMM_OK;
+}
+
+}  // extern "C"

@@ -3,6 +3,7 @@
 // dependency, pure functions of the shape and the compute-unit count.
 #pragma once
 
+#include <initializer_list>
 #include "plan.hpp"
 
 namespace tg {
@@ -183,6 +184,15 @@ constexpr int kMaxSplits = 64;
 // M x N (0: the product writes its bf16 result itself).
 inline int64_t slot_bytes(int64_t M, int64_t N) { return M * ceil_div(N, 4) * 16; }
 
+// A product of two sizes, at most kManyBytes (more than any memory holds, and
+// a sum of eight of them still fits): the sizes of a shape that no workspace
+// can serve stay comparable.
+constexpr int64_t kManyBytes = (int64_t)1 << 59;
+inline int64_t bytes_of(int64_t n, int64_t each) {
+  const __int128 b = (__int128)n * each;
+  return b < kManyBytes ? (int64_t)b : kManyBytes;
+}
+
 // Bytes of one workspace region, and the running offset past it: regions
 // start at multiples of 256 bytes.
 inline int64_t region(int64_t& at, int64_t bytes) {
@@ -285,17 +295,17 @@ inline GluGradPlan plan_glu_grad(int64_t M, int64_t N, int64_t K, bool want_dx, 
   p.ldz = ceil_div(N, 8) * 8;
   p.ldzt = ceil_div(M, 16) * 16;
   int64_t at = 0;
-  if (want_dx) p.off_z = region(at, M * p.ldz * 2);
-  if (want_dw) p.off_zt = region(at, N * p.ldzt * 2);
+  if (want_dx) p.off_z = region(at, bytes_of(M, p.ldz * 2));
+  if (want_dw) p.off_zt = region(at, bytes_of(N, p.ldzt * 2));
   int64_t part = 0;
-  if (want_dx && p.dx.splits > 1) part = p.dx.splits * slot_bytes(M, K);
+  if (want_dx && p.dx.splits > 1) part = bytes_of(p.dx.splits, slot_bytes(M, K));
   if (want_dw && p.dw.splits > 1) {
-    const int64_t b = p.dw.splits * slot_bytes(N, K);
+    const int64_t b = bytes_of(p.dw.splits, slot_bytes(N, K));
     if (b > part) part = b;  // the two products run one after the other
   }
   p.off_part = region(at, part);
   p.bias_rows = (int64_t)p.z.map.tiles_m * f.row_groups;
-  p.off_bias = region(at, want_bias ? p.bias_rows * N * 4 : 0);
+  p.off_bias = region(at, want_bias ? bytes_of(p.bias_rows, N * 4) : 0);
   p.bytes = at;
   return p;
 }
@@ -315,8 +325,8 @@ inline XentPlan plan_xent(int64_t M, int64_t N, int64_t K, bool smooth, int cu) 
   p.l = plan_forward(M, N, K, cu);
   p.segs = ceil_div(N, p.l.seg_cols);
   int64_t at = 0;
-  p.off_part = region(at, p.segs * M * 8);
-  p.off_sum = region(at, smooth ? p.segs * M * 4 : 0);
+  p.off_part = region(at, bytes_of(p.segs, M * 8));
+  p.off_sum = region(at, smooth ? bytes_of(p.segs, M * 4) : 0);
   p.off_hit = region(at, M * 4);
   p.bytes = at;
   return p;
@@ -362,23 +372,24 @@ inline XentGradPlan plan_xent_grad(int64_t M, int64_t N, int64_t K, int64_t ldw,
   p.piece = piece;
   p.n_pieces = ceil_div(N, piece);
   p.ldz = ceil_div(piece, 8) * 8;
+  // every piece but the last has the same plan
+  const int64_t last = N - (p.n_pieces - 1) * piece;
   int64_t at = 0;
   p.off_rows = region(at, M * 16);
   p.off_scale = region(at, 4);
   if (want_dx) {
-    p.off_z = region(at, M * p.ldz * 2);
-    for (int64_t v = 0; v < N; v += piece)
-      p.slots += plan_xent_dx(M, K, N - v < piece ? N - v : piece, cu).splits;
+    p.off_z = region(at, bytes_of(M, p.ldz * 2));
+    p.slots = plan_xent_dx(M, K, last, cu).splits;
+    if (p.n_pieces > 1) p.slots += (p.n_pieces - 1) * plan_xent_dx(M, K, piece, cu).splits;
     if (p.slots == 1) p.slots = 0;
-    p.off_dx = region(at, p.slots * slot_bytes(M, K));
+    p.off_dx = region(at, bytes_of(p.slots, slot_bytes(M, K)));
   }
   if (want_dw) {
-    p.off_zt = region(at, piece * p.ldzt * 2);
+    p.off_zt = region(at, bytes_of(piece, p.ldzt * 2));
     int64_t part = 0;
-    for (int64_t v = 0; v < N; v += piece) {
-      const int64_t cols = N - v < piece ? N - v : piece;
+    for (const int64_t cols : {piece, last}) {
       const TrainProduct q = plan_xent_dw(M, K, cols, cu);
-      const int64_t b = q.splits > 1 ? q.splits * slot_bytes(cols, K) : 0;
+      const int64_t b = q.splits > 1 ? bytes_of(q.splits, slot_bytes(cols, K)) : 0;
       if (b > part) part = b;
     }
     p.off_dw = region(at, part);

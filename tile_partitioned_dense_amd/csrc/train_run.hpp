@@ -303,17 +303,6 @@ tile_gemm_status_t tile_gemm_run_glu_backward(tile_gemm_t h, const void* A, cons
                           workspace, workspace_bytes, stream);
 }
 
-tile_gemm_status_t tile_gemm_check_glu_backward(const void* A, const void* B, const void* dC, const void* dA,
-                                                const void* dB, int64_t M, int64_t N, int64_t K,
-                                                const tile_gemm_strides_t* strides,
-                                                const tile_gemm_strides_t* grad_strides, const float* bias,
-                                                const float* dbias, tile_gemm_gate_t gate,
-                                                const void* workspace, int64_t workspace_bytes) {
-  tg::GluGradPlan p;
-  return check_glu_backward(A, B, dC, dA, dB, M, N, K, strides, grad_strides, bias, dbias, (int)gate, workspace,
-                            workspace_bytes, kDefaultCus, &p);
-}
-
 tile_gemm_status_t tile_gemm_glu_backward_workspace(tile_gemm_t h, int64_t M, int64_t N, int64_t K,
                                                     int64_t* bytes) {
   if (!bytes) return fail(TILE_GEMM_ERR_NULL_ARG, "bytes: NULL");
@@ -322,36 +311,11 @@ tile_gemm_status_t tile_gemm_glu_backward_workspace(tile_gemm_t h, int64_t M, in
   return TILE_GEMM_OK;
 }
 
-tile_gemm_status_t tile_gemm_plan_train(int64_t M, int64_t N, int64_t K, tile_gemm_train_product_t product,
-                                        int cu_count, tile_gemm_plan_t* out) {
-  g_detail[0] = '\0';
-  if (!out) return fail(TILE_GEMM_ERR_NULL_ARG, "out: NULL");
-  if (M < 1 || N < 1 || K < 1 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
-    return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: M, N and K must be in [1, 2^31)");
-  if (product < TILE_GEMM_TRAIN_LOGITS || product > TILE_GEMM_TRAIN_GRADIENT)
-    return fail(TILE_GEMM_ERR_BAD_SHAPE, "product: unknown value %d", (int)product);
-  if (cu_count <= 0) return fail(TILE_GEMM_ERR_DEVICE, "cu_count: %d", cu_count);
-  const tg::TrainProduct q = product == TILE_GEMM_TRAIN_GRADIENT
-                                 ? tg::plan_product(M, N, K, tg::kMaxSplits, cu_count)
-                                 : tg::plan_forward(M, N, K, cu_count, product == TILE_GEMM_TRAIN_GATED).z;
-  fill_plan(tg::train_plan(q), out);
-  return TILE_GEMM_OK;
-}
-
 tile_gemm_status_t tile_gemm_run_xent(tile_gemm_t h, const void* A, const void* B, const void* target,
                                       float* loss, float* lse, int64_t M, int64_t N, int64_t K,
                                       const tile_gemm_strides_t* strides, const tile_gemm_xent_t* options,
                                       void* workspace, int64_t workspace_bytes, void* stream) {
   return run_xent(h, A, B, target, loss, lse, M, N, K, strides, options, workspace, workspace_bytes, stream);
-}
-
-tile_gemm_status_t tile_gemm_check_xent(const void* A, const void* B, const void* target, const float* loss,
-                                        const float* lse, int64_t M, int64_t N, int64_t K,
-                                        const tile_gemm_strides_t* strides, const tile_gemm_xent_t* options,
-                                        const void* workspace, int64_t workspace_bytes) {
-  tg::XentPlan p;
-  return check_xent(A, B, target, loss, lse, M, N, K, strides, options, workspace, workspace_bytes, kDefaultCus,
-                    &p);
 }
 
 tile_gemm_status_t tile_gemm_xent_workspace(tile_gemm_t h, int64_t M, int64_t N, int64_t K,
@@ -371,18 +335,6 @@ tile_gemm_status_t tile_gemm_run_xent_backward(tile_gemm_t h, const void* A, con
                                                int64_t workspace_bytes, void* stream) {
   return run_xent_backward(h, A, B, target, lse, dloss, dA, dB, M, N, K, strides, grad_strides, options,
                            workspace, workspace_bytes, stream);
-}
-
-tile_gemm_status_t tile_gemm_check_xent_backward(const void* A, const void* B, const void* target,
-                                                 const float* lse, const float* dloss, const void* dA,
-                                                 const void* dB, int64_t M, int64_t N, int64_t K,
-                                                 const tile_gemm_strides_t* strides,
-                                                 const tile_gemm_strides_t* grad_strides,
-                                                 const tile_gemm_xent_t* options, const void* workspace,
-                                                 int64_t workspace_bytes) {
-  tg::XentGradPlan p;
-  return check_xent_backward(A, B, target, lse, dloss, dA, dB, M, N, K, strides, grad_strides, options, workspace,
-                             workspace_bytes, kDefaultCus, &p);
 }
 
 tile_gemm_status_t tile_gemm_xent_backward_workspace(tile_gemm_t h, int64_t M, int64_t N, int64_t K,
