@@ -67,6 +67,7 @@ void plans() {
             ++g_calls;
             require(g.piece >= 1 && g.piece <= N && g.n_pieces == tg::ceil_div(N, g.piece), "pieces", M, N, K);
             require(g.piece * ld * 2 < ((int64_t)1 << 32), "a piece of W fits 32-bit offsets", M, N, K);
+            require(256 * g.ldz * 2 < ((int64_t)1 << 31), "256 rows of G fit 32-bit offsets", M, N, K);
             require(g.off_rows == 0 && g.off_scale >= M * 16 && g.off_z >= g.off_scale + 4 &&
                         g.off_dx >= g.off_z + tg::bytes_of(M, g.ldz * 2) &&
                         g.off_zt >= g.off_dx + tg::bytes_of(g.slots, tg::slot_bytes(M, K)) &&

@@ -84,7 +84,7 @@ tile_gemm_status_t check_train_shape(int64_t M, int64_t N, int64_t K, int64_t ma
                 (long long)N, (long long)K, (long long)max_n);
   // the kernels number tiles (32 x 64 at the smallest) in 32 bits, those of
   // the gradients M x K and N x K too
-  const int64_t cols = tg::ceil_div(K, 64) > 0 ? tg::ceil_div(K, 64) : 1;
+  const int64_t cols = tg::ceil_div(K, 64);
   if (tg::ceil_div(M, 32) * tg::ceil_div(N, 64) >= kMaxDim || tg::ceil_div(M, 32) * cols >= kMaxDim ||
       tg::ceil_div(N, 32) * cols >= kMaxDim)
     return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: M=%lld N=%lld K=%lld, too many tiles for one call",

@@ -344,6 +344,7 @@ struct XentGradPlan {
 // within 1 GiB. Fewer, larger pieces need fewer partial results of dx and
 // leave fewer ragged rounds of tiles.
 constexpr int64_t kXentPieceBytes = (int64_t)1 << 30;
+constexpr int64_t kXentPieceMax = ((int64_t)1 << 22) - 256;
 
 inline TrainProduct plan_xent_dx(int64_t M, int64_t K, int64_t cols, int cu) {
   return plan_product(M, K, cols, kMaxSplits, cu);
@@ -357,8 +358,10 @@ inline XentGradPlan plan_xent_grad(int64_t M, int64_t N, int64_t K, int64_t ldw,
   XentGradPlan p{};
   if (M <= 0 || N <= 0) return p;
   p.ldzt = ceil_div(M, 16) * 16;
-  // the dx product reads a piece of W through 32-bit offsets
-  const int64_t rows = ((int64_t)1 << 31) / (2 * ldw);
+  // the dx product reads a piece of W, and 256 rows of its G, through 32-bit
+  // offsets
+  int64_t rows = ((int64_t)1 << 31) / (2 * ldw);
+  if (rows > kXentPieceMax) rows = kXentPieceMax;
   if (piece <= 0) {
     piece = kXentPieceBytes / (4 * p.ldzt) / 256 * 256;
     if (piece < 256) piece = 256;
