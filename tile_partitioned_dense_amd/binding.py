@@ -438,9 +438,9 @@ def tile_gemm_run_mx(h, A, Bt, C, a_scale, b_scale, bias=None, act=Act.NONE, str
 # form of a check only to word its error.
 
 def _matrix(name, t, rows, cols):
-    """Checks a 2-D bf16 tensor (rows, cols None: any)."""
+    """Checks a 2-D bf16 tensor (rows, cols None: any); its shape."""
     import torch
-    if not _is_tensor(t):
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
@@ -448,11 +448,13 @@ def _matrix(name, t, rows, cols):
     if len(s) != 2 or (rows is not None and s[0] != rows) or (cols is not None and s[1] != cols):
         raise ValueError(f"{name} must have shape ({'any' if rows is None else rows}, "
                          f"{'any' if cols is None else cols}), got {tuple(s)}")
+    return s
 
 
 def _vector(name, t, n, dtypes):
     """Checks a contiguous vector of n values."""
-    if not _is_tensor(t):
+    import torch
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
@@ -465,7 +467,9 @@ def _vector(name, t, n, dtypes):
 def _current_device(names, tensors):
     """The current device, on which every tensor has to be."""
     import torch
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    # (the first tensor on a GPU means that there is one; asking torch whether
+    # there is costs as much as a launch's share of the call)
+    cur = torch._C._cuda_getDevice() if tensors[0].is_cuda else None
     for t in tensors:
         if t is not None and t.get_device() != cur:
             _check_devices(zip(names, tensors))
@@ -486,7 +490,8 @@ def _col_major_strides(b):
 
 def _row_major_strides(t):
     """(row, column) strides of a row-major matrix; see _col_major_strides."""
-    return t.stride(0), (1 if t.shape[1] <= 1 else t.stride(1))
+    row, col = t.stride()
+    return row, (1 if col != 1 and t.shape[1] <= 1 else col)
 
 
 def _launch_stream(stream, device):
@@ -504,11 +509,11 @@ def _launch_stream(stream, device):
     return raw, stream
 
 
-def _own_workspace(nbytes, device, other):
-    """A workspace for one call; torch keeps its memory until the stream has
-    passed the call."""
+def _own_workspace(nbytes, near, device, other):
+    """A workspace for one call beside the tensor `near`; torch keeps its
+    memory until the stream has passed the call."""
     import torch
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=f"cuda:{device}")
+    ws = near.new_empty(nbytes or 1, dtype=torch.uint8)
     if other is not None:
         ws.record_stream(other)
         # the block may have been freed on the current stream while work
@@ -535,10 +540,8 @@ def tile_gemm_run_glu(h, A, B, C, gate=Gate.SILU, bias=None, stream=None, check:
     """Enqueue the gated block C := act(A.B_gate + b_gate) * (A.B_up + b_up)
     (torch tensors; B is K x N with the N/2 gate columns first, either layout;
     C is M x N/2, float32 or bfloat16)."""
-    _matrix("A", A, None, None)
-    M, K = A.shape
-    _matrix("B", B, K, None)
-    N = B.shape[1]
+    M, K = _matrix("A", A, None, None)
+    N = _matrix("B", B, K, None)[1]
     if not _is_tensor(C) or C.dim() != 2 or N % 2 or tuple(C.shape) != (M, N // 2):
         raise ValueError(f"C must be a tensor of shape {(M, N // 2)} for B{tuple(B.shape)}")
     dt = _c_dtype(C)
@@ -570,10 +573,8 @@ def tile_gemm_run_glu_backward(h, A, B, dC, dA=None, dB=None, gate=Gate.SILU, bi
     any of the three may be left out. Without `workspace` one is allocated for
     the call."""
     import torch
-    _matrix("A", A, None, None)
-    M, K = A.shape
-    _matrix("B", B, K, None)
-    N = B.shape[1]
+    M, K = _matrix("A", A, None, None)
+    N = _matrix("B", B, K, None)[1]
     _matrix("dC", dC, M, N // 2)
     s = Strides(*_row_major_strides(A), *_col_major_strides(B), 0, 0)
     g = Strides(0, 1, 1, 0, *_row_major_strides(dC))
@@ -597,7 +598,7 @@ def tile_gemm_run_glu_backward(h, A, B, dC, dA=None, dB=None, gate=Gate.SILU, bi
     raw, other = _launch_stream(stream, dev)
     if workspace is None:
         nbytes = tile_gemm_glu_backward_workspace(h, M, N, K)
-        workspace = _own_workspace(nbytes, dev, other)
+        workspace = _own_workspace(nbytes, A, dev, other)
     else:
         nbytes = _workspace_bytes(workspace)
     st = load_library().tile_gemm_run_glu_backward(
@@ -608,13 +609,12 @@ def tile_gemm_run_glu_backward(h, A, B, dC, dA=None, dB=None, gate=Gate.SILU, bi
 
 def _xent_operands(A, B, target, ignore_index, label_smoothing, z_loss, piece):
     import torch
-    _matrix("A", A, None, None)
-    M, K = A.shape
-    _matrix("B", B, K, None)
+    M, K = _matrix("A", A, None, None)
+    N = _matrix("B", B, K, None)[1]
     _vector("target", target, M, (torch.int64, torch.int32))
     s = Strides(*_row_major_strides(A), *_col_major_strides(B), 0, 0)
     o = XentOptions(ignore_index, label_smoothing, z_loss, piece, target.dtype is torch.int64)
-    return M, B.shape[1], K, s, o
+    return M, N, K, s, o
 
 
 def tile_gemm_xent_workspace(h, M, N, K, label_smoothing=0.0) -> int:
@@ -641,13 +641,16 @@ def tile_gemm_run_xent(h, A, B, target, loss=None, lse=None, ignore_index=-100, 
         p_lse = lse.data_ptr()
     dev = _current_device(("A", "B", "target", "loss", "lse", "workspace"),
                           (A, B, target, loss, lse, workspace))
+    lib = load_library()
     raw, other = _launch_stream(stream, dev)
     if workspace is None:
-        nbytes = tile_gemm_xent_workspace(h, M, N, K, label_smoothing)
-        workspace = _own_workspace(nbytes, dev, other)
+        n = ctypes.c_int64()
+        _raise_if(lib.tile_gemm_xent_workspace(h, M, N, K, ctypes.byref(o), ctypes.byref(n)))
+        nbytes = n.value
+        workspace = _own_workspace(nbytes, A, dev, other)
     else:
         nbytes = _workspace_bytes(workspace)
-    st = load_library().tile_gemm_run_xent(h, A.data_ptr(), B.data_ptr(), target.data_ptr(), p_loss, p_lse,
+    st = lib.tile_gemm_run_xent(h, A.data_ptr(), B.data_ptr(), target.data_ptr(), p_loss, p_lse,
                                            M, N, K, ctypes.byref(s), ctypes.byref(o),
                                            workspace.data_ptr(), nbytes, raw)
     return _result(st, check)
@@ -686,13 +689,17 @@ def tile_gemm_run_xent_backward(h, A, B, target, lse, dloss, dA=None, dB=None, i
         p_dB = dB.data_ptr()
     dev = _current_device(("A", "B", "target", "lse", "dloss", "dA", "dB", "workspace"),
                           (A, B, target, lse, dloss, dA, dB, workspace))
+    lib = load_library()
     raw, other = _launch_stream(stream, dev)
     if workspace is None:
-        nbytes = tile_gemm_xent_backward_workspace(h, M, N, K, s.b_n, piece)
-        workspace = _own_workspace(nbytes, dev, other)
+        n = ctypes.c_int64()
+        _raise_if(lib.tile_gemm_xent_backward_workspace(h, M, N, K, ctypes.byref(s), ctypes.byref(o),
+                                                        ctypes.byref(n)))
+        nbytes = n.value
+        workspace = _own_workspace(nbytes, A, dev, other)
     else:
         nbytes = _workspace_bytes(workspace)
-    st = load_library().tile_gemm_run_xent_backward(
+    st = lib.tile_gemm_run_xent_backward(
         h, A.data_ptr(), B.data_ptr(), target.data_ptr(), lse.data_ptr(), dloss.data_ptr(), p_dA, p_dB, M,
         N, K, ctypes.byref(s), ctypes.byref(g), ctypes.byref(o), workspace.data_ptr(), nbytes, raw)
     return _result(st, check)

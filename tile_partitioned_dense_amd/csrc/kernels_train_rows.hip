@@ -8,10 +8,6 @@ namespace tg {
 
 namespace {
 
-__device__ __forceinline__ int64_t target_of(const void* target, int is64, int64_t row) {
-  return is64 ? static_cast<const int64_t*>(target)[row] : (int64_t) static_cast<const int32_t*>(target)[row];
-}
-
 // (m, s) of two disjoint sets of columns: s counts e^(l - m).
 __device__ __forceinline__ void join(float& m, float& s, float m1, float s1) {
   const float hi = fmaxf(m, m1);
@@ -92,20 +88,11 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(RowsArgs p) {
   if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = c;
   __syncthreads();
   c = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  if (!(c > 0.0f && c < INFINITY)) c = 1.0f;
+  c = xent_scale(c);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale = c;
   const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (row >= p.M) return;
-  const int64_t t = target_of(p.target, p.target64, row);
-  const float lse = p.lse[row];
-  XentRow r{lse * kLog2e, 0.0f, 0.0f, -1};
-  if (t != p.ignore) {
-    const bool known = t >= 0 && t < p.N;
-    r.b = known ? p.dloss[row] / c : NAN;
-    r.a = r.b * fmaf(2.0f * p.z_loss, lse, 1.0f);
-    r.target = known ? (int32_t)t : -1;
-  }
-  p.rows[row] = r;
+  p.rows[row] = xent_row(target_of(p.target, p.target64, row), p.ignore, p.N, p.lse[row], p.dloss[row], c, p.z_loss);
 }
 
 __global__ __launch_bounds__(256) void add_parts_kernel(AddArgs p) {
@@ -151,6 +138,17 @@ __global__ __launch_bounds__(256) void zero_kernel(uint16_t* p, int64_t rows, in
     p[i / cols * pitch + i % cols] = 0;
 }
 
+// Workgroups of the outer product, and their share of the rows: about eight
+// per compute unit (their waves fill its SIMDs), but at least 64 rows each, so
+// that the x fragments are read for several blocks.
+unsigned outer_groups(OuterArgs& a, int cu_count) {
+  a.col_groups = (int32_t)ceil_div(a.K, kOuterCols);
+  int64_t rows = ceil_div((int64_t)a.V * a.col_groups, 8 * cu_count);
+  rows = ceil_div(rows < 64 ? 64 : rows, 16) * 16;
+  a.rows_per_group = (int32_t)rows;
+  return (unsigned)(a.col_groups * ceil_div(a.V, rows));
+}
+
 unsigned blocks_for(int64_t items) {
   const int64_t b = ceil_div(items, 256);
   return (unsigned)(b < 1 ? 1 : b > 4096 ? 4096 : b);
@@ -184,17 +182,27 @@ hipError_t launch_add_rows(const float* part, int64_t rows, int64_t cols, float*
 }
 
 hipError_t launch_outer(OuterArgs a, int cu_count, hipStream_t stream) {
-  a.col_groups = (int32_t)ceil_div(a.K, kOuterCols);
-  // about eight workgroups per compute unit (their waves fill its SIMDs), but
-  // at least 64 rows each, so that the x fragments are read for several blocks
-  int64_t rows = ceil_div((int64_t)a.V * a.col_groups, 8 * cu_count);
-  rows = ceil_div(rows < 64 ? 64 : rows, 16) * 16;
-  a.rows_per_group = (int32_t)rows;
-  const dim3 grid((unsigned)(a.col_groups * ceil_div(a.V, rows)));
+  const dim3 grid(outer_groups(a, cu_count));
   const void* fn = a.T <= 32   ? reinterpret_cast<const void*>(&outer_kernel<1>)
                    : a.T <= 64 ? reinterpret_cast<const void*>(&outer_kernel<2>)
                                : reinterpret_cast<const void*>(&outer_kernel<4>);
   return launch_raw(fn, grid, dim3(256), a, stream);
+}
+
+hipError_t launch_pair(const TrainArgs& product, int64_t grid, bool bf16, const OuterArgs& outer, int cu_count,
+                       hipStream_t stream) {
+  constexpr TrainTile t = kTrainTiles[kSmallTile];
+  static_assert(t.wm * t.wn * 64 == 256, "the threads of both kernels");
+  PairArgs a{};
+  static_cast<TrainArgs&>(a) = product;
+  a.outer = outer;
+  a.n_first = (int32_t)grid;
+  const unsigned groups = outer_groups(a.outer, cu_count);
+  const void* fn =
+      bf16 ? reinterpret_cast<const void*>(&tile16_gemm_kernel<t.bm, t.bn, t.wm, t.wn, 4, false, true, false, kEpiPair>)
+           : reinterpret_cast<const void*>(
+                 &tile16_gemm_kernel<t.bm, t.bn, t.wm, t.wn, 4, false, false, false, kEpiPair>);
+  return launch_raw(fn, dim3((unsigned)grid + groups), dim3(256), a, stream);
 }
 
 hipError_t launch_zero(void* p, int64_t rows, int64_t bytes, int64_t pitch, hipStream_t stream) {

@@ -34,14 +34,23 @@ struct OuterArgs {
   int32_t rows_per_group;  // rows of a workgroup, a multiple of 16
 };
 
+// A gradient's product in the first `n_first` workgroups of a launch, and the
+// weight gradient of the same G in the others. Neither needs the other, and at
+// few tokens each is mostly latency: side by side they take the longer's time.
+struct PairArgs : TrainArgs {
+  OuterArgs outer;
+  int32_t n_first;
+};
+
+// Workgroup `group` of the product, with 4 * 16 * kOuterPitch bytes of LDS.
+constexpr int kOuterPitch = 64 * 2 + 16;
 template <int STEPS>
-__global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
-  constexpr int kPitch = 64 * 2 + 16;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[4 * 16 * kPitch];
+__device__ __forceinline__ void outer_group(const OuterArgs& p, int group, const void* smem) {
+  constexpr int kPitch = kOuterPitch;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t strip = (uint32_t)(uintptr_t)smem + (uint32_t)(wave * 16 * kPitch);
   const int l16 = lane & 15, lg = lane >> 4;
-  const int cg = blockIdx.x % p.col_groups, rg = blockIdx.x / p.col_groups;
+  const int cg = group % p.col_groups, rg = group / p.col_groups;
   const int col0 = cg * kOuterCols + wave * 64;
   if (col0 >= p.K) return;
   const float scale = p.scale ? *p.scale : 1.0f;
@@ -118,6 +127,12 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) g[b][s] = gn[b][s];
   }
+}
+
+template <int STEPS>
+__global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[4 * 16 * kOuterPitch];
+  outer_group<STEPS>(p, blockIdx.x, smem);
 }
 
 }  // namespace tg

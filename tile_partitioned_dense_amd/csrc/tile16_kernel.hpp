@@ -39,7 +39,7 @@
 // within the 256 registers a wave has at two waves per SIMD.
 #pragma once
 
-#include "train_epilogue.hpp"
+#include "outer_kernel.hpp"
 
 namespace tg {
 
@@ -156,17 +156,32 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
   __shared__ __attribute__((aligned(1024))) uint4 smem[kStages * STAGE / 16];
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
+  [[maybe_unused]] int n_groups = gridDim.x;
+  if constexpr (EPI == kEpiPair) {
+    n_groups = p.n_first;
+    if ((int)blockIdx.x >= n_groups) {
+      const int group = (int)blockIdx.x - n_groups;
+      if (p.outer.T <= 32)
+        outer_group<1>(p.outer, group, smem);
+      else if (p.outer.T <= 64)
+        outer_group<2>(p.outer, group, smem);
+      else
+        outer_group<4>(p.outer, group, smem);
+      return;
+    }
+  }
+
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave - (wave / WN) * WN;
 
   const int n_tiles = p.map.tiles_m * p.map.tiles_n;
   int n_work = n_tiles;
-  if constexpr (EPI == kEpiPartial) n_work *= p.splits;  // every tile once for each part of K
-  for (int wg_it = blockIdx.x; wg_it < n_work; wg_it += gridDim.x) {
+  if constexpr (epi_partial(EPI)) n_work *= p.splits;  // every tile once for each part of K
+  for (int wg_it = blockIdx.x; wg_it < n_work; wg_it += n_groups) {
     int wg = wg_it;
     [[maybe_unused]] int part = 0;
-    if constexpr (EPI == kEpiPartial) {
+    if constexpr (epi_partial(EPI)) {
       part = wg_it / n_tiles;
       wg = wg_it - part * n_tiles;
     }
@@ -195,7 +210,7 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
     // this part of K (kEpiPartial: a whole number of slabs but for the last part)
     int K = p.K;
     const uint16_t *pA = p.A, *pB = p.B;
-    if constexpr (EPI == kEpiPartial) {
+    if constexpr (epi_partial(EPI)) {
       const int k_lo = part * p.k_per;
       pA += k_lo;
       pB += BCOL ? (int64_t)k_lo : (int64_t)k_lo * ldb;
@@ -615,7 +630,7 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
     constexpr int CH = WTN * ESZ / 16;  // 16-byte chunks per staged row
     constexpr int EPC = 16 / ESZ;       // elements per chunk
     __syncthreads();  // every wave is done reading the ring
-    if constexpr (EPI != kEpiNone && EPI != kEpiPartial) {
+    if constexpr (EPI != kEpiNone && !epi_partial(EPI)) {
       // strip of 16 rows, private to the wave: bf16 values, or fp32 values of
       // half as many columns
       constexpr int TP = FN * 32 + 16;
@@ -677,7 +692,7 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
     // own slice of C
     float scale = 1.0f;
     char* c_out = static_cast<char*>(p.C);
-    if constexpr (EPI == kEpiPartial) {
+    if constexpr (epi_partial(EPI)) {
       if (OUT_BF16 && p.scale) scale = *p.scale;
       c_out += (int64_t)part * p.part_stride * ESZ;
     }
@@ -689,7 +704,7 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
       for (int j = 0; j < FN; ++j) {
         const uint32_t a = stg + (uint32_t)(l16 * OPITCH + (16 * j + 4 * lg) * ESZ);
         floatx4 v = acc[i][j];
-        if constexpr (EPI == kEpiPartial && OUT_BF16) v *= scale;
+        if constexpr (epi_partial(EPI) && OUT_BF16) v *= scale;
         if constexpr (OUT_BF16) {
           const u32x2v w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
           *(__attribute__((address_space(3))) u32x2v*)(uintptr_t)a = w;

@@ -19,6 +19,8 @@
 //   kEpiPartial   a gradient's product with K cut into `splits` parts: fp32
 //                 partial results of each part, or (one part) the bf16 result
 //                 times a device scalar.
+//   kEpiPair      kEpiPartial in the first workgroups of a launch, the weight
+//                 gradient over few tokens (outer_kernel.hpp) in the others.
 //
 // G and dz feed two products each: dx contracts their columns, dW their rows.
 // Both want the contracted axis contiguous, so they are written twice, as
@@ -41,7 +43,9 @@
 
 namespace tg {
 
-constexpr int kEpiNone = 0, kEpiStats = 1, kEpiXentGrad = 2, kEpiGluGrad = 3, kEpiPartial = 4, kEpiGlu = 5;
+constexpr int kEpiNone = 0, kEpiStats = 1, kEpiXentGrad = 2, kEpiGluGrad = 3, kEpiPartial = 4, kEpiGlu = 5,
+              kEpiPair = 6;
+constexpr bool epi_partial(int epi) { return epi == kEpiPartial || epi == kEpiPair; }
 
 // A gated store can have its gate compiled in, EPI = kind + 16 (gate + 1): the
 // one-wave-per-SIMD kernel's 256 accumulators stay where the MFMAs left them
@@ -67,7 +71,12 @@ struct TrainArgs : TileArgs {
   float* part_sum;  // [segment][M]: sum of the logits, or NULL
   float* hit;       // [M]: the target's logit (rows without one are not written)
   // kEpiXentGrad
-  const XentRow* rows;
+  const XentRow* rows;   // NULL (at most 64 rows, stream kernel): formed from the fields below
+  const float* lse;
+  const float* dloss;
+  int64_t ignore, vocab;
+  float z_loss;
+  float* row_scale;      // where the largest |dloss| goes
   int32_t first;  // vocabulary column of this piece's column 0
   float smooth;   // u = b * smooth (label smoothing over the vocabulary size)
   float keep;     // the target's share: b * keep is subtracted there
@@ -87,8 +96,9 @@ struct TrainArgs : TileArgs {
   const float* scale;   // bf16 result: one fp32 value, or NULL
 };
 
+struct PairArgs;  // outer_kernel.hpp
 template <int EPI>
-using EpiArgs = std::conditional_t<EPI == kEpiNone, TileArgs, TrainArgs>;
+using EpiArgs = std::conditional_t<EPI == kEpiNone, TileArgs, std::conditional_t<EPI == kEpiPair, PairArgs, TrainArgs>>;
 
 constexpr float kLog2e = 1.44269504088896341f;
 
@@ -109,6 +119,26 @@ __device__ __forceinline__ float join_lanes(float v, Op op) {
     return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
   }
 }
+
+__device__ __forceinline__ int64_t target_of(const void* target, int is64, int64_t row) {
+  return is64 ? static_cast<const int64_t*>(target)[row] : (int64_t) static_cast<const int32_t*>(target)[row];
+}
+
+// Constants of the loss gradient of one row: target t, log-sum-exp, dloss / c
+// (see xent_rows_kernel).
+__device__ __forceinline__ XentRow xent_row(int64_t t, int64_t ignore, int64_t vocab, float lse, float dloss,
+                                            float c, float z_loss) {
+  XentRow r{lse * kLog2e, 0.0f, 0.0f, -1};
+  if (t != ignore) {
+    const bool known = t >= 0 && t < vocab;
+    r.b = known ? dloss / c : NAN;
+    r.a = r.b * fmaf(2.0f * z_loss, lse, 1.0f);
+    r.target = known ? (int32_t)t : -1;
+  }
+  return r;
+}
+// The common factor of the loss gradients from their largest absolute value.
+__device__ __forceinline__ float xent_scale(float c) { return c > 0.0f && c < INFINITY ? c : 1.0f; }
 
 // Column of row `row`'s target, relative to `first`; a value no column has
 // where the row or its target is outside.
@@ -610,6 +640,20 @@ __device__ __forceinline__ void train_store_32(floatx16 (&acc)[FM], uint32_t str
   static_assert(EPI == kEpiStats || EPI == kEpiXentGrad, "logits only; kEpiGlu has its own");
   const int lrow = lane & 31, lgrp = lane >> 5;
   if (col0 >= p.N) return;
+  // At most 64 rows and few tiles: each wave finds the largest |dloss| and its
+  // rows' constants itself, a lane a row, which spares a launch
+  // (24 rows of 1024 against 8191 columns: 3.5 of 47 us with its issue).
+  [[maybe_unused]] float scale = 1.0f;
+  if constexpr (EPI == kEpiXentGrad) {
+    if (!p.rows) {
+      float c = 0.0f;
+      if (lane < p.M && target_of(p.target, p.target64, lane) != p.ignore) c = fabsf(p.dloss[lane]);
+#pragma unroll
+      for (int h = 32; h > 0; h /= 2) c = fmaxf(c, lane_xor(c, h));
+      scale = xent_scale(c);
+      if (lane == 0 && row0 == 0 && col0 == 0) *p.row_scale = scale;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int row = row0 + 32 * i + lrow;
@@ -621,7 +665,10 @@ __device__ __forceinline__ void train_store_32(floatx16 (&acc)[FM], uint32_t str
       stats_row<4, false>(v, 8, lgrp, col0, row, target_col(p, row, col0), seg, p);
     } else {
       XentRow r{0.0f, 0.0f, 0.0f, -1};
-      if (row < p.M) r = p.rows[row];
+      if (row < p.M)
+        r = p.rows ? p.rows[row]
+                   : xent_row(target_of(p.target, p.target64, row), p.ignore, p.vocab, p.lse[row], p.dloss[row],
+                              scale, p.z_loss);
       r.target -= p.first + col0;
       float g[16];
       xent_grad(g, [&](int k) { return acc[i][k]; },

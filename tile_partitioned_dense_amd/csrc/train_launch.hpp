@@ -56,6 +56,11 @@ hipError_t launch_add_parts(const AddArgs& a, hipStream_t stream);
 // The weight gradient over at most kOuterMaxT tokens (outer_kernel.hpp).
 hipError_t launch_outer(OuterArgs a, int cu_count, hipStream_t stream);
 
+// A gradient's product on the small tile (plan_product's kSmallTile; bf16: its
+// result rather than the partial ones) and that weight gradient in one launch.
+hipError_t launch_pair(const TrainArgs& product, int64_t grid, bool bf16, const OuterArgs& outer, int cu_count,
+                       hipStream_t stream);
+
 // out[c] = sum over rows of part[r][c], fp32.
 hipError_t launch_add_rows(const float* part, int64_t rows, int64_t cols, float* out, hipStream_t stream);
 

@@ -26,6 +26,17 @@ hipError_t launch_product(const tg::TrainProduct& q, int store, tg::TrainArgs& a
   return dispatch_train_from<0>(tg::train_kernel(store, q.tile, a.gate, bcol, bf16), a, q.grid, st);
 }
 
+// A gradient's product over a row-major right operand, `with` a few-token
+// weight gradient in the same launch.
+hipError_t launch_gradient(const tg::TrainProduct& q, tg::TrainArgs& a, bool bf16, const tg::OuterArgs* with,
+                           int cu, hipStream_t st) {
+  if (!with) return launch_product(q, bf16 ? tg::kStoreBf16 : tg::kStoreParts, a, st, false, bf16);
+  a.map = q.map;
+  a.splits = q.splits;
+  a.k_per = (int32_t)q.k_per;
+  return tg::launch_pair(a, q.grid, bf16, *with, cu, st);
+}
+
 tile_gemm_status_t hip_status(hipError_t e) {
   if (e == hipSuccess) return TILE_GEMM_OK;
   return fail(TILE_GEMM_ERR_HIP, "launch: %s", hipGetErrorString(e));
@@ -44,12 +55,24 @@ void log_product(tile_gemm_handle* h, const char* kind, int64_t M, int64_t N, in
   if (h->log) log_plan(h, kind, M, N, K, 1, 1, 0, tg::train_plan(q));
 }
 
+// Whether the few-token weight gradient (rows x cols over `tokens`) rides along
+// with the launch of the other gradient's product q. On the small tile both
+// are mostly latency (40 tokens, 2736 x 1024: 29.8 to 24.1 us for the whole
+// backward pass; 100 tokens, 32000 x 4096: 347 to 317). Few workgroups of the
+// pair fit a compute unit, though: up to 64 tokens, where the weight gradient
+// alone would run at the rate of its writes, the pair loses from 64 MiB on
+// (24 tokens: 32000 x 1024 80 to 78 us, 8 tokens: 10000 x 4096 63 to 66).
+bool pairs(const tg::TrainProduct& q, int64_t tokens, int64_t rows, int64_t cols) {
+  return q.tile == tg::kSmallTile && tokens <= tg::kOuterMaxT &&
+         (tokens > 64 || rows * cols * 2 <= ((int64_t)64 << 20));
+}
+
 // One gradient: out (bf16) = scale * (left [rows x len]) . (right [len x cols],
 // row-major), by parts of the contraction when the plan says so.
 tile_gemm_status_t run_gradient(const tg::TrainProduct& q, const uint16_t* left, int64_t ldl,
                                 const uint16_t* right, int64_t ldr, int64_t rows, int64_t cols, int64_t len,
                                 uint16_t* out, int64_t ldo, const float* scale, float* part,
-                                hipStream_t st) {
+                                hipStream_t st, const tg::OuterArgs* with = nullptr, int cu = 0) {
   tg::TrainArgs a{};
   a.A = left;
   a.B = right;
@@ -62,12 +85,12 @@ tile_gemm_status_t run_gradient(const tg::TrainProduct& q, const uint16_t* left,
     a.C = out;
     a.ldc = ldo;
     a.scale = scale;
-    return hip_status(launch_product(q, tg::kStoreBf16, a, st, false));
+    return hip_status(launch_gradient(q, a, true, with, cu, st));
   }
   a.C = part;
   a.ldc = tg::ceil_div(cols, 4) * 4;
   a.part_stride = rows * a.ldc;
-  TG_LAUNCH(launch_product(q, tg::kStoreParts, a, st, false, false));
+  TG_LAUNCH(launch_gradient(q, a, false, with, cu, st));
   return hip_status(tg::launch_add_parts(tg::AddArgs{part, a.part_stride, q.splits, (int32_t)rows, (int32_t)cols,
                                                      a.ldc, scale, out, ldo},
                                          st));
@@ -160,10 +183,13 @@ tile_gemm_status_t run_glu_backward(tile_gemm_t h, const void* A, const void* B,
   log_product(h, "run_glu_backward", M, N, K, p.z);
   TG_LAUNCH(launch_product(p.z, tg::kStoreGluGrad, a, st));
   if (dbias) TG_LAUNCH(tg::launch_add_rows(a.dbias_part, p.bias_rows, N, dbias, st));
+  const tg::OuterArgs outer{zt, p.ldzt, a.A, a.lda, static_cast<uint16_t*>(dB), g->b_n, nullptr, (int32_t)M,
+                            (int32_t)N, (int32_t)K, 0, 0};
+  const bool pair = dA && dB && pairs(p.dx, M, N, K);
   if (dA)
-    TG_TRY(run_gradient(p.dx, z, p.ldz, a.B, a.ldb, M, K, N, static_cast<uint16_t*>(dA), g->a_m, nullptr, part,
-                        st));
-  if (dB)
+    TG_TRY(run_gradient(p.dx, z, p.ldz, a.B, a.ldb, M, K, N, static_cast<uint16_t*>(dA), g->a_m, nullptr, part, st,
+                        pair ? &outer : nullptr, h->cu_count));
+  if (dB && !pair)
     TG_TRY(run_weight_gradient(p.dw, zt, p.ldzt, a.A, a.lda, N, K, M, static_cast<uint16_t*>(dB), g->b_n, nullptr,
                                part, h->cu_count, st));
   return TILE_GEMM_OK;
@@ -217,8 +243,18 @@ tile_gemm_status_t run_xent_backward(tile_gemm_t h, const void* A, const void* B
   float* scale = reinterpret_cast<float*>(ws + p.off_scale);
   float* dx_part = reinterpret_cast<float*>(ws + p.off_dx);
   const int target64 = o->target_type == TILE_GEMM_INDEX_I64;
-  TG_LAUNCH(tg::launch_xent_rows(
-      tg::RowsArgs{target, target64, o->ignore_index, (int32_t)M, N, lse, dloss, o->z_loss, rows, scale}, st));
+  // The stream kernel's waves can form the row constants of up to 64 rows
+  // themselves. Each tile then costs about 0.7 us more and the launch of
+  // xent_rows_kernel 3 to 5 us: worth it up to two tiles a workgroup (24 rows,
+  // 32000 x 4096 231 to 225 us; 50 rows, 131072 x 512, eight tiles, 160 to 163).
+  auto streams = [&](int64_t cols) {
+    const tg::TrainProduct z = tg::plan_forward(M, cols, K, cu).z;
+    return z.tile >= tg::kNumTrainTiles && (int64_t)z.map.tiles_m * z.map.tiles_n <= 2 * cu;
+  };
+  const bool few = M <= 64 && streams(p.piece) && streams(N - (p.n_pieces - 1) * p.piece);
+  if (!few)
+    TG_LAUNCH(tg::launch_xent_rows(
+        tg::RowsArgs{target, target64, o->ignore_index, (int32_t)M, N, lse, dloss, o->z_loss, rows, scale}, st));
   const int64_t part_ld = tg::ceil_div(K, 4) * 4;
   int slot = 0;
   for (int64_t v = 0; v < N; v += p.piece) {
@@ -232,7 +268,18 @@ tile_gemm_status_t run_xent_backward(tile_gemm_t h, const void* A, const void* B
     a.K = (int32_t)K;
     a.lda = s->a_m;
     a.ldb = s->b_n;
-    a.rows = rows;
+    if (few) {
+      a.target = target;
+      a.target64 = target64;
+      a.lse = lse;
+      a.dloss = dloss;
+      a.ignore = o->ignore_index;
+      a.vocab = N;
+      a.z_loss = o->z_loss;
+      a.row_scale = scale;
+    } else {
+      a.rows = rows;
+    }
     a.first = (int32_t)v;
     a.smooth = o->label_smoothing / (float)N;
     a.keep = 1.0f - o->label_smoothing;
@@ -243,11 +290,15 @@ tile_gemm_status_t run_xent_backward(tile_gemm_t h, const void* A, const void* B
     const tg::ForwardPlan l = tg::plan_forward(M, cols, K, cu);
     log_product(h, "run_xent_backward", M, cols, K, l.z);
     TG_LAUNCH(launch_product(l.z, tg::kStoreXentGrad, a, st));
+    const tg::TrainProduct q = tg::plan_xent_dx(M, K, cols, cu);
+    uint16_t* dw = dB ? static_cast<uint16_t*>(dB) + v * g->b_n : nullptr;
+    const tg::OuterArgs outer{a.Zt,  p.ldzt, a.A, a.lda, dw, g->b_n, scale, (int32_t)M, (int32_t)cols, (int32_t)K,
+                              0, 0};
+    const bool pair = dA && dB && pairs(q, M, cols, K);
     if (dA) {
-      const tg::TrainProduct q = tg::plan_xent_dx(M, K, cols, cu);
       if (p.slots == 0) {
         TG_TRY(run_gradient(q, a.Z, p.ldz, w, s->b_n, M, K, cols, static_cast<uint16_t*>(dA), g->a_m, scale,
-                            nullptr, st));
+                            nullptr, st, pair ? &outer : nullptr, cu));
       } else {
         tg::TrainArgs d{};
         d.A = a.Z;
@@ -260,13 +311,13 @@ tile_gemm_status_t run_xent_backward(tile_gemm_t h, const void* A, const void* B
         d.C = dx_part + slot * M * part_ld;
         d.ldc = part_ld;
         d.part_stride = M * part_ld;
-        TG_LAUNCH(launch_product(q, tg::kStoreParts, d, st, false, false));
+        TG_LAUNCH(launch_gradient(q, d, false, pair ? &outer : nullptr, cu, st));
         slot += q.splits;
       }
     }
-    if (dB)
+    if (dB && !pair)
       TG_TRY(run_weight_gradient(tg::plan_xent_dw(M, K, cols, cu), a.Zt, p.ldzt, a.A, a.lda, cols, K, M,
-                                 static_cast<uint16_t*>(dB) + v * g->b_n, g->b_n, scale,
+                                 dw, g->b_n, scale,
                                  reinterpret_cast<float*>(ws + p.off_dw), cu, st));
   }
   if (dA && p.slots)
