@@ -76,21 +76,27 @@ __global__ __launch_bounds__(256) void xent_finish_kernel(FinishArgs p) {
 // every row would put one and the same rounding error on all of them; so the
 // largest |dloss| is taken out (exactly 1 stays where they are equal) and
 // multiplied onto the finished gradients in fp32 instead. Every workgroup
-// finds that maximum itself: dloss is small and stays in the caches.
-__global__ __launch_bounds__(256) void xent_rows_kernel(RowsArgs p) {
-  __shared__ float sm[4];
+// finds that maximum itself: dloss is small and stays in the caches. (1024
+// threads: 3001 rows take three rounds of loads.)
+constexpr int kRowsThreads = 1024;
+__global__ __launch_bounds__(kRowsThreads) void xent_rows_kernel(RowsArgs p) {
+  __shared__ float sm[kRowsThreads / 64];
   float c = 0.0f;
-#pragma unroll 8
-  for (int i = threadIdx.x; i < p.M; i += 256)
-    if (target_of(p.target, p.target64, i) != p.ignore) c = fmaxf(c, fabsf(p.dloss[i]));
+#pragma unroll 4
+  for (int i = threadIdx.x; i < p.M; i += kRowsThreads) {
+    // both loads at once: one latency for each round of the threads, not two
+    const float d = fabsf(p.dloss[i]);
+    c = fmaxf(c, target_of(p.target, p.target64, i) != p.ignore ? d : 0.0f);
+  }
 #pragma unroll
   for (int h = 32; h > 0; h /= 2) c = fmaxf(c, lane_xor(c, h));
   if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = c;
   __syncthreads();
-  c = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+#pragma unroll
+  for (int w = 0; w < kRowsThreads / 64; ++w) c = fmaxf(c, sm[w]);
   c = xent_scale(c);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.scale = c;
-  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x;
   if (row >= p.M) return;
   p.rows[row] = xent_row(target_of(p.target, p.target64, row), p.ignore, p.N, p.lse[row], p.dloss[row], c, p.z_loss);
 }
@@ -166,8 +172,8 @@ hipError_t launch_xent_finish(const FinishArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_xent_rows(const RowsArgs& a, hipStream_t stream) {
-  return launch_raw(reinterpret_cast<const void*>(&xent_rows_kernel), dim3((unsigned)ceil_div(a.M, 256)),
-                    dim3(256), a, stream);
+  return launch_raw(reinterpret_cast<const void*>(&xent_rows_kernel), dim3((unsigned)ceil_div(a.M, kRowsThreads)),
+                    dim3(kRowsThreads), a, stream);
 }
 
 hipError_t launch_add_parts(const AddArgs& a, hipStream_t stream) {

@@ -162,11 +162,11 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
     if ((int)blockIdx.x >= n_groups) {
       const int group = (int)blockIdx.x - n_groups;
       if (p.outer.T <= 32)
-        outer_group<1>(p.outer, group, smem);
+        outer_group<1, true>(p.outer, group, smem);
       else if (p.outer.T <= 64)
-        outer_group<2>(p.outer, group, smem);
+        outer_group<2, true>(p.outer, group, smem);
       else
-        outer_group<4>(p.outer, group, smem);
+        outer_group<4, true>(p.outer, group, smem);
       return;
     }
   }

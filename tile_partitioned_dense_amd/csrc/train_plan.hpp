@@ -159,10 +159,13 @@ inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits
   for (int c = 0; c < kNumTrainTiles; ++c) {
     const TrainTile& t = kTrainTiles[c];
     if (gated && !t.gated) continue;
-    for (int s = 1; s <= max_splits; s *= 2) {
+    const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
+    for (int s = 1; s <= max_splits; ++s) {
       const int64_t k_per = ceil_div(ceil_div(K, s), 64) * 64;
-      // parts of at least 256 keep the load pipeline longer than its ramp
-      if (s > 1 && (k_per < 256 || ceil_div(K, k_per) != s)) continue;
+      // parts of at least 256 keep the load pipeline longer than its ramp; past
+      // four rounds of tiles more parts even nothing out
+      if (s > 1 && (k_per < 256 || tiles * (s - 1) >= 4 * (int64_t)cu * t.occ)) break;
+      if (ceil_div(K, k_per) != s && s > 1) continue;
       const double us = product_us(t, M, N, s == 1 ? K : k_per, s, max_splits > 1, cu);
       if (best_us == 0.0 || us < best_us * 0.999) {
         best_us = us;
