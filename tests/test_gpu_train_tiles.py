@@ -11,11 +11,11 @@ from test_gpu_glu import DEV, integers, put
 from train_helpers import GATES, Glu, Xent, close
 
 pytestmark = pytest.mark.gpu
-N_TILES = 8  # five tiles, three stream configurations
+N_TILES = 9  # five tiles, four stream configurations
 ROWS = (40, 70, 130, 200, 300, 520, 770, 1030, 1300, 1540, 2050)
-COLS = (64, 144, 272, 528, 784, 1040, 2064, 3600, 5008, 6160, 8208)
+COLS = (64, 144, 272, 528, 784, 1040, 2064, 3600, 4112, 5008, 6160, 8208)
 DEPTHS = {tg.TrainProduct.LOGITS: (72, 100), tg.TrainProduct.GATED: (72, 100),
-          tg.TrainProduct.GRADIENT: (80, 144, 528, 1040, 4112)}
+          tg.TrainProduct.GRADIENT: (80, 144, 528, 1040, 4112, 10256)}
 
 
 @pytest.fixture(scope="module")

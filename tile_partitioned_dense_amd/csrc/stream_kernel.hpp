@@ -73,7 +73,7 @@ __device__ __forceinline__ bf16x8 keep_first(const bf16x8& v, int valid) {
 template <int BM, int BN, int SB, int NST, int KS, bool OUT_BF16, bool DEBUG, int EPI = kEpiNone>
 __global__ __launch_bounds__(BN / 32 * KS * 64, 1) void stream_gemm_kernel(EpiArgs<EPI> p) {
   static_assert(BM == 16 || BM == 32 || BM == 64, "half a 32-row block, or one or two blocks");
-  static_assert(BN % 64 == 0 && BN <= 256, "whole waves, even gate and up halves");
+  static_assert((BN % 64 == 0 || (BN == 32 && EPI != kEpiNone)) && BN <= 256, "whole waves, even gate and up halves");
   static_assert(SB == 128 || SB == 256 || SB == 512, "stage rows of whole 128-byte lines");
   static_assert(KS == 1 || KS == 2 || KS == 4, "one, two or four waves per 32-column block");
   constexpr int NCB = BN / 32;               // 32-column blocks

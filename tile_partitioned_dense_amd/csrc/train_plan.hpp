@@ -35,16 +35,20 @@ constexpr TrainTile kTrainTiles[kNumTrainTiles] = {
 // few tiles, where a tile's K loop is latency and long stages shared by many
 // waves win. (Four waves on each 32-column block instead of the two of the
 // plain configurations: 64 x 64 tiles 7.2 to 4.2 us per 1000 of K, 32 x 64
-// tiles 3.9 to 3.3.)
+// tiles 3.9 to 3.3.) The 32 x 32 tiles are for one round of them: the loss of
+// 24 rows, 8191 x 1024 10.5 to 9.6 us, 8191 x 4096 19.7 to 17.6, the gated block
+// of 27 rows, 6000 x 3696 16.0 to 13.3; in two rounds (12000 x 1024, the loss)
+// they take 14.2 for the 10.9 of 32 x 64.
 struct TrainStream {
   int bm, bn, sb, stages, ks;
   double us_k, us_tile;
 };
-constexpr int kNumTrainStreams = 3;
+constexpr int kNumTrainStreams = 4;
 constexpr TrainStream kTrainStreams[kNumTrainStreams] = {
     {32, 64, 512, 3, 4, 3.3, 2.0},
     {64, 128, 256, 3, 2, 8.0, 2.5},
     {64, 64, 512, 2, 4, 4.2, 2.5},
+    {32, 32, 512, 3, 4, 2.4, 2.0},
 };
 
 // What a product is turned into (train_epilogue.hpp; a gradient's bf16 result
@@ -60,7 +64,7 @@ struct TrainKernel {
   int store, tile, gate;
   bool bcol, bf16;
 };
-constexpr int kNumTrainKernels = 109;
+constexpr int kNumTrainKernels = 114;
 struct TrainKernels {
   TrainKernel k[kNumTrainKernels] = {};
   int n = 0;
