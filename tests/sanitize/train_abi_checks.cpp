@@ -56,7 +56,9 @@ void plans() {
           if (check_train_shape(M, N, K, kMaxDim) != TILE_GEMM_OK || M == 0 || N == 0) continue;
           const tg::XentPlan x = tg::plan_xent(M, N, K, true, cu);
           ++g_calls;
-          check_product(x.l.z, M, N, K);
+          require(x.head >= 1 && x.head <= N && (x.head == N || x.head % 32 == 0), "loss: first launch", M, N, K);
+          check_product(x.l.z, M, x.head, K);
+          if (x.head < N) check_product(x.rest.z, M, N - x.head, K);
           require(x.off_part == 0 && x.off_sum >= tg::bytes_of(x.segs, M * 8) && x.off_hit >= x.off_sum + x.segs * M * 4 &&
                       x.bytes >= x.off_hit + M * 4,
                   "loss: workspace regions", M, N, K);

@@ -123,3 +123,31 @@ def test_weight_gradient_lengths(g, T):
         dw = put(w.bfloat16(), 8)
         g.glu_backward(put(x.bfloat16(), 8), put(w.bfloat16()).t(), put(dh.bfloat16()), dB=dw.t(), gate=tg.Gate.RELU)
         assert torch.equal(dw.cpu(), (dz.T @ x.double()).bfloat16())
+
+
+@pytest.mark.parametrize("T,K,V", [(660, 264, 22197), (320, 520, 33054), (830, 264, 33054)])
+def test_last_round_of_its_own(g, T, K, V):
+    """Sizes whose last round of tiles is nearly empty: the logits (first two)
+    and the weight gradient (last two) go in two launches, cut at a column. The
+    targets lie on both sides of every multiple of 1024 columns, and in the
+    last ones."""
+    gen = torch.Generator().manual_seed(70 + T)
+    x = torch.randn(T, K, generator=gen).bfloat16()
+    w = (torch.randn(V, K, generator=gen) * 2 * K ** -0.5).bfloat16()
+    t = torch.randint(0, V, (T,), generator=gen)
+    edges = torch.arange(1024, V, 1024)
+    edges = torch.cat([edges, edges - 1, torch.arange(V - 120, V)])
+    t[:len(edges)] = edges
+    t[-1] = -100
+    d = torch.rand(T, generator=gen) / T
+    opts = dict(label_smoothing=0.1, z_loss=1e-3)
+    ref = Xent(x, w, t, dloss=d, smoothing=0.1, z_loss=1e-3)
+    xd, wd, td = put(x), put(w), t.to(DEV)
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    g.xent(xd, wd.t(), td, loss, lse, **opts)
+    close(lse, ref.lse, ref.lse_err, False, "lse")
+    close(loss, ref.loss, ref.loss_err, False, "loss")
+    dx, dw = put(x), put(w)
+    g.xent_backward(xd, wd.t(), td, lse, d.to(DEV), dA=dx, dB=dw.t(), **opts)
+    close(dx, ref.dx, ref.dx_err, True, "dx")
+    close(dw, ref.dw, ref.dw_err, True, "dw")

@@ -77,7 +77,7 @@ struct TrainArgs : TileArgs {
   int64_t ignore, vocab;
   float z_loss;
   float* row_scale;      // where the largest |dloss| goes
-  int32_t first;  // vocabulary column of this piece's column 0
+  int32_t first;  // vocabulary column of this launch's column 0 (kEpiStats too)
   float smooth;   // u = b * smooth (label smoothing over the vocabulary size)
   float keep;     // the target's share: b * keep is subtracted there
   // kEpiXentGrad, kEpiGluGrad: the result as rows and transposed (either NULL)
@@ -140,13 +140,12 @@ __device__ __forceinline__ XentRow xent_row(int64_t t, int64_t ignore, int64_t v
 // The common factor of the loss gradients from their largest absolute value.
 __device__ __forceinline__ float xent_scale(float c) { return c > 0.0f && c < INFINITY ? c : 1.0f; }
 
-// Column of row `row`'s target, relative to `first`; a value no column has
+// Column of row `row`'s target, relative to column `first` of this launch; -1
 // where the row or its target is outside.
 __device__ __forceinline__ int target_col(const TrainArgs& p, int row, int first) {
   if (row >= p.M) return -1;
-  const int64_t t = p.target64 ? static_cast<const int64_t*>(p.target)[row]
-                               : (int64_t) static_cast<const int32_t*>(p.target)[row];
-  return (t < first || t >= p.N) ? -1 : (int)(t - first);
+  const uint64_t c = (uint64_t)target_of(p.target, p.target64, row) - (uint64_t)((int64_t)p.first + first);
+  return c < (uint64_t)(int64_t)(p.N - first) ? (int)c : -1;
 }
 
 // Maximum, sum of exponentials, (sum) and target of one row held as NJ groups

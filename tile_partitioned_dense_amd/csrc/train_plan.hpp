@@ -219,13 +219,15 @@ struct ForwardPlan {
   int seg_cols, row_groups;
 };
 
-inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu, bool gated = false) {
+inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu, bool gated = false,
+                                double* us_out = nullptr) {
   ForwardPlan f{};
   double us = 0.0;
   f.z = plan_product(M, N, K, 1, cu, gated, &us);
   const TrainTile& t = kTrainTiles[f.z.tile];
   f.seg_cols = t.bn / t.wn;
   f.row_groups = t.wm;
+  if (us_out) *us_out = us;
   if (K % 2 != 0) return f;
   const double bytes_us = (double)N * (double)K * 2.0 / 6.0e6;
   if (us < bytes_us) us = bytes_us;
@@ -241,6 +243,7 @@ inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu, bool ga
       us = s;
     }
   }
+  if (us_out) *us_out = us;
   if (best < 0) return f;
   const TrainStream& sc = kTrainStreams[best];
   f.z.tile = kNumTrainTiles + best;
@@ -250,6 +253,48 @@ inline ForwardPlan plan_forward(int64_t M, int64_t N, int64_t K, int cu, bool ga
   f.seg_cols = 32;
   f.row_groups = sc.bm / 32;
   return f;
+}
+
+// Outputs of several rounds of tiles, the last one nearly empty, are cut in
+// two launches: whole rounds of some tile, and what is left on a plan of its
+// own (smaller tiles, more of the compute units). The axis of length N is cut,
+// in steps of a tile's `step(t)`; `across(t)` tiles lie side by side over it;
+// `plan(n, &us)` plans n of it. Returns the first launch's share; N where one
+// launch is expected to be as fast. kLaunchUs: what the second launch costs.
+constexpr double kLaunchUs = 4.0;
+template <class Step, class Across, class Plan>
+int64_t head_of(int64_t N, int cu, Step step, Across across, Plan plan) {
+  double us = 0.0;
+  if (plan(N, &us).tile >= kNumTrainTiles) return N;
+  int64_t best = N;
+  us *= 0.98;
+  for (const TrainTile& t : kTrainTiles) {
+    const int64_t side = across(t), slots = (int64_t)cu * t.occ;
+    const int64_t rounds = side * ceil_div(N, (int64_t)step(t)) / slots;
+    const int64_t n = rounds * slots / side * step(t);
+    if (n <= 0 || n >= N) continue;
+    double head = 0.0, rest = 0.0;
+    plan(n, &head);
+    plan(N - n, &rest);
+    if (head + rest + kLaunchUs < us) {
+      us = head + rest + kLaunchUs;
+      best = n;
+    }
+  }
+  return best;
+}
+// Columns of the logits M x N in their first launch.
+inline int64_t head_logits(int64_t M, int64_t N, int64_t K, int cu) {
+  return head_of(N, cu, [](const TrainTile& t) { return t.bn; },
+                 [&](const TrainTile& t) { return ceil_div(M, t.bm); },
+                 [&](int64_t n, double* us) { return plan_forward(M, n, K, cu, false, us).z; });
+}
+// Rows of the weight gradient N x K over M tokens in its first launch (no
+// parts of the contraction in either).
+inline int64_t head_rows(int64_t N, int64_t K, int64_t M, int cu) {
+  return head_of(N, cu, [](const TrainTile& t) { return t.bm; },
+                 [&](const TrainTile& t) { return ceil_div(K, t.bn); },
+                 [&](int64_t n, double* us) { return plan_product(n, K, M, 1, cu, false, us); });
 }
 
 // A training product as a launch plan (log lines, introspection).
@@ -320,8 +365,9 @@ inline GluGradPlan plan_glu_grad(int64_t M, int64_t N, int64_t K, bool want_dx, 
 // ----------------------------------------------- cross entropy of a product
 
 struct XentPlan {
-  ForwardPlan l;
-  int64_t segs;
+  ForwardPlan l, rest;  // of the first `head` columns and of the others
+  int64_t head;
+  int64_t segs, rest_segs;
   int64_t off_part, off_sum, off_hit;
   int64_t bytes;
 };
@@ -329,8 +375,13 @@ struct XentPlan {
 inline XentPlan plan_xent(int64_t M, int64_t N, int64_t K, bool smooth, int cu) {
   XentPlan p{};
   if (M <= 0) return p;
-  p.l = plan_forward(M, N, K, cu);
-  p.segs = ceil_div(N, p.l.seg_cols);
+  p.head = head_logits(M, N, K, cu);
+  p.l = plan_forward(M, p.head, K, cu);
+  if (p.head < N) {
+    p.rest = plan_forward(M, N - p.head, K, cu);
+    p.rest_segs = ceil_div(N - p.head, p.rest.seg_cols);
+  }
+  p.segs = ceil_div(p.head, p.l.seg_cols) + p.rest_segs;
   int64_t at = 0;
   p.off_part = region(at, bytes_of(p.segs, M * 8));
   p.off_sum = region(at, smooth ? bytes_of(p.segs, M * 4) : 0);

@@ -139,7 +139,12 @@ tile_gemm_status_t run_weight_gradient(const tg::TrainProduct& q, const uint16_t
     return hip_status(tg::launch_outer(tg::OuterArgs{left, ldl, right, ldr, out, ldo, scale, (int32_t)len,
                                                      (int32_t)rows, (int32_t)cols, 0, 0},
                                        cu, st));
-  return run_gradient(q, left, ldl, right, ldr, rows, cols, len, out, ldo, scale, part, st);
+  const int64_t head = q.splits == 1 ? tg::head_rows(rows, cols, len, cu) : rows;
+  if (head == rows) return run_gradient(q, left, ldl, right, ldr, rows, cols, len, out, ldo, scale, part, st);
+  TG_TRY(run_gradient(tg::plan_product(head, cols, len, 1, cu), left, ldl, right, ldr, head, cols, len, out, ldo,
+                      scale, nullptr, st));
+  return run_gradient(tg::plan_product(rows - head, cols, len, 1, cu), left + head * ldl, ldl, right, ldr, rows - head,
+                      cols, len, out + head * ldo, ldo, scale, nullptr, st);
 }
 
 tile_gemm_status_t run_glu_backward(tile_gemm_t h, const void* A, const void* B, const void* dC, void* dA,
@@ -210,7 +215,6 @@ tile_gemm_status_t run_xent(tile_gemm_t h, const void* A, const void* B, const v
   a.A = static_cast<const uint16_t*>(A);
   a.B = static_cast<const uint16_t*>(B);
   a.M = (int32_t)M;
-  a.N = (int32_t)N;
   a.K = (int32_t)K;
   a.lda = s->a_m;
   a.ldb = s->b_n;
@@ -219,8 +223,19 @@ tile_gemm_status_t run_xent(tile_gemm_t h, const void* A, const void* B, const v
   a.part = reinterpret_cast<float2*>(ws + p.off_part);
   a.part_sum = smooth ? reinterpret_cast<float*>(ws + p.off_sum) : nullptr;
   a.hit = reinterpret_cast<float*>(ws + p.off_hit);
-  log_product(h, "run_xent", M, N, K, p.l.z);
+  a.N = (int32_t)p.head;
+  log_product(h, "run_xent", M, p.head, K, p.l.z);
   TG_LAUNCH(launch_product(p.l.z, tg::kStoreStats, a, st));
+  if (p.head < N) {
+    tg::TrainArgs b = a;
+    b.N = (int32_t)(N - p.head);
+    b.B += p.head * b.ldb;
+    b.first = (int32_t)p.head;
+    b.part += (p.segs - p.rest_segs) * M;
+    if (smooth) b.part_sum += (p.segs - p.rest_segs) * M;
+    log_product(h, "run_xent", M, N - p.head, K, p.rest.z);
+    TG_LAUNCH(launch_product(p.rest.z, tg::kStoreStats, b, st));
+  }
   tg::FinishArgs f{a.part,    a.part_sum, a.hit, target, a.target64, o->ignore_index, (int32_t)M,
                    (int32_t)p.segs, N, o->label_smoothing, o->z_loss, loss, lse};
   return hip_status(tg::launch_xent_finish(f, st));
@@ -287,9 +302,19 @@ tile_gemm_status_t run_xent_backward(tile_gemm_t h, const void* A, const void* B
     a.ldz = p.ldz;
     a.Zt = dB ? reinterpret_cast<uint16_t*>(ws + p.off_zt) : nullptr;
     a.ldzt = p.ldzt;
-    const tg::ForwardPlan l = tg::plan_forward(M, cols, K, cu);
-    log_product(h, "run_xent_backward", M, cols, K, l.z);
-    TG_LAUNCH(launch_product(l.z, tg::kStoreXentGrad, a, st));
+    const int64_t head = few ? cols : tg::head_logits(M, cols, K, cu);
+    for (int64_t c = 0; c < cols; c += head) {
+      tg::TrainArgs b = a;
+      b.N = (int32_t)(c ? cols - head : head);
+      b.B += c * b.ldb;
+      b.first += (int32_t)c;
+      if (b.Z) b.Z += c;
+      if (b.Zt) b.Zt += c * b.ldzt;
+      const tg::TrainProduct l = tg::plan_forward(M, b.N, K, cu).z;
+      log_product(h, "run_xent_backward", M, b.N, K, l);
+      TG_LAUNCH(launch_product(l, tg::kStoreXentGrad, b, st));
+      if (c) break;
+    }
     const tg::TrainProduct q = tg::plan_xent_dx(M, K, cols, cu);
     uint16_t* dw = dB ? static_cast<uint16_t*>(dB) + v * g->b_n : nullptr;
     const tg::OuterArgs outer{a.Zt,  p.ldzt, a.A, a.lda, dw, g->b_n, scale, (int32_t)M, (int32_t)cols, (int32_t)K,
