@@ -226,9 +226,12 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
         return r + (r >= BN / 2 ? gshift : 0);
     };
 
+    // the values of A's rows that may be read: past K only where they are zero
+    int Ka = K;
+    if constexpr (epi_partial(EPI)) Ka = p.a_chunks ? (K + 7) & ~7 : K;
     // ---- panels, their valid extents (to the operand's last element), steps
     const char* a_panel = reinterpret_cast<const char*>(pA + (int64_t)m0 * lda);
-    const int64_t a_bytes = K > 0 ? (((int64_t)(M - 1) * lda + K) - (int64_t)m0 * lda) * 2 : 0;
+    const int64_t a_bytes = K > 0 ? (((int64_t)(M - 1) * lda + Ka) - (int64_t)m0 * lda) * 2 : 0;
     const char* b_panel = reinterpret_cast<const char*>(BCOL ? pB + (int64_t)n0 * ldb : pB + n0);
     const int64_t b_bytes = K <= 0 ? 0
                             : BCOL ? (((int64_t)(N - 1) * ldb + K) - (int64_t)n0 * ldb) * 2
@@ -272,7 +275,7 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
     const int nk_full = (!BCOL && (N & 1)) ? (K - 1) / BK : K / BK;
 
     // (see tile64_kernel.hpp)
-    [[maybe_unused]] const bool dma_tail = EPI != kEpiNone && K % 8 == 0 && (BCOL || !(N & 1));
+    [[maybe_unused]] const bool dma_tail = EPI != kEpiNone && Ka % 8 == 0 && (BCOL || !(N & 1));
     auto issue_slab = [&](int s) {
       const int st = s % kStages;
       const uint32_t la = lds0 + st * STAGE;

@@ -78,11 +78,11 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
 
   const int n_tiles = p.map.tiles_m * p.map.tiles_n;
   int n_work = n_tiles;
-  if constexpr (EPI == kEpiPartial) n_work *= p.splits;  // every tile once for each part of K
+  if constexpr (epi_partial(EPI)) n_work *= p.splits;  // every tile once for each part of K
   for (int wg_it = blockIdx.x; wg_it < n_work; wg_it += gridDim.x) {
     int wg = wg_it;
     [[maybe_unused]] int part = 0;
-    if constexpr (EPI == kEpiPartial) {
+    if constexpr (epi_partial(EPI)) {
       part = wg_it / n_tiles;
       wg = wg_it - part * n_tiles;
     }
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
     // this part of K (kEpiPartial: a whole number of slabs but for the last part)
     int K = p.K;
     const uint16_t *pA = p.A, *pB = p.B;
-    if constexpr (EPI == kEpiPartial) {
+    if constexpr (epi_partial(EPI)) {
       const int k_lo = part * p.k_per;
       pA += k_lo;
       pB += BCOL ? (int64_t)k_lo : (int64_t)k_lo * ldb;
@@ -121,8 +121,11 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
         return r + (r >= BN / 2 ? gshift : 0);
     };
 
+    // the values of A's rows that may be read: past K only where they are zero
+    int Ka = K;
+    if constexpr (epi_partial(EPI)) Ka = p.a_chunks ? (K + 7) & ~7 : K;
     const char* a_panel = reinterpret_cast<const char*>(pA + (int64_t)m0 * lda);
-    const int64_t a_bytes = K > 0 ? (((int64_t)(M - 1) * lda + K) - (int64_t)m0 * lda) * 2 : 0;
+    const int64_t a_bytes = K > 0 ? (((int64_t)(M - 1) * lda + Ka) - (int64_t)m0 * lda) * 2 : 0;
     const char* b_panel = reinterpret_cast<const char*>(BCOL ? pB + (int64_t)n0 * ldb : pB + n0);
     const int64_t b_bytes = K <= 0 ? 0
                             : BCOL ? (((int64_t)(N - 1) * ldb + K) - (int64_t)n0 * ldb) * 2
@@ -169,7 +172,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
     // past K sent to an offset that no operand's resource covers (they arrive
     // as zeros); measured 9 us less per tile than through registers. Only for
     // the training products: the plain ones keep the path they were tuned on.
-    [[maybe_unused]] const bool dma_tail = EPI != kEpiNone && K % 8 == 0 && (BCOL || !(N & 1));
+    [[maybe_unused]] const bool dma_tail = EPI != kEpiNone && Ka % 8 == 0 && (BCOL || !(N & 1));
     // Whole slab s into stage s & 1 (DMA, or the register path past nk_full).
     auto issue_slab = [&](int s) {
       const int st = s & 1;
@@ -615,7 +618,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
     constexpr int CH = WTN * ESZ / 16;
     constexpr int EPC = 16 / ESZ;
     __syncthreads();
-    if constexpr (EPI != kEpiNone && EPI != kEpiPartial) {
+    if constexpr (EPI != kEpiNone && !epi_partial(EPI)) {
       // strip of 16 rows, private to the wave: bf16 values, or fp32 values of
       // half as many columns
       constexpr int TP = FN * 32 + 16;
@@ -679,7 +682,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
     // own slice of C
     float scale = 1.0f;
     char* c_out = static_cast<char*>(p.C);
-    if constexpr (EPI == kEpiPartial) {
+    if constexpr (epi_partial(EPI)) {
       if (OUT_BF16 && p.scale) scale = *p.scale;
       c_out += (int64_t)part * p.part_stride * ESZ;
     }
@@ -692,7 +695,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
       for (int j = 0; j < FN; ++j) {
         const uint32_t a = stg + (uint32_t)(l16 * OPITCH + (16 * j + 4 * lg) * ESZ);
         floatx4 v = acc[i][j];
-        if constexpr (EPI == kEpiPartial && OUT_BF16) v *= scale;
+        if constexpr (epi_partial(EPI) && OUT_BF16) v *= scale;
         if constexpr (OUT_BF16) {
           const u32x2v w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
           *(__attribute__((address_space(3))) u32x2v*)(uintptr_t)a = w;

@@ -92,6 +92,7 @@ struct TrainArgs : TileArgs {
   int32_t gate;
   // kEpiPartial
   int32_t splits, k_per;
+  int32_t a_chunks;     // A's rows are zero from K up to a whole chunk of 8 (and that long)
   int64_t part_stride;  // elements between the partial results
   const float* scale;   // bf16 result: one fp32 value, or NULL
 };

@@ -72,8 +72,10 @@ bool pairs(const tg::TrainProduct& q, int64_t tokens, int64_t rows, int64_t cols
 tile_gemm_status_t run_gradient(const tg::TrainProduct& q, const uint16_t* left, int64_t ldl,
                                 const uint16_t* right, int64_t ldr, int64_t rows, int64_t cols, int64_t len,
                                 uint16_t* out, int64_t ldo, const float* scale, float* part,
-                                hipStream_t st, const tg::OuterArgs* with = nullptr, int cu = 0) {
+                                hipStream_t st, const tg::OuterArgs* with = nullptr, int cu = 0,
+                                bool whole_chunks = false) {
   tg::TrainArgs a{};
+  a.a_chunks = whole_chunks;
   a.A = left;
   a.B = right;
   a.M = (int32_t)rows;
@@ -140,11 +142,13 @@ tile_gemm_status_t run_weight_gradient(const tg::TrainProduct& q, const uint16_t
                                                      (int32_t)rows, (int32_t)cols, 0, 0},
                                        cu, st));
   const int64_t head = q.splits == 1 ? tg::head_rows(rows, cols, len, cu) : rows;
-  if (head == rows) return run_gradient(q, left, ldl, right, ldr, rows, cols, len, out, ldo, scale, part, st);
+  // left's rows are stored in whole chunks of tokens, zero past the last
+  if (head == rows)
+    return run_gradient(q, left, ldl, right, ldr, rows, cols, len, out, ldo, scale, part, st, nullptr, cu, true);
   TG_TRY(run_gradient(tg::plan_product(head, cols, len, 1, cu), left, ldl, right, ldr, head, cols, len, out, ldo,
-                      scale, nullptr, st));
+                      scale, nullptr, st, nullptr, cu, true));
   return run_gradient(tg::plan_product(rows - head, cols, len, 1, cu), left + head * ldl, ldl, right, ldr, rows - head,
-                      cols, len, out + head * ldo, ldo, scale, nullptr, st);
+                      cols, len, out + head * ldo, ldo, scale, nullptr, st, nullptr, cu, true);
 }
 
 tile_gemm_status_t run_glu_backward(tile_gemm_t h, const void* A, const void* B, const void* dC, void* dA,
