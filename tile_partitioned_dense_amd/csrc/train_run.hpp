@@ -55,16 +55,24 @@ void log_product(tile_gemm_handle* h, const char* kind, int64_t M, int64_t N, in
   if (h->log) log_plan(h, kind, M, N, K, 1, 1, 0, tg::train_plan(q));
 }
 
-// Whether the few-token weight gradient (rows x cols over `tokens`) rides along
-// with the launch of the other gradient's product q. On the small tile both
-// are mostly latency (40 tokens, 2736 x 1024: 29.8 to 24.1 us for the whole
-// backward pass; 100 tokens, 32000 x 4096: 347 to 317). Few workgroups of the
-// pair fit a compute unit, though: up to 64 tokens, where the weight gradient
-// alone would run at the rate of its writes, the pair loses from 64 MiB on
+// Whether the weight gradient (rows x cols over `tokens`) takes the few-token
+// kernel. Up to 32 tokens it runs near the rate of its writes (the whole
+// backward pass of 1 token, 14000 x 8192, 144 us for the 164 with the tile
+// kernel). Past them its registers leave too few waves for that, and the tile
+// kernel is faster unless the result is small and the launch that the pair
+// saves counts: 64 tokens, 8000 x 512 42.9 and 45.0, 16000 x 1024 66.2 and
+// 64.6, 10000 x 4096 86.9 and 76.9; 100 tokens, 272 x 264 20.5 and 23.3, 8000 x
+// 1024 45.2 and 41.3; 128 tokens, 32000 x 1024 137 and 107.
+bool few_tokens(int64_t tokens, int64_t rows, int64_t cols) {
+  return tokens <= 32 || (tokens <= tg::kOuterMaxT && rows * cols * 2 <= ((int64_t)8 << 20));
+}
+// Whether it then rides along with the launch of the other gradient's product
+// q. On the small tile both are mostly latency (40 tokens, 2736 x 1024: 29.8 to
+// 24.1 us for the whole backward pass). Few workgroups of the pair fit a
+// compute unit, though, and from 64 MiB on the weight gradient alone is faster
 // (24 tokens: 32000 x 1024 80 to 78 us, 8 tokens: 10000 x 4096 63 to 66).
 bool pairs(const tg::TrainProduct& q, int64_t tokens, int64_t rows, int64_t cols) {
-  return q.tile == tg::kSmallTile && tokens <= tg::kOuterMaxT &&
-         (tokens > 64 || rows * cols * 2 <= ((int64_t)64 << 20));
+  return q.tile == tg::kSmallTile && few_tokens(tokens, rows, cols) && rows * cols * 2 <= ((int64_t)64 << 20);
 }
 
 // One gradient: out (bf16) = scale * (left [rows x len]) . (right [len x cols],
@@ -137,7 +145,7 @@ tile_gemm_status_t run_weight_gradient(const tg::TrainProduct& q, const uint16_t
                                        const uint16_t* right, int64_t ldr, int64_t rows, int64_t cols,
                                        int64_t len, uint16_t* out, int64_t ldo, const float* scale, float* part,
                                        int cu, hipStream_t st) {
-  if (len <= tg::kOuterMaxT)
+  if (few_tokens(len, rows, cols))
     return hip_status(tg::launch_outer(tg::OuterArgs{left, ldl, right, ldr, out, ldo, scale, (int32_t)len,
                                                      (int32_t)rows, (int32_t)cols, 0, 0},
                                        cu, st));
