@@ -6,7 +6,7 @@ import torch
 
 import tile_partitioned_dense_amd as tg
 from test_gpu_glu import DEV, put, strided
-from train_helpers import Glu, Xent, close
+from train_helpers import HALF, Glu, Xent, close
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +136,33 @@ def test_captured_and_replayed(g):
         torch.cuda.synchronize()
         for a, b in zip(held, want):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("T", [40, 200, 600])
+@pytest.mark.parametrize("V", [601, 1026])
+def test_columns_past_a_ragged_vocabulary(g, T, V):
+    """Logits of about -200 throughout: the zero logits of columns that are none
+    would have exponentials past all bounds, and rows past the last token
+    likewise; neither reaches a gradient.
+
+    The gradients are held to their bounds element by element only. close()'s
+    rule for the 2-norm takes a result for as large as its terms; here dx = G w
+    with w = -3 +- 0.1 and rows of G that sum to zero keeps 0.1 of its terms'
+    3, so G's rounding, at most HALF of a term, is up to 30 HALF of the result."""
+    K = 64
+    gen = torch.Generator().manual_seed(65)
+    x = (1.0 + 0.1 * torch.randn(T, K, generator=gen)).bfloat16()
+    w = (-3.0 + 0.1 * torch.randn(V, K, generator=gen)).bfloat16()
+    t = torch.randint(0, V, (T,), generator=gen)
+    d = torch.rand(T, generator=gen) / T
+    ref = Xent(x, w, t, dloss=d)
+    assert float(ref.lse.max()) < -150
+    xd, wd, td = put(x), put(w), t.to(DEV)
+    lse = torch.empty(T, device=DEV)
+    g.xent(xd, wd.t(), td, None, lse)
+    close(lse, ref.lse, ref.lse_err, False, "lse")
+    dx, dw = like(xd), like(wd)
+    g.xent_backward(xd, wd.t(), td, lse, d.to(DEV), dA=dx, dB=dw.t())
+    for got, want, err in ((dx, ref.dx, ref.dx_err), (dw, ref.dw, ref.dw_err)):
+        err = err + HALF * (want.abs() + err) + 2.0 ** -133
+        assert bool(((got.double().cpu() - want).abs() <= err).all())

@@ -226,9 +226,10 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
         return r + (r >= BN / 2 ? gshift : 0);
     };
 
-    // the values of A's rows that may be read: past K only where they are zero
+    // the values of A's rows that may be read: the gradients' left operands are
+    // stored in whole chunks of 8, zero past K (train_epilogue.hpp)
     int Ka = K;
-    if constexpr (epi_partial(EPI)) Ka = p.a_chunks ? (K + 7) & ~7 : K;
+    if constexpr (epi_partial(EPI)) Ka = (K + 7) & ~7;
     // ---- panels, their valid extents (to the operand's last element), steps
     const char* a_panel = reinterpret_cast<const char*>(pA + (int64_t)m0 * lda);
     const int64_t a_bytes = K > 0 ? (((int64_t)(M - 1) * lda + Ka) - (int64_t)m0 * lda) * 2 : 0;

@@ -121,9 +121,10 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
         return r + (r >= BN / 2 ? gshift : 0);
     };
 
-    // the values of A's rows that may be read: past K only where they are zero
+    // the values of A's rows that may be read: the gradients' left operands are
+    // stored in whole chunks of 8, zero past K (train_epilogue.hpp)
     int Ka = K;
-    if constexpr (epi_partial(EPI)) Ka = p.a_chunks ? (K + 7) & ~7 : K;
+    if constexpr (epi_partial(EPI)) Ka = (K + 7) & ~7;
     const char* a_panel = reinterpret_cast<const char*>(pA + (int64_t)m0 * lda);
     const int64_t a_bytes = K > 0 ? (((int64_t)(M - 1) * lda + Ka) - (int64_t)m0 * lda) * 2 : 0;
     const char* b_panel = reinterpret_cast<const char*>(BCOL ? pB + (int64_t)n0 * ldb : pB + n0);

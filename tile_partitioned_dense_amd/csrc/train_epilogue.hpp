@@ -92,7 +92,6 @@ struct TrainArgs : TileArgs {
   int32_t gate;
   // kEpiPartial
   int32_t splits, k_per;
-  int32_t a_chunks;     // A's rows are zero from K up to a whole chunk of 8 (and that long)
   int64_t part_stride;  // elements between the partial results
   const float* scale;   // bf16 result: one fp32 value, or NULL
 };
@@ -301,8 +300,8 @@ __device__ __forceinline__ uint32_t lds_load_u32(uint32_t addr) {
 // p.Zt. col_of(c) gives the output column of strip column c (a multiple of
 // 8's worth of columns stays together), or -1 where it is outside. Both
 // leading dimensions are padded (ldz to 8 columns, ldzt to 16 rows), so whole
-// chunks are written wherever their first value is inside; the padding is
-// never read. No waits are written between the strip's writes, its reads and
+// chunks are written wherever their first value is inside, with zeros past the
+// last column or row: the products that follow load whole chunks. No waits are written between the strip's writes, its reads and
 // the next writes: a wave's LDS operations run in order.
 template <int ROWS, int COLS, class ColOf>
 __device__ __forceinline__ void store_both(uint32_t strip, int lane, int grow0, const TrainArgs& p,
@@ -315,10 +314,17 @@ __device__ __forceinline__ void store_both(uint32_t strip, int lane, int grow0, 
       const int c = c0 + lane;
       if (ROWS * CH % 64 != 0 && c >= ROWS * CH) break;
       const int r = c / CH, ch = c - (c / CH) * CH;
-      const u32x4s v =
+      u32x4s v =
           *(const __attribute__((address_space(3))) u32x4s*)(uintptr_t)(strip + (uint32_t)(r * PITCH + ch * 16));
       const int col = col_of(ch * 8), row = grow0 + r;
-      if (row < p.M && col >= 0) *reinterpret_cast<u32x4s*>(p.Z + (int64_t)row * p.ldz + col) = v;
+      if (row < p.M && col >= 0) {
+        if (col + 8 > p.N) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            v[w] &= col + 2 * w + 2 <= p.N ? 0xffffffffu : col + 2 * w < p.N ? 0xffffu : 0u;
+        }
+        *reinterpret_cast<u32x4s*>(p.Z + (int64_t)row * p.ldz + col) = v;
+      }
     }
   }
   if (p.Zt) {

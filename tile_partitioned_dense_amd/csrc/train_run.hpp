@@ -76,14 +76,13 @@ bool pairs(const tg::TrainProduct& q, int64_t tokens, int64_t rows, int64_t cols
 }
 
 // One gradient: out (bf16) = scale * (left [rows x len]) . (right [len x cols],
-// row-major), by parts of the contraction when the plan says so.
+// row-major), by parts of the contraction when the plan says so. left is G or
+// dz as a store wrote it: its rows are zero past len up to a multiple of 8.
 tile_gemm_status_t run_gradient(const tg::TrainProduct& q, const uint16_t* left, int64_t ldl,
                                 const uint16_t* right, int64_t ldr, int64_t rows, int64_t cols, int64_t len,
                                 uint16_t* out, int64_t ldo, const float* scale, float* part,
-                                hipStream_t st, const tg::OuterArgs* with = nullptr, int cu = 0,
-                                bool whole_chunks = false) {
+                                hipStream_t st, const tg::OuterArgs* with = nullptr, int cu = 0) {
   tg::TrainArgs a{};
-  a.a_chunks = whole_chunks;
   a.A = left;
   a.B = right;
   a.M = (int32_t)rows;
@@ -150,13 +149,11 @@ tile_gemm_status_t run_weight_gradient(const tg::TrainProduct& q, const uint16_t
                                                      (int32_t)rows, (int32_t)cols, 0, 0},
                                        cu, st));
   const int64_t head = q.splits == 1 ? tg::head_rows(rows, cols, len, cu) : rows;
-  // left's rows are stored in whole chunks of tokens, zero past the last
-  if (head == rows)
-    return run_gradient(q, left, ldl, right, ldr, rows, cols, len, out, ldo, scale, part, st, nullptr, cu, true);
+  if (head == rows) return run_gradient(q, left, ldl, right, ldr, rows, cols, len, out, ldo, scale, part, st);
   TG_TRY(run_gradient(tg::plan_product(head, cols, len, 1, cu), left, ldl, right, ldr, head, cols, len, out, ldo,
-                      scale, nullptr, st, nullptr, cu, true));
+                      scale, nullptr, st));
   return run_gradient(tg::plan_product(rows - head, cols, len, 1, cu), left + head * ldl, ldl, right, ldr, rows - head,
-                      cols, len, out + head * ldo, ldo, scale, nullptr, st, nullptr, cu, true);
+                      cols, len, out + head * ldo, ldo, scale, nullptr, st);
 }
 
 tile_gemm_status_t run_glu_backward(tile_gemm_t h, const void* A, const void* B, const void* dC, void* dA,
