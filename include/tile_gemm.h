@@ -481,8 +481,11 @@ tile_gemm_status_t tile_gemm_plan(int64_t M, int64_t N, int64_t K, int b_col_maj
  * logits or gated pre-activations of an M x N output over K, or a gradient's
  * M x N result contracted over K. config counts the compiled training tiles
  * (256 rows x 256, 224, 192 or 160 columns, 128 x 128, then the stream
- * configurations of 32 x 64, 64 x 128 and 64 x 64); k_split is the number of
- * parts a gradient's contraction is cut into.
+ * configurations of 32 x 64, 64 x 128, 64 x 64 and 32 x 32); k_split is the
+ * number of parts a gradient's contraction is cut into. Where the last round of
+ * tiles would be nearly empty, the logits and the weight gradient go in two
+ * launches, each planned so; few tokens take kernels of their own for the
+ * weight gradient.
  */
 typedef enum {
   TILE_GEMM_TRAIN_LOGITS = 0,
