@@ -170,10 +170,20 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
     const int nk_full = (!BCOL && (N & 1)) ? (K - 1) / BK : K / BK;
 
     // A K tail of whole 16-byte chunks is loaded like any slab, with the chunks
-    // past K sent to an offset that no operand's resource covers (they arrive
-    // as zeros); measured 9 us less per tile than through registers. Only for
-    // the training products: the plain ones keep the path they were tuned on.
-    [[maybe_unused]] const bool dma_tail = EPI != kEpiNone && Ka % 8 == 0 && (BCOL || !(N & 1));
+    // past K sent to kDmaPast (they arrive as zeros); measured 9 us less per
+    // tile than through registers. Only for the training products: the plain
+    // ones keep the path they were tuned on. The resources end there at the
+    // latest, so what the tile reads of both operands must lie before it,
+    // counted from the panel (of a row-major B: from the tail's first row). All
+    // but operands within 256 bytes of 4 GiB do: x and gated weights span less
+    // than 4 GiB, the columns of a vocabulary are less than 2^23 bytes apart.
+    [[maybe_unused]] bool dma_tail = false;
+    if constexpr (EPI != kEpiNone) {
+      const int64_t a_reach = ((int64_t)(tg_min(BM, M - m0) - 1) * lda + Ka) * 2;
+      const int64_t b_reach = BCOL ? ((int64_t)tg_min(b_col(BN - 1), N - 1 - n0) * ldb + K) * 2
+                                   : b_bytes - (nk - 1) * b_step;
+      dma_tail = Ka % 8 == 0 && (BCOL || !(N & 1)) && a_reach <= kDmaPast && b_reach <= kDmaPast;
+    }
     // Whole slab s into stage s & 1 (DMA, or the register path past nk_full).
     auto issue_slab = [&](int s) {
       const int st = s & 1;
@@ -188,20 +198,19 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
         for (int t = 0; t < B_MAX; ++t)
           if (t < B_MIN || t < b_cnt) dma16(lb + 1024 * (wave + NW * t), rsB, voB[t], 0u);
       } else if (EPI != kEpiNone && dma_tail) {
-        constexpr int64_t kReach = (int64_t)1 << 31;  // no panel is this long
         const int64_t a_left = a_bytes - s * a_step, b_left = b_bytes - s * b_step;
-        const i32x4 rsA = make_rsrc(a_panel + s * a_step, a_left < kReach ? a_left : kReach);
-        const i32x4 rsB = make_rsrc(b_panel + s * b_step, b_left < kReach ? b_left : kReach);
+        const i32x4 rsA = make_rsrc(a_panel + s * a_step, a_left < kDmaPast ? a_left : kDmaPast);
+        const i32x4 rsB = make_rsrc(b_panel + s * b_step, b_left < kDmaPast ? b_left : kDmaPast);
         auto past = [&](int r) { return s * BK + 8 * ((lane & 7) ^ swz64(r)) >= K; };
 #pragma unroll
         for (int t = 0; t < A_PER; ++t)
-          dma16(la + 1024 * (wave + NW * t), rsA, past(8 * (wave + NW * t) + (lane >> 3)) ? 0x80000000u : voA[t], 0u);
+          dma16(la + 1024 * (wave + NW * t), rsA, past(8 * (wave + NW * t) + (lane >> 3)) ? kDmaPast : voA[t], 0u);
 #pragma unroll
         for (int t = 0; t < B_MAX; ++t)
           if (t < B_MIN || t < b_cnt) {
             bool out = false;  // a row-major B: rows past K are past its resource
             if constexpr (BCOL) out = past(8 * (wave + NW * t) + (lane >> 3));
-            dma16(lb + 1024 * (wave + NW * t), rsB, out ? 0x80000000u : voB[t], 0u);
+            dma16(lb + 1024 * (wave + NW * t), rsB, out ? kDmaPast : voB[t], 0u);
           }
       } else {
         const int k0 = s * BK;

@@ -99,6 +99,11 @@ __device__ __forceinline__ i32x4 make_rsrc(const void* base, int64_t bytes) {
   return r;
 }
 
+// Loads that are to arrive as zeros are sent to offset kDmaPast: past the end
+// of every resource of at most so many bytes, and whole chunks behind it are
+// still below 2^32.
+constexpr uint32_t kDmaPast = 0xffffff00u;
+
 // 16 bytes per lane from rsrc + voff + soff straight into LDS at lds + 16 *
 // lane (one contiguous KiB per wave). Tracked by vmcnt only. gfx9 LDS
 // instructions do not read M0, and nothing else in these kernels sets it.
