@@ -30,6 +30,11 @@ def far(t, pitch):
     return view
 
 
+def widest(rows, cols):
+    """The largest pitch that an operand of this many rows may have."""
+    return ((SPAN // 2 - cols - 8) // (rows - 1)) // 8 * 8
+
+
 def values(T, K, N, seed):
     gen = torch.Generator(device=DEV).manual_seed(seed)
     x = torch.randn(T, K, generator=gen, device=DEV).bfloat16()
@@ -106,6 +111,32 @@ def test_far_rows_of_a_row_major_weight(g, T, K, F, pitch):
         g.glu(x, far(wr, pitch), h[0], gate=gate)
         g.glu(x, wr, h[1], gate=gate)
         same(h[:1], h[1:])
+
+
+# The step of a contraction that ends inside it names rows past the last one,
+# whose 32-bit offsets wrap to the NaN between the first rows where rows lie as
+# far apart as they may: the contractions over tokens (a weight gradient) and
+# over a row-major weight's rows. (48 tokens span so near to 4 GiB that their
+# step goes through registers, 63 take 128-row tiles.)
+@pytest.mark.parametrize("T,K,V", [(36, 136, 40000), (48, 136, 40000), (63, 264, 40000)])
+def test_farthest_tokens(g, T, K, V):
+    gen, x, w = values(T, K, V, 6)
+    t = torch.randint(0, V, (T,), generator=gen, device=DEV)
+    d = torch.rand(T, generator=gen, device=DEV)
+    same(head(g, far(x, widest(T, K)), w, t, d), head(g, x, w, t, d))
+    gen, x, w = values(T, K, V, 7)
+    dh = torch.randn(T, V // 2, generator=gen, device=DEV).bfloat16()
+    same(block(g, far(x, widest(T, K)), w, dh, tg.Gate.SILU), block(g, x, w, dh, tg.Gate.SILU))
+
+
+@pytest.mark.parametrize("T,K,F", [(200, 24, 1000), (4096, 56, 2048), (4096, 40, 2048), (300, 8, 512)])
+def test_farthest_rows_of_a_row_major_weight(g, T, K, F):
+    _, x, w = values(T, K, 2 * F, 8)
+    wr = w.t().contiguous()
+    h = [torch.full((T, F), float("nan"), device=DEV) for _ in range(2)]
+    g.glu(x, far(wr, widest(K, 2 * F)), h[0], gate=tg.Gate.GELU)
+    g.glu(x, wr, h[1], gate=tg.Gate.GELU)
+    same(h[:1], h[1:])
 
 
 # Weights of a vocabulary with the widest rows allowed (8 MiB apart).

@@ -306,8 +306,11 @@ void tile16_gemm_kernel(EpiArgs<EPI> p) {
 #pragma unroll
         for (int t = 0; t < B_MAX; ++t)
           if (t < B_MIN || t < b_cnt) {
-            bool out = false;  // a row-major B: rows past K are past its resource
-            if constexpr (BCOL) out = past(16 * (wave + NW * t) + (lane >> 2));
+            bool out;  // a row-major B: whole rows past K (their offsets may wrap to live values)
+            if constexpr (BCOL)
+              out = past(16 * (wave + NW * t) + (lane >> 2));
+            else
+              out = s * BK + (64 * (wave + NW * t) + lane) / CPR >= K;
             dma16(lb + 1024 * (wave + NW * t), rsB, out ? kDmaPast : voB[t], 0u);
           }
       } else {

@@ -208,8 +208,11 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void tile64_gemm_kernel(EpiArgs<EP
 #pragma unroll
         for (int t = 0; t < B_MAX; ++t)
           if (t < B_MIN || t < b_cnt) {
-            bool out = false;  // a row-major B: rows past K are past its resource
-            if constexpr (BCOL) out = past(8 * (wave + NW * t) + (lane >> 3));
+            bool out;  // a row-major B: whole rows past K (their offsets may wrap to live values)
+            if constexpr (BCOL)
+              out = past(8 * (wave + NW * t) + (lane >> 3));
+            else
+              out = s * BK + (64 * (wave + NW * t) + lane) / CPR >= K;
             dma16(lb + 1024 * (wave + NW * t), rsB, out ? kDmaPast : voB[t], 0u);
           }
       } else {
