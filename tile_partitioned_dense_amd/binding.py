@@ -548,10 +548,9 @@ def tile_gemm_run_glu(h, A, B, C, gate=Gate.SILU, bias=None, stream=None, check:
     if bias is not None:
         _check_bias(bias, N)
     dev = _current_device(("A", "B", "C", "bias"), (A, B, C, bias if _is_tensor(bias) else None))
-    if M == 1:  # the stride of a single row is never used
-        s = Strides((K + 7) // 8 * 8, 1, *B.stride(), (N // 2 + 7) // 8 * 8, 1)
-    else:
-        s = Strides(*A.stride(), *B.stride(), *C.stride())
+    s = Strides(*_row_major_strides(A), *B.stride(), *C.stride())
+    if M == 1:  # the stride from a single row to the next is never used
+        s.a_m, s.c_m = (K + 7) // 8 * 8, (N // 2 + 7) // 8 * 8
     raw, _ = _launch_stream(stream, dev)
     st = load_library().tile_gemm_run_glu(h, A.data_ptr(), B.data_ptr(), C.data_ptr(), M, N, K,
                                           ctypes.byref(s), dt,
