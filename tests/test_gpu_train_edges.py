@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import tile_partitioned_dense_amd as tg
-from test_gpu_glu import DEV
+from test_gpu_glu import DEV, put
+from train_helpers import Xent, close
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +30,67 @@ def test_columns_apart_are_refused(g, rows):
         assert tg.tile_gemm_run_glu(g.handle, x, w.t(), bad_h, gate=gate, check=False) == tg.Status.ERR_BAD_STRIDE
     torch.cuda.synchronize()
     assert not bool(h.any()) and not bool(wide_h.any())
+
+
+def masked_head(T, K, V, masked, seed):
+    """x, w and targets of a head whose columns `masked` have logit -inf, by a
+    last value of 1 in x and of -inf in their weights (0 in the others'), and
+    the reference over the other columns, their numbers in `kept`."""
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, K, generator=gen).bfloat16()
+    w = (torch.randn(V, K, generator=gen) * 2 * K ** -0.5).bfloat16()
+    x[:, -1], w[:, -1] = 1.0, 0.0
+    w[masked, -1] = -float("inf")
+    kept = torch.ones(V, dtype=torch.bool)
+    kept[masked] = False
+    kept = kept.nonzero()[:, 0]
+    at = torch.randint(0, len(kept), (T,), generator=gen)
+    d = torch.rand(T, generator=gen)
+    return x, w, kept[at], d, kept, Xent(x, w[kept], at, dloss=d)
+
+
+# one to many tokens: 32-column segments, then those of 64 to 128 columns
+@pytest.mark.parametrize("T,K,V", [(1, 64, 33), (7, 72, 65), (40, 64, 1300), (300, 72, 4129), (1300, 72, 6161),
+                                   (2050, 72, 8209), (50, 65, 300), (700, 65, 900)])
+@pytest.mark.parametrize("which", ["last", "first segments", "last segments", "all but one"])
+def test_columns_of_minus_infinity(g, T, K, V, which):
+    """Logits of -inf count for nothing, alone in the last segment of a row as
+    well as over whole segments; the gradients of their weights are zero."""
+    wide = min(V - 1, 256)
+    masked = {"last": [V - 1], "first segments": list(range(wide)), "last segments": list(range(V - wide, V)),
+              "all but one": [v for v in range(V) if v != V // 2]}[which]
+    x, w, t, d, kept, ref = masked_head(T, K, V, masked, 3)
+    xd, wd, td = put(x), put(w), t.to(DEV)
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    g.xent(xd, wd.t(), td, loss, lse)
+    close(lse, ref.lse, ref.lse_err, False, "lse")
+    close(loss, ref.loss, ref.loss_err, False, "loss")
+    dx, dw = put(torch.zeros_like(x)), put(torch.zeros_like(w))
+    g.xent_backward(xd, wd.t(), td, lse, d.to(DEV), dA=dx, dB=dw.t())
+    # (the last value of dx is the sum over 0 * -inf)
+    close(dx[:, :-1], ref.dx[:, :-1], ref.dx_err[:, :-1], True, "dx")
+    close(dw[kept.to(DEV)], ref.dw, ref.dw_err, True, "dw")
+    assert not bool(dw[masked].any())
+
+
+@pytest.mark.parametrize("T,V", [(5, 300), (200, 2000)])
+def test_rows_of_infinities(g, T, V):
+    """A row whose logits are all -inf has a log-sum-exp of -inf, one with a
+    logit of inf one of inf; the other rows do not see it."""
+    K = 64
+    gen = torch.Generator().manual_seed(4)
+    x = torch.randn(T, K, generator=gen).bfloat16()
+    w = (torch.randn(V, K, generator=gen) * K ** -0.5).bfloat16()
+    x[:, -2:] = 0.0
+    w[:, -1], w[:, -2] = 1.0, 0.0
+    w[V // 3, -2] = 1.0
+    t = torch.randint(0, V, (T,), generator=gen)
+    want = Xent(x, w, t)
+    x[1, -1], x[3, -2] = -float("inf"), 3e38
+    x[3, :-2], w[V // 3, -2] = 0.0, 3e38
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    g.xent(put(x), put(w).t(), t.to(DEV), loss, lse)
+    assert float(lse[1]) == -float("inf") and float(lse[3]) == float("inf")
+    others = [i for i in range(T) if i not in (1, 3)]
+    close(lse[others], want.lse[others], want.lse_err[others], False, "lse")
+    close(loss[others], want.loss[others], want.loss_err[others], False, "loss")

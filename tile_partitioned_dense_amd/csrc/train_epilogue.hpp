@@ -181,9 +181,11 @@ __device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, in
 #pragma unroll
     for (int e = 0; e < 4; ++e) m = fmaxf(m, v[j][e]);
   m = join(m, most);
+  // An infinite maximum is not subtracted: a segment of logits that are all
+  // -inf has the sum 0 (not the NaN of inf - inf), one with an inf the sum inf.
+  const float m2 = fabsf(m) < INFINITY ? m * kLog2e : 0.0f;
   // written as passes over independent values: the exponential's latency
   // would otherwise be paid once per value, with no other wave to hide it
-  const float m2 = m * kLog2e;
   float x[4 * NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
