@@ -94,3 +94,29 @@ def test_rows_of_infinities(g, T, V):
     others = [i for i in range(T) if i not in (1, 3)]
     close(lse[others], want.lse[others], want.lse_err[others], False, "lse")
     close(loss[others], want.loss[others], want.loss_err[others], False, "loss")
+
+
+@pytest.mark.parametrize("T,V", [(1, 40), (30, 1300), (300, 4129), (1300, 6161), (2050, 8209)])
+def test_nearly_certain_tokens(g, T, V):
+    """Logits given exactly: the target's m of 20 to 127.5, one that is 2 to 20
+    below it, the others 1000 below. The loss log(1 + e^-(2 to 20)) is never
+    negative and off by at most 2^-21: the hardware exponentials of the maximum
+    and of the factor that takes the rounding of its multiple out again are
+    within 2^-23 each, and the sum, the product and two joins of segments add
+    half a unit in the last place, 2^-24, each."""
+    K = 64
+    gen = torch.Generator().manual_seed(5)
+    top = 20 + 0.5 * torch.randint(0, 216, (K,), generator=gen)
+    gap = torch.randint(2, 21, (K,), generator=gen)
+    hit = torch.randint(0, V, (K,), generator=gen)
+    near = (hit + torch.randint(1, V, (K,), generator=gen)) % V
+    w = (top - 1000).expand(V, K).clone()
+    w[hit, torch.arange(K)], w[near, torch.arange(K)] = top, top - gap
+    k = torch.randint(0, K, (T,), generator=gen)  # a token takes one column of w
+    x = torch.nn.functional.one_hot(k, K).bfloat16()
+    assert torch.equal(w.bfloat16()[hit, torch.arange(K)].float(), top)
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    g.xent(put(x), put(w.bfloat16()).t(), hit[k].to(DEV), loss, lse)
+    want = torch.log1p(torch.exp(-gap.double()))[k]
+    off = (loss.cpu().double() - want).abs().max()
+    assert float(loss.min()) >= 0 and float(off) <= 2.0 ** -21, (float(loss.min()), float(off))

@@ -183,7 +183,8 @@ __device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, in
   m = join(m, most);
   // An infinite maximum is not subtracted: a segment of logits that are all
   // -inf has the sum 0 (not the NaN of inf - inf), one with an inf the sum inf.
-  const float m2 = fabsf(m) < INFINITY ? m * kLog2e : 0.0f;
+  const bool finite = fabsf(m) < INFINITY;
+  const float ref = finite ? m : 0.0f, m2 = ref * kLog2e;
   // written as passes over independent values: the exponential's latency
   // would otherwise be paid once per value, with no other wave to hide it
   float x[4 * NJ];
@@ -198,6 +199,11 @@ __device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, in
   for (int k = 4; k < 4 * NJ; ++k) part4[k & 3] += x[k];
   float s = (part4[0] + part4[1]) + (part4[2] + part4[3]);
   s = join(s, add);
+  // The rounding of m2 is a common factor of all exponentials (5e-6 for a
+  // maximum of 100, the whole loss of a nearly certain token): taken out again.
+  // The maximum itself counts 1, so what is below that is rounding too.
+  s *= __builtin_amdgcn_exp2f(-fmaf(ref, kLog2e, -m2));
+  if (finite && s < 1.0f) s = 1.0f;
   if (c >= 0 && c < step * NJ) {
     // few rows have their target in this segment: the search is skipped by
     // every other wave
