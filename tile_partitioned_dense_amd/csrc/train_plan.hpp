@@ -169,7 +169,7 @@ inline TrainProduct plan_product(int64_t M, int64_t N, int64_t K, int max_splits
       // parts of at least 256 keep the load pipeline longer than its ramp; past
       // four rounds of tiles more parts even nothing out
       if (s > 1 && (k_per < 256 || tiles * (s - 1) >= 4 * (int64_t)cu * t.occ)) break;
-      if (ceil_div(K, k_per) != s && s > 1) continue;
+      if (s > 1 && ceil_div(K, k_per) != s) continue;
       const double us = product_us(t, M, N, s == 1 ? K : k_per, s, max_splits > 1, cu);
       if (best_us == 0.0 || us < best_us * 0.999) {
         best_us = us;
