@@ -5,7 +5,7 @@ import torch
 
 import tile_partitioned_dense_amd as tg
 from test_gpu_glu import DEV, put
-from train_helpers import Xent, close
+from train_helpers import Glu, Xent, close
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,41 @@ def test_nearly_certain_tokens(g, T, V):
     want = torch.log1p(torch.exp(-gap.double()))[k]
     off = (loss.cpu().double() - want).abs().max()
     assert float(loss.min()) >= 0 and float(off) <= 2.0 ** -21, (float(loss.min()), float(off))
+
+
+@pytest.mark.parametrize("gate", ["RELU", "SIGMOID"])
+@pytest.mark.parametrize("T,K,F", [(1, 64, 16), (33, 136, 200), (300, 72, 1032), (1300, 72, 4112)])
+def test_units_switched_off(g, gate, T, K, F):
+    """A gate bias of -inf gives zeros in its column of h and of both gradients
+    of the pre-activations, one of NaN NaN in its column of h alone. The
+    reference has -1e4 in the place of -inf: no difference in 64 bits, but for
+    the error bounds, which the exact zeros stand for here."""
+    gen = torch.Generator().manual_seed(6)
+    x = torch.randn(T, K, generator=gen).bfloat16()
+    w = (torch.randn(2 * F, K, generator=gen) * K ** -0.5).bfloat16()
+    b = torch.randn(2 * F, generator=gen)
+    dh = torch.randn(T, F, generator=gen).bfloat16()
+    off = torch.arange(0, F, 3)
+    b[off] = -1e4
+    ref = Glu(x, w, b, gate, dh)
+    on = torch.ones(F, dtype=torch.bool)
+    on[off] = False
+    b[off] = -float("inf")
+    xd, wd, bd = put(x), put(w), b.to(DEV)
+    for weights in (wd.t(), put(w.T.contiguous())):
+        for dt in (torch.float32, torch.bfloat16):
+            h = torch.full((T, F), float("nan"), device=DEV, dtype=dt)
+            g.glu(xd, weights, h, gate=tg.Gate[gate], bias=bd)
+            assert not bool(h[:, off].any())
+            close(h[:, on], ref.h[:, on], ref.h_err[:, on], dt == torch.bfloat16, "h")
+    dx, dw, db = torch.empty_like(xd), torch.empty_like(wd), torch.empty_like(bd)
+    g.glu_backward(xd, wd.t(), put(dh), dA=dx, dB=dw.t(), dbias=db, gate=tg.Gate[gate], bias=bd)
+    both = torch.cat([off, F + off])
+    assert not bool(db[both].any()) and not bool(dw[both].any())
+    keep = torch.cat([on, on])
+    close(db[keep], ref.dbias[keep], ref.dbias_err[keep], False, "dbias")
+    close(dw[keep], ref.dw[keep], ref.dw_err[keep], True, "dw")
+    close(dx, ref.dx, ref.dx_err, True, "dx")
+    b[1] = float("nan")
+    g.glu(xd, wd.t(), h, gate=tg.Gate[gate], bias=b.to(DEV))
+    assert bool(h[:, 1].isnan().all()) and int(h.isnan().sum()) == T

@@ -257,7 +257,7 @@ __device__ __forceinline__ void xent_grad(float (&g)[NV], Get logit, Col col, co
 //            s + z s (1 - s) 2 c (1 + 0.134145 z^2); in both this and silu
 //            the rounding of 1 - s near s = 1 is small against the slope of
 //            about 1 there
-//   relu     z, 1 for z > 0, else 0 (NaN stays)
+//   relu     z, 1 for z > 0, else 0 (also of -inf; NaN stays)
 //   sigmoid  s, s (1 - s), 1 - s from its own exponential (it is the value)
 constexpr int kGateSilu = 0, kGateGelu = 1, kGateGeluTanh = 2, kGateRelu = 3, kGateSigmoid = 4;
 
@@ -285,7 +285,7 @@ __device__ __forceinline__ void gate_both(float z, float& act, float& slope) {
     slope = fmaf(z * s, (1.0f - s) * (1.5957691216057308f * fmaf(0.134145f * z, z, 1.0f)), s);
   } else if constexpr (GATE == kGateRelu) {
     slope = z > 0.0f ? 1.0f : 0.0f;
-    act = z * slope;
+    act = z < 0.0f ? 0.0f : z;
   } else {
     const float s = sigmoid_hw(z);
     act = s;
