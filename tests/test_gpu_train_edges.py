@@ -5,7 +5,7 @@ import torch
 
 import tile_partitioned_dense_amd as tg
 from test_gpu_glu import DEV, put
-from train_helpers import Glu, Xent, close
+from train_helpers import EVAL, GATES, Glu, Xent, act_slope, close
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +158,27 @@ def test_units_switched_off(g, gate, T, K, F):
     b[1] = float("nan")
     g.glu(xd, wd.t(), h, gate=tg.Gate[gate], bias=b.to(DEV))
     assert bool(h[:, 1].isnan().all()) and int(h.isnan().sum()) == T
+
+
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("T", [4, 300])
+def test_largest_preactivations(g, gate, T):
+    """Gate pre-activations of up to 3e38, whose squares and cubes overflow:
+    gates are 0 or z (or 1) there and their slopes 0 or 1 (or 0). x is zero, so
+    the pre-activations are the biases; up is 1 and dh 1/4 in four rows, so h is
+    the gate and dbias slope and gate."""
+    K, size = 64, torch.tensor([20.0, 1e3, 1e10, 1e13, 1.7e19, 5e19, 1e20, 3e38])
+    z = torch.cat([size, -size]).repeat(20)
+    F = len(z)
+    b = torch.cat([z, torch.ones(F)])
+    x, w = torch.zeros(T, K).bfloat16(), torch.zeros(2 * F, K).bfloat16()
+    dh = torch.zeros(T, F).bfloat16()
+    dh[:4] = 0.25
+    act, slope = act_slope(z.double(), gate)
+    xd, wd, bd = put(x), put(w), b.to(DEV)
+    h, db = torch.empty(T, F, device=DEV), torch.empty(2 * F, device=DEV)
+    g.glu(xd, wd.t(), h, gate=tg.Gate[gate], bias=bd)
+    g.glu_backward(xd, wd.t(), put(dh), dbias=db, gate=tg.Gate[gate], bias=bd)
+    # e^-20 is 2e-9: what gate and slope are off their limits at 20 already
+    close(h, act.expand(T, F), EVAL * act.abs() + 1e-7, False, "h")
+    close(db, torch.cat([slope, act]), EVAL * torch.cat([slope, act]).abs() + 1e-6, False, "dbias")

@@ -282,7 +282,9 @@ __device__ __forceinline__ void gate_both(float z, float& act, float& slope) {
     const float y2 = 1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f);
     const float s = sigmoid_hw(y2);
     act = z * s;
-    slope = fmaf(z * s, (1.0f - s) * (1.5957691216057308f * fmaf(0.134145f * z, z, 1.0f)), s);
+    // (1 - s is 0 long before the square is cut off)
+    const float sq = fminf(z * z, 1e30f);
+    slope = fmaf(z * s, (1.0f - s) * (1.5957691216057308f * fmaf(0.134145f, sq, 1.0f)), s);
   } else if constexpr (GATE == kGateRelu) {
     slope = z > 0.0f ? 1.0f : 0.0f;
     act = z < 0.0f ? 0.0f : z;
