@@ -182,3 +182,34 @@ def test_largest_preactivations(g, gate, T):
     # e^-20 is 2e-9: what gate and slope are off their limits at 20 already
     close(h, act.expand(T, F), EVAL * act.abs() + 1e-7, False, "h")
     close(db, torch.cat([slope, act]), EVAL * torch.cat([slope, act]).abs() + 1e-6, False, "dbias")
+
+
+@pytest.mark.parametrize("pitch", [0, 3, 8, 2 ** 31 + 4, 2 ** 40])
+@pytest.mark.parametrize("K", [65, 72, 1032])
+def test_one_row_of_any_stride(g, pitch, K):
+    """A single row of x, dC and the results has no row stride that counts."""
+    V, F = 1300, 200
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    ld = (K + 7) // 8 * 8
+    w = (torch.randn(V, ld, generator=gen, device=DEV) * K ** -0.5).bfloat16()[:, :K]
+    w2 = w[:2 * F]
+    x = torch.randn(ld, generator=gen, device=DEV).bfloat16()[:K]
+    dh = torch.randn(F, generator=gen, device=DEV).bfloat16()
+    t, d = torch.tensor([V // 2], device=DEV), torch.ones(1, device=DEV)
+
+    def row(v, apart):
+        return v.as_strided((1, len(v)), (apart, 1))
+
+    def run(apart):
+        o = [torch.full((n,), float("nan"), device=DEV) for n in (1, 1, 2 * F)]
+        r = [torch.full((n,), float("nan"), dtype=torch.bfloat16, device=DEV) for n in (F, ld, ld)]
+        m = [torch.full((n, ld), float("nan"), dtype=torch.bfloat16, device=DEV)[:, :K] for n in (V, 2 * F)]
+        xr = row(x, apart)
+        g.xent(xr, w.t(), t, o[0], o[1])
+        g.xent_backward(xr, w.t(), t, o[1], d, dA=row(r[1][:K], apart), dB=m[0].t())
+        g.glu(xr, w2.t(), row(r[0], apart), gate=tg.Gate.GELU)
+        g.glu_backward(xr, w2.t(), row(dh, apart), dA=row(r[2][:K], apart), dB=m[1].t(), dbias=o[2], gate=tg.Gate.GELU)
+        return o + [r[0], r[1][:K], r[2][:K]] + m
+
+    for a, b in zip(run(pitch), run(ld)):
+        assert bool(b.isfinite().all()) and torch.equal(a, b)

@@ -75,6 +75,11 @@ bool pairs(const tg::TrainProduct& q, int64_t tokens, int64_t rows, int64_t cols
   return q.tile == tg::kSmallTile && few_tokens(tokens, rows, cols) && rows * cols * 2 <= ((int64_t)64 << 20);
 }
 
+// The row stride the kernels take for x: a single row may come with any, but
+// the offsets of a tile's other rows are formed from it, and whole chunks
+// loaded there need them to be multiples of 16 bytes.
+int64_t row_stride(int64_t rows, int64_t ld, int64_t cols) { return rows > 1 ? ld : tg::ceil_div(cols, 8) * 8; }
+
 // One gradient: out (bf16) = scale * (left [rows x len]) . (right [len x cols],
 // row-major), by parts of the contraction when the plan says so. left is G or
 // dz as a store wrote it: its rows are zero past len up to a multiple of 8.
@@ -182,7 +187,7 @@ tile_gemm_status_t run_glu_backward(tile_gemm_t h, const void* A, const void* B,
   a.M = (int32_t)M;
   a.N = (int32_t)N;
   a.K = (int32_t)K;
-  a.lda = s->a_m;
+  a.lda = row_stride(M, s->a_m, K);
   a.ldb = s->b_n;
   a.bias = bias;
   a.glu_half = (int32_t)(N / 2);
@@ -225,7 +230,7 @@ tile_gemm_status_t run_xent(tile_gemm_t h, const void* A, const void* B, const v
   a.B = static_cast<const uint16_t*>(B);
   a.M = (int32_t)M;
   a.K = (int32_t)K;
-  a.lda = s->a_m;
+  a.lda = row_stride(M, s->a_m, K);
   a.ldb = s->b_n;
   a.target = target;
   a.target64 = o->target_type == TILE_GEMM_INDEX_I64;
@@ -290,7 +295,7 @@ tile_gemm_status_t run_xent_backward(tile_gemm_t h, const void* A, const void* B
     a.M = (int32_t)M;
     a.N = (int32_t)cols;
     a.K = (int32_t)K;
-    a.lda = s->a_m;
+    a.lda = row_stride(M, s->a_m, K);
     a.ldb = s->b_n;
     if (few) {
       a.target = target;
