@@ -213,3 +213,23 @@ def test_one_row_of_any_stride(g, pitch, K):
 
     for a, b in zip(run(pitch), run(ld)):
         assert bool(b.isfinite().all()) and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,K,V", [(1, 64, 1), (1, 136, 50), (33, 72, 40), (70, 65, 33), (300, 72, 21)])
+def test_pieces_of_one_column(g, T, K, V):
+    """The smallest pieces of a vocabulary: a column at a time."""
+    gen = torch.Generator().manual_seed(8)
+    x = torch.randn(T, K, generator=gen).bfloat16()
+    w = (torch.randn(V, K, generator=gen) * 2 * K ** -0.5).bfloat16()
+    t = torch.randint(0, V, (T,), generator=gen)
+    t[1::5] = -100
+    d = torch.rand(T, generator=gen)
+    ref = Xent(x, w, t, smoothing=0.1, z_loss=1e-3, dloss=d)
+    opts = dict(label_smoothing=0.1, z_loss=1e-3)
+    xd, wd, td = put(x), put(w), t.to(DEV)
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    g.xent(xd, wd.t(), td, loss, lse, **opts)
+    dx, dw = put(torch.zeros_like(x)), put(torch.zeros_like(w))
+    g.xent_backward(xd, wd.t(), td, lse, d.to(DEV), dA=dx, dB=dw.t(), piece=1, **opts)
+    close(dx, ref.dx, ref.dx_err, True, "dx")
+    close(dw, ref.dw, ref.dw_err, True, "dw")
