@@ -229,6 +229,8 @@ tile_gemm_status_t tile_gemm_run_mx(tile_gemm_t h, const void* A, const void* B,
  * column-major B its kernels, and so its last bits, may be others). One
  * kernel: both projections, the activation and the product; shapes, layouts,
  * types, bias, errors and ownership as for tile_gemm_run_epilogue with that act.
+ * A pre-activation of -inf (a unit switched off by its bias) is 0 with RELU and
+ * SIGMOID; with SILU, GELU and GELU_TANH it is NaN, -inf * 0.
  */
 typedef enum {
   TILE_GEMM_GATE_SILU = 0,      /* x / (1 + e^-x) */
@@ -285,7 +287,9 @@ tile_gemm_status_t tile_gemm_run_glu_backward(tile_gemm_t h, const void* A, cons
  * has loss 0 (its lse is still given); any other target outside [0, N) gives
  * loss NaN. Every tile of l is turned into per-row maxima and sums by the
  * workgroup that owns it and the pieces are joined in a fixed order: results
- * are bit-identical run to run. A few rows stream B once.
+ * are bit-identical run to run. A few rows stream B once. A logit of -inf (a
+ * column masked by its weights) counts for nothing; a row of nothing else has
+ * lse -inf and loss NaN, a row with a logit of inf has lse inf.
  *
  * A is M x K, bf16, row-major; B K x N, bf16, column-major (b_k = 1; the usual
  * storage of weights, N rows of K); target M int32 or int64 values; loss and
