@@ -73,6 +73,27 @@ def test_columns_of_minus_infinity(g, T, K, V, which):
     assert not bool(dw[masked].any())
 
 
+@pytest.mark.parametrize("T,K,V", [(1, 64, 33), (40, 64, 1300), (300, 72, 4129), (1300, 72, 6161), (700, 65, 900)])
+@pytest.mark.parametrize("lowest", [torch.finfo(torch.bfloat16).min, -2e38, -1e30, -1e10, -1e9])
+def test_columns_of_the_lowest_value(g, T, K, V, lowest):
+    """Logits of the type's lowest value, whose multiples overflow, and of other
+    large negative values, whose multiples are rounded by more than any exponent,
+    count for nothing like those of -inf, whole segments of them too."""
+    for masked in ([V - 1], list(range(min(V - 1, 256))), [v for v in range(V) if v != V // 2]):
+        x, w, t, d, kept, ref = masked_head(T, K, V, masked, 9)
+        w[masked, -1] = lowest
+        xd, wd, td = put(x), put(w), t.to(DEV)
+        loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+        g.xent(xd, wd.t(), td, loss, lse)
+        close(lse, ref.lse, ref.lse_err, False, "lse")
+        close(loss, ref.loss, ref.loss_err, False, "loss")
+        dx, dw = put(torch.zeros_like(x)), put(torch.zeros_like(w))
+        g.xent_backward(xd, wd.t(), td, lse, d.to(DEV), dA=dx, dB=dw.t())
+        close(dx, ref.dx, ref.dx_err, True, "dx")
+        close(dw[kept.to(DEV)], ref.dw, ref.dw_err, True, "dw")
+        assert not bool(dw[masked].any())
+
+
 @pytest.mark.parametrize("T,V", [(5, 300), (200, 2000)])
 def test_rows_of_infinities(g, T, V):
     """A row whose logits are all -inf has a log-sum-exp of -inf, one with a

@@ -183,15 +183,19 @@ __device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, in
   m = join(m, most);
   // An infinite maximum is not subtracted: a segment of logits that are all
   // -inf has the sum 0 (not the NaN of inf - inf), one with an inf the sum inf.
-  const bool finite = fabsf(m) < INFINITY;
-  const float ref = finite ? m : 0.0f, m2 = ref * kLog2e;
+  // Subtracted before the scaling, not with it in one fma: the maximum's own
+  // exponential is then exactly 1. The rounding of its multiple would be a
+  // common factor of the sum: 5e-6 at 100, the whole loss of a nearly certain
+  // token; inf from 1e10 on, and so NaN where columns are masked by a large
+  // negative value. (Loss and gradients of 3001 x 2048 x 50257: 2189 to 2201 us.)
+  const float ref = fabsf(m) < INFINITY ? m : 0.0f;
   // written as passes over independent values: the exponential's latency
   // would otherwise be paid once per value, with no other wave to hide it
   float x[4 * NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[4 * j + e] = fmaf(v[j][e], kLog2e, -m2);
+    for (int e = 0; e < 4; ++e) x[4 * j + e] = (v[j][e] - ref) * kLog2e;
 #pragma unroll
   for (int k = 0; k < 4 * NJ; ++k) x[k] = __builtin_amdgcn_exp2f(x[k]);
   float part4[4] = {x[0], x[1], x[2], x[3]};
@@ -199,11 +203,6 @@ __device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, in
   for (int k = 4; k < 4 * NJ; ++k) part4[k & 3] += x[k];
   float s = (part4[0] + part4[1]) + (part4[2] + part4[3]);
   s = join(s, add);
-  // The rounding of m2 is a common factor of all exponentials (5e-6 for a
-  // maximum of 100, the whole loss of a nearly certain token): taken out again.
-  // The maximum itself counts 1, so what is below that is rounding too.
-  s *= __builtin_amdgcn_exp2f(-fmaf(ref, kLog2e, -m2));
-  if (finite && s < 1.0f) s = 1.0f;
   if (c >= 0 && c < step * NJ) {
     // few rows have their target in this segment: the search is skipped by
     // every other wave
