@@ -1,11 +1,13 @@
 """Edge calls of the gated block and of the cross entropy head on the GPU."""
 
+import math
+
 import pytest
 import torch
 
 import tile_partitioned_dense_amd as tg
 from test_gpu_glu import DEV, put
-from train_helpers import EVAL, GATES, Glu, Xent, act_slope, close
+from train_helpers import EVAL, GATES, HALF, TAU, Glu, Xent, act_slope, close
 
 pytestmark = pytest.mark.gpu
 
@@ -92,6 +94,44 @@ def test_columns_of_the_lowest_value(g, T, K, V, lowest):
         close(dx, ref.dx, ref.dx_err, True, "dx")
         close(dw[kept.to(DEV)], ref.dw, ref.dw_err, True, "dw")
         assert not bool(dw[masked].any())
+
+
+@pytest.mark.parametrize("T,K,V", [(6, 64, 300), (70, 72, 1300), (300, 72, 2051)])
+@pytest.mark.parametrize("lowest", [torch.finfo(torch.bfloat16).min, -1e30, -1e10])
+def test_rows_of_the_lowest_value(g, T, K, V, lowest):
+    """Rows of which nothing is left (every third): all logits are the same large
+    negative value, so the loss is log V and lse that value, the sum of V of them
+    to the last place; every column's e^(l - lse) is 1 by that lse, and the
+    gradients are those of the formula, without an infinity."""
+    gen = torch.Generator().manual_seed(10)
+    x = torch.randn(T, K, generator=gen).bfloat16()
+    w = (torch.randn(V, K, generator=gen) * 2 * K ** -0.5).bfloat16()
+    t = torch.randint(0, V, (T,), generator=gen)
+    d = torch.rand(T, generator=gen)
+    out = torch.zeros(T, dtype=torch.bool)
+    out[::3] = True
+    x[:, -1], x[out], w[:, -1] = 0.0, 0.0, 0.0
+    ref = Xent(x, w, t, dloss=d)
+    x[out, -1], w[:, -1] = 1.0, lowest
+    one = float(w[0, -1].float())
+    xd, wd, td = put(x), put(w), t.to(DEV)
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    g.xent(xd, wd.t(), td, loss, lse)
+    assert bool((lse.cpu()[out] == one).all())
+    assert float((loss.cpu()[out].double() - math.log(V)).abs().max()) <= EVAL * math.log(V)
+    close(lse[~out.to(DEV)], ref.lse[~out], ref.lse_err[~out], False, "lse")
+    close(loss[~out.to(DEV)], ref.loss[~out], ref.loss_err[~out], False, "loss")
+    dx, dw = put(torch.zeros_like(x)), put(torch.zeros_like(w))
+    g.xent_backward(xd, wd.t(), td, lse, d.to(DEV), dA=dx, dB=dw.t())
+    close(dx[~out.to(DEV), :-1], ref.dx[~out, :-1], ref.dx_err[~out, :-1], True, "dx")
+    # G = d (1 - [target]) in those rows, held in bf16
+    G = d[out].double()[:, None] * (1 - torch.nn.functional.one_hot(t[out], V).double())
+    w64 = w.double()[:, :-1]
+    err = HALF * G.abs() @ w64.abs() + TAU * G.abs() @ w64.abs()
+    close(dx[out.to(DEV), :-1], G @ w64, err, True, "dx of the masked rows")
+    # x is zero in those rows but for its last value
+    close(dw[:, :-1], ref.dw[:, :-1], ref.dw_err[:, :-1], True, "dw")
+    close(dw[:, -1], G.sum(0), (HALF + TAU) * G.sum(0), True, "dw of the last value")
 
 
 @pytest.mark.parametrize("T,V", [(5, 300), (200, 2000)])

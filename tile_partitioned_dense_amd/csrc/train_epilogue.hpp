@@ -56,10 +56,10 @@ constexpr int epi_gate(int epi) { return (epi >> 4) - 1; }
 constexpr int with_gate(int kind, int gate) { return kind + 16 * (gate + 1); }
 constexpr bool epi_gated(int epi) { return epi_kind(epi) == kEpiGluGrad || epi_kind(epi) == kEpiGlu; }
 
-// Per-row constants of kEpiXentGrad (xent_rows_kernel): lse * log2 e, a, b and
-// the target's column (-1: none).
+// Per-row constants of kEpiXentGrad (xent_rows_kernel): the log-sum-exp, a, b
+// and the target's column (-1: none).
 struct XentRow {
-  float lse2, a, b;
+  float lse, a, b;
   int32_t target;
 };
 
@@ -128,7 +128,7 @@ __device__ __forceinline__ int64_t target_of(const void* target, int is64, int64
 // (see xent_rows_kernel).
 __device__ __forceinline__ XentRow xent_row(int64_t t, int64_t ignore, int64_t vocab, float lse, float dloss,
                                             float c, float z_loss) {
-  XentRow r{lse * kLog2e, 0.0f, 0.0f, -1};
+  XentRow r{lse, 0.0f, 0.0f, -1};
   if (t != ignore) {
     const bool known = t >= 0 && t < vocab;
     r.b = known ? dloss / c : NAN;
@@ -223,12 +223,14 @@ __device__ __forceinline__ void stats_row(floatx4 (&v)[NJ], int step, int lg, in
 // (XentRow's constants, its target relative to the segment). Rows that count
 // for nothing (b = 0) give exact zeros whatever their logits are. `near`:
 // whether any row of the wave has its target in the segment; few do, and the
-// others skip the comparisons.
+// others skip the comparisons. (The subtraction comes before the scaling, as in
+// stats_row: a multiple of the log-sum-exp is off by more than any exponent
+// where that is large.)
 template <int NV, class Get, class Col>
 __device__ __forceinline__ void xent_grad(float (&g)[NV], Get logit, Col col, const XentRow& r, bool near,
                                           const TrainArgs& p) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) g[k] = fmaf(logit(k), kLog2e, -r.lse2);
+  for (int k = 0; k < NV; ++k) g[k] = (logit(k) - r.lse) * kLog2e;
 #pragma unroll
   for (int k = 0; k < NV; ++k) g[k] = __builtin_amdgcn_exp2f(g[k]);
 #pragma unroll
