@@ -20,7 +20,7 @@ namespace tg {
 // compute unit. `gated`: compiled with the gated block's stores too. us_tile is
 // that of the loss's stores for every product: the gated backward's store takes
 // longer (1501 x 5488 over 4104, one round of 210 tiles of 256 x 160: 62 us by
-// these figures, 91 under the profiler).
+// these figures, 87 to 94 under the profiler).
 struct TrainTile {
   int bm, bn, wm, wn;
   double us_k, us_tile, us_k1;
