@@ -161,10 +161,11 @@ def test_rows_of_infinities(g, T, V):
 def test_nearly_certain_tokens(g, T, V):
     """Logits given exactly: the target's m of 20 to 127.5, one that is 2 to 20
     below it, the others 1000 below. The loss log(1 + e^-(2 to 20)) is never
-    negative and off by at most 2^-21: the hardware exponentials of the maximum
-    and of the factor that takes the rounding of its multiple out again are
-    within 2^-23 each, and the sum, the product and two joins of segments add
-    half a unit in the last place, 2^-24, each."""
+    negative and off by at most 2^-21: the maximum's exponential is 1, the
+    other's is at most e^-2 and within 2^-20 of itself (2^-23 for the hardware's,
+    two roundings of an exponent of at most 29, and a product), and the sums, two
+    joins of segments and the logarithm add half a unit in the last place of a
+    value below 2, 2^-24, each."""
     K = 64
     gen = torch.Generator().manual_seed(5)
     top = 20 + 0.5 * torch.randint(0, 216, (K,), generator=gen)
