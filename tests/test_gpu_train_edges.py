@@ -162,7 +162,7 @@ def test_nearly_certain_tokens(g, T, V):
     """Logits given exactly: the target's m of 20 to 127.5, one that is 2 to 20
     below it, the others 1000 below. The loss log(1 + e^-(2 to 20)) is never
     negative and off by at most 2^-21: the maximum's exponential is 1, the
-    other's is at most e^-2 and within 2^-20 of itself (2^-23 for the hardware's,
+    other's is at most e^-2 and within 2^-19 of itself (2^-23 for the hardware's,
     two roundings of an exponent of at most 29, and a product), and the sums, two
     joins of segments and the logarithm add half a unit in the last place of a
     value below 2, 2^-24, each."""
