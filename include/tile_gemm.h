@@ -341,6 +341,176 @@ tile_gemm_status_t tile_gemm_run_xent_backward(tile_gemm_t h, const void* A, con
                                                int64_t workspace_bytes, void* stream);
 
 /*
+ * E4M3 products with float32 scales for blocks of 128, the form in which 8-bit
+ * weights and activations are kept for answering, beside the microscaled
+ * products above (whose scales are powers of two, one for 32 values):
+ *
+ *   C[i][j] = act(sum_b a_scale[b][i] b_scale[j / 128][b] sum_{k in block b} A[i][k] B[j][k] + bias[j])
+ *
+ * with block b = [128 b, 128 b + 128) of K (the last may be shorter). A is M x K
+ * E4M3 bytes, row-major; B is given as its N x K transpose, K-contiguous
+ * (strides b_k = 1, b_n >= K), as weights are stored. a_scale holds a value for
+ * each row and block of K, the rows of one block next to each other (block b of
+ * row i at a_scale[b * a_scale_stride + i], a_scale_stride >= M); b_scale one
+ * for each 128 x 128 block of B (rows 128 r .. of block b at
+ * b_scale[r * b_scale_stride + b]). C, dtype, bias and act (not
+ * TILE_GEMM_ACT_SWIGLU) are as for tile_gemm_run_epilogue. A block's products
+ * are summed in the matrix instruction, the blocks' sums scaled and added in
+ * fp32 in ascending order (outputs of up to 64 rows: up to four such sums, added
+ * in a fixed order), each element written once: results are bit-identical from
+ * run to run. A NaN or infinite scale reaches the rows (or columns) it scales.
+ *
+ * Limits: K a multiple of 16; M, N, K and the strides of A and B below 2^22; A
+ * and B 16-byte aligned with leading dimensions of whole 16 bytes, scales
+ * 4-byte aligned. A, B and the scales may span 4 GiB or more. M = 0 or N = 0 is
+ * a no-op; K = 0 stores act(bias). Errors and ownership as for
+ * tile_gemm_run_epilogue. Enqueue-only, allocates nothing.
+ */
+typedef struct {
+  int64_t a_stride;       /* bytes between rows of A */
+  int64_t b_stride;       /* bytes between rows of B */
+  int64_t c_stride;       /* elements between rows of C */
+  int64_t a_scale_stride; /* floats between A's blocks of K */
+  int64_t b_scale_stride; /* floats between B's blocks of 128 rows */
+  int64_t b_expert_stride;       /* tile_gemm_run_fp8_experts: bytes between the experts' B, */
+  int64_t b_scale_expert_stride; /* floats between their b_scale */
+} tile_gemm_fp8_strides_t;
+
+tile_gemm_status_t tile_gemm_run_fp8(tile_gemm_t h, const void* A, const void* B, void* C, int64_t M,
+                                     int64_t N, int64_t K, const tile_gemm_fp8_strides_t* strides,
+                                     const float* a_scale, const float* b_scale,
+                                     tile_gemm_dtype_t dtype, const float* bias, tile_gemm_act_t act,
+                                     void* stream);
+
+/*
+ * The same product over rows sorted by expert: expert e has rows
+ * [offsets[e], offsets[e + 1]) of A and C (offsets: E + 1 int32 values on the
+ * device, as tile_gemm_run_place gives them) and an N x K matrix and scales of
+ * its own, b_expert_stride bytes and b_scale_expert_stride floats apart.
+ * No bias, no activation. Rows of C outside every expert's are left as they
+ * were. Offsets are cut to [0, M]; where they decrease an expert is empty, and
+ * rows that two experts claim hold either one's result. 1 <= E <= 1024; one
+ * expert's matrix spans less than 2 GiB.
+ */
+tile_gemm_status_t tile_gemm_run_fp8_experts(tile_gemm_t h, const void* A, const void* B, void* C,
+                                             int64_t M, int64_t N, int64_t K, int64_t E,
+                                             const int32_t* offsets,
+                                             const tile_gemm_fp8_strides_t* strides,
+                                             const float* a_scale, const float* b_scale,
+                                             tile_gemm_dtype_t dtype, void* stream);
+
+/*
+ * bf16 values to E4M3 and their scales, as the products above take them:
+ *   a = max(largest |x| of the block, 2^-100), scale = a / 448,
+ *   q = x * (448 / a), rounded to the nearest E4M3 value (ties to even)
+ * in fp32 arithmetic. A block that holds a NaN or an infinity has that as its
+ * scale, so that products which read it are NaN.
+ *   ROWS: blocks of 128 values of a row. X is M x K, block b of row i has
+ *     scale[b * scale_stride + i].
+ *   GATED_ROWS: the same of x = act(g) * u, with g the first K columns of X
+ *     (M x 2 K) and u the last K, formed in fp32: the second half of a gated
+ *     block whose first half was a product onto a merged gate+up weight.
+ *   BLOCKS: blocks of 128 x 128 values. X is M x K, the block of rows 128 r ..
+ *     and columns 128 b .. has scale[r * scale_stride + b].
+ * With `rows` (M int32 values, not with BLOCKS) row i of Q is made of row
+ * rows[i] of X, which has x_rows rows; where rows[i] is none of them (the -1
+ * behind the last expert's rows), row i and its scales are left as they were.
+ * Without `rows`, x_rows is not looked at.
+ * X is bf16, Q E4M3 bytes, both row-major with leading dimensions of whole 16
+ * bytes; K a multiple of 16; M, K and the strides of X and Q below 2^22.
+ */
+typedef enum {
+  TILE_GEMM_QUANT_ROWS = 0,
+  TILE_GEMM_QUANT_GATED_ROWS = 1,
+  TILE_GEMM_QUANT_BLOCKS = 2
+} tile_gemm_quant_t;
+
+tile_gemm_status_t tile_gemm_run_quantize(tile_gemm_t h, const void* X, void* Q, float* scale, int64_t M,
+                                          int64_t K, int64_t x_stride, int64_t q_stride,
+                                          int64_t scale_stride, tile_gemm_quant_t form,
+                                          tile_gemm_gate_t gate, const int32_t* rows, int64_t x_rows,
+                                          void* stream);
+
+/*
+ * Routing: each token's k experts of E and their weights from its logits
+ * (T x E, fp32 or bf16, `logit_stride` elements apart; a product of
+ * tile_gemm_run, say).
+ *   s = softmax(logits) or sigmoid(logits)             (score)
+ *   v = s + bias                                       (bias: E values or NULL)
+ *   groups > 1: the experts are `groups` equal runs; a group's value is the sum
+ *     of its group_top (1 or 2) largest v (of one where it has one only), and
+ *     only experts of the top_groups best groups can be chosen
+ *   ids = the k experts of largest v, largest first; of equal ones, and of
+ *     equal groups, the lowest index first
+ *   weights = scale * s[ids], with `renormalize` divided by the sum of s[ids]
+ *     (0 where that is 0)
+ * Scores, values and sums are held in 64 bits, so that the order of close ones
+ * is that of the formula. A NaN logit counts as -inf (score 0), a NaN value as
+ * -inf; experts at -inf are chosen last. Softmax: logits of +inf share the
+ * weight; a token without a finite logit has scores 0.
+ * 1 <= E <= 1024, groups <= 64 a divisor of E, k <= 32 and at most the experts
+ * of top_groups groups; T and the strides below 2^31.
+ */
+typedef enum { TILE_GEMM_SCORE_SOFTMAX = 0, TILE_GEMM_SCORE_SIGMOID = 1 } tile_gemm_score_t;
+typedef enum { TILE_GEMM_LOGITS_F32 = 0, TILE_GEMM_LOGITS_BF16 = 1 } tile_gemm_logits_t;
+
+typedef struct {
+  int32_t score;       /* tile_gemm_score_t */
+  int32_t logits_type; /* tile_gemm_logits_t */
+  int32_t groups, top_groups, group_top;
+  int32_t renormalize;
+  float scale;
+} tile_gemm_route_t;
+
+tile_gemm_status_t tile_gemm_run_route(tile_gemm_t h, const void* logits, const float* bias, int32_t* ids,
+                                       float* weights, int64_t T, int64_t E, int64_t k,
+                                       int64_t logit_stride, const tile_gemm_route_t* options,
+                                       void* stream);
+
+/*
+ * Gradient of sum dweights * weights for the ids chosen (the choice itself has
+ * none, nor has the bias): dlogits, T x E, of the logits' type. score, scale,
+ * renormalize and logits_type are read of the options. An id outside [0, E)
+ * (a place that was masked) counts for nothing; one that a token names twice
+ * counts twice.
+ */
+tile_gemm_status_t tile_gemm_run_route_backward(tile_gemm_t h, const void* logits, const int32_t* ids,
+                                                const float* dweights, void* dlogits, int64_t T,
+                                                int64_t E, int64_t k, int64_t logit_stride,
+                                                int64_t dlogit_stride,
+                                                const tile_gemm_route_t* options, void* stream);
+
+/*
+ * The order of the tokens by expert: the n = T k entries of ids (T x k) with an
+ * expert in [first, first + E) (the experts that are here; other ids, -1 among
+ * them, are left out), sorted by expert and, of one expert, by entry.
+ *   offsets[e] = the first place of expert first + e, offsets[E] = the entries
+ *     that are here
+ *   rows[p]   = the token at place p, -1 from offsets[E] on  (n values or NULL)
+ *   places[t][j] = the place of entry (t, j), or -1           (T x k, or NULL)
+ * Integers only, no atomics whose order shows: results are the same every run.
+ * `workspace` as for tile_gemm_run_glu_backward (tile_gemm_place_workspace
+ * gives its size, 0 up to 4096 entries). 1 <= E <= 1024, n below 2^31.
+ */
+tile_gemm_status_t tile_gemm_run_place(tile_gemm_t h, const int32_t* ids, int64_t T, int64_t k,
+                                       int64_t first, int64_t E, int32_t* offsets, int32_t* rows,
+                                       int32_t* places, void* workspace, int64_t workspace_bytes,
+                                       void* stream);
+
+/*
+ * Each token's weighted sum of its experts' rows:
+ *   Y[t] = sum_j weights[t][j] Z[places[t][j]]
+ * over the places inside Z's z_rows rows (others, -1 among them, are left out),
+ * in fp32 in the order of j. Z is bf16, Y bf16 or fp32 (dtype), both row-major
+ * with leading dimensions of whole 16 bytes; weights T x k fp32 or NULL (ones).
+ * 1 <= k <= 64.
+ */
+tile_gemm_status_t tile_gemm_run_combine(tile_gemm_t h, const void* Z, const int32_t* places,
+                                         const float* weights, void* Y, int64_t T, int64_t N, int64_t k,
+                                         int64_t z_rows, int64_t z_stride, int64_t y_stride,
+                                         tile_gemm_dtype_t dtype, void* stream);
+
+/*
  * Release a handle (host memory only). NULL is accepted and returns OK.
  * Source: the counterpart of the one-time preparation ("Rust Compute
  * Kernels", section "Quick example"); it touches no device memory, since the
@@ -435,6 +605,39 @@ tile_gemm_status_t tile_gemm_check_xent_backward(const void* A, const void* B, c
                                                  const tile_gemm_xent_t* options,
                                                  const void* workspace, int64_t workspace_bytes);
 
+/* The checks of the E4M3 products, of the routing and of what stands between
+ * them, before any launch, with the same results. */
+tile_gemm_status_t tile_gemm_check_fp8(const void* A, const void* B, const void* C, int64_t M, int64_t N,
+                                       int64_t K, const tile_gemm_fp8_strides_t* strides,
+                                       const float* a_scale, const float* b_scale,
+                                       tile_gemm_dtype_t dtype, const float* bias, tile_gemm_act_t act);
+tile_gemm_status_t tile_gemm_check_fp8_experts(const void* A, const void* B, const void* C, int64_t M,
+                                               int64_t N, int64_t K, int64_t E, const int32_t* offsets,
+                                               const tile_gemm_fp8_strides_t* strides,
+                                               const float* a_scale, const float* b_scale,
+                                               tile_gemm_dtype_t dtype);
+tile_gemm_status_t tile_gemm_check_quantize(const void* X, const void* Q, const float* scale, int64_t M,
+                                            int64_t K, int64_t x_stride, int64_t q_stride,
+                                            int64_t scale_stride, tile_gemm_quant_t form,
+                                            tile_gemm_gate_t gate, const int32_t* rows, int64_t x_rows);
+tile_gemm_status_t tile_gemm_check_route(const void* logits, const float* bias, const int32_t* ids,
+                                         const float* weights, int64_t T, int64_t E, int64_t k,
+                                         int64_t logit_stride, const tile_gemm_route_t* options);
+tile_gemm_status_t tile_gemm_check_route_backward(const void* logits, const int32_t* ids,
+                                                  const float* dweights, const void* dlogits, int64_t T,
+                                                  int64_t E, int64_t k, int64_t logit_stride,
+                                                  int64_t dlogit_stride,
+                                                  const tile_gemm_route_t* options);
+tile_gemm_status_t tile_gemm_check_place(const int32_t* ids, int64_t T, int64_t k, int64_t first,
+                                         int64_t E, const int32_t* offsets, const int32_t* rows,
+                                         const int32_t* places, const void* workspace,
+                                         int64_t workspace_bytes);
+tile_gemm_status_t tile_gemm_place_workspace(int64_t T, int64_t k, int64_t E, int64_t* bytes);
+tile_gemm_status_t tile_gemm_check_combine(const void* Z, const int32_t* places, const float* weights,
+                                           const void* Y, int64_t T, int64_t N, int64_t k,
+                                           int64_t z_rows, int64_t z_stride, int64_t y_stride,
+                                           tile_gemm_dtype_t dtype);
+
 /* Kernel variants the planner chooses between. */
 typedef enum {
   TILE_GEMM_VARIANT_NONE = 0,   /* M == 0 or N == 0: nothing to launch */
@@ -506,6 +709,13 @@ tile_gemm_status_t tile_gemm_plan_train(int64_t M, int64_t N, int64_t K,
  * E2M1). An unknown fmt is TILE_GEMM_ERR_DTYPE. */
 tile_gemm_status_t tile_gemm_plan_mx(int64_t M, int64_t N, int64_t K, tile_gemm_mx_format_t fmt,
                                      int cu_count, tile_gemm_plan_t* out);
+
+/* The plan of tile_gemm_run_fp8 (E = 0) or of tile_gemm_run_fp8_experts (E
+ * experts; tiles is then the most there can be) for a shape. config counts the
+ * compiled tiles of these products, k_split the waves of a workgroup that share
+ * each stage of K. */
+tile_gemm_status_t tile_gemm_plan_fp8(int64_t M, int64_t N, int64_t K, int64_t E,
+                                      tile_gemm_dtype_t dtype, int cu_count, tile_gemm_plan_t* out);
 
 /*
  * Tile number `wg` (0 <= wg < plan->tiles) under `plan`: rows [m0, m0 + rows)

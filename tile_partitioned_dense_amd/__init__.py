@@ -21,6 +21,9 @@ __all__ = ["tile_gemm_create", "tile_gemm_run", "tile_gemm_run_debug", "tile_gem
            "tile_gemm_check_glu_backward", "Gate", "tile_gemm_run_xent", "tile_gemm_xent_workspace",
            "tile_gemm_check_xent", "tile_gemm_run_xent_backward", "tile_gemm_xent_backward_workspace",
            "tile_gemm_check_xent_backward", "XentOptions", "IndexType",
+           "tile_gemm_run_fp8", "tile_gemm_run_fp8_experts", "tile_gemm_run_quantize", "tile_gemm_run_route",
+           "tile_gemm_run_route_backward", "tile_gemm_run_place", "tile_gemm_place_workspace",
+           "tile_gemm_run_combine", "tile_gemm_plan_fp8", "Quant", "Score", "Fp8Strides", "RouteOptions",
            "TrainProduct", "tile_gemm_plan_train",
            "tile_gemm_status_str", "tile_gemm_check_args", "tile_gemm_plan",
            "tile_gemm_tile_of", "TileGemm", "TileGemmError", "Status", "Dtype",

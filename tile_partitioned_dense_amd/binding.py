@@ -65,6 +65,19 @@ class IndexType(enum.IntEnum):
     I64 = 1
 
 
+class Quant(enum.IntEnum):
+    """What shares a scale (tile_gemm_quant_t)."""
+    ROWS = 0
+    GATED_ROWS = 1
+    BLOCKS = 2
+
+
+class Score(enum.IntEnum):
+    """A router's scores (tile_gemm_score_t)."""
+    SOFTMAX = 0
+    SIGMOID = 1
+
+
 DEBUG_COUNT_WRITES = 1
 DEBUG_COLLIDE = 2
 
@@ -120,6 +133,19 @@ class XentOptions(ctypes.Structure):
     """Options of the cross entropy (tile_gemm_xent_t)."""
     _fields_ = [("ignore_index", ctypes.c_int64), ("label_smoothing", ctypes.c_float),
                 ("z_loss", ctypes.c_float), ("piece", ctypes.c_int64), ("target_type", ctypes.c_int32)]
+
+
+class Fp8Strides(ctypes.Structure):
+    """Strides of the E4M3 products (tile_gemm_fp8_strides_t)."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("a_stride", "b_stride", "c_stride", "a_scale_stride",
+                                              "b_scale_stride", "b_expert_stride", "b_scale_expert_stride")]
+
+
+class RouteOptions(ctypes.Structure):
+    """Options of the routing to experts (tile_gemm_route_t)."""
+    _fields_ = [("score", ctypes.c_int32), ("logits_type", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class TileGemmError(RuntimeError):
@@ -200,6 +226,28 @@ def load_library():
                  "run_xent", "check_xent", "xent_workspace", "run_xent_backward",
                  "check_xent_backward", "xent_backward_workspace"):
         getattr(lib, "tile_gemm_" + name).restype = i32
+    PF, PR = P(Fp8Strides), P(RouteOptions)
+    lib.tile_gemm_check_fp8.argtypes = [vp, vp, vp, i64, i64, i64, PF, vp, vp, i32, vp, i32]
+    lib.tile_gemm_run_fp8.argtypes = [vp, *lib.tile_gemm_check_fp8.argtypes, vp]
+    lib.tile_gemm_check_fp8_experts.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp, PF, vp, vp, i32]
+    lib.tile_gemm_run_fp8_experts.argtypes = [vp, *lib.tile_gemm_check_fp8_experts.argtypes, vp]
+    lib.tile_gemm_check_quantize.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i32, i32, vp, i64]
+    lib.tile_gemm_run_quantize.argtypes = [vp, *lib.tile_gemm_check_quantize.argtypes, vp]
+    lib.tile_gemm_check_route.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, PR]
+    lib.tile_gemm_run_route.argtypes = [vp, *lib.tile_gemm_check_route.argtypes, vp]
+    lib.tile_gemm_check_route_backward.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, PR]
+    lib.tile_gemm_run_route_backward.argtypes = [vp, *lib.tile_gemm_check_route_backward.argtypes, vp]
+    lib.tile_gemm_check_place.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, vp, i64]
+    lib.tile_gemm_run_place.argtypes = [vp, *lib.tile_gemm_check_place.argtypes, vp]
+    lib.tile_gemm_place_workspace.argtypes = [i64, i64, i64, P(i64)]
+    lib.tile_gemm_check_combine.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i32]
+    lib.tile_gemm_run_combine.argtypes = [vp, *lib.tile_gemm_check_combine.argtypes, vp]
+    lib.tile_gemm_plan_fp8.argtypes = [i64, i64, i64, i64, i32, i32, P(Plan)]
+    for name in ("fp8", "fp8_experts", "quantize", "route", "route_backward", "place", "combine"):
+        getattr(lib, "tile_gemm_run_" + name).restype = i32
+        getattr(lib, "tile_gemm_check_" + name).restype = i32
+    lib.tile_gemm_place_workspace.restype = i32
+    lib.tile_gemm_plan_fp8.restype = i32
     lib.tile_gemm_tile_of.argtypes = [P(Plan), i64, i64, i64, P(i64), P(i64), P(i64), P(i64)]
     lib.tile_gemm_tile_of.restype = i32
     _lib = lib
@@ -743,6 +791,281 @@ def tile_gemm_check_xent_backward(A, B, target, lse, dloss, dA, dB, M, N, K, str
         _ref(_strides(grad_strides)), _ref(options), workspace, int(workspace_bytes)))
 
 
+# ---------------------------- E4M3 products with block scales, routing to experts
+
+def _e4m3(name, t, dims):
+    """Checks a tensor of E4M3 codes (float8_e4m3fn, or their bytes as uint8)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not torch.float8_e4m3fn and t.dtype is not torch.uint8:
+        raise TypeError(f"{name} must be float8_e4m3fn (or uint8 codes), got {t.dtype}")
+    s = t.shape
+    if len(s) != dims or (t.stride(-1) != 1 and s[-1] > 1):
+        raise ValueError(f"{name} must have {dims} dimensions, the last of stride 1; got shape {tuple(s)} "
+                         f"strides {tuple(t.stride())}")
+    return s
+
+
+def _row_scales(name, t, M, K):
+    """Checks the scales of M rows, (M, blocks of K) with rows next to each
+    other; the stride between blocks."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be a float32 tensor")
+    kb = (K + 127) // 128
+    s = t.shape
+    if len(s) != 2 or s[0] != M or s[1] != kb or (M > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must have shape ({M}, {kb}) and a row stride of 1, got shape {tuple(s)} strides "
+                         f"{tuple(t.stride())}")
+    return t.stride(1) if kb > 1 else max(M, 1)
+
+
+def _block_scales(name, t, lead, rows, K):
+    """Checks the scales of blocks of 128 x 128, (*lead, blocks of rows, blocks of K)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be a float32 tensor")
+    want = (*lead, (rows + 127) // 128, (K + 127) // 128)
+    if tuple(t.shape) != want or (want[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have shape {want} and a last stride of 1, got shape {tuple(t.shape)} strides "
+                         f"{tuple(t.stride())}")
+    return t.stride(-2) if want[-2] > 1 else want[-1]
+
+
+def _rows_apart(t, least):
+    """The row stride; of a single row, whose stride is any, the least."""
+    return t.stride(-2) if t.shape[-2] > 1 else least
+
+
+def _fp8_c(C, M, N):
+    if not _is_tensor(C) or tuple(C.shape) != (M, N):
+        raise ValueError(f"C must be a tensor of shape {(M, N)}")
+    if N > 1 and C.stride(1) != 1:
+        raise ValueError(f"C must have a column stride of 1, got {tuple(C.stride())}")
+    return _c_dtype(C), _rows_apart(C, (N + 7) // 8 * 8)
+
+
+def tile_gemm_run_fp8(h, A, Bt, C, a_scale, b_scale, bias=None, act=Act.NONE, stream=None, check: bool = True):
+    """Enqueue C := act((a_scale * A) . (b_scale * Bt)^T + bias) with E4M3 A
+    (M x K) and Bt (N x K; float8_e4m3fn or uint8 codes) and float32 scales:
+    a_scale (M, ceil(K / 128)) with rows next to each other (stride(0) == 1),
+    b_scale (ceil(N / 128), ceil(K / 128)), one for each 128 x 128 block."""
+    M, K = _e4m3("A", A, 2)
+    N, K2 = _e4m3("Bt", Bt, 2)
+    if K2 != K:
+        raise ValueError(f"shapes do not chain: A{tuple(A.shape)} Bt{tuple(Bt.shape)}")
+    dt, ldc = _fp8_c(C, M, N)
+    s = Fp8Strides(_rows_apart(A, K), _rows_apart(Bt, K), ldc, _row_scales("a_scale", a_scale, M, K),
+                   _block_scales("b_scale", b_scale, (), N, K), 0, 0)
+    _check_bias(bias, N)
+    dev = _current_device(("A", "Bt", "C", "a_scale", "b_scale", "bias"),
+                          (A, Bt, C, a_scale, b_scale, bias if _is_tensor(bias) else None))
+    raw, _ = _launch_stream(stream, dev)
+    st = load_library().tile_gemm_run_fp8(h, A.data_ptr(), Bt.data_ptr(), C.data_ptr(), M, N, K, ctypes.byref(s),
+                                          a_scale.data_ptr(), b_scale.data_ptr(), dt,
+                                          bias.data_ptr() if _is_tensor(bias) else bias, act, raw)
+    return _result(st, check)
+
+
+def tile_gemm_run_fp8_experts(h, A, Bt, C, a_scale, b_scale, offsets, stream=None, check: bool = True):
+    """Enqueue the experts' products: rows [offsets[e], offsets[e + 1]) of C are
+    those rows of A times expert e's matrix. Bt (E, N, K), b_scale
+    (E, ceil(N / 128), ceil(K / 128)), offsets E + 1 int32 values; A and a_scale
+    as for tile_gemm_run_fp8."""
+    import torch
+    M, K = _e4m3("A", A, 2)
+    E, N, K2 = _e4m3("Bt", Bt, 3)
+    if K2 != K:
+        raise ValueError(f"shapes do not chain: A{tuple(A.shape)} Bt{tuple(Bt.shape)}")
+    dt, ldc = _fp8_c(C, M, N)
+    one = N * K
+    s = Fp8Strides(_rows_apart(A, K), _rows_apart(Bt, K), ldc, _row_scales("a_scale", a_scale, M, K),
+                   _block_scales("b_scale", b_scale, (E,), N, K), Bt.stride(0) if E > 1 else one,
+                   b_scale.stride(0) if E > 1 else 0)
+    _vector("offsets", offsets, E + 1, (torch.int32,))
+    dev = _current_device(("A", "Bt", "C", "a_scale", "b_scale", "offsets"), (A, Bt, C, a_scale, b_scale, offsets))
+    raw, _ = _launch_stream(stream, dev)
+    st = load_library().tile_gemm_run_fp8_experts(h, A.data_ptr(), Bt.data_ptr(), C.data_ptr(), M, N, K, E,
+                                                  offsets.data_ptr(), ctypes.byref(s), a_scale.data_ptr(),
+                                                  b_scale.data_ptr(), dt, raw)
+    return _result(st, check)
+
+
+def tile_gemm_run_quantize(h, X, Q, scale, form=Quant.ROWS, gate=None, rows=None, stream=None, check: bool = True):
+    """Enqueue bf16 X to E4M3 codes Q (M x K, float8_e4m3fn or uint8) and float32
+    scales, as the E4M3 products take them. form=Quant.ROWS: scale (M,
+    ceil(K / 128)) with rows next to each other; with `gate`, Q is made of
+    act(first half of X's columns) * (second half). form=Quant.BLOCKS: scale
+    (ceil(M / 128), ceil(K / 128)). `rows`: M int32 row numbers of X."""
+    import torch
+    M, K = _e4m3("Q", Q, 2)
+    if gate is not None:
+        if form == Quant.BLOCKS:
+            raise ValueError("gate: not with blocks of 128 x 128")
+        form = Quant.GATED_ROWS
+    elif form == Quant.GATED_ROWS:
+        raise ValueError("form=Quant.GATED_ROWS needs a gate")
+    x_rows = _matrix("X", X, M if rows is None else None, K if gate is None else 2 * K)[0]
+    if X.shape[1] > 1 and X.stride(1) != 1:
+        raise ValueError(f"X must have a column stride of 1, got {tuple(X.stride())}")
+    if form == Quant.BLOCKS:
+        lds = _block_scales("scale", scale, (), M, K)
+    else:
+        lds = _row_scales("scale", scale, M, K)
+    if rows is not None:
+        _vector("rows", rows, M, (torch.int32,))
+    dev = _current_device(("X", "Q", "scale", "rows"), (X, Q, scale, rows))
+    raw, _ = _launch_stream(stream, dev)
+    st = load_library().tile_gemm_run_quantize(h, X.data_ptr(), Q.data_ptr(), scale.data_ptr(), M, K,
+                                               _rows_apart(X, X.shape[1]), _rows_apart(Q, K), lds, form,
+                                               0 if gate is None else gate,
+                                               None if rows is None else rows.data_ptr(), x_rows, raw)
+    return _result(st, check)
+
+
+def _logits(name, t, T, E):
+    """Checks a router's logits; their type and the stride between tokens."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not torch.float32 and t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    s = t.shape
+    if len(s) != 2 or (T is not None and (s[0] != T or s[1] != E)) or (s[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must have shape ({'any' if T is None else T}, {'any' if E is None else E}) and a "
+                         f"column stride of 1, got shape {tuple(s)} strides {tuple(t.stride())}")
+    return t.dtype is torch.bfloat16, _rows_apart(t, s[1])
+
+
+def _per_place(name, t, T, k, dtype):
+    """Checks a contiguous (T, k) tensor."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    s = t.shape
+    if len(s) != 2 or (T is not None and s[0] != T) or (k is not None and s[1] != k) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape ({'any' if T is None else T}, "
+                         f"{'any' if k is None else k}); got shape {tuple(s)} strides {tuple(t.stride())}")
+    return s
+
+
+def tile_gemm_run_route(h, logits, ids, weights, score=Score.SOFTMAX, bias=None, groups=1, top_groups=1, group_top=2,
+                        renormalize=True, scale=1.0, stream=None, check: bool = True):
+    """Enqueue the routing of T tokens: ids (T, k) int32, the k experts of each,
+    and weights (T, k) float32, from logits (T, E) float32 or bfloat16. `bias`
+    (E float32 values) is added to the scores for the choice only; with groups
+    only experts of the top_groups best of `groups` runs of experts are chosen."""
+    import torch
+    T, k = _per_place("ids", ids, None, None, torch.int32)
+    bf16, ld = _logits("logits", logits, None, None)
+    if logits.shape[0] != T:
+        raise ValueError(f"logits{tuple(logits.shape)} and ids{tuple(ids.shape)} are of different tokens")
+    E = logits.shape[1]
+    _per_place("weights", weights, T, k, torch.float32)
+    if bias is not None:
+        _vector("bias", bias, E, (torch.float32,))
+    dev = _current_device(("logits", "ids", "weights", "bias"), (logits, ids, weights, bias))
+    raw, _ = _launch_stream(stream, dev)
+    o = RouteOptions(score, bf16, groups, top_groups, group_top, renormalize, scale)
+    st = load_library().tile_gemm_run_route(h, logits.data_ptr(), None if bias is None else bias.data_ptr(),
+                                            ids.data_ptr(), weights.data_ptr(), T, E, k, ld, ctypes.byref(o), raw)
+    return _result(st, check)
+
+
+def tile_gemm_run_route_backward(h, logits, ids, dweights, dlogits, score=Score.SOFTMAX, renormalize=True, scale=1.0,
+                                 stream=None, check: bool = True):
+    """Enqueue the gradient of tile_gemm_run_route's weights: dlogits (T, E, of
+    the logits' type) from dweights (T, k) float32 and the ids chosen."""
+    import torch
+    T, k = _per_place("ids", ids, None, None, torch.int32)
+    bf16, ld = _logits("logits", logits, None, None)
+    if logits.shape[0] != T:
+        raise ValueError(f"logits{tuple(logits.shape)} and ids{tuple(ids.shape)} are of different tokens")
+    E = logits.shape[1]
+    dbf16, ldd = _logits("dlogits", dlogits, T, E)
+    if dbf16 != bf16:
+        raise TypeError(f"dlogits must be of the logits' type {logits.dtype}, got {dlogits.dtype}")
+    _per_place("dweights", dweights, T, k, torch.float32)
+    dev = _current_device(("logits", "ids", "dweights", "dlogits"), (logits, ids, dweights, dlogits))
+    raw, _ = _launch_stream(stream, dev)
+    o = RouteOptions(score, bf16, 1, 1, 1, renormalize, scale)
+    st = load_library().tile_gemm_run_route_backward(h, logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(),
+                                                     dlogits.data_ptr(), T, E, k, ld, ldd, ctypes.byref(o), raw)
+    return _result(st, check)
+
+
+def tile_gemm_place_workspace(T, k, E) -> int:
+    """Workspace bytes of tile_gemm_run_place."""
+    n = ctypes.c_int64()
+    _raise_if(load_library().tile_gemm_place_workspace(T, k, E, ctypes.byref(n)))
+    return n.value
+
+
+def tile_gemm_run_place(h, ids, offsets, rows=None, places=None, first=0, workspace=None, stream=None,
+                        check: bool = True):
+    """Enqueue the order of the tokens by expert: offsets (E + 1 int32 values,
+    E experts from number `first` on), rows (T k) and places (T, k), either of
+    which may be left out, from ids (T, k) int32. Without `workspace` one is
+    allocated for the call where it needs one."""
+    import torch
+    T, k = _per_place("ids", ids, None, None, torch.int32)
+    if not _is_tensor(offsets) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be a vector of at least 2 values")
+    E = offsets.shape[0] - 1
+    _vector("offsets", offsets, E + 1, (torch.int32,))
+    if rows is not None:
+        _vector("rows", rows, T * k, (torch.int32,))
+    if places is not None:
+        _per_place("places", places, T, k, torch.int32)
+    dev = _current_device(("ids", "offsets", "rows", "places", "workspace"), (ids, offsets, rows, places, workspace))
+    raw, other = _launch_stream(stream, dev)
+    lib = load_library()
+    if workspace is None:
+        n = ctypes.c_int64()
+        _raise_if(lib.tile_gemm_place_workspace(T, k, E, ctypes.byref(n)))
+        nbytes = n.value
+        if nbytes:
+            workspace = _own_workspace(nbytes, ids, dev, other)
+    else:
+        nbytes = _workspace_bytes(workspace)
+    st = lib.tile_gemm_run_place(h, ids.data_ptr(), T, k, first, E, offsets.data_ptr(),
+                                 None if rows is None else rows.data_ptr(),
+                                 None if places is None else places.data_ptr(),
+                                 None if workspace is None else workspace.data_ptr(), nbytes, raw)
+    return _result(st, check)
+
+
+def tile_gemm_run_combine(h, Z, places, weights, Y, stream=None, check: bool = True):
+    """Enqueue Y[t] := sum_j weights[t, j] Z[places[t, j]] (Z bf16, Y bf16 or
+    float32; places (T, k) int32, those outside Z's rows left out; weights
+    (T, k) float32 or None for ones)."""
+    import torch
+    T, k = _per_place("places", places, None, None, torch.int32)
+    z_rows, N = _matrix("Z", Z, None, None)
+    if N > 1 and Z.stride(1) != 1:
+        raise ValueError(f"Z must have a column stride of 1, got {tuple(Z.stride())}")
+    if not _is_tensor(Y) or tuple(Y.shape) != (T, N) or (N > 1 and Y.stride(1) != 1):
+        raise ValueError(f"Y must be a tensor of shape {(T, N)} with a column stride of 1")
+    dt = _c_dtype(Y)
+    if weights is not None:
+        _per_place("weights", weights, T, k, torch.float32)
+    dev = _current_device(("Z", "places", "weights", "Y"), (Z, places, weights, Y))
+    raw, _ = _launch_stream(stream, dev)
+    least = (N + 7) // 8 * 8
+    st = load_library().tile_gemm_run_combine(h, Z.data_ptr(), places.data_ptr(),
+                                              None if weights is None else weights.data_ptr(), Y.data_ptr(), T, N, k,
+                                              z_rows, _rows_apart(Z, least), _rows_apart(Y, least), dt, raw)
+    return _result(st, check)
+
+
+def tile_gemm_plan_fp8(M, N, K, experts=0, dtype=Dtype.BF16_TO_BF16, cu_count=256) -> Plan:
+    p = Plan()
+    _raise_if(load_library().tile_gemm_plan_fp8(int(M), int(N), int(K), int(experts), int(dtype), int(cu_count),
+                                                ctypes.byref(p)))
+    return p
+
+
 def tile_gemm_check_mx(A, B, C, M, N, K, strides, a_scale, b_scale, scale_stride, dtype,
                        bias=None, act=Act.NONE, fmt=MX_E4M3) -> Status:
     """Host-only checks of tile_gemm_run_mx's arguments (pointers are integers)."""
@@ -834,6 +1157,41 @@ class TileGemm:
         return tile_gemm_run_xent_backward(self.handle, A, B, target, lse, dloss, dA=dA, dB=dB,
                                            ignore_index=ignore_index, label_smoothing=label_smoothing,
                                            z_loss=z_loss, piece=piece, workspace=workspace, stream=stream)
+
+    def fp8(self, A, Bt, C, a_scale, b_scale, bias=None, act=None, stream=None):
+        """E4M3 product with block scales (tile_gemm_run_fp8) into C."""
+        return tile_gemm_run_fp8(self.handle, A, Bt, C, a_scale, b_scale, bias=bias,
+                                 act=Act.NONE if act is None else act, stream=stream)
+
+    def fp8_experts(self, A, Bt, C, a_scale, b_scale, offsets, stream=None):
+        """The same over rows sorted by expert (tile_gemm_run_fp8_experts)."""
+        return tile_gemm_run_fp8_experts(self.handle, A, Bt, C, a_scale, b_scale, offsets, stream=stream)
+
+    def quantize(self, X, Q, scale, form=Quant.ROWS, gate=None, rows=None, stream=None):
+        """bf16 to E4M3 and scales (tile_gemm_run_quantize)."""
+        return tile_gemm_run_quantize(self.handle, X, Q, scale, form=form, gate=gate, rows=rows, stream=stream)
+
+    def route(self, logits, ids, weights, score=Score.SOFTMAX, bias=None, groups=1, top_groups=1, group_top=2,
+              renormalize=True, scale=1.0, stream=None):
+        """Experts of each token and their weights (tile_gemm_run_route)."""
+        return tile_gemm_run_route(self.handle, logits, ids, weights, score=score, bias=bias, groups=groups,
+                                   top_groups=top_groups, group_top=group_top, renormalize=renormalize,
+                                   scale=scale, stream=stream)
+
+    def route_backward(self, logits, ids, dweights, dlogits, score=Score.SOFTMAX, renormalize=True, scale=1.0,
+                       stream=None):
+        """Gradient of the routing weights (tile_gemm_run_route_backward)."""
+        return tile_gemm_run_route_backward(self.handle, logits, ids, dweights, dlogits, score=score,
+                                            renormalize=renormalize, scale=scale, stream=stream)
+
+    def place(self, ids, offsets, rows=None, places=None, first=0, workspace=None, stream=None):
+        """The tokens' order by expert (tile_gemm_run_place)."""
+        return tile_gemm_run_place(self.handle, ids, offsets, rows=rows, places=places, first=first,
+                                   workspace=workspace, stream=stream)
+
+    def combine(self, Z, places, weights, Y, stream=None):
+        """Weighted sums of the experts' rows (tile_gemm_run_combine)."""
+        return tile_gemm_run_combine(self.handle, Z, places, weights, Y, stream=stream)
 
     def close(self):
         if self.handle is not None:

@@ -29,6 +29,7 @@ ARCH = "gfx950"
 N_TILE_CONFIGS = 29
 N_SKINNY_CONFIGS = 6
 N_MX_CONFIGS = 8
+N_BLOCK_CONFIGS = 5
 N_TRAIN_KERNELS = 114  # kernels_train.hip: products with the stores of train_epilogue.hpp
 
 COMMON_FLAGS = [
@@ -54,6 +55,11 @@ def _units():
     for i in range(N_TRAIN_KERNELS):
         units.append((f"kernels_train_{i}", os.path.join(CSRC, "kernels_train.hip"),
                       [f"-DTG_TRAIN_KERNEL={i}"]))
+    for i in range(N_BLOCK_CONFIGS):
+        units.append((f"kernels_block_{i}", os.path.join(CSRC, "kernels_block.hip"),
+                      [f"-DTG_BLOCK_CONFIG={i}"]))
+    for name in ("kernels_quant", "kernels_route"):
+        units.append((name, os.path.join(CSRC, name + ".hip"), []))
     units.append(("kernels_train_rows", os.path.join(CSRC, "kernels_train_rows.hip"), []))
     return units
 
