@@ -56,6 +56,94 @@ __device__ __forceinline__ i32x4 panel_rsrc(const void* base, int64_t bytes) {
   return make_rsrc(base, bytes > 0x7fffffffll ? 0x7fffffffll : bytes);
 }
 
+// --- owned tiles
+struct BlockTile {
+  int m0, n0, m_end;  // first row and column, end of the rows it may store
+  const uint8_t* B;
+  const float* sB;
+};
+
+__device__ __forceinline__ int32_t lds_load_i32(uint32_t addr) {
+  return *(const __attribute__((address_space(3))) int32_t*)(uintptr_t)addr;
+}
+__device__ __forceinline__ void lds_store_i32(uint32_t addr, int32_t v) {
+  *(__attribute__((address_space(3))) int32_t*)(uintptr_t)addr = v;
+}
+__device__ __forceinline__ float lds_load_f32(uint32_t addr) {
+  return *(const __attribute__((address_space(3))) float*)(uintptr_t)addr;
+}
+
+// Experts: the row tiles before each expert into LDS at pre0 (groups + 1
+// values); the tiles there are.
+template <int BM>
+__device__ __forceinline__ int expert_tiles(const BlockArgs& p, uint32_t pre0, int wave, int lane) {
+  if (wave == 0) {
+    int base = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 64) {
+      const int g = g0 + lane;
+      int t = 0;
+      if (g < p.groups) {
+        const int lo = min(max(p.offsets[g], 0), p.M);
+        const int hi = min(max(p.offsets[g + 1], lo), p.M);
+        t = (hi - lo + BM - 1) / BM;
+      }
+      int incl = t;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int up = __shfl_up(incl, d, 64);
+        if (lane >= d) incl += up;
+      }
+      if (g < p.groups) lds_store_i32(pre0 + 4u * g, base + incl - t);
+      base += __shfl(incl, 63, 64);
+    }
+    if (lane == 0) lds_store_i32(pre0 + 4u * p.groups, base);
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(lds_load_i32(pre0 + 4u * p.groups)) * p.map.tiles_n;
+}
+
+// The tile of index wg: of the output, or (experts) of one expert's rows, 8 row
+// tiles of it at a time before the next columns; consecutive tiles on one XCD.
+template <int BM, int BN, bool EXPERTS>
+__device__ __forceinline__ BlockTile block_tile(const BlockArgs& p, uint32_t pre0, int wg, int n_tiles) {
+  BlockTile at;
+  at.B = p.B;
+  at.sB = p.sB;
+  if constexpr (EXPERTS) {
+    const int q = n_tiles / kXcds, r = n_tiles % kXcds, x = wg % kXcds;
+    const int t = x * q + min(x, r) + wg / kXcds;
+    const int row_tile = t / p.map.tiles_n;
+    // the last expert whose first row tile is not past this one
+    int lo = 0, hi = p.groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (lds_load_i32(pre0 + 4u * mid) <= row_tile) lo = mid;
+      else hi = mid - 1;
+    }
+    const int e = __builtin_amdgcn_readfirstlane(lo);
+    const int first = __builtin_amdgcn_readfirstlane(lds_load_i32(pre0 + 4u * e));
+    const int next = __builtin_amdgcn_readfirstlane(lds_load_i32(pre0 + 4u * e + 4u));
+    const int e_lo = min(max(p.offsets[e], 0), p.M);
+    at.m_end = min(max(p.offsets[e + 1], e_lo), p.M);
+    const int local = t - first * p.map.tiles_n;
+    const int per = 8 * p.map.tiles_n;
+    const int grp = local / per;
+    const int gsz = min(8, next - first - 8 * grp);
+    const int in = local - grp * per;
+    at.m0 = e_lo + (8 * grp + in % gsz) * BM;
+    at.n0 = (in / gsz) * BN;
+    at.B += (int64_t)e * p.eb;
+    at.sB += (int64_t)e * p.esb;
+  } else {
+    int32_t tm, tn;
+    tile_of(p.map, wg, tm, tn);
+    at.m0 = tm * BM;
+    at.n0 = tn * BN;
+    at.m_end = p.M;
+  }
+  return at;
+}
+
 template <int BM, int BN, int WM, int WN, int KS, int SB, int NST, bool EXPERTS, bool OUT_BF16>
 __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockArgs p) {
   constexpr int NW = WM * WN * KS;
@@ -119,81 +207,13 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
   const uint32_t scA = lds0 + A_BYTES + B_BYTES + (uint32_t)((wm * WTM + l16) * 4);
   const uint32_t scB = lds0 + A_BYTES + B_BYTES + (uint32_t)((S_DMA - 1) * 256);
 
-  // experts: row tiles before each expert, in LDS
   const uint32_t pre0 = lds0 + RING;
-  int n_tiles;
-  if constexpr (EXPERTS) {
-    if (wave == 0) {
-      int base = 0;
-      for (int g0 = 0; g0 < p.groups; g0 += 64) {
-        const int g = g0 + lane;
-        int t = 0;
-        if (g < p.groups) {
-          const int lo = min(max(p.offsets[g], 0), p.M);
-          const int hi = min(max(p.offsets[g + 1], lo), p.M);
-          t = (hi - lo + BM - 1) / BM;
-        }
-        int incl = t;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-          const int up = __shfl_up(incl, d, 64);
-          if (lane >= d) incl += up;
-        }
-        if (g < p.groups)
-          *(__attribute__((address_space(3))) int32_t*)(uintptr_t)(pre0 + 4u * g) = base + incl - t;
-        base += __shfl(incl, 63, 64);
-      }
-      if (lane == 0) *(__attribute__((address_space(3))) int32_t*)(uintptr_t)(pre0 + 4u * p.groups) = base;
-    }
-    __syncthreads();
-    n_tiles = *(const __attribute__((address_space(3))) int32_t*)(uintptr_t)(pre0 + 4u * p.groups) * p.map.tiles_n;
-    n_tiles = __builtin_amdgcn_readfirstlane(n_tiles);
-  } else {
-    n_tiles = p.map.tiles_m * p.map.tiles_n;
-  }
-
+  const int n_tiles = EXPERTS ? expert_tiles<BM>(p, pre0, wave, lane) : p.map.tiles_m * p.map.tiles_n;
   for (int wg = blockIdx.x; wg < n_tiles; wg += gridDim.x) {
-    int m0, n0, m_end;
-    const uint8_t* Bp = p.B;
-    const float* sBp = p.sB;
-    if constexpr (EXPERTS) {
-      const int q = n_tiles / kXcds, r = n_tiles % kXcds;
-      const int x = wg % kXcds;
-      const int t = x * q + min(x, r) + wg / kXcds;
-      const int row_tile = t / p.map.tiles_n;
-      // the last expert whose first row tile is not past this one
-      int lo = 0, hi = p.groups - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        const int first = *(const __attribute__((address_space(3))) int32_t*)(uintptr_t)(pre0 + 4u * mid);
-        if (first <= row_tile) lo = mid;
-        else hi = mid - 1;
-      }
-      const int e = __builtin_amdgcn_readfirstlane(lo);
-      const int first = __builtin_amdgcn_readfirstlane(
-          *(const __attribute__((address_space(3))) int32_t*)(uintptr_t)(pre0 + 4u * e));
-      const int next = __builtin_amdgcn_readfirstlane(
-          *(const __attribute__((address_space(3))) int32_t*)(uintptr_t)(pre0 + 4u * e + 4u));
-      const int e_lo = min(max(p.offsets[e], 0), p.M);
-      m_end = min(max(p.offsets[e + 1], e_lo), p.M);
-      // down the expert's rows (8 at a time) before the next columns
-      const int local = t - first * p.map.tiles_n;
-      const int rows = next - first;
-      const int per = 8 * p.map.tiles_n;
-      const int grp = local / per;
-      const int gsz = min(8, rows - 8 * grp);
-      const int in = local - grp * per;
-      m0 = e_lo + (8 * grp + in % gsz) * BM;
-      n0 = (in / gsz) * BN;
-      Bp += (int64_t)e * p.eb;
-      sBp += (int64_t)e * p.esb;
-    } else {
-      int32_t tm, tn;
-      tile_of(p.map, wg, tm, tn);
-      m0 = tm * BM;
-      n0 = tn * BN;
-      m_end = p.M;
-    }
+    const BlockTile at = block_tile<BM, BN, EXPERTS>(p, pre0, wg, n_tiles);
+    const int m0 = at.m0, n0 = at.n0, m_end = at.m_end;
+    const uint8_t* Bp = at.B;
+    const float* sBp = at.sB;
     const uint8_t* a_panel = p.A + (int64_t)m0 * p.lda;
     const uint8_t* b_panel = Bp + (int64_t)n0 * p.ldb;
     const int64_t a_bytes = (int64_t)(p.M - 1 - m0) * p.lda + K;
@@ -241,9 +261,6 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
       const uint4 y = __builtin_bit_cast(uint4, lds_read16(b + (uint32_t)(((8 * kb + 4 + lg) ^ sw) << 4)));
       return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
     };
-    auto lds_f32 = [&](uint32_t a) {
-      return *(const __attribute__((address_space(3))) float*)(uintptr_t)a;
-    };
 
     floatx4 acc[FM][FN];
 #pragma unroll
@@ -266,7 +283,7 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
       static_for<0, KBS / KS>([&](auto q_c) {
         const int kb = ks + KS * decltype(q_c)::value;
         if (KBS == 1 || s * KBS + kb < nkb) {
-          const float sb = lds_f32(scB + so + (uint32_t)(8 * kb + (BN > kScaleBlock ? 4 * ((wn * WTN) / kScaleBlock) : 0)));
+          const float sb = lds_load_f32(scB + so + (uint32_t)(8 * kb + (BN > kScaleBlock ? 4 * ((wn * WTN) / kScaleBlock) : 0)));
           i32x8 bq[FN];
           bf16x32 bw[OUT_BF16 ? 1 : FN];
 #pragma unroll
@@ -276,7 +293,7 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
           }
           float sc[FM];
 #pragma unroll
-          for (int i = 0; i < FM; ++i) sc[i] = lds_f32(scA + so + (uint32_t)(kb * SROW * 4 + i * 64)) * sb;
+          for (int i = 0; i < FM; ++i) sc[i] = lds_load_f32(scA + so + (uint32_t)(kb * SROW * 4 + i * 64)) * sb;
 #pragma unroll
           for (int i = 0; i < FM; ++i) {
             const i32x8 a = frag(rowA + so, kb, i);

@@ -3,7 +3,7 @@
 // routing to experts (kernels_route.hip).
 #pragma once
 
-#include "block_kernel.hpp"
+#include "block_tile_kernel.hpp"
 #include "launch.hpp"
 
 namespace tg {

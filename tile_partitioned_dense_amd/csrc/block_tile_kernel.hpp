@@ -1,0 +1,232 @@
+// block_tile_kernel.hpp -- E4M3 products with block scales for outputs of many
+// rows and columns in bf16 (the operands, formula, scales and owned tiles of
+// block_kernel.hpp).
+#pragma once
+
+#include "block_kernel.hpp"
+
+namespace tg {
+
+template <int BM, int BN, int WM, int WN, bool EXPERTS>
+__global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p) {
+  constexpr int NW = WM * WN;
+  constexpr int WTM = BM / WM, WTN = BN / WN;
+  constexpr int FM = WTM / 16, FN = WTN / 16;
+  static_assert(FM % 2 == 0 && FM >= 4 && FN >= 3 && 128 % WTN == 0, "row parity; one block of B's rows a wave");
+  constexpr int RB = kScaleBlock;         // bytes of a row and stage
+  constexpr int A_BYTES = BM * RB, B_BYTES = BN * RB;
+  constexpr int A_DMA = A_BYTES / 1024, B_DMA = B_BYTES / 1024;
+  static_assert(A_DMA % NW == 0 && B_DMA % NW == 0 && BM % 64 == 0 && NW % 2 == 0, "loads split evenly over the waves");
+  constexpr int A_PER = A_DMA / NW, B_PER = B_DMA / NW;
+  constexpr int S_DMA = BM / 64 + 1;
+  static_assert(S_DMA <= NW, "a scale load each at most");
+  constexpr int STAGE = A_BYTES + B_BYTES + S_DMA * 256;
+  constexpr int RING = 2 * STAGE;
+  constexpr int LDS_EXTRA = EXPERTS ? (kBlockMaxGroups + 4) * 4 : 0;
+  static_assert(RING + LDS_EXTRA <= 160 * 1024, "LDS");
+  constexpr int NU = A_PER + B_PER + 1;   // a wave's loads of a stage
+  // MFMA n of a stage: row by row of blocks, the last two rows together, column
+  // by column
+  constexpr int PAIR = (FM - 2) * FN;
+  constexpr auto mfma_row = [](int n) { return n < PAIR ? n / FN : FM - 2 + (n - PAIR) % 2; };
+  constexpr auto mfma_col = [](int n) { return n < PAIR ? n % FN : (n - PAIR) / 2; };
+  // where load u goes out: MFMAs after the barrier
+  constexpr int LD = FM * FN / 2;
+  constexpr auto load_pos = [](int u) { return ((2 * u + 1) * LD) / (2 * NU); };
+  constexpr int NU1 = [] {  // loads before the end of the stage
+    int n = 0;
+    while (n < NU && ((2 * n + 1) * LD) / (2 * NU) < 2 * FN) ++n;
+    return n;
+  }();
+
+  __shared__ __attribute__((aligned(1024))) uint4 smem[(RING + LDS_EXTRA) / 16];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int l16 = lane & 15, lg = lane >> 4;
+  const int N = p.N, K = p.K;
+  const int nst = (K + RB - 1) / RB;
+
+  // load sources: instruction u = wave + NW t covers rows 8 u ..; lane l fills
+  // position l % 8 of row 8 u + l / 8, i.e. fetches chunk (l % 8) ^ ((row >> 1) & 7)
+  // (the same for all t: NW is even)
+  const int row0 = 8 * wave + (lane >> 3);
+  const int chunk = (lane & 7) ^ ((row0 >> 1) & 7);
+  const uint32_t voA = (uint32_t)(row0 * (int)p.lda + 16 * chunk), voB = (uint32_t)(row0 * (int)p.ldb + 16 * chunk);
+  const uint32_t stepA = (uint32_t)(8 * NW * (int)p.lda), stepB = (uint32_t)(8 * NW * (int)p.ldb);
+  const uint32_t ldsw = __builtin_amdgcn_readfirstlane(lds0 + 1024 * wave);
+  // fragment reads: row l16 of the wave's first block, chunks lg and 4 + lg
+  const int sw = (l16 >> 1) & 7;
+  const uint32_t ch0 = (uint32_t)((lg ^ sw) << 4), ch1 = (uint32_t)(((4 + lg) ^ sw) << 4);
+  uint32_t fA[2][2], fB[2][2];  // of buffer and chunk
+#pragma unroll
+  for (int st = 0; st < 2; ++st)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      fA[st][c] = lds0 + (uint32_t)(st * STAGE + (wm * WTM + l16) * RB) + (c ? ch1 : ch0);
+      fB[st][c] = lds0 + (uint32_t)(st * STAGE + A_BYTES + (wn * WTN + l16) * RB) + (c ? ch1 : ch0);
+      asm volatile("" : "+v"(fA[st][c]), "+v"(fB[st][c]));  // (blocks by immediate offsets from these)
+    }
+  const uint32_t scA = lds0 + A_BYTES + B_BYTES + (uint32_t)((wm * WTM + l16) * 4);
+  const uint32_t scB = lds0 + A_BYTES + B_BYTES + (uint32_t)((S_DMA - 1) * 256 + ((wn * WTN) / kScaleBlock) * 4);
+
+  const uint32_t pre0 = lds0 + RING;
+  const int n_tiles = EXPERTS ? expert_tiles<BM>(p, pre0, wave, lane) : p.map.tiles_m * p.map.tiles_n;
+  for (int wg = blockIdx.x; wg < n_tiles; wg += gridDim.x) {
+    const BlockTile at = block_tile<BM, BN, EXPERTS>(p, pre0, wg, n_tiles);
+    const int m0 = at.m0, n0 = at.n0;
+    const uint8_t* a_panel = p.A + (int64_t)m0 * p.lda;
+    const uint8_t* b_panel = at.B + (int64_t)n0 * p.ldb;
+    const int64_t a_bytes = (int64_t)(p.M - 1 - m0) * p.lda + K;
+    const int64_t b_bytes = (int64_t)(N - 1 - n0) * p.ldb + K;
+    // this wave's scales: 64 rows of A, or (one wave) the tile's blocks of B
+    // (lane i < BN / 128); the other waves repeat the last of these
+    const int su = wave < S_DMA ? wave : S_DMA - 1;
+    const bool sA_wave = su < S_DMA - 1;
+    const int nb0 = n0 / kScaleBlock;
+    const char* s_base = sA_wave ? reinterpret_cast<const char*>(p.sA + m0 + 64 * su)
+                                 : reinterpret_cast<const char*>(at.sB + (int64_t)nb0 * p.lsb);
+    const int64_t s_step = sA_wave ? p.lsa * 4 : 4;
+    const int64_t s_bytes = sA_wave ? ((int64_t)(nst - 1) * p.lsa + (p.M - m0 - 64 * su)) * 4
+                                    : ((int64_t)((N - 1) / kScaleBlock - nb0) * p.lsb + nst) * 4;
+    const uint32_t voS = sA_wave ? 4u * lane : lane < BN / kScaleBlock ? (uint32_t)(lane * (int)p.lsb) * 4u : kDmaPast;
+
+    // load n of stage s into buffer ST = s % 2: A's, B's, then the scales. Chunks
+    // past K are sent to an offset past their resource's end (2 GiB at most),
+    // where they arrive as zeros.
+    auto load = [&](auto st_c, int s, int n) {
+      constexpr uint32_t st = (uint32_t)(decltype(st_c)::value * STAGE);
+      const bool in = chunk * 16 < K - s * RB;
+      if (n < A_PER)
+        dma16(ldsw + st + 1024 * NW * n, panel_rsrc(a_panel + (int64_t)s * RB, a_bytes - (int64_t)s * RB),
+              (in ? voA : 0x80000000u) + n * stepA, 0u);
+      else if (n < A_PER + B_PER)
+        dma16(ldsw + st + A_BYTES + 1024 * NW * (n - A_PER),
+              panel_rsrc(b_panel + (int64_t)s * RB, b_bytes - (int64_t)s * RB),
+              (in ? voB : 0x80000000u) + (n - A_PER) * stepB, 0u);
+      else
+        dma4(lds0 + st + A_BYTES + B_BYTES + 256 * su, panel_rsrc(s_base + s * s_step, s < nst ? s_bytes - s * s_step : 0), voS, 0u);
+    };
+    auto frag = [&](const uint32_t (&f)[2][2], int st, int blk) -> i32x8 {
+      const uint4 x = __builtin_bit_cast(uint4, lds_read16(f[st][0] + (uint32_t)(blk * 16 * RB)));
+      const uint4 y = __builtin_bit_cast(uint4, lds_read16(f[st][1] + (uint32_t)(blk * 16 * RB)));
+      return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+    };
+
+    floatx4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        acc[i][j] = floatx4{};
+        asm volatile("" : "+v"(acc[i][j]));  // (not folded into a first stage of its own)
+      }
+
+    wait_vmcnt<0>();  // the previous tile's stores are not counted with this one's loads
+    static_for<0, NU>([&](auto u_c) { load(std::integral_constant<int, 0>{}, 0, decltype(u_c)::value); });
+    static_for<0, NU>([&](auto u_c) {
+      if constexpr (decltype(u_c)::value < NU1) load(std::integral_constant<int, 1>{}, 1, decltype(u_c)::value);
+    });
+    wait_vmcnt<NU1>();
+    block_barrier();
+    // B of the stage; A: rows r < FM - 1 alternate between two sets, which the
+    // stages take in turn, row FM - 1 has the third
+    i32x8 bq[FN], a[3];
+    floatx4 d[4];            // sums of the last MFMAs, scaled and added two later
+    float raw[2], sc[2], sb; // A's scales as read, and times B's, by the row's parity
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bq[j] = frag(fB, 0, j);
+    a[0] = frag(fA, 0, 0);
+    raw[0] = lds_load_f32(scA);
+    sb = lds_load_f32(scB);
+    sc[0] = sc[1] = raw[1] = 0.0f;
+    d[2] = d[3] = floatx4{};
+    auto add = [&](auto m_c) {
+      constexpr int m = decltype(m_c)::value, i = mfma_row(m), j = mfma_col(m);
+      asm volatile("" : "+v"(d[m % 4]));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(d[m % 4][e], sc[i & 1], acc[i][j][e]);
+      asm volatile("" : "+v"(acc[i][j]));
+    };
+
+    // One stage, in buffer ST. Its last phase and the next stage's first one
+    // load stage s + 2; one past the last arrives as zeros, without traffic.
+    auto step = [&](auto st_c, int s) {
+      constexpr int ST = decltype(st_c)::value;
+      static_for<0, FM * FN>([&](auto n_c) {
+        constexpr int n = decltype(n_c)::value;
+        constexpr int i = mfma_row(n), j = mfma_col(n);
+        constexpr int q = n - PAIR;       // MFMA of the last two rows
+        constexpr int slot = i == FM - 1 ? 2 : (i + ST) & 1;
+        if constexpr (q == 0) {
+          // stage s + 1 has landed, every wave has read this stage's last rows
+          wait_vmcnt<0>();
+          wait_lgkmcnt0();
+          block_barrier();
+        }
+        asm volatile("" : "+v"(a[slot]), "+v"(bq[j]));
+        d[n % 4] = mma_fp8(a[slot], bq[j]);
+        // reads: the next row of A and its scale; in the last two rows the next
+        // stage's first one, and its blocks of B as this stage's are done with
+        if constexpr (q < 0) {
+          if constexpr (j == 0) a[(i + 1 + ST) & 1] = frag(fA, ST, i + 1);
+          if constexpr (j == 0 && i == FM - 3) a[2] = frag(fA, ST, FM - 1);
+          if constexpr (j == 1) raw[(i + 1) & 1] = lds_load_f32(scA + (uint32_t)(ST * STAGE + (i + 1) * 64));
+          if constexpr (j == FN - 1 && i == FM - 3) raw[1] = lds_load_f32(scA + (uint32_t)(ST * STAGE + (FM - 1) * 64));
+        } else {
+          if constexpr (q == 0) a[ST ^ 1] = frag(fA, ST ^ 1, 0);
+          if constexpr (i == FM - 1) bq[j] = frag(fB, ST ^ 1, j);
+          if constexpr (q == 4) {
+            raw[0] = lds_load_f32(scA + (uint32_t)((ST ^ 1) * STAGE));
+            sb = lds_load_f32(scB + (uint32_t)((ST ^ 1) * STAGE));
+          }
+        }
+        // loads of stage s + 2 (from the barrier on) and of s + 1 (the rest)
+        static_for<0, NU>([&](auto u_c) {
+          constexpr int u = decltype(u_c)::value;
+          if constexpr (q >= 0 && load_pos(u) == q) load(std::integral_constant<int, ST>{}, s + 2, u);
+          if constexpr (q < 0 && load_pos(u) == FM * FN - PAIR + n) load(std::integral_constant<int, ST ^ 1>{}, s + 1, u);
+        });
+        // the scale of a row before its first sum is added; the sums of the MFMA
+        // two before this one
+        constexpr int m = (n + FM * FN - 2) % (FM * FN), mi = mfma_row(m);
+        if constexpr (mfma_col(m) == 0) sc[mi & 1] = raw[mi & 1] * sb;
+        add(std::integral_constant<int, m>{});
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    // (two at a time, so that the buffers are fixed; with an odd number the last
+    // one is of zeros: a way out in between kept a copy of the accumulators)
+    for (int s = 0; s < nst; s += 2) {
+      step(std::integral_constant<int, 0>{}, s);
+      step(std::integral_constant<int, 1>{}, s + 1);
+    }
+    add(std::integral_constant<int, FM * FN - 2>{});
+    add(std::integral_constant<int, FM * FN - 1>{});
+
+    // store: 16-row strips staged as fp32 in the free ring
+    wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    block_barrier();
+    {
+      constexpr int OPF = WTN * 4 + 16;
+      static_assert(NW * 16 * OPF <= RING, "a strip of every wave fits the ring");
+      const uint32_t stf = lds0 + (uint32_t)(wave * 16 * OPF);
+      const EpiOut eo{p.C, p.ldc, at.m_end, N, p.bias, p.act, nullptr, 0};
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) lds_store_f4(stf + (uint32_t)(l16 * OPF + (16 * j + 4 * lg) * 4), acc[i][j]);
+        wait_lgkmcnt0();
+        store_staged_fused<true, false>(stf, OPF, 16, WTN, m0 + wm * WTM + 16 * i, n0 + wn * WTN, lane, 64, eo);
+        wait_lgkmcnt0();
+      }
+    }
+    wait_lgkmcnt0();
+    block_barrier();
+  }
+}
+
+}  // namespace tg
