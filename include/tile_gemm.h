@@ -360,7 +360,7 @@ tile_gemm_status_t tile_gemm_run_xent_backward(tile_gemm_t h, const void* A, con
  * in a fixed order), each element written once: results are bit-identical from
  * run to run. A NaN or infinite scale reaches the rows (or columns) it scales.
  *
- * Limits: K a multiple of 16; M, N, K and the strides of A and B below 2^22; A
+ * Limits: K a multiple of 16; M, N, K and the strides of A, B and C below 2^22; A
  * and B 16-byte aligned with leading dimensions of whole 16 bytes, scales
  * 4-byte aligned. A, B and the scales may span 4 GiB or more. M = 0 or N = 0 is
  * a no-op; K = 0 stores act(bias). Errors and ownership as for

@@ -62,6 +62,7 @@ tile_gemm_status_t check_fp8(const void* A, const void* B, const void* C, int64_
   const int64_t kb = tg::ceil_div(K, tg::kScaleBlock), nb = tg::ceil_div(N, tg::kScaleBlock);
   TG_TRY(check_stride("a_stride", s->a_stride, K, kMax22, M));
   TG_TRY(check_stride("b_stride", s->b_stride, K, kMax22, N));
+  TG_TRY(check_stride("c_stride", s->c_stride, N, kMax22, M));
   TG_TRY(check_stride("a_scale_stride", s->a_scale_stride, M, kMaxDim, kb));
   TG_TRY(check_stride("b_scale_stride", s->b_scale_stride, kb, kMax22, nb));
   const int64_t esz = dtype == TILE_GEMM_BF16_TO_F32 ? 4 : 2;

@@ -7,6 +7,34 @@
 
 namespace tg {
 
+// The fused epilogue on the accumulators: column col + 16 j + e in acc[][j][e].
+template <int FM, int FN, int ACT>
+__device__ __forceinline__ void finish_act(floatx4 (&acc)[FM][FN], const BlockArgs& p, int col) {
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    floatx4 b = floatx4{};
+    if (p.bias) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = p.bias[min(col + 16 * j + e, p.N - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = act_fn<ACT>(acc[i][j][e] + b[e]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+template <int FM, int FN>
+__device__ __forceinline__ void finish(floatx4 (&acc)[FM][FN], const BlockArgs& p, int col) {
+  switch (p.act) {
+    case kActRelu: finish_act<FM, FN, kActRelu>(acc, p, col); break;
+    case kActSigmoid: finish_act<FM, FN, kActSigmoid>(acc, p, col); break;
+    case kActTanh: finish_act<FM, FN, kActTanh>(acc, p, col); break;
+    case kActSilu: finish_act<FM, FN, kActSilu>(acc, p, col); break;
+    default: finish_act<FM, FN, kActNone>(acc, p, col);
+  }
+}
+
 template <int BM, int BN, int WM, int WN, bool EXPERTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p) {
   constexpr int NW = WM * WN;
@@ -38,6 +66,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     while (n < NU && ((2 * n + 1) * LD) / (2 * NU) < 2 * FN) ++n;
     return n;
   }();
+
+  constexpr int STORES = FM * (FN / 2);   // of a tile, per wave
+  static_assert(FN % 2 == 0 && NU1 + STORES <= 63, "pairs of blocks; the counter");
 
   __shared__ __attribute__((aligned(1024))) uint4 smem[(RING + LDS_EXTRA) / 16];
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
@@ -74,46 +105,96 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
 
   const uint32_t pre0 = lds0 + RING;
   const int n_tiles = EXPERTS ? expert_tiles<BM>(p, pre0, wave, lane) : p.map.tiles_m * p.map.tiles_n;
-  for (int wg = blockIdx.x; wg < n_tiles; wg += gridDim.x) {
-    const BlockTile at = block_tile<BM, BN, EXPERTS>(p, pre0, wg, n_tiles);
-    const int m0 = at.m0, n0 = at.n0;
-    const uint8_t* a_panel = p.A + (int64_t)m0 * p.lda;
-    const uint8_t* b_panel = at.B + (int64_t)n0 * p.ldb;
-    const int64_t a_bytes = (int64_t)(p.M - 1 - m0) * p.lda + K;
-    const int64_t b_bytes = (int64_t)(N - 1 - n0) * p.ldb + K;
-    // this wave's scales: 64 rows of A, or (one wave) the tile's blocks of B
-    // (lane i < BN / 128); the other waves repeat the last of these
-    const int su = wave < S_DMA ? wave : S_DMA - 1;
-    const bool sA_wave = su < S_DMA - 1;
-    const int nb0 = n0 / kScaleBlock;
-    const char* s_base = sA_wave ? reinterpret_cast<const char*>(p.sA + m0 + 64 * su)
-                                 : reinterpret_cast<const char*>(at.sB + (int64_t)nb0 * p.lsb);
-    const int64_t s_step = sA_wave ? p.lsa * 4 : 4;
-    const int64_t s_bytes = sA_wave ? ((int64_t)(nst - 1) * p.lsa + (p.M - m0 - 64 * su)) * 4
-                                    : ((int64_t)((N - 1) / kScaleBlock - nb0) * p.lsb + nst) * 4;
-    const uint32_t voS = sA_wave ? 4u * lane : lane < BN / kScaleBlock ? (uint32_t)(lane * (int)p.lsb) * 4u : kDmaPast;
+  if ((int)blockIdx.x >= n_tiles) return;
 
-    // load n of stage s into buffer ST = s % 2: A's, B's, then the scales. Chunks
-    // past K are sent to an offset past their resource's end (2 GiB at most),
-    // where they arrive as zeros.
-    auto load = [&](auto st_c, int s, int n) {
-      constexpr uint32_t st = (uint32_t)(decltype(st_c)::value * STAGE);
-      const bool in = chunk * 16 < K - s * RB;
-      if (n < A_PER)
-        dma16(ldsw + st + 1024 * NW * n, panel_rsrc(a_panel + (int64_t)s * RB, a_bytes - (int64_t)s * RB),
-              (in ? voA : 0x80000000u) + n * stepA, 0u);
-      else if (n < A_PER + B_PER)
-        dma16(ldsw + st + A_BYTES + 1024 * NW * (n - A_PER),
-              panel_rsrc(b_panel + (int64_t)s * RB, b_bytes - (int64_t)s * RB),
-              (in ? voB : 0x80000000u) + (n - A_PER) * stepB, 0u);
-      else
-        dma4(lds0 + st + A_BYTES + B_BYTES + 256 * su, panel_rsrc(s_base + s * s_step, s < nst ? s_bytes - s * s_step : 0), voS, 0u);
-    };
-    auto frag = [&](const uint32_t (&f)[2][2], int st, int blk) -> i32x8 {
-      const uint4 x = __builtin_bit_cast(uint4, lds_read16(f[st][0] + (uint32_t)(blk * 16 * RB)));
-      const uint4 y = __builtin_bit_cast(uint4, lds_read16(f[st][1] + (uint32_t)(blk * 16 * RB)));
-      return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
-    };
+  // the tile whose loads are issued
+  int m0, n0, m_end;
+  const uint8_t *a_panel, *b_panel;
+  int64_t a_bytes, b_bytes;
+  // this wave's scales: 64 rows of A, or (one wave) the tile's blocks of B
+  // (lane i < BN / 128); the other waves repeat the last of these
+  const int su = wave < S_DMA ? wave : S_DMA - 1;
+  const bool sA_wave = su < S_DMA - 1;
+  const int64_t s_step = sA_wave ? p.lsa * 4 : 4;
+  const uint32_t voS = sA_wave ? 4u * lane : lane < BN / kScaleBlock ? (uint32_t)(lane * (int)p.lsb) * 4u : kDmaPast;
+  const char* s_base;
+  int64_t s_bytes;
+  auto take = [&](int wg) {
+    const BlockTile at = block_tile<BM, BN, EXPERTS>(p, pre0, wg, n_tiles);
+    m0 = at.m0;
+    n0 = at.n0;
+    m_end = at.m_end;
+    a_panel = p.A + (int64_t)m0 * p.lda;
+    b_panel = at.B + (int64_t)n0 * p.ldb;
+    a_bytes = (int64_t)(p.M - 1 - m0) * p.lda + K;
+    b_bytes = (int64_t)(N - 1 - n0) * p.ldb + K;
+    const int nb0 = n0 / kScaleBlock;
+    s_base = sA_wave ? reinterpret_cast<const char*>(p.sA + m0 + 64 * su)
+                     : reinterpret_cast<const char*>(at.sB + (int64_t)nb0 * p.lsb);
+    s_bytes = sA_wave ? ((int64_t)(nst - 1) * p.lsa + (p.M - m0 - 64 * su)) * 4
+                      : ((int64_t)((N - 1) / kScaleBlock - nb0) * p.lsb + nst) * 4;
+  };
+  // load n of stage s into buffer ST = s % 2: A's, B's, then the scales. Chunks
+  // past K are sent to an offset past their resource's end (2 GiB at most),
+  // where they arrive as zeros.
+  auto load = [&](auto st_c, int s, int n) {
+    constexpr uint32_t st = (uint32_t)(decltype(st_c)::value * STAGE);
+    const bool in = chunk * 16 < K - s * RB;
+    if (n < A_PER)
+      dma16(ldsw + st + 1024 * NW * n, panel_rsrc(a_panel + (int64_t)s * RB, a_bytes - (int64_t)s * RB),
+            (in ? voA : 0x80000000u) + n * stepA, 0u);
+    else if (n < A_PER + B_PER)
+      dma16(ldsw + st + A_BYTES + 1024 * NW * (n - A_PER),
+            panel_rsrc(b_panel + (int64_t)s * RB, b_bytes - (int64_t)s * RB),
+            (in ? voB : 0x80000000u) + (n - A_PER) * stepB, 0u);
+    else
+      dma4(lds0 + st + A_BYTES + B_BYTES + 256 * su, panel_rsrc(s_base + s * s_step, s < nst ? s_bytes - s * s_step : 0), voS, 0u);
+  };
+  auto frag = [&](const uint32_t (&f)[2][2], int st, int blk) -> i32x8 {
+    const uint4 x = __builtin_bit_cast(uint4, lds_read16(f[st][0] + (uint32_t)(blk * 16 * RB)));
+    const uint4 y = __builtin_bit_cast(uint4, lds_read16(f[st][1] + (uint32_t)(blk * 16 * RB)));
+    return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+  };
+
+  auto first_loads = [&] {
+    static_for<0, NU>([&](auto u_c) { load(std::integral_constant<int, 0>{}, 0, decltype(u_c)::value); });
+    static_for<0, NU1>([&](auto u_c) { load(std::integral_constant<int, 1>{}, 1, decltype(u_c)::value); });
+  };
+
+  take(blockIdx.x);
+  first_loads();
+  wait_vmcnt<NU1>();
+  for (int wg = blockIdx.x; wg < n_tiles;) {
+    // stage 0 has landed (memory operations count down in order: the stores of
+    // the tile before came after the loads)
+    wait_vmcnt<NU1 + STORES>();
+    block_barrier();
+
+    // a wave whose rows are all past the tile's last (an expert's last tile)
+    // only takes part in the loads
+    if (m0 + wm * WTM >= m_end) {
+      // a stage's loads and barrier alone
+      auto idle = [&](auto st_c, int s) {
+        constexpr int ST = decltype(st_c)::value;
+        static_for<NU1, NU>([&](auto u_c) { load(std::integral_constant<int, ST ^ 1>{}, s + 1, decltype(u_c)::value); });
+        wait_vmcnt<0>();
+        block_barrier();
+        static_for<0, NU1>([&](auto u_c) { load(std::integral_constant<int, ST>{}, s + 2, decltype(u_c)::value); });
+      };
+
+      for (int s = 0; s < nst; s += 2) {
+        idle(std::integral_constant<int, 0>{}, s);
+        idle(std::integral_constant<int, 1>{}, s + 1);
+      }
+      block_barrier();
+      wg += gridDim.x;
+      if (wg < n_tiles) {
+        take(wg);
+        first_loads();
+      }
+      wait_vmcnt<NU1>();  // (no stores behind these loads)
+      continue;
+    }
 
     floatx4 acc[FM][FN];
 #pragma unroll
@@ -124,13 +205,6 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
         asm volatile("" : "+v"(acc[i][j]));  // (not folded into a first stage of its own)
       }
 
-    wait_vmcnt<0>();  // the previous tile's stores are not counted with this one's loads
-    static_for<0, NU>([&](auto u_c) { load(std::integral_constant<int, 0>{}, 0, decltype(u_c)::value); });
-    static_for<0, NU>([&](auto u_c) {
-      if constexpr (decltype(u_c)::value < NU1) load(std::integral_constant<int, 1>{}, 1, decltype(u_c)::value);
-    });
-    wait_vmcnt<NU1>();
-    block_barrier();
     // B of the stage; A: rows r < FM - 1 alternate between two sets, which the
     // stages take in turn, row FM - 1 has the third
     i32x8 bq[FN], a[3];
@@ -205,27 +279,55 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     }
     add(std::integral_constant<int, FM * FN - 2>{});
     add(std::integral_constant<int, FM * FN - 1>{});
+    wait_lgkmcnt0();
+    block_barrier();  // the ring is free
 
-    // store: 16-row strips staged as fp32 in the free ring
-    wait_vmcnt<0>();
-    wait_lgkmcnt0();
-    block_barrier();
-    {
-      constexpr int OPF = WTN * 4 + 16;
-      static_assert(NW * 16 * OPF <= RING, "a strip of every wave fits the ring");
-      const uint32_t stf = lds0 + (uint32_t)(wave * 16 * OPF);
-      const EpiOut eo{p.C, p.ldc, at.m_end, N, p.bias, p.act, nullptr, 0};
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j) lds_store_f4(stf + (uint32_t)(l16 * OPF + (16 * j + 4 * lg) * 4), acc[i][j]);
-        wait_lgkmcnt0();
-        store_staged_fused<true, false>(stf, OPF, 16, WTN, m0 + wm * WTM + 16 * i, n0 + wn * WTN, lane, 64, eo);
-        wait_lgkmcnt0();
-      }
+    // the next tile's first loads, then this one's store, from registers
+    const int row0_c = m0, col0_c = n0, end_c = m_end;
+    const bool edge = n0 + BN > N;
+    if (p.bias || p.act != kActNone) finish(acc, p, n0 + wn * WTN + 4 * lg);
+    wg += gridDim.x;
+    if (wg < n_tiles) {
+      take(wg);
+      first_loads();
     }
-    wait_lgkmcnt0();
-    block_barrier();
+    // v_permlane exchanges of the packed blocks j and j + 1 leave a lane 8
+    // consecutive columns: of block j + lg / 2, columns 8 (lg % 2) ..
+    int row = wm * WTM + l16, col = wn * WTN + 16 * (lg >> 1) + 8 * (lg & 1);
+    asm volatile("" : "+v"(row), "+v"(col));  // (formed here: held over the stages they spilled)
+    const int64_t c_bytes = ((int64_t)(end_c - 1 - row0_c) * p.ldc + (N - col0_c)) * 2;
+    uint16_t* const c_tile = static_cast<uint16_t*>(p.C) + (int64_t)row0_c * p.ldc + col0_c;
+    const auto rsC = __builtin_amdgcn_make_buffer_rsrc(c_tile, 0, c_bytes > 0x7fffffffll ? 0x7fffffff : (int)c_bytes,
+                                                       0x00020000);
+    static_for<0, FM>([&](auto i_c) {
+      constexpr int i = decltype(i_c)::value;
+      static_for<0, FN / 2>([&](auto h_c) {
+        constexpr int j = 2 * decltype(h_c)::value;
+        u32x4v v;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const auto r = __builtin_amdgcn_permlane32_swap(pack_bf16x2(acc[i][j][2 * e], acc[i][j][2 * e + 1]),
+                                                          pack_bf16x2(acc[i][j + 1][2 * e], acc[i][j + 1][2 * e + 1]),
+                                                          false, false);
+          const auto t = __builtin_amdgcn_permlane16_swap(r[0], r[1], false, false);
+          v[e] = t[0];
+          v[2 + e] = t[1];
+        }
+        if (!edge) {
+          // rows past the last lie past the end of the resource
+          __builtin_amdgcn_raw_buffer_store_b128(v, rsC, (int)(((row + 16 * i) * (int)p.ldc + col + 16 * j) * 2), 0, 0);
+        } else if (row0_c + row + 16 * i < end_c) {
+          const int c = col0_c + col + 16 * j;
+          uint16_t* o = c_tile + (int64_t)(row + 16 * i) * p.ldc + col + 16 * j;
+          if (c + 8 <= N) *reinterpret_cast<u32x4v*>(o) = v;
+          else
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (c + e < N) o[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+        }
+      });
+    });
+    if (edge) wait_vmcnt<0>();  // (any number of stores)
   }
 }
 
