@@ -68,6 +68,7 @@ tg::RouteArgs route_args(const void* logits, int64_t T, int64_t E, int64_t k, in
   a.group_top = o->group_top;
   a.sigmoid = o->score == TILE_GEMM_SCORE_SIGMOID;
   a.renorm = o->renormalize != 0;
+  a.wide = (uintptr_t)logits % 16 == 0 && ld * (o->logits_type == TILE_GEMM_LOGITS_BF16 ? 2 : 4) % 16 == 0;
   a.scale = o->scale;
   return a;
 }

@@ -7,7 +7,7 @@ namespace tg {
 
 namespace {
 
-constexpr int kRouteMaxE = 1024;
+constexpr int kRouteMaxE = 1024, kRouteMaxK = 32;
 
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
@@ -47,93 +47,217 @@ __device__ __forceinline__ void scores_of(const float (&l)[PL], int E, int lane,
   for (int i = 0; i < PL; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
 }
 
-template <int PL, bool BF16>
+// --- choice
+// L lanes work on a token, lane l of them on the experts l PL .. l PL + PL - 1, so
+// that the lowest lane and then the lowest slot is the lowest index. Measured on
+// 8191 tokens of 256 experts, 8 of them (sigmoid, bias, 8 groups), with scores in
+// 64 bits: a whole wave a token, its steps by LDS exchanges, 34 us; this form
+// ROUTE_US.
+
+// v of the lane at the other end of a step of 16 lanes (ror), or of 32 and 64
+template <int STEP>
+__device__ __forceinline__ uint32_t lane_step(uint32_t v) {
+  if constexpr (STEP >= 16) return (uint32_t)__shfl_xor((int)v, STEP, 64);
+  else return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + STEP, 0xf, 0xf, false);  // row_ror:STEP
+}
+template <int STEP>
+__device__ __forceinline__ uint64_t lane_step64(uint64_t v) {
+  return (uint64_t)lane_step<STEP>((uint32_t)(v >> 32)) << 32 | lane_step<STEP>((uint32_t)v);
+}
+// f(v, of another lane) over a token's lanes, the same in all of them (f commutes)
+template <int L, class F>
+__device__ __forceinline__ uint64_t join_token64(uint64_t v, F f) {
+  v = f(v, lane_step64<8>(v));
+  v = f(v, lane_step64<4>(v));
+  v = f(v, lane_step64<2>(v));
+  v = f(v, lane_step64<1>(v));
+  if constexpr (L > 16) v = f(v, lane_step64<16>(v));
+  if constexpr (L > 32) v = f(v, lane_step64<32>(v));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float max_token(float v) {
+  v = fmaxf(v, __uint_as_float(lane_step<8>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(lane_step<4>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(lane_step<2>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(lane_step<1>(__float_as_uint(v))));
+  if constexpr (L > 16) v = fmaxf(v, __uint_as_float(lane_step<16>(__float_as_uint(v))));
+  if constexpr (L > 32) v = fmaxf(v, __uint_as_float(lane_step<32>(__float_as_uint(v))));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ double sum_token(double v) {
+  return __builtin_bit_cast(double, join_token64<L>(__builtin_bit_cast(uint64_t, v), [](uint64_t x, uint64_t y) {
+    return __builtin_bit_cast(uint64_t, __builtin_bit_cast(double, x) + __builtin_bit_cast(double, y));
+  }));
+}
+// An unsigned integer of the same order; 0 is below every value's.
+__device__ __forceinline__ uint64_t order_key(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return (int64_t)b < 0 ? ~b : b | (1ull << 63);
+}
+
+struct Chosen {
+  double score;
+  int32_t id, pad;
+};
+
+// A wave's own LDS: what its lanes wrote is read by its other lanes.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int L, int PL, bool BF16>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
-  extern __shared__ double val[];  // with groups: E values per wave
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = (int)blockIdx.x * 4 + wave;
-  if (t >= p.T) return;  // (no barrier below: a wave works alone)
+  constexpr int TPW = 64 / L, TPG = 256 / L;  // tokens of a wave and of the workgroup
+  __shared__ Chosen chosen[TPG][kRouteMaxK];
+  extern __shared__ double groups_lds[];      // with groups: E values and `groups` of them a token
+  const int lane = threadIdx.x & 63, sub = lane % L, q = lane / L;
+  const int slot = threadIdx.x / L;
+  const int64_t t = (int64_t)blockIdx.x * TPG + slot;
+  const bool live = t < p.T;  // (no barrier below: a wave works alone)
+  const int e0 = sub * PL;
   float l[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = e < p.E ? load_logit<BF16>(p.logits, (int64_t)t * p.ld + e) : -INFINITY;
+  for (int i = 0; i < PL; ++i) l[i] = -INFINITY;
+  if (live) {
+    const int64_t at = t * p.ld + e0;
+    if (p.wide && e0 + PL <= p.E) {
+      constexpr int V = BF16 ? 8 : 4;  // of 16 bytes
+      if constexpr (PL >= V) {
+#pragma unroll
+        for (int i = 0; i < PL; i += V) {
+          const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.logits) + (at + i) * (BF16 ? 2 : 4));
+          const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const uint32_t u = BF16 ? (e & 1 ? d[e / 2] & 0xffff0000u : d[e / 2] << 16) : d[e % 4];
+            const float x = __uint_as_float(u);
+            l[i + e] = x == x ? x : -INFINITY;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) l[i] = load_logit<BF16>(p.logits, at + i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PL; ++i)
+        if (e0 + i < p.E) l[i] = load_logit<BF16>(p.logits, at + i);
+    }
   }
-  double s[PL], v[PL];
-  scores_of<PL>(l, p.E, lane, p.sigmoid, s);
-  uint32_t open = 0;  // experts of this lane that may still be chosen
+  double s[PL];
+  if (p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) m = fmaxf(m, l[i]);
+    m = max_token<L>(m);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      // (an infinite largest logit: those experts share the weight; no finite
+      // logit at all: every score is 0)
+      s[i] = l[i] == m ? (m == -INFINITY ? 0.0 : 1.0) : exp((double)l[i] - (double)m);
+      sum += s[i];
+    }
+    sum = sum_token<L>(sum);
+#pragma unroll
+    for (int i = 0; i < PL; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
+  }
+  uint64_t key[PL];  // of the experts that may still be chosen, else 0
+  double* const value = groups_lds + slot * (p.E + p.groups);
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
-    const int e = lane + 64 * i;
-    v[i] = s[i];
-    if (e < p.E) {
-      open |= 1u << i;
-      if (p.bias) v[i] += (double)p.bias[e];
-      if (!(v[i] == v[i])) v[i] = -INFINITY;
+    key[i] = 0;
+    if (e0 + i < p.E) {
+      double v = s[i];
+      if (p.bias) v += (double)p.bias[e0 + i];
+      if (!(v == v)) v = -INFINITY;
+      key[i] = order_key(v);
+      if (p.groups > 1) value[e0 + i] = v;
     }
   }
   if (p.groups > 1) {
-    double* mine = val + wave * p.E;
+    double* const best = value + p.E;
     const int size = p.E / p.groups;
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (lane + 64 * i < p.E) mine[lane + 64 * i] = v[i];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // (other lanes read them)
-    __builtin_amdgcn_wave_barrier();
-    double a = -INFINITY, b = -INFINITY;  // the group's two largest
-    if (lane < p.groups)
-      for (int j = 0; j < size; ++j) {
-        const double x = mine[lane * size + j];
-        if (x > a) { b = a; a = x; }
-        else if (x > b) b = x;
+    wave_lds_sync();
+    for (int g = sub; g < p.groups; g += L) {
+      double a = -INFINITY, b = -INFINITY;  // the group's two largest
+      int j = g % size;                     // (groups start at different banks)
+      for (int n = 0; n < size; ++n) {
+        const double x = value[g * size + j];
+        if (++j == size) j = 0;
+        b = fmax(b, fmin(a, x));
+        a = fmax(a, x);
       }
-    double best = p.group_top > 1 && size > 1 ? a + b : a;
-    if (!(best == best)) best = -INFINITY;
-    int better = 0;  // groups before this one
-    for (int g = 0; g < p.groups; ++g) {
-      const double x = __shfl(best, g, 64);
-      better += x > best || (x == best && g < lane);
+      double v = p.group_top > 1 && size > 1 ? a + b : a;
+      if (!(v == v)) v = -INFINITY;
+      best[g] = v;
     }
-    const uint64_t chosen = __ballot(lane < p.groups && better < p.top_groups);
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (!((chosen >> ((lane + 64 * i) / size)) & 1)) open &= ~(1u << i);
-  }
-  double total = 0.0, w = 0.0;
-  int id = 0;
-  for (int j = 0; j < p.k; ++j) {
-    double bv = -INFINITY, bs = 0.0;
-    int be = 0x7fffffff;
+    wave_lds_sync();
+    uint64_t open = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += L) {
+      const int g = g0 + sub;
+      int before = 0;  // groups before this one
+      if (g < p.groups) {
+        const double v = best[g];
+        for (int h = 0; h < p.groups; ++h) {
+          const double x = best[h];
+          before += x > v || (x == v && h < g);
+        }
+      }
+      uint64_t on = __ballot(g < p.groups && before < p.top_groups);
+      if constexpr (L < 64) on = on >> (q * L) & ((1ull << L) - 1);
+      open |= on << g0;
+    }
+    int g = e0 / size, left = size - (e0 - g * size);
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      const int e = lane + 64 * i;
-      if ((open >> i & 1) && (be == 0x7fffffff || v[i] > bv)) {
-        bv = v[i];
-        bs = s[i];
-        be = e;
+      if (!(open >> g & 1)) key[i] = 0;
+      if (--left == 0) {
+        left = size;
+        g = min(g + 1, 63);
       }
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) {
-      const double ov = shfl_xor_f64(bv, d), os = shfl_xor_f64(bs, d);
-      const int oe = __shfl_xor(be, d, 64);
-      if (ov > bv || (ov == bv && oe < be)) {
-        bv = ov;
-        bs = os;
-        be = oe;
-      }
-    }
-    if ((be & 63) == lane) open &= ~(1u << (be >> 6));
-    total += bs;
-    if (lane == j) {
-      w = bs;
-      id = be;
     }
   }
-  if (lane < p.k) {
+  for (int j = 0; j < p.k; ++j) {
+    uint64_t mine = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+      if (key[i] > mine) {
+        mine = key[i];
+        at = i;
+      }
+    const uint64_t top = join_token64<L>(mine, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
+    uint64_t equal = __ballot(mine == top);
+    if constexpr (L < 64) equal = equal >> (q * L) & ((1ull << L) - 1);
+    if (sub == __builtin_ctzll(equal)) {
+      double x = 0.0;
+#pragma unroll
+      for (int i = 0; i < PL; ++i)
+        if (i == at) {
+          x = s[i];
+          key[i] = 0;
+        }
+      chosen[slot][j].score = x;
+      chosen[slot][j].id = e0 + at;
+    }
+  }
+  wave_lds_sync();
+  if (!live) return;
+  double total = 0.0;
+  if (p.renorm)
+    for (int j = 0; j < p.k; ++j) total += chosen[slot][j].score;
+  for (int j = sub; j < p.k; j += L) {
+    double w = chosen[slot][j].score;
     if (p.renorm) w = total > 0.0 ? w / total : 0.0;
-    p.ids[(int64_t)t * p.k + lane] = id;
-    p.weights[(int64_t)t * p.k + lane] = (float)(w * (double)p.scale);
+    p.ids[t * p.k + j] = chosen[slot][j].id;
+    p.weights[t * p.k + j] = (float)(w * (double)p.scale);
   }
 }
 
@@ -224,10 +348,15 @@ __global__ __launch_bounds__(1024) void place_kernel(PlaceArgs p) {
   int before = 0, all = 0;
   if (p.chunks > 1) {
     if (tid < p.E)
-      for (int c = 0; c < p.chunks; ++c) {
-        const int h = p.hist[(int64_t)c * p.E + tid];
-        before += c < (int)blockIdx.x ? h : 0;
-        all += h;
+      for (int c0 = 0; c0 < p.chunks; c0 += 16) {  // (16 loads in flight)
+        int h[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) h[c] = c0 + c < p.chunks ? p.hist[(int64_t)(c0 + c) * p.E + tid] : 0;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          before += c0 + c < (int)blockIdx.x ? h[c] : 0;
+          all += h[c];
+        }
       }
   } else {
     next[tid] = 0;
@@ -351,11 +480,16 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs p) {
   }
 }
 
+// The kernel for E experts and the tokens of a workgroup.
 template <bool BF16>
-const void* route_of(int E, bool backward) {
-#define TG_ROUTE(PL)                                                                  \
-  return backward ? reinterpret_cast<const void*>(&route_backward_kernel<PL, BF16>) \
-                  : reinterpret_cast<const void*>(&route_kernel<PL, BF16>)
+const void* route_of(int E, bool backward, int* tokens) {
+#define TG_ROUTE(PL)                                                                                          \
+  {                                                                                                           \
+    constexpr int L = PL > 4 ? 64 : 16;                                                                       \
+    *tokens = backward ? 4 : 256 / L;                                                                         \
+    return backward ? reinterpret_cast<const void*>(&route_backward_kernel<PL, BF16>)                         \
+                    : reinterpret_cast<const void*>(&route_kernel<L, PL * 64 / L, BF16>);                     \
+  }
   if (E <= 64) TG_ROUTE(1);
   if (E <= 128) TG_ROUTE(2);
   if (E <= 256) TG_ROUTE(4);
@@ -373,14 +507,16 @@ hipError_t launch_with_lds(const void* fn, dim3 grid, dim3 block, size_t lds, co
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t stream) {
-  const size_t lds = a.groups > 1 ? (size_t)a.E * 4 * sizeof(double) : 0;
-  return launch_with_lds(bf16 ? route_of<true>(a.E, false) : route_of<false>(a.E, false),
-                         dim3((unsigned)ceil_div(a.T, 4)), dim3(256), lds, a, stream);
+  int tokens;
+  const void* fn = bf16 ? route_of<true>(a.E, false, &tokens) : route_of<false>(a.E, false, &tokens);
+  const size_t lds = a.groups > 1 ? (size_t)tokens * (a.E + a.groups) * sizeof(double) : 0;
+  return launch_with_lds(fn, dim3((unsigned)ceil_div(a.T, tokens)), dim3(256), lds, a, stream);
 }
 
 hipError_t launch_route_backward(const RouteArgs& a, bool bf16, hipStream_t stream) {
-  return launch_raw(bf16 ? route_of<true>(a.E, true) : route_of<false>(a.E, true), dim3((unsigned)ceil_div(a.T, 4)),
-                    dim3(256), a, stream);
+  int tokens;
+  const void* fn = bf16 ? route_of<true>(a.E, true, &tokens) : route_of<false>(a.E, true, &tokens);
+  return launch_raw(fn, dim3((unsigned)ceil_div(a.T, tokens)), dim3(256), a, stream);
 }
 
 hipError_t launch_place(const PlaceArgs& a, hipStream_t stream) {
