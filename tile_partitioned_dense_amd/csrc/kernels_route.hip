@@ -54,25 +54,57 @@ __device__ __forceinline__ void scores_of(const float (&l)[PL], int E, int lane,
 // 64 bits: a whole wave a token, its steps by LDS exchanges, 34 us; this form
 // ROUTE_US.
 
-// v of the lane at the other end of a step of 16 lanes (ror), or of 32 and 64
+// v of the lane STEP before in its row of 16
 template <int STEP>
 __device__ __forceinline__ uint32_t lane_step(uint32_t v) {
-  if constexpr (STEP >= 16) return (uint32_t)__shfl_xor((int)v, STEP, 64);
-  else return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + STEP, 0xf, 0xf, false);  // row_ror:STEP
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + STEP, 0xf, 0xf, false);  // row_ror:STEP
+}
+// both values of lanes 16 (32) apart, the same pair in both
+template <int STEP>
+__device__ __forceinline__ void lane_pair(uint32_t v, uint32_t& x, uint32_t& y) {
+  if constexpr (STEP == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    x = r[0];
+    y = r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    x = r[0];
+    y = r[1];
+  }
 }
 template <int STEP>
-__device__ __forceinline__ uint64_t lane_step64(uint64_t v) {
-  return (uint64_t)lane_step<STEP>((uint32_t)(v >> 32)) << 32 | lane_step<STEP>((uint32_t)v);
+__device__ __forceinline__ void lane_pair64(uint64_t v, uint64_t& x, uint64_t& y) {
+  if constexpr (STEP < 16) {
+    x = v;
+    y = (uint64_t)lane_step<STEP>((uint32_t)(v >> 32)) << 32 | lane_step<STEP>((uint32_t)v);
+  } else {
+    uint32_t xl, yl, xh, yh;
+    lane_pair<STEP>((uint32_t)v, xl, yl);
+    lane_pair<STEP>((uint32_t)(v >> 32), xh, yh);
+    x = (uint64_t)xh << 32 | xl;
+    y = (uint64_t)yh << 32 | yl;
+  }
 }
-// f(v, of another lane) over a token's lanes, the same in all of them (f commutes)
+// f over a token's lanes, the same in all of them (f commutes)
 template <int L, class F>
 __device__ __forceinline__ uint64_t join_token64(uint64_t v, F f) {
-  v = f(v, lane_step64<8>(v));
-  v = f(v, lane_step64<4>(v));
-  v = f(v, lane_step64<2>(v));
-  v = f(v, lane_step64<1>(v));
-  if constexpr (L > 16) v = f(v, lane_step64<16>(v));
-  if constexpr (L > 32) v = f(v, lane_step64<32>(v));
+  uint64_t x, y;
+  lane_pair64<8>(v, x, y);
+  v = f(x, y);
+  lane_pair64<4>(v, x, y);
+  v = f(x, y);
+  lane_pair64<2>(v, x, y);
+  v = f(x, y);
+  lane_pair64<1>(v, x, y);
+  v = f(x, y);
+  if constexpr (L > 16) {
+    lane_pair64<16>(v, x, y);
+    v = f(x, y);
+  }
+  if constexpr (L > 32) {
+    lane_pair64<32>(v, x, y);
+    v = f(x, y);
+  }
   return v;
 }
 template <int L>
@@ -81,8 +113,15 @@ __device__ __forceinline__ float max_token(float v) {
   v = fmaxf(v, __uint_as_float(lane_step<4>(__float_as_uint(v))));
   v = fmaxf(v, __uint_as_float(lane_step<2>(__float_as_uint(v))));
   v = fmaxf(v, __uint_as_float(lane_step<1>(__float_as_uint(v))));
-  if constexpr (L > 16) v = fmaxf(v, __uint_as_float(lane_step<16>(__float_as_uint(v))));
-  if constexpr (L > 32) v = fmaxf(v, __uint_as_float(lane_step<32>(__float_as_uint(v))));
+  uint32_t x, y;
+  if constexpr (L > 16) {
+    lane_pair<16>(__float_as_uint(v), x, y);
+    v = fmaxf(__uint_as_float(x), __uint_as_float(y));
+  }
+  if constexpr (L > 32) {
+    lane_pair<32>(__float_as_uint(v), x, y);
+    v = fmaxf(__uint_as_float(x), __uint_as_float(y));
+  }
   return v;
 }
 template <int L>
@@ -485,7 +524,7 @@ template <bool BF16>
 const void* route_of(int E, bool backward, int* tokens) {
 #define TG_ROUTE(PL)                                                                                          \
   {                                                                                                           \
-    constexpr int L = PL > 4 ? 64 : 16;                                                                       \
+    constexpr int L = PL > 4 ? 64 : PL > 2 ? 32 : 16;                                                                      \
     *tokens = backward ? 4 : 256 / L;                                                                         \
     return backward ? reinterpret_cast<const void*>(&route_backward_kernel<PL, BF16>)                         \
                     : reinterpret_cast<const void*>(&route_kernel<L, PL * 64 / L, BF16>);                     \
