@@ -792,58 +792,68 @@ def tile_gemm_check_xent_backward(A, B, target, lse, dloss, dA, dB, M, N, K, str
 
 
 # ---------------------------- E4M3 products with block scales, routing to experts
+# (as above, one look at each tensor's shape and strides; these calls are often
+# a microsecond or two of GPU work)
+
+def _bad(name, t, what):
+    raise ValueError(f"{name} must have {what}, got shape {tuple(t.shape)} strides {tuple(t.stride())}")
+
+
+def _typed(name, t, dtype):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
 
 def _e4m3(name, t, dims):
-    """Checks a tensor of E4M3 codes (float8_e4m3fn, or their bytes as uint8)."""
+    """Shape and row stride of a tensor of E4M3 codes (float8_e4m3fn, or their bytes as uint8)."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not torch.float8_e4m3fn and t.dtype is not torch.uint8:
         raise TypeError(f"{name} must be float8_e4m3fn (or uint8 codes), got {t.dtype}")
-    s = t.shape
-    if len(s) != dims or (t.stride(-1) != 1 and s[-1] > 1):
-        raise ValueError(f"{name} must have {dims} dimensions, the last of stride 1; got shape {tuple(s)} "
-                         f"strides {tuple(t.stride())}")
-    return s
+    s, d = t.shape, t.stride()
+    if len(s) != dims or (d[-1] != 1 and s[-1] > 1):
+        _bad(name, t, f"{dims} dimensions, the last of stride 1")
+    return s, d
 
 
-def _row_scales(name, t, M, K):
-    """Checks the scales of M rows, (M, blocks of K) with rows next to each
-    other; the stride between blocks."""
+def _row_scales(name, t, M, kb):
+    """The stride between blocks of K of the scales of M rows, (M, blocks of K)
+    with rows next to each other."""
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
-        raise TypeError(f"{name} must be a float32 tensor")
-    kb = (K + 127) // 128
-    s = t.shape
-    if len(s) != 2 or s[0] != M or s[1] != kb or (M > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must have shape ({M}, {kb}) and a row stride of 1, got shape {tuple(s)} strides "
-                         f"{tuple(t.stride())}")
-    return t.stride(1) if kb > 1 else max(M, 1)
+    _typed(name, t, torch.float32)
+    s, d = t.shape, t.stride()
+    if len(s) != 2 or s[0] != M or s[1] != kb or (d[0] != 1 and M > 1):
+        _bad(name, t, f"shape ({M}, {kb}) and a row stride of 1")
+    return d[1] if kb > 1 else max(M, 1)
 
 
-def _block_scales(name, t, lead, rows, K):
-    """Checks the scales of blocks of 128 x 128, (*lead, blocks of rows, blocks of K)."""
+def _block_scales(name, t, lead, nb, kb):
+    """The strides of the scales of blocks of 128 x 128, (*lead, blocks of rows, blocks of K)."""
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
-        raise TypeError(f"{name} must be a float32 tensor")
-    want = (*lead, (rows + 127) // 128, (K + 127) // 128)
-    if tuple(t.shape) != want or (want[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must have shape {want} and a last stride of 1, got shape {tuple(t.shape)} strides "
-                         f"{tuple(t.stride())}")
-    return t.stride(-2) if want[-2] > 1 else want[-1]
+    _typed(name, t, torch.float32)
+    s, d = t.shape, t.stride()
+    if s != (*lead, nb, kb) or (d[-1] != 1 and kb > 1):
+        _bad(name, t, f"shape {(*lead, nb, kb)} and a last stride of 1")
+    return d[-2] if nb > 1 else kb, d[0]
 
 
-def _rows_apart(t, least):
-    """The row stride; of a single row, whose stride is any, the least."""
-    return t.stride(-2) if t.shape[-2] > 1 else least
+def _rows_of(name, t, M, N):
+    """The row stride of an M x N matrix (of a single row, whose stride is any, the
+    least that is a whole 16 bytes)."""
+    s, d = t.shape, t.stride()
+    if s != (M, N) or (d[1] != 1 and N > 1):
+        _bad(name, t, f"shape {(M, N)} and a column stride of 1")
+    return d[0] if M > 1 else (N + 7) // 8 * 8
 
 
-def _fp8_c(C, M, N):
-    if not _is_tensor(C) or tuple(C.shape) != (M, N):
-        raise ValueError(f"C must be a tensor of shape {(M, N)}")
-    if N > 1 and C.stride(1) != 1:
-        raise ValueError(f"C must have a column stride of 1, got {tuple(C.stride())}")
-    return _c_dtype(C), _rows_apart(C, (N + 7) // 8 * 8)
+def _result_rows(name, t, M, N):
+    if not _is_tensor(t):
+        raise TypeError(f"{name} must be a torch tensor")
+    return _c_dtype(t), _rows_of(name, t, M, N)
 
 
 def tile_gemm_run_fp8(h, A, Bt, C, a_scale, b_scale, bias=None, act=Act.NONE, stream=None, check: bool = True):
@@ -851,21 +861,25 @@ def tile_gemm_run_fp8(h, A, Bt, C, a_scale, b_scale, bias=None, act=Act.NONE, st
     (M x K) and Bt (N x K; float8_e4m3fn or uint8 codes) and float32 scales:
     a_scale (M, ceil(K / 128)) with rows next to each other (stride(0) == 1),
     b_scale (ceil(N / 128), ceil(K / 128)), one for each 128 x 128 block."""
-    M, K = _e4m3("A", A, 2)
-    N, K2 = _e4m3("Bt", Bt, 2)
+    (M, K), a = _e4m3("A", A, 2)
+    (N, K2), b = _e4m3("Bt", Bt, 2)
     if K2 != K:
         raise ValueError(f"shapes do not chain: A{tuple(A.shape)} Bt{tuple(Bt.shape)}")
-    dt, ldc = _fp8_c(C, M, N)
-    s = Fp8Strides(_rows_apart(A, K), _rows_apart(Bt, K), ldc, _row_scales("a_scale", a_scale, M, K),
-                   _block_scales("b_scale", b_scale, (), N, K), 0, 0)
-    _check_bias(bias, N)
+    dt, ldc = _result_rows("C", C, M, N)
+    kb = (K + 127) // 128
+    s = Fp8Strides(a[0] if M > 1 else K, b[0] if N > 1 else K, ldc, _row_scales("a_scale", a_scale, M, kb),
+                   _block_scales("b_scale", b_scale, (), (N + 127) // 128, kb)[0], 0, 0)
+    p_bias = None
+    if bias is not None:
+        _check_bias(bias, N)
+        p_bias = bias.data_ptr() if _is_tensor(bias) else bias
     dev = _current_device(("A", "Bt", "C", "a_scale", "b_scale", "bias"),
                           (A, Bt, C, a_scale, b_scale, bias if _is_tensor(bias) else None))
     raw, _ = _launch_stream(stream, dev)
-    st = load_library().tile_gemm_run_fp8(h, A.data_ptr(), Bt.data_ptr(), C.data_ptr(), M, N, K, ctypes.byref(s),
-                                          a_scale.data_ptr(), b_scale.data_ptr(), dt,
-                                          bias.data_ptr() if _is_tensor(bias) else bias, act, raw)
-    return _result(st, check)
+    st = (_lib or load_library()).tile_gemm_run_fp8(h, A.data_ptr(), Bt.data_ptr(), C.data_ptr(), M, N, K,
+                                                    ctypes.byref(s), a_scale.data_ptr(), b_scale.data_ptr(), dt,
+                                                    p_bias, act, raw)
+    return _result(st, check) if st else Status.OK
 
 
 def tile_gemm_run_fp8_experts(h, A, Bt, C, a_scale, b_scale, offsets, stream=None, check: bool = True):
@@ -874,22 +888,22 @@ def tile_gemm_run_fp8_experts(h, A, Bt, C, a_scale, b_scale, offsets, stream=Non
     (E, ceil(N / 128), ceil(K / 128)), offsets E + 1 int32 values; A and a_scale
     as for tile_gemm_run_fp8."""
     import torch
-    M, K = _e4m3("A", A, 2)
-    E, N, K2 = _e4m3("Bt", Bt, 3)
+    (M, K), a = _e4m3("A", A, 2)
+    (E, N, K2), b = _e4m3("Bt", Bt, 3)
     if K2 != K:
         raise ValueError(f"shapes do not chain: A{tuple(A.shape)} Bt{tuple(Bt.shape)}")
-    dt, ldc = _fp8_c(C, M, N)
-    one = N * K
-    s = Fp8Strides(_rows_apart(A, K), _rows_apart(Bt, K), ldc, _row_scales("a_scale", a_scale, M, K),
-                   _block_scales("b_scale", b_scale, (E,), N, K), Bt.stride(0) if E > 1 else one,
-                   b_scale.stride(0) if E > 1 else 0)
+    dt, ldc = _result_rows("C", C, M, N)
+    kb = (K + 127) // 128
+    lsb, esb = _block_scales("b_scale", b_scale, (E,), (N + 127) // 128, kb)
+    s = Fp8Strides(a[0] if M > 1 else K, b[1] if N > 1 else K, ldc, _row_scales("a_scale", a_scale, M, kb), lsb,
+                   b[0] if E > 1 else N * K, esb if E > 1 else 0)
     _vector("offsets", offsets, E + 1, (torch.int32,))
     dev = _current_device(("A", "Bt", "C", "a_scale", "b_scale", "offsets"), (A, Bt, C, a_scale, b_scale, offsets))
     raw, _ = _launch_stream(stream, dev)
-    st = load_library().tile_gemm_run_fp8_experts(h, A.data_ptr(), Bt.data_ptr(), C.data_ptr(), M, N, K, E,
-                                                  offsets.data_ptr(), ctypes.byref(s), a_scale.data_ptr(),
-                                                  b_scale.data_ptr(), dt, raw)
-    return _result(st, check)
+    st = (_lib or load_library()).tile_gemm_run_fp8_experts(h, A.data_ptr(), Bt.data_ptr(), C.data_ptr(), M, N, K, E,
+                                                            offsets.data_ptr(), ctypes.byref(s), a_scale.data_ptr(),
+                                                            b_scale.data_ptr(), dt, raw)
+    return _result(st, check) if st else Status.OK
 
 
 def tile_gemm_run_quantize(h, X, Q, scale, form=Quant.ROWS, gate=None, rows=None, stream=None, check: bool = True):
@@ -899,54 +913,56 @@ def tile_gemm_run_quantize(h, X, Q, scale, form=Quant.ROWS, gate=None, rows=None
     act(first half of X's columns) * (second half). form=Quant.BLOCKS: scale
     (ceil(M / 128), ceil(K / 128)). `rows`: M int32 row numbers of X."""
     import torch
-    M, K = _e4m3("Q", Q, 2)
+    (M, K), q = _e4m3("Q", Q, 2)
+    blocks = form == 2  # Quant.BLOCKS
     if gate is not None:
-        if form == Quant.BLOCKS:
+        if blocks:
             raise ValueError("gate: not with blocks of 128 x 128")
-        form = Quant.GATED_ROWS
-    elif form == Quant.GATED_ROWS:
+        form = 1  # Quant.GATED_ROWS
+    elif form == 1:
         raise ValueError("form=Quant.GATED_ROWS needs a gate")
-    x_rows = _matrix("X", X, M if rows is None else None, K if gate is None else 2 * K)[0]
-    if X.shape[1] > 1 and X.stride(1) != 1:
-        raise ValueError(f"X must have a column stride of 1, got {tuple(X.stride())}")
-    if form == Quant.BLOCKS:
-        lds = _block_scales("scale", scale, (), M, K)
-    else:
-        lds = _row_scales("scale", scale, M, K)
+    _typed("X", X, torch.bfloat16)
+    x_rows = M
+    p_rows = None
     if rows is not None:
         _vector("rows", rows, M, (torch.int32,))
+        p_rows = rows.data_ptr()
+        if X.dim() == 2:
+            x_rows = X.shape[0]
+    ldx = _rows_of("X", X, x_rows, K if gate is None else 2 * K)
+    kb = (K + 127) // 128
+    if blocks:
+        lds = _block_scales("scale", scale, (), (M + 127) // 128, kb)[0]
+    else:
+        lds = _row_scales("scale", scale, M, kb)
     dev = _current_device(("X", "Q", "scale", "rows"), (X, Q, scale, rows))
     raw, _ = _launch_stream(stream, dev)
-    st = load_library().tile_gemm_run_quantize(h, X.data_ptr(), Q.data_ptr(), scale.data_ptr(), M, K,
-                                               _rows_apart(X, X.shape[1]), _rows_apart(Q, K), lds, form,
-                                               0 if gate is None else gate,
-                                               None if rows is None else rows.data_ptr(), x_rows, raw)
-    return _result(st, check)
+    st = (_lib or load_library()).tile_gemm_run_quantize(h, X.data_ptr(), Q.data_ptr(), scale.data_ptr(), M, K, ldx,
+                                                         q[0] if M > 1 else K, lds, form, 0 if gate is None else gate,
+                                                         p_rows, x_rows, raw)
+    return _result(st, check) if st else Status.OK
 
 
-def _logits(name, t, T, E):
-    """Checks a router's logits; their type and the stride between tokens."""
+def _logits(name, t, T):
+    """Experts, type (bfloat16 or not) and row stride of a router's logits of T tokens."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype is not torch.float32 and t.dtype is not torch.bfloat16:
+    bf16 = t.dtype is torch.bfloat16
+    if not bf16 and t.dtype is not torch.float32:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    s = t.shape
-    if len(s) != 2 or (T is not None and (s[0] != T or s[1] != E)) or (s[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must have shape ({'any' if T is None else T}, {'any' if E is None else E}) and a "
-                         f"column stride of 1, got shape {tuple(s)} strides {tuple(t.stride())}")
-    return t.dtype is torch.bfloat16, _rows_apart(t, s[1])
+    s, d = t.shape, t.stride()
+    if len(s) != 2 or s[0] != T or (d[1] != 1 and s[1] > 1):
+        _bad(name, t, f"a row for each of the {T} tokens and a column stride of 1")
+    return s[1], bf16, d[0] if T > 1 else s[1]
 
 
 def _per_place(name, t, T, k, dtype):
-    """Checks a contiguous (T, k) tensor."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
-        raise TypeError(f"{name} must be a {dtype} tensor")
+    """Checks a contiguous (T, k) tensor; its shape."""
+    _typed(name, t, dtype)
     s = t.shape
-    if len(s) != 2 or (T is not None and s[0] != T) or (k is not None and s[1] != k) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, of shape ({'any' if T is None else T}, "
-                         f"{'any' if k is None else k}); got shape {tuple(s)} strides {tuple(t.stride())}")
+    if len(s) != 2 or (T is not None and (s[0] != T or s[1] != k)) or not t.is_contiguous():
+        _bad(name, t, "contiguous values for each token's experts" if T is None else f"shape ({T}, {k}), contiguous")
     return s
 
 
@@ -958,19 +974,18 @@ def tile_gemm_run_route(h, logits, ids, weights, score=Score.SOFTMAX, bias=None,
     only experts of the top_groups best of `groups` runs of experts are chosen."""
     import torch
     T, k = _per_place("ids", ids, None, None, torch.int32)
-    bf16, ld = _logits("logits", logits, None, None)
-    if logits.shape[0] != T:
-        raise ValueError(f"logits{tuple(logits.shape)} and ids{tuple(ids.shape)} are of different tokens")
-    E = logits.shape[1]
+    E, bf16, ld = _logits("logits", logits, T)
     _per_place("weights", weights, T, k, torch.float32)
+    p_bias = None
     if bias is not None:
         _vector("bias", bias, E, (torch.float32,))
+        p_bias = bias.data_ptr()
     dev = _current_device(("logits", "ids", "weights", "bias"), (logits, ids, weights, bias))
     raw, _ = _launch_stream(stream, dev)
     o = RouteOptions(score, bf16, groups, top_groups, group_top, renormalize, scale)
-    st = load_library().tile_gemm_run_route(h, logits.data_ptr(), None if bias is None else bias.data_ptr(),
-                                            ids.data_ptr(), weights.data_ptr(), T, E, k, ld, ctypes.byref(o), raw)
-    return _result(st, check)
+    st = (_lib or load_library()).tile_gemm_run_route(h, logits.data_ptr(), p_bias, ids.data_ptr(),
+                                                      weights.data_ptr(), T, E, k, ld, ctypes.byref(o), raw)
+    return _result(st, check) if st else Status.OK
 
 
 def tile_gemm_run_route_backward(h, logits, ids, dweights, dlogits, score=Score.SOFTMAX, renormalize=True, scale=1.0,
@@ -979,20 +994,20 @@ def tile_gemm_run_route_backward(h, logits, ids, dweights, dlogits, score=Score.
     the logits' type) from dweights (T, k) float32 and the ids chosen."""
     import torch
     T, k = _per_place("ids", ids, None, None, torch.int32)
-    bf16, ld = _logits("logits", logits, None, None)
-    if logits.shape[0] != T:
-        raise ValueError(f"logits{tuple(logits.shape)} and ids{tuple(ids.shape)} are of different tokens")
-    E = logits.shape[1]
-    dbf16, ldd = _logits("dlogits", dlogits, T, E)
+    E, bf16, ld = _logits("logits", logits, T)
+    dE, dbf16, ldd = _logits("dlogits", dlogits, T)
+    if dE != E:
+        _bad("dlogits", dlogits, f"shape ({T}, {E})")
     if dbf16 != bf16:
         raise TypeError(f"dlogits must be of the logits' type {logits.dtype}, got {dlogits.dtype}")
     _per_place("dweights", dweights, T, k, torch.float32)
     dev = _current_device(("logits", "ids", "dweights", "dlogits"), (logits, ids, dweights, dlogits))
     raw, _ = _launch_stream(stream, dev)
     o = RouteOptions(score, bf16, 1, 1, 1, renormalize, scale)
-    st = load_library().tile_gemm_run_route_backward(h, logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(),
-                                                     dlogits.data_ptr(), T, E, k, ld, ldd, ctypes.byref(o), raw)
-    return _result(st, check)
+    st = (_lib or load_library()).tile_gemm_run_route_backward(h, logits.data_ptr(), ids.data_ptr(),
+                                                               dweights.data_ptr(), dlogits.data_ptr(), T, E, k, ld,
+                                                               ldd, ctypes.byref(o), raw)
+    return _result(st, check) if st else Status.OK
 
 
 def tile_gemm_place_workspace(T, k, E) -> int:
@@ -1010,30 +1025,36 @@ def tile_gemm_run_place(h, ids, offsets, rows=None, places=None, first=0, worksp
     allocated for the call where it needs one."""
     import torch
     T, k = _per_place("ids", ids, None, None, torch.int32)
-    if not _is_tensor(offsets) or offsets.dim() != 1 or offsets.shape[0] < 2:
-        raise ValueError("offsets must be a vector of at least 2 values")
-    E = offsets.shape[0] - 1
-    _vector("offsets", offsets, E + 1, (torch.int32,))
+    _typed("offsets", offsets, torch.int32)
+    E = offsets.numel() - 1
+    if E < 1 or offsets.dim() != 1 or not offsets.is_contiguous():
+        _bad("offsets", offsets, "one dimension of at least 2 contiguous values")
+    p_rows = p_places = p_ws = None
     if rows is not None:
         _vector("rows", rows, T * k, (torch.int32,))
+        p_rows = rows.data_ptr()
     if places is not None:
         _per_place("places", places, T, k, torch.int32)
+        p_places = places.data_ptr()
     dev = _current_device(("ids", "offsets", "rows", "places", "workspace"), (ids, offsets, rows, places, workspace))
     raw, other = _launch_stream(stream, dev)
-    lib = load_library()
-    if workspace is None:
+    lib = _lib or load_library()
+    nbytes = 0
+    if workspace is not None:
+        nbytes = _workspace_bytes(workspace)
+    else:
         n = ctypes.c_int64()
-        _raise_if(lib.tile_gemm_place_workspace(T, k, E, ctypes.byref(n)))
+        st = lib.tile_gemm_place_workspace(T, k, E, n)
+        if st:
+            return _result(st, check)
         nbytes = n.value
         if nbytes:
             workspace = _own_workspace(nbytes, ids, dev, other)
-    else:
-        nbytes = _workspace_bytes(workspace)
-    st = lib.tile_gemm_run_place(h, ids.data_ptr(), T, k, first, E, offsets.data_ptr(),
-                                 None if rows is None else rows.data_ptr(),
-                                 None if places is None else places.data_ptr(),
-                                 None if workspace is None else workspace.data_ptr(), nbytes, raw)
-    return _result(st, check)
+    if workspace is not None:
+        p_ws = workspace.data_ptr()
+    st = lib.tile_gemm_run_place(h, ids.data_ptr(), T, k, first, E, offsets.data_ptr(), p_rows, p_places, p_ws, nbytes,
+                                 raw)
+    return _result(st, check) if st else Status.OK
 
 
 def tile_gemm_run_combine(h, Z, places, weights, Y, stream=None, check: bool = True):
@@ -1043,20 +1064,17 @@ def tile_gemm_run_combine(h, Z, places, weights, Y, stream=None, check: bool = T
     import torch
     T, k = _per_place("places", places, None, None, torch.int32)
     z_rows, N = _matrix("Z", Z, None, None)
-    if N > 1 and Z.stride(1) != 1:
-        raise ValueError(f"Z must have a column stride of 1, got {tuple(Z.stride())}")
-    if not _is_tensor(Y) or tuple(Y.shape) != (T, N) or (N > 1 and Y.stride(1) != 1):
-        raise ValueError(f"Y must be a tensor of shape {(T, N)} with a column stride of 1")
-    dt = _c_dtype(Y)
+    ldz = _rows_of("Z", Z, z_rows, N)
+    dt, ldy = _result_rows("Y", Y, T, N)
+    p_weights = None
     if weights is not None:
         _per_place("weights", weights, T, k, torch.float32)
+        p_weights = weights.data_ptr()
     dev = _current_device(("Z", "places", "weights", "Y"), (Z, places, weights, Y))
     raw, _ = _launch_stream(stream, dev)
-    least = (N + 7) // 8 * 8
-    st = load_library().tile_gemm_run_combine(h, Z.data_ptr(), places.data_ptr(),
-                                              None if weights is None else weights.data_ptr(), Y.data_ptr(), T, N, k,
-                                              z_rows, _rows_apart(Z, least), _rows_apart(Y, least), dt, raw)
-    return _result(st, check)
+    st = (_lib or load_library()).tile_gemm_run_combine(h, Z.data_ptr(), places.data_ptr(), p_weights, Y.data_ptr(), T,
+                                                        N, k, z_rows, ldz, ldy, dt, raw)
+    return _result(st, check) if st else Status.OK
 
 
 def tile_gemm_plan_fp8(M, N, K, experts=0, dtype=Dtype.BF16_TO_BF16, cu_count=256) -> Plan:
