@@ -80,29 +80,91 @@ def test_product(g, M, N, K, dtype):
     assert untouched(whole, c)
 
 
-def big_config_shape():
-    """The smallest square output that takes the large bf16 tile."""
-    for n in range(256, 8192, 256):
-        if tg.tile_gemm_plan_fp8(n + 10, n - 6, 1024).bm == 256:
-            return n + 10, n - 6
-    raise AssertionError("no shape takes the large tile")
+N_CONFIGS = 11  # compiled tiles
+
+
+def smallest_shapes(experts):
+    """{(configuration, dtype): the smallest shape (M, N, K) that is planned to it}, odd ones."""
+    found = {}
+    for dtype in (torch.bfloat16, torch.float32):
+        for M in (1, 7, 20, 45, 70, 150, 300, 500, 700, 1030, 2050, 4100):
+            for N in (9, 40, 130, 264, 530, 1030, 2056, 4104, 8200, 28690):
+                for K in (16, 144, 272, 528, 1040, 2064, 4112, 8208):
+                    c = tg.tile_gemm_plan_fp8(M, N, K, experts, tg.Dtype(int(dtype is torch.bfloat16))).config
+                    old = found.get((c, dtype))
+                    if old is None or M * N * K < old[0] * old[1] * old[2]:
+                        found[c, dtype] = (M, N, K)
+    return found
+
+
+def integers(seed, *shape):
+    return torch.randint(-3, 4, shape, generator=gen(seed)).float().to(bh.FP8)
+
+
+def powers(seed, *shape):
+    return (2.0 ** torch.randint(-2, 3, shape, generator=gen(seed))).float()
+
+
+def wide(q, s, high):
+    """As bh.widen, in fp32 on the GPU: exact here."""
+    return (q.cuda().float() * s.cuda().repeat_interleave(128, -1)[..., :q.shape[-1]].repeat_interleave(
+        high, -2)[..., :q.shape[-2], :])
+
+
+@pytest.mark.parametrize("config", range(N_CONFIGS))
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_every_tile(g, config, dtype):
+    """Each compiled tile on the smallest shape planned to it: integers and
+    scales that are powers of two, whose sums are exact in any order."""
+    shape = smallest_shapes(0).get((config, dtype))
+    if shape is None:
+        assert (config, dtype) == (0, torch.float32)
+        return
+    M, N, K = shape
+    for K in (K, K + 112):  # and one that ends inside a block
+        print(f"[fp8 {config}: {M}x{N}x{K} {dtype}]", flush=True)
+        a, b, sa, sb = (integers(K, M, K), integers(K + 1, N, K), powers(K, M, bh.blocks(K)),
+                        powers(K + 1, bh.blocks(N), bh.blocks(K)))
+        want = wide(a, sa, 1).double() @ wide(b, sb, 128).double().T
+        whole, c = out_like(M, N, dtype)
+        g.fp8(a.cuda(), b.cuda(), c, to_row_scales(sa), sb.cuda())
+        assert torch.equal(c.double(), want.to(dtype).double())
+        assert untouched(whole, c)
+
+
+@pytest.mark.parametrize("config", range(N_CONFIGS))
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_every_tile_of_experts(g, config, dtype):
+    """The same with 6 experts: one with most of the rows, a row, none."""
+    shape = smallest_shapes(6).get((config, dtype))
+    if shape is None:
+        assert (config, dtype) == (0, torch.float32)
+        return
+    M, N, K = shape
+    print(f"[experts {config}: {M}x{N}x{K} {dtype}]", flush=True)
+    cuts = sorted([0, M // 50, M // 50, M - M // 5 - M // 50, M - M // 5 - min(M // 50, 1), M - M // 5, M])
+    a, b = integers(1, M, K), integers(2, 6, N, K)
+    sa, sb = powers(3, M, bh.blocks(K)), powers(4, 6, bh.blocks(N), bh.blocks(K))
+    whole, c = out_like(M, N, dtype)
+    g.fp8_experts(a.cuda(), b.cuda(), c, to_row_scales(sa), sb.cuda(), torch.tensor(cuts, dtype=torch.int32).cuda())
+    for e in range(6):
+        rows = slice(cuts[e], cuts[e + 1])
+        want = wide(a[rows], sa[rows], 1).double() @ wide(b[e], sb[e], 128).double().T
+        assert torch.equal(c[rows].double(), want.to(dtype).double()), e
+    assert untouched(whole, c)
 
 
 @pytest.mark.parametrize("K", [16, 128, 272, 1424])
 def test_large_tile(g, K):
-    """Integers and scales that are powers of two: every sum is exact, so the
-    results are, whatever the order."""
-    M, N = big_config_shape()
+    """Many tiles of the large kernels, ragged at every edge."""
+    M, N = 4100, 2042
     print(f"[fp8 {M}x{N}x{K}]", flush=True)
-    r = gen(K)
-    a = torch.randint(-3, 4, (M, K), generator=r).float().to(bh.FP8)
-    b = torch.randint(-3, 4, (N, K), generator=r).float().to(bh.FP8)
-    sa = 2.0 ** torch.randint(-2, 3, (M, bh.blocks(K)), generator=r)
-    sb = 2.0 ** torch.randint(-2, 3, (bh.blocks(N), bh.blocks(K)), generator=r)
-    want = (bh.widen(a, sa, 1).cuda() @ bh.widen(b, sb, 128).cuda().T)
+    a, b, sa, sb = (integers(K, M, K), integers(K + 1, N, K), powers(K, M, bh.blocks(K)),
+                    powers(K + 1, bh.blocks(N), bh.blocks(K)))
+    want = wide(a, sa, 1).double() @ wide(b, sb, 128).double().T
     for dtype in (torch.bfloat16, torch.float32):
         whole, c = out_like(M, N, dtype)
-        g.fp8(a.cuda(), b.cuda(), c, to_row_scales(sa.float()), sb.float().cuda())
+        g.fp8(a.cuda(), b.cuda(), c, to_row_scales(sa), sb.cuda())
         assert torch.equal(c.double(), want.to(dtype).double())
         assert untouched(whole, c)
 
@@ -216,14 +278,10 @@ def test_experts(g, sizes, N, K, more, dtype):
     run_experts(g, sizes, N, K, dtype, **more)
 
 
-def test_experts_take_every_tile(g):
-    """A few rows of one expert beside many of another, at every average."""
-    seen = set()
-    for total in (40, 160, 400, 1000, 5000):
-        sizes = [1, 0, total - 20, 0, 19, 0, 0, 0]
-        seen.add(tg.tile_gemm_plan_fp8(total, 136, 144, 8).config)
-        run_experts(g, sizes, 136, 144, torch.bfloat16, seed=total)
-    assert len(seen) >= 4
+@pytest.mark.parametrize("total", [40, 160, 400, 1000, 5000])
+def test_experts_of_different_sizes(g, total):
+    """A few rows of one expert beside many of another."""
+    run_experts(g, [1, 0, total - 20, 0, 19, 0, 0, 0], 136, 144, torch.bfloat16, seed=total)
 
 
 def test_experts_bad_offsets(g):

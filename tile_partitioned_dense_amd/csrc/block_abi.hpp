@@ -309,7 +309,7 @@ tile_gemm_status_t tile_gemm_plan_fp8(int64_t M, int64_t N, int64_t K, int64_t E
   if ((tg::ceil_div(M, 16) + E) * tg::ceil_div(N, 64) >= kMaxDim)
     return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: too many tiles");
   if (cu_count <= 0) return fail(TILE_GEMM_ERR_DEVICE, "cu_count: %d", cu_count);
-  fill_plan(E ? tg::make_plan_experts(M, N, E, fp32, cu_count) : tg::make_plan_block(M, N, fp32, cu_count), out);
+  fill_plan(E ? tg::make_plan_experts(M, N, K, E, fp32, cu_count) : tg::make_plan_block(M, N, K, fp32, cu_count), out);
   return TILE_GEMM_OK;
 }
 

@@ -24,6 +24,7 @@ struct BlockArgs {
   const int32_t* offsets;
   int32_t groups;
   int64_t eb, esb;
+  int32_t once;  // B's bytes are read by one tile only
 };
 
 // (an unscaled product: with both scale operands a constant 0 the plain form
@@ -55,6 +56,21 @@ __device__ __forceinline__ void widen_e4m3(const i32x8& v, bf16x32& out) {
 __device__ __forceinline__ i32x4 panel_rsrc(const void* base, int64_t bytes) {
   return make_rsrc(base, bytes > 0x7fffffffll ? 0x7fffffffll : bytes);
 }
+
+// dma16 past the caches, for bytes that are read once
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma16_once(uint32_t lds, const i32x4& rsrc_in, uint32_t voff) {
+  const i32x4 rsrc = uniform_rsrc(rsrc_in);
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "buffer_load_dwordx4 %1, %2, 0 offen nt lds"
+      :
+      : "s"(lds), "v"(voff), "s"(rsrc)
+      : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 // --- owned tiles
 struct BlockTile {
@@ -233,9 +249,15 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
         const int u = wave + NW * t < A_DMA ? wave + NW * t : A_DMA - 1;
         dma16(st + 1024 * u, rsA, chA[t] < left ? voA[t] : kDmaPast, 0u);
       }
+      if (p.once) {
 #pragma unroll
-      for (int t = 0; t < B_PER; ++t)
-        dma16(st + A_BYTES + 1024 * (wave + NW * t), rsB, chB[t] < left ? voB[t] : kDmaPast, 0u);
+        for (int t = 0; t < B_PER; ++t)
+          dma16_once(st + A_BYTES + 1024 * (wave + NW * t), rsB, chB[t] < left ? voB[t] : kDmaPast);
+      } else {
+#pragma unroll
+        for (int t = 0; t < B_PER; ++t)
+          dma16(st + A_BYTES + 1024 * (wave + NW * t), rsB, chB[t] < left ? voB[t] : kDmaPast, 0u);
+      }
       const int kb = s * KBS;
 #pragma unroll
       for (int t = 0; t < S_PER; ++t) {

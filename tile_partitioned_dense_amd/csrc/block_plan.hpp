@@ -9,24 +9,38 @@ namespace tg {
 constexpr int kScaleBlock = 128;      // values of K that share a scale (and rows of B)
 constexpr int kBlockMaxGroups = 1024;  // experts of one call
 
-// Compiled configurations of block_kernel.hpp: tiles of bm x bn, wm x wn waves
-// on it times ks that share every stage's K, stages of sb bytes of K per row.
+// Compiled configurations: tiles of bm x bn, wm x wn waves on it times ks that
+// share every stage's K, stages of sb bytes of K per row. `tile`: those of
+// block_tile_kernel.hpp, the others of block_kernel.hpp.
 struct BlockConfig {
   int bm, bn, wm, wn, ks, sb, stages;
-  int occ;    // workgroups that fit on one compute unit at once
-  float eff;  // rate relative to configuration 0; 0: a stream configuration
+  int occ;     // workgroups that fit on one compute unit at once
+  bool tile;
+  // Microseconds of a launch, for bf16 and for fp32 outputs: c0 + rounds (a +
+  // stages b), with b going to b2 as a round's tiles come to fill the chip (two
+  // tiles a compute unit where occ is 2). Fitted to 207 shapes of 1 to 4000 rows,
+  // 48 to 28672 columns and K of 128 to 8192: the configuration it picks takes
+  // 1.8% longer than the fastest on average (9% or less on 95 of 100).
+  float cost[2][4];
 };
-constexpr int kNumBlockConfigs = 5;
+constexpr int kNumBlockConfigs = 11;
 constexpr BlockConfig kBlockConfigs[kNumBlockConfigs] = {
-    {256, 256, 2, 4, 1, 128, 2, 1, 1.00f},  // 0: 8 waves of 128x64
-    {128, 128, 2, 2, 1, 128, 2, 2, 0.70f},  // 1: 4 waves of 64x64
-    {16, 64, 1, 2, 4, 512, 3, 1, 0.0f},     // 2: up to 16 rows
-    {32, 64, 1, 2, 4, 512, 3, 1, 0.0f},     // 3: up to 32 rows
-    {64, 128, 1, 4, 2, 256, 3, 1, 0.0f},    // 4: up to 64 rows
+    {256, 256, 2, 4, 1, 128, 2, 1, true, {{0.00f, 8.34f, 1.01f, 1.87f}, {}}},   // 0: 8 waves of 128x64 (bf16 outputs)
+    {256, 128, 4, 2, 1, 128, 2, 1, true, {{1.16f, 4.73f, 0.70f, 1.12f}, {0.00f, 7.61f, 0.98f, 1.59f}}},   // 1: 8 waves of 64x64
+    {128, 128, 2, 2, 1, 128, 2, 2, true, {{0.65f, 4.58f, 0.62f, 1.16f}, {0.00f, 6.36f, 0.94f, 1.91f}}},   // 2: 4 waves of 64x64
+    {16, 128, 1, 4, 2, 256, 3, 1, false, {{2.57f, 1.61f, 0.67f, 0.75f}, {2.58f, 1.72f, 0.80f, 0.88f}}},   // 3
+    {32, 128, 1, 4, 2, 256, 3, 1, false, {{2.50f, 1.97f, 0.76f, 0.86f}, {2.49f, 2.39f, 1.00f, 1.11f}}},   // 4
+    {64, 128, 1, 4, 2, 256, 3, 1, false, {{2.50f, 3.03f, 1.06f, 1.24f}, {2.33f, 3.39f, 1.45f, 1.63f}}},   // 5
+    {16, 64, 1, 2, 4, 512, 3, 1, false, {{2.52f, 1.63f, 0.66f, 0.74f}, {2.56f, 1.67f, 0.81f, 0.90f}}},    // 6
+    {32, 64, 1, 2, 4, 512, 3, 1, false, {{2.64f, 2.02f, 0.82f, 0.95f}, {2.55f, 2.40f, 1.06f, 1.18f}}},    // 7
+    {64, 64, 2, 2, 4, 512, 2, 1, false, {{2.99f, 2.35f, 1.04f, 1.29f}, {2.90f, 2.71f, 1.42f, 1.60f}}},    // 8
+    {16, 32, 1, 1, 8, 1024, 3, 1, false, {{2.62f, 1.70f, 0.79f, 0.90f}, {2.69f, 1.64f, 0.94f, 1.08f}}},   // 9
+    {32, 32, 1, 1, 8, 1024, 2, 1, false, {{2.78f, 1.74f, 0.97f, 1.22f}, {2.78f, 1.95f, 1.20f, 1.39f}}},   // 10
 };
 
 inline int block_lds_bytes(const BlockConfig& c) {
-  return c.stages * ((c.bm + c.bn) * c.sb + c.bm * (c.sb / kScaleBlock) * 4 + 256);
+  const int rows = (c.bm + 63) / 64 * 64;  // of scales
+  return c.stages * ((c.bm + c.bn) * c.sb + rows * (c.sb / kScaleBlock) * 4 + 256);
 }
 
 inline Plan plan_block_for(int config, int64_t M, int64_t N, int cu_count) {
@@ -45,40 +59,66 @@ inline Plan plan_block_for(int config, int64_t M, int64_t N, int cu_count) {
   p.map.group_m = pick_group_m(p.map.tiles_m, p.map.tiles_n);
   p.map.xcds = kXcds;
   p.tiles = (int64_t)p.map.tiles_m * p.map.tiles_n;
-  p.grid = persistent_grid(p.tiles, cu_count * c.occ);
+  const int64_t all = (int64_t)cu_count * c.occ;
+  p.grid = c.occ > 1 ? (p.tiles < all ? p.tiles : all) : persistent_grid(p.tiles, cu_count);
   return p;
 }
 
-// fp32: outputs of that type, whose products run on bf16 instructions
-// (block_kernel.hpp): their operands take twice the registers, so they have the
-// 64 x 64 wave tiles.
-inline int pick_block_config(int64_t M, int64_t N, bool fp32, int cu_count) {
-  if (M <= 16) return 2;
-  if (M <= 32) return 3;
-  if (M <= 64) return 4;
-  if (fp32) return 1;
-  const int64_t big = ceil_div(M, 256) * ceil_div(N, 256);
-  const int64_t small = ceil_div(M, 128) * ceil_div(N, 128);
-  const double t0 = (double)ceil_div(big, cu_count) * 4.0 / kBlockConfigs[0].eff;
-  const double t1 = (double)ceil_div(small, 2 * cu_count) * 2.0 / kBlockConfigs[1].eff;
-  return t1 < t0 ? 1 : 0;
+// The launch's estimated microseconds for `tiles` tiles (see BlockConfig::cost).
+inline double block_cost(int config, bool fp32, int64_t tiles, int64_t K, int cu_count) {
+  const BlockConfig& c = kBlockConfigs[config];
+  const float* f = c.cost[fp32];
+  const double st = (double)ceil_div(K, c.sb), a = f[1], b = f[2], b2 = f[3];
+  if (c.occ > 1) {
+    const int64_t full = tiles / (2 * cu_count), rest = tiles - full * 2 * cu_count;
+    double t = f[0] + (double)full * (a + b2 * st);
+    if (rest > cu_count) t += a + b2 * st;
+    else if (rest > 0) t += a + b * st;
+    return t;
+  }
+  const int64_t rounds = ceil_div(tiles, cu_count);
+  const double fill = (double)ceil_div(tiles, rounds) / cu_count;
+  return f[0] + (double)rounds * (a + (b + (b2 - b) * (fill < 1.0 ? fill : 1.0)) * st);
 }
 
-inline Plan make_plan_block(int64_t M, int64_t N, bool fp32, int cu_count) {
+// fp32: outputs of that type, whose products run on bf16 instructions
+// (block_kernel.hpp): their operands take twice the registers, so they have no
+// 256 x 256 tiles.
+template <class Tiles>
+int pick_block_config(bool fp32, int64_t K, int cu_count, Tiles tiles) {
+  int best = -1;
+  double best_cost = 0.0;
+  for (int i = fp32 ? 1 : 0; i < kNumBlockConfigs; ++i) {
+    const double cost = block_cost(i, fp32, tiles(kBlockConfigs[i]), K, cu_count);
+    if (best < 0 || cost < best_cost) {
+      best = i;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+inline Plan make_plan_block(int64_t M, int64_t N, int64_t K, bool fp32, int cu_count) {
   if (M <= 0 || N <= 0) return plan_for(0, 0, M, N, cu_count);
-  return plan_block_for(pick_block_config(M, N, fp32, cu_count), M, N, cu_count);
+  const int config = pick_block_config(fp32, K, cu_count, [&](const BlockConfig& c) {
+    return ceil_div(M, c.bm) * ceil_div(N, c.bn);
+  });
+  return plan_block_for(config, M, N, cu_count);
 }
 
 // Rows sorted by expert: a tile is bm rows of one expert. Which rows are whose
-// is known on the device only, so the configuration goes by the rows an expert
-// has on average, and the grid by the most tiles there can be.
-inline Plan make_plan_experts(int64_t M, int64_t N, int64_t groups, bool fp32, int cu_count) {
+// is known on the device only, so the configuration goes by the tiles to be
+// expected (live experts of e rows on average end half a tile short) and the
+// grid by the most there can be.
+inline Plan make_plan_experts(int64_t M, int64_t N, int64_t K, int64_t groups, bool fp32, int cu_count) {
   if (M <= 0 || N <= 0 || groups <= 0) return plan_for(0, 0, M, N, cu_count);
-  const int64_t avg = ceil_div(M, groups);
-  const int config = avg <= 8 ? 2 : avg <= 24 ? 3 : avg <= 64 ? 4 : avg <= 384 || fp32 ? 1 : 0;
+  const int64_t live = groups < M ? groups : M;
+  const int config = pick_block_config(fp32, K, cu_count, [&](const BlockConfig& c) {
+    const int64_t rows = M / c.bm + (live + 1) / 2;
+    return (rows > live ? rows : live) * ceil_div(N, c.bn);
+  });
   Plan p = plan_block_for(config, M, N, cu_count);
-  const int64_t most = ceil_div(M, p.bm) + (groups < M ? groups : M);
-  p.tiles = most * p.map.tiles_n;
+  p.tiles = (ceil_div(M, p.bm) + live) * p.map.tiles_n;
   const int64_t all = (int64_t)cu_count * kBlockConfigs[config].occ;
   p.grid = p.tiles < all ? p.tiles : all;
   return p;

@@ -26,8 +26,8 @@ tile_gemm_status_t run_fp8(tile_gemm_t h, const void* A, const void* B, void* C,
   TG_TRY(check_fp8(A, B, C, M, N, K, experts, offsets, s, sa, sb, dtype, bias, act));
   if (M == 0 || N == 0) return TILE_GEMM_OK;
   TG_TRY(check_device(h));
-  const tg::Plan p = experts < 0 ? tg::make_plan_block(M, N, dtype == TILE_GEMM_BF16_TO_F32, h->cu_count)
-                                 : tg::make_plan_experts(M, N, experts, dtype == TILE_GEMM_BF16_TO_F32, h->cu_count);
+  const tg::Plan p = experts < 0 ? tg::make_plan_block(M, N, K, dtype == TILE_GEMM_BF16_TO_F32, h->cu_count)
+                                 : tg::make_plan_experts(M, N, K, experts, dtype == TILE_GEMM_BF16_TO_F32, h->cu_count);
   tg::BlockArgs a{};
   a.A = static_cast<const uint8_t*>(A);
   a.B = static_cast<const uint8_t*>(B);
@@ -50,6 +50,8 @@ tile_gemm_status_t run_fp8(tile_gemm_t h, const void* A, const void* B, void* C,
   a.groups = (int32_t)experts;
   a.eb = s->b_expert_stride;
   a.esb = s->b_scale_expert_stride;
+  // (experts: whose rows mostly fit one tile)
+  a.once = experts < 0 ? p.map.tiles_m == 1 : 2 * M <= experts * p.bm;
   log_plan(h, experts < 0 ? "run_fp8" : "run_fp8_experts", M, N, K, 1, dtype, act, p);
   return hip_status(dispatch_block<0>(p.config, a, experts >= 0, dtype == TILE_GEMM_BF16_TO_BF16, p.grid,
                                       static_cast<hipStream_t>(stream)));

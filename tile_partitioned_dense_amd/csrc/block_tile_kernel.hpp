@@ -1,5 +1,5 @@
 // block_tile_kernel.hpp -- E4M3 products with block scales for outputs of many
-// rows and columns in bf16 (the operands, formula, scales and owned tiles of
+// rows and columns (the operands, formula, scales and owned tiles of
 // block_kernel.hpp).
 #pragma once
 
@@ -35,12 +35,13 @@ __device__ __forceinline__ void finish(floatx4 (&acc)[FM][FN], const BlockArgs& 
   }
 }
 
-template <int BM, int BN, int WM, int WN, bool EXPERTS>
+// WIDE: an fp32 output, its products on bf16 instructions (widen_e4m3).
+template <int BM, int BN, int WM, int WN, bool EXPERTS, bool WIDE>
 __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p) {
   constexpr int NW = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN;
   constexpr int FM = WTM / 16, FN = WTN / 16;
-  static_assert(FM % 2 == 0 && FM >= 4 && FN >= 3 && 128 % WTN == 0, "row parity; one block of B's rows a wave");
+  static_assert(FM % 2 == 0 && FM >= 4 && FN % 2 == 0 && FN >= 4 && 128 % WTN == 0, "row parity; one block of B's rows a wave");
   constexpr int RB = kScaleBlock;         // bytes of a row and stage
   constexpr int A_BYTES = BM * RB, B_BYTES = BN * RB;
   constexpr int A_DMA = A_BYTES / 1024, B_DMA = B_BYTES / 1024;
@@ -67,7 +68,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     return n;
   }();
 
-  constexpr int STORES = FM * (FN / 2);   // of a tile, per wave
+  constexpr int STORES = WIDE ? FM * FN : FM * (FN / 2);  // of a tile, per wave
+  constexpr int ESZ = WIDE ? 4 : 2;       // bytes of an output
   static_assert(FN % 2 == 0 && NU1 + STORES <= 63, "pairs of blocks; the counter");
 
   __shared__ __attribute__((aligned(1024))) uint4 smem[(RING + LDS_EXTRA) / 16];
@@ -186,6 +188,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
         idle(std::integral_constant<int, 0>{}, s);
         idle(std::integral_constant<int, 1>{}, s + 1);
       }
+      wait_vmcnt<0>();
       block_barrier();
       wg += gridDim.x;
       if (wg < n_tiles) {
@@ -208,6 +211,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     // B of the stage; A: rows r < FM - 1 alternate between two sets, which the
     // stages take in turn, row FM - 1 has the third
     i32x8 bq[FN], a[3];
+    bf16x32 aw[WIDE ? 2 : 1], bw[WIDE ? FN : 1];  // WIDE: of the row's parity; of the stage
     floatx4 d[4];            // sums of the last MFMAs, scaled and added two later
     float raw[2], sc[2], sb; // A's scales as read, and times B's, by the row's parity
 #pragma unroll
@@ -240,8 +244,20 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
           wait_lgkmcnt0();
           block_barrier();
         }
-        asm volatile("" : "+v"(a[slot]), "+v"(bq[j]));
-        d[n % 4] = mma_fp8(a[slot], bq[j]);
+        if constexpr (WIDE) {
+          if constexpr (j == 0) widen_e4m3(a[slot], aw[i & 1]);
+          if constexpr (i == 0) widen_e4m3(bq[j], bw[j]);
+          floatx4 c = floatx4{};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            asm volatile("" : "+v"(aw[i & 1][k]), "+v"(bw[j][k]));
+            c = mfma16(bw[j][k], aw[i & 1][k], c);
+          }
+          d[n % 4] = c;
+        } else {
+          asm volatile("" : "+v"(a[slot]), "+v"(bq[j]));
+          d[n % 4] = mma_fp8(a[slot], bq[j]);
+        }
         // reads: the next row of A and its scale; in the last two rows the next
         // stage's first one, and its blocks of B as this stage's are done with
         if constexpr (q < 0) {
@@ -279,6 +295,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     }
     add(std::integral_constant<int, FM * FN - 2>{});
     add(std::integral_constant<int, FM * FN - 1>{});
+    wait_vmcnt<0>();  // (zeros past the last stage)
     wait_lgkmcnt0();
     block_barrier();  // the ring is free
 
@@ -293,37 +310,45 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     }
     // v_permlane exchanges of the packed blocks j and j + 1 leave a lane 8
     // consecutive columns: of block j + lg / 2, columns 8 (lg % 2) ..
-    int row = wm * WTM + l16, col = wn * WTN + 16 * (lg >> 1) + 8 * (lg & 1);
+    int row = wm * WTM + l16, col = wn * WTN + (WIDE ? 4 * lg : 16 * (lg >> 1) + 8 * (lg & 1));
     asm volatile("" : "+v"(row), "+v"(col));  // (formed here: held over the stages they spilled)
-    const int64_t c_bytes = ((int64_t)(end_c - 1 - row0_c) * p.ldc + (N - col0_c)) * 2;
-    uint16_t* const c_tile = static_cast<uint16_t*>(p.C) + (int64_t)row0_c * p.ldc + col0_c;
+    const int64_t c_bytes = ((int64_t)(end_c - 1 - row0_c) * p.ldc + (N - col0_c)) * ESZ;
+    char* const c_tile = static_cast<char*>(p.C) + ((int64_t)row0_c * p.ldc + col0_c) * ESZ;
     const auto rsC = __builtin_amdgcn_make_buffer_rsrc(c_tile, 0, c_bytes > 0x7fffffffll ? 0x7fffffff : (int)c_bytes,
                                                        0x00020000);
     static_for<0, FM>([&](auto i_c) {
       constexpr int i = decltype(i_c)::value;
-      static_for<0, FN / 2>([&](auto h_c) {
-        constexpr int j = 2 * decltype(h_c)::value;
+      static_for<0, WIDE ? FN : FN / 2>([&](auto h_c) {
+        constexpr int j = (WIDE ? 1 : 2) * decltype(h_c)::value;
         u32x4v v;
+        if constexpr (WIDE) {
+          v = __builtin_bit_cast(u32x4v, acc[i][j]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const auto r = __builtin_amdgcn_permlane32_swap(pack_bf16x2(acc[i][j][2 * e], acc[i][j][2 * e + 1]),
-                                                          pack_bf16x2(acc[i][j + 1][2 * e], acc[i][j + 1][2 * e + 1]),
-                                                          false, false);
-          const auto t = __builtin_amdgcn_permlane16_swap(r[0], r[1], false, false);
-          v[e] = t[0];
-          v[2 + e] = t[1];
+          for (int e = 0; e < 2; ++e) {
+            const auto r = __builtin_amdgcn_permlane32_swap(
+                pack_bf16x2(acc[i][j][2 * e], acc[i][j][2 * e + 1]),
+                pack_bf16x2(acc[i][j + 1][2 * e], acc[i][j + 1][2 * e + 1]), false, false);
+            const auto t = __builtin_amdgcn_permlane16_swap(r[0], r[1], false, false);
+            v[e] = t[0];
+            v[2 + e] = t[1];
+          }
         }
         if (!edge) {
           // rows past the last lie past the end of the resource
-          __builtin_amdgcn_raw_buffer_store_b128(v, rsC, (int)(((row + 16 * i) * (int)p.ldc + col + 16 * j) * 2), 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(v, rsC, (int)(((row + 16 * i) * (int)p.ldc + col + 16 * j) * ESZ), 0, 0);
         } else if (row0_c + row + 16 * i < end_c) {
+          constexpr int EPC = 16 / ESZ;
           const int c = col0_c + col + 16 * j;
-          uint16_t* o = c_tile + (int64_t)(row + 16 * i) * p.ldc + col + 16 * j;
-          if (c + 8 <= N) *reinterpret_cast<u32x4v*>(o) = v;
+          char* o = c_tile + ((int64_t)(row + 16 * i) * p.ldc + col + 16 * j) * ESZ;
+          if (c + EPC <= N) *reinterpret_cast<u32x4v*>(o) = v;
           else
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (c + e < N) o[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+            for (int e = 0; e < EPC; ++e)
+              if (c + e < N) {
+                if constexpr (WIDE) reinterpret_cast<uint32_t*>(o)[e] = v[e];
+                else reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+              }
         }
       });
     });
