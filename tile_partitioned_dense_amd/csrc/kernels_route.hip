@@ -471,7 +471,7 @@ __global__ __launch_bounds__(1024) void place_kernel(PlaceArgs p) {
   }
 }
 
-// Eight columns of a token per thread.
+// Eight columns of a token per thread, eight of its rows in flight at a time.
 template <bool BF16>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs p) {
   const int per = (p.N + 7) / 8;
@@ -483,20 +483,30 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs p) {
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-#pragma unroll 4
-  for (int j = 0; j < p.k; ++j) {
-    const int at_j = p.places[t * p.k + j];
-    if ((uint32_t)at_j >= (uint32_t)p.z_rows) continue;
-    const float w = p.weights ? p.weights[t * p.k + j] : 1.0f;
-    const uint16_t* z = p.Z + (int64_t)at_j * p.ldz + c;
-    uint4 v;
-    if (full) v = *reinterpret_cast<const uint4*>(z);
-    else v = load8_masked(z - c, c, p.N);
-    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+  for (int j0 = 0; j0 < p.k; j0 += 8) {
+    uint4 v[8];
+    float w[8];
+    bool on[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y[2 * e] = fmaf(w, __builtin_bit_cast(float, d[e] << 16), y[2 * e]);
-      y[2 * e + 1] = fmaf(w, __builtin_bit_cast(float, d[e] & 0xffff0000u), y[2 * e + 1]);
+    for (int j = 0; j < 8; ++j) {
+      const int row = j0 + j < p.k ? p.places[t * p.k + j0 + j] : -1;
+      on[j] = (uint32_t)row < (uint32_t)p.z_rows;
+      w[j] = on[j] && p.weights ? p.weights[t * p.k + j0 + j] : 1.0f;
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (on[j]) {
+        const uint16_t* z = p.Z + (int64_t)row * p.ldz;
+        v[j] = full ? load16_stream(z + c) : load8_masked(z, c, p.N);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!on[j]) continue;  // (a weight that is not finite counts for its place only)
+      const uint32_t d[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[2 * e] = fmaf(w[j], __uint_as_float(d[e] << 16), y[2 * e]);
+        y[2 * e + 1] = fmaf(w[j], __uint_as_float(d[e] & 0xffff0000u), y[2 * e + 1]);
+      }
     }
   }
   if constexpr (BF16) {
