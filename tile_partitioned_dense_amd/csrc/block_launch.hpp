@@ -33,7 +33,7 @@ struct RouteArgs {
   int32_t T, E, k;
   int32_t groups, top_groups, group_top;
   int32_t sigmoid, renorm;
-  int32_t wide;        // rows of whole 16 bytes, 16-byte aligned
+  int32_t wide;        // rows of whole 16 bytes, they and the bias 16-byte aligned
   float scale;
   // gradient
   const float* dweights;

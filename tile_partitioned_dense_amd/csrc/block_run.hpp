@@ -57,10 +57,11 @@ tile_gemm_status_t run_fp8(tile_gemm_t h, const void* A, const void* B, void* C,
                                       static_cast<hipStream_t>(stream)));
 }
 
-tg::RouteArgs route_args(const void* logits, int64_t T, int64_t E, int64_t k, int64_t ld,
+tg::RouteArgs route_args(const void* logits, const float* bias, int64_t T, int64_t E, int64_t k, int64_t ld,
                          const tile_gemm_route_t* o) {
   tg::RouteArgs a{};
   a.logits = logits;
+  a.bias = bias;
   a.ld = ld;
   a.T = (int32_t)T;
   a.E = (int32_t)E;
@@ -70,7 +71,7 @@ tg::RouteArgs route_args(const void* logits, int64_t T, int64_t E, int64_t k, in
   a.group_top = o->group_top;
   a.sigmoid = o->score == TILE_GEMM_SCORE_SIGMOID;
   a.renorm = o->renormalize != 0;
-  a.wide = (uintptr_t)logits % 16 == 0 && ld * (o->logits_type == TILE_GEMM_LOGITS_BF16 ? 2 : 4) % 16 == 0;
+  a.wide = (uintptr_t)logits % 16 == 0 && (uintptr_t)bias % 16 == 0 && ld * (o->logits_type == TILE_GEMM_LOGITS_BF16 ? 2 : 4) % 16 == 0;
   a.scale = o->scale;
   return a;
 }
@@ -125,8 +126,7 @@ tile_gemm_status_t tile_gemm_run_route(tile_gemm_t h, const void* logits, const 
   TG_TRY(check_route(logits, bias, ids, weights, T, E, k, logit_stride, options));
   if (T == 0) return TILE_GEMM_OK;
   TG_TRY(check_device(h));
-  tg::RouteArgs a = route_args(logits, T, E, k, logit_stride, options);
-  a.bias = bias;
+  tg::RouteArgs a = route_args(logits, bias, T, E, k, logit_stride, options);
   a.ids = ids;
   a.weights = weights;
   return hip_status(tg::launch_route(a, options->logits_type == TILE_GEMM_LOGITS_BF16,
@@ -141,7 +141,7 @@ tile_gemm_status_t tile_gemm_run_route_backward(tile_gemm_t h, const void* logit
   TG_TRY(check_route_backward(logits, ids, dweights, dlogits, T, E, k, logit_stride, dlogit_stride, options));
   if (T == 0) return TILE_GEMM_OK;
   TG_TRY(check_device(h));
-  tg::RouteArgs a = route_args(logits, T, E, k, logit_stride, options);
+  tg::RouteArgs a = route_args(logits, nullptr, T, E, k, logit_stride, options);
   a.ids = const_cast<int32_t*>(ids);
   a.dweights = dweights;
   a.dlogits = dlogits;

@@ -10,11 +10,9 @@ namespace {
 constexpr int kRouteMaxE = 1024, kRouteMaxK = 32;
 
 template <bool BF16>
-__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
-  float v;
-  if constexpr (BF16) v = __builtin_bit_cast(float, (uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
-  else v = static_cast<const float*>(p)[i];
-  return v == v ? v : -INFINITY;  // NaN: an expert that is not there
+__device__ __forceinline__ float load_value(const void* p, int64_t i) {
+  if constexpr (BF16) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+  else return static_cast<const float*>(p)[i];
 }
 
 __device__ __forceinline__ double shfl_xor_f64(double v, int m) { return __shfl_xor(v, m, 64); }
@@ -52,7 +50,7 @@ __device__ __forceinline__ void scores_of(const float (&l)[PL], int E, int lane,
 // that the lowest lane and then the lowest slot is the lowest index. Measured on
 // 8191 tokens of 256 experts, 8 of them (sigmoid, bias, 8 groups), with scores in
 // 64 bits: a whole wave a token, its steps by LDS exchanges, 34 us; this form
-// ROUTE_US.
+// 13.5 us (with the two-half keys and the groups below).
 
 // v of the lane STEP before in its row of 16
 template <int STEP>
@@ -136,10 +134,30 @@ __device__ __forceinline__ uint64_t order_key(double v) {
   return (int64_t)b < 0 ? ~b : b | (1ull << 63);
 }
 
-struct Chosen {
-  double score;
-  int32_t id, pad;
-};
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t l = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, false);
+  const uint32_t h = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+}
+template <int L>
+__device__ __forceinline__ uint32_t max_token_u32(uint32_t v) {
+  v = max(v, lane_step<8>(v));
+  v = max(v, lane_step<4>(v));
+  v = max(v, lane_step<2>(v));
+  v = max(v, lane_step<1>(v));
+  uint32_t x, y;
+  if constexpr (L > 16) {
+    lane_pair<16>(v, x, y);
+    v = max(x, y);
+  }
+  if constexpr (L > 32) {
+    lane_pair<32>(v, x, y);
+    v = max(x, y);
+  }
+  return v;
+}
 
 // A wave's own LDS: what its lanes wrote is read by its other lanes.
 __device__ __forceinline__ void wave_lds_sync() {
@@ -150,153 +168,248 @@ __device__ __forceinline__ void wave_lds_sync() {
 template <int L, int PL, bool BF16>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
   constexpr int TPW = 64 / L, TPG = 256 / L;  // tokens of a wave and of the workgroup
-  __shared__ Chosen chosen[TPG][kRouteMaxK];
+  __shared__ int32_t chosen[TPG][kRouteMaxK];
   extern __shared__ double groups_lds[];      // with groups: E values and `groups` of them a token
   const int lane = threadIdx.x & 63, sub = lane % L, q = lane / L;
   const int slot = threadIdx.x / L;
   const int64_t t = (int64_t)blockIdx.x * TPG + slot;
   const bool live = t < p.T;  // (no barrier below: a wave works alone)
   const int e0 = sub * PL;
-  float l[PL];
+  // (no branch around a load: each would be waited for by itself; experts and
+  // tokens past the last read the last one's)
+  float l[PL], bias[PL];
+  const int64_t row = (live ? t : p.T - 1) * p.ld;
+  constexpr int V = BF16 ? 8 : 4;  // logits of 16 bytes
+  if (PL % V == 0 && p.wide && e0 + PL <= p.E) {
+    if constexpr (PL % V == 0) {
+      uint4 w[PL / V];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) l[i] = -INFINITY;
-  if (live) {
-    const int64_t at = t * p.ld + e0;
-    if (p.wide && e0 + PL <= p.E) {
-      constexpr int V = BF16 ? 8 : 4;  // of 16 bytes
-      if constexpr (PL >= V) {
+      for (int i = 0; i < PL / V; ++i)
+        w[i] = reinterpret_cast<const uint4*>(static_cast<const char*>(p.logits) + (row + e0) * (BF16 ? 2 : 4))[i];
 #pragma unroll
-        for (int i = 0; i < PL; i += V) {
-          const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.logits) + (at + i) * (BF16 ? 2 : 4));
-          const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const uint32_t u = BF16 ? (e & 1 ? d[e / 2] & 0xffff0000u : d[e / 2] << 16) : d[e % 4];
-            const float x = __uint_as_float(u);
-            l[i + e] = x == x ? x : -INFINITY;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < PL; ++i) l[i] = load_logit<BF16>(p.logits, at + i);
+      for (int i = 0; i < PL; ++i) {
+        const uint32_t d[4] = {w[i / V].x, w[i / V].y, w[i / V].z, w[i / V].w};
+        const uint32_t u = BF16 ? (i & 1 ? d[i % V / 2] & 0xffff0000u : d[i % V / 2] << 16) : d[i % V % 4];
+        l[i] = __uint_as_float(u);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < PL; ++i)
-        if (e0 + i < p.E) l[i] = load_logit<BF16>(p.logits, at + i);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) l[i] = load_value<BF16>(p.logits, row + min(e0 + i, p.E - 1));
   }
+  if (!p.bias) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) bias[i] = 0.0f;
+  } else if (p.wide && e0 + PL <= p.E) {
+#pragma unroll
+    for (int i = 0; i < PL; i += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(p.bias + e0 + i);
+      bias[i] = b.x;
+      bias[i + 1] = b.y;
+      bias[i + 2] = b.z;
+      bias[i + 3] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) bias[i] = p.bias[min(e0 + i, p.E - 1)];
+  }
+#pragma unroll
+  for (int i = 0; i < PL; ++i)  // (NaN: an expert that is not there)
+    l[i] = e0 + i < p.E && l[i] == l[i] ? l[i] : -INFINITY;
+  // the score of a logit: 1 / (1 + e^-l), or e^(l - m) / sum (an infinite largest
+  // logit: those experts share the weight; no finite logit at all: every score
+  // is 0)
+  float m = 0.0f;
+  double sum = 1.0;
+  auto part = [&](float x) { return x == m ? (m == -INFINITY ? 0.0 : 1.0) : exp((double)x - (double)m); };
   double s[PL];
   if (p.sigmoid) {
 #pragma unroll
     for (int i = 0; i < PL; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
   } else {
-    float m = -INFINITY;
+    m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PL; ++i) m = fmaxf(m, l[i]);
     m = max_token<L>(m);
-    double sum = 0.0;
+    sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      // (an infinite largest logit: those experts share the weight; no finite
-      // logit at all: every score is 0)
-      s[i] = l[i] == m ? (m == -INFINITY ? 0.0 : 1.0) : exp((double)l[i] - (double)m);
+      s[i] = part(l[i]);
       sum += s[i];
     }
     sum = sum_token<L>(sum);
 #pragma unroll
     for (int i = 0; i < PL; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
   }
-  uint64_t key[PL];  // of the experts that may still be chosen, else 0
-  double* const value = groups_lds + slot * (p.E + p.groups);
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    key[i] = 0;
-    if (e0 + i < p.E) {
-      double v = s[i];
-      if (p.bias) v += (double)p.bias[e0 + i];
-      if (!(v == v)) v = -INFINITY;
-      key[i] = order_key(v);
-      if (p.groups > 1) value[e0 + i] = v;
-    }
+  for (int i = 0; i < PL; ++i) {  // values from here on
+    s[i] += (double)bias[i];
+    if (!(s[i] == s[i])) s[i] = -INFINITY;
   }
+  bool open = true;      // whether this lane's experts may be chosen, all of them
+  uint64_t groups_open = ~0ull;  // or those of these groups
+  const int size = p.E / p.groups;
+  const int per = size / PL;  // lanes of a group
   if (p.groups > 1) {
+    double* const value = groups_lds + slot * (p.E + p.groups);
     double* const best = value + p.E;
-    const int size = p.E / p.groups;
-    wave_lds_sync();
-    for (int g = sub; g < p.groups; g += L) {
-      double a = -INFINITY, b = -INFINITY;  // the group's two largest
-      int j = g % size;                     // (groups start at different banks)
-      for (int n = 0; n < size; ++n) {
-        const double x = value[g * size + j];
-        if (++j == size) j = 0;
-        b = fmax(b, fmin(a, x));
-        a = fmax(a, x);
+    // whole lanes, 1, 2, 4, 8 or 16 of them, to a group: its two largest by lane
+    // exchanges (8191 tokens of 256 experts in 8 groups: 2.5 us less than
+    // through LDS)
+    if (size % PL == 0 && (per & (per - 1)) == 0 && per <= 16) {
+      double a = -INFINITY, b = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < PL; ++i) {
+        b = fmax(b, fmin(a, s[i]));
+        a = fmax(a, s[i]);
       }
+      auto both = [&](auto step) {
+        const double x = step(a), y = step(b);
+        b = fmax(fmin(a, x), fmax(b, y));
+        a = fmax(a, x);
+      };
+      // (each step's lanes hold one pair in every 1, 2, 4, 8: mirrors exchange them)
+      if (per > 1) both([](double v) { return dpp_f64<0xb1>(v); });    // quad_perm 1 0 3 2
+      if (per > 2) both([](double v) { return dpp_f64<0x4e>(v); });    // quad_perm 2 3 0 1
+      if (per > 4) both([](double v) { return dpp_f64<0x141>(v); });   // row_half_mirror
+      if (per > 8) both([](double v) { return dpp_f64<0x140>(v); });   // row_mirror
       double v = p.group_top > 1 && size > 1 ? a + b : a;
       if (!(v == v)) v = -INFINITY;
-      best[g] = v;
-    }
-    wave_lds_sync();
-    uint64_t open = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += L) {
-      const int g = g0 + sub;
-      int before = 0;  // groups before this one
-      if (g < p.groups) {
-        const double v = best[g];
-        for (int h = 0; h < p.groups; ++h) {
-          const double x = best[h];
-          before += x > v || (x == v && h < g);
-        }
+      const int g = e0 / size;
+      if (g < p.groups && sub % per == 0) best[g] = v;
+      wave_lds_sync();
+      int before = 0;
+      for (int h0 = 0; h0 < p.groups; h0 += 8) {
+        double x[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) x[h] = best[min(h0 + h, p.groups - 1)];
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+          before += h0 + h < p.groups && (x[h] > v || (x[h] == v && h0 + h < g));
       }
-      uint64_t on = __ballot(g < p.groups && before < p.top_groups);
-      if constexpr (L < 64) on = on >> (q * L) & ((1ull << L) - 1);
-      open |= on << g0;
+      open = before < p.top_groups;
+    } else {
+#pragma unroll
+      for (int i = 0; i < PL; ++i)
+        if (e0 + i < p.E) value[e0 + i] = s[i];
+      wave_lds_sync();
+      for (int g = sub; g < p.groups; g += L) {
+        double a = -INFINITY, b = -INFINITY;  // the group's two largest
+        int j = g % size;                     // (groups start at different banks)
+        for (int n = 0; n < size; ++n) {
+          const double x = value[g * size + j];
+          if (++j == size) j = 0;
+          b = fmax(b, fmin(a, x));
+          a = fmax(a, x);
+        }
+        double v = p.group_top > 1 && size > 1 ? a + b : a;
+        if (!(v == v)) v = -INFINITY;
+        best[g] = v;
+      }
+      wave_lds_sync();
+      groups_open = 0;
+      for (int g0 = 0; g0 < p.groups; g0 += L) {
+        const int g = g0 + sub;
+        int before = 0;  // groups before this one
+        if (g < p.groups) {
+          const double v = best[g];
+          for (int h = 0; h < p.groups; ++h) {
+            const double x = best[h];
+            before += x > v || (x == v && h < g);
+          }
+        }
+        uint64_t on = __ballot(g < p.groups && before < p.top_groups);
+        if constexpr (L < 64) on = on >> (q * L) & ((1ull << L) - 1);
+        groups_open |= on << g0;
+      }
     }
+  }
+  // order keys in two halves; 0 where an expert cannot be chosen (any more)
+  uint32_t hi[PL], lo[PL];
+  {
     int g = e0 / size, left = size - (e0 - g * size);
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      if (!(open >> g & 1)) key[i] = 0;
+      const uint64_t k = order_key(s[i]);
+      const bool on = e0 + i < p.E && open && (groups_open >> min(g, 63) & 1);
+      hi[i] = on ? (uint32_t)(k >> 32) : 0u;
+      lo[i] = on ? (uint32_t)k : 0u;
       if (--left == 0) {
         left = size;
-        g = min(g + 1, 63);
+        ++g;
       }
     }
   }
   for (int j = 0; j < p.k; ++j) {
-    uint64_t mine = 0;
-    int at = 0;
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (key[i] > mine) {
-        mine = key[i];
-        at = i;
+    for (int i = 0; i < PL; ++i) top = max(top, hi[i]);
+    top = max_token_u32<L>(top);
+    // the experts with that upper half: nearly always one of each token, which
+    // is then the largest value's
+    int at = -1, n = 0;
+#pragma unroll
+    for (int i = PL - 1; i >= 0; --i) {
+      const bool same = hi[i] == top;
+      n += same;
+      at = same ? i : at;
+    }
+    const uint64_t lanes = __ballot(n > 0);
+    bool one = __ballot(n > 1) == 0;
+#pragma unroll
+    for (int x = 0; x < TPW; ++x) {
+      const uint64_t m = L < 64 ? lanes >> (x * (L % 64)) & ((1ull << (L % 64)) - 1) : lanes;
+      one = one && (m & (m - 1)) == 0;
+    }
+    if (!one) {  // by the lower halves, then the lowest index
+      uint32_t low = 0;
+      at = -1;
+#pragma unroll
+      for (int i = PL - 1; i >= 0; --i) {
+        const bool more = hi[i] == top && lo[i] >= low;
+        low = more ? lo[i] : low;
+        at = more ? i : at;
       }
-    const uint64_t top = join_token64<L>(mine, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
-    uint64_t equal = __ballot(mine == top);
-    if constexpr (L < 64) equal = equal >> (q * L) & ((1ull << L) - 1);
-    if (sub == __builtin_ctzll(equal)) {
-      double x = 0.0;
+      const uint32_t best = max_token_u32<L>(low);
+      uint64_t equal = __ballot(at >= 0 && low == best);
+      if constexpr (L < 64) equal = equal >> (q * L) & ((1ull << L) - 1);
+      if (sub != __builtin_ctzll(equal)) at = -1;
+    }
+    if (at >= 0) {
 #pragma unroll
-      for (int i = 0; i < PL; ++i)
-        if (i == at) {
-          x = s[i];
-          key[i] = 0;
-        }
-      chosen[slot][j].score = x;
-      chosen[slot][j].id = e0 + at;
+      for (int i = 0; i < PL; ++i) hi[i] = i == at ? 0u : hi[i];
+      chosen[slot][j] = e0 + at;
     }
   }
   wave_lds_sync();
   if (!live) return;
-  double total = 0.0;
-  if (p.renorm)
-    for (int j = 0; j < p.k; ++j) total += chosen[slot][j].score;
-  for (int j = sub; j < p.k; j += L) {
-    double w = chosen[slot][j].score;
-    if (p.renorm) w = total > 0.0 ? w / total : 0.0;
-    p.ids[t * p.k + j] = chosen[slot][j].id;
-    p.weights[t * p.k + j] = (float)(w * (double)p.scale);
+  // each lane the weights of places sub, sub + L, ..: from the logits again
+  double w[(kRouteMaxK + L - 1) / L], total = 0.0;
+  int id[(kRouteMaxK + L - 1) / L];
+#pragma unroll
+  for (int r = 0; r < (kRouteMaxK + L - 1) / L; ++r) {
+    const int j = sub + r * L;
+    w[r] = 0.0;
+    if (j < p.k) {
+      id[r] = chosen[slot][j];
+      float x = load_value<BF16>(p.logits, row + id[r]);
+      x = x == x ? x : -INFINITY;
+      w[r] = p.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : sum > 0.0 ? part(x) / sum : 0.0;
+    }
+    total += w[r];
+  }
+  if (p.renorm) {
+    total = sum_token<L>(total);
+#pragma unroll
+    for (int r = 0; r < (kRouteMaxK + L - 1) / L; ++r) w[r] = total > 0.0 ? w[r] / total : 0.0;
+  }
+#pragma unroll
+  for (int r = 0; r < (kRouteMaxK + L - 1) / L; ++r) {
+    const int j = sub + r * L;
+    if (j < p.k) {
+      p.ids[t * p.k + j] = id[r];
+      p.weights[t * p.k + j] = (float)(w[r] * (double)p.scale);
+    }
   }
 }
 
@@ -309,7 +422,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteArgs p) {
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = lane + 64 * i;
-    l[i] = e < p.E ? load_logit<BF16>(p.logits, (int64_t)t * p.ld + e) : -INFINITY;
+    l[i] = load_value<BF16>(p.logits, (int64_t)t * p.ld + min(e, p.E - 1));
+    if (e >= p.E || !(l[i] == l[i])) l[i] = -INFINITY;  // (NaN: an expert that is not there)
   }
   double s[PL];
   scores_of<PL>(l, p.E, lane, p.sigmoid, s);
