@@ -356,9 +356,13 @@ tile_gemm_status_t tile_gemm_run_xent_backward(tile_gemm_t h, const void* A, con
  * b_scale[r * b_scale_stride + b]). C, dtype, bias and act (not
  * TILE_GEMM_ACT_SWIGLU) are as for tile_gemm_run_epilogue. A block's products
  * are summed in the matrix instruction, the blocks' sums scaled and added in
- * fp32 in ascending order (outputs of up to 64 rows: up to four such sums, added
- * in a fixed order), each element written once: results are bit-identical from
- * run to run. A NaN or infinite scale reaches the rows (or columns) it scales.
+ * fp32 in ascending order (on tiles of few rows or columns two to eight such
+ * sums, of every second to every eighth block, added in a fixed order), each
+ * element written once: results are bit-identical from run to run. fp32 outputs
+ * come of bf16 matrix instructions, which add the exact products in fp32; bf16
+ * outputs of the E4M3 ones, which cut each run of 8 products at 2^-14 of its
+ * largest (1.5e-5 of the result, far below the rounding to bf16). A NaN or
+ * infinite scale reaches the rows (or columns) it scales.
  *
  * Limits: K a multiple of 16; M, N, K and the strides of A, B and C below 2^22; A
  * and B 16-byte aligned with leading dimensions of whole 16 bytes, scales
@@ -388,9 +392,10 @@ tile_gemm_status_t tile_gemm_run_fp8(tile_gemm_t h, const void* A, const void* B
  * device, as tile_gemm_run_place gives them) and an N x K matrix and scales of
  * its own, b_expert_stride bytes and b_scale_expert_stride floats apart.
  * No bias, no activation. Rows of C outside every expert's are left as they
- * were. Offsets are cut to [0, M]; where they decrease an expert is empty, and
- * rows that two experts claim hold either one's result. 1 <= E <= 1024; one
- * expert's matrix spans less than 2 GiB.
+ * were. Offsets are cut to [0, M]. Where they decrease an expert is empty, and
+ * it is open which one's result a row holds that several claim; where more rows
+ * are claimed than M and E more tiles of one kernel hold, rows may be left as
+ * they were. 1 <= E <= 1024; one expert's matrix spans less than 2 GiB.
  */
 tile_gemm_status_t tile_gemm_run_fp8_experts(tile_gemm_t h, const void* A, const void* B, void* C,
                                              int64_t M, int64_t N, int64_t K, int64_t E,
@@ -449,7 +454,7 @@ tile_gemm_status_t tile_gemm_run_quantize(tile_gemm_t h, const void* X, void* Q,
  * -inf; experts at -inf are chosen last. Softmax: logits of +inf share the
  * weight; a token without a finite logit has scores 0.
  * 1 <= E <= 1024, groups <= 64 a divisor of E, k <= 32 and at most the experts
- * of top_groups groups; T and the strides below 2^31.
+ * of top_groups groups; T below 2^25, the strides below 2^31.
  */
 typedef enum { TILE_GEMM_SCORE_SOFTMAX = 0, TILE_GEMM_SCORE_SIGMOID = 1 } tile_gemm_score_t;
 typedef enum { TILE_GEMM_LOGITS_F32 = 0, TILE_GEMM_LOGITS_BF16 = 1 } tile_gemm_logits_t;
@@ -503,7 +508,7 @@ tile_gemm_status_t tile_gemm_run_place(tile_gemm_t h, const int32_t* ids, int64_
  * over the places inside Z's z_rows rows (others, -1 among them, are left out),
  * in fp32 in the order of j. Z is bf16, Y bf16 or fp32 (dtype), both row-major
  * with leading dimensions of whole 16 bytes; weights T x k fp32 or NULL (ones).
- * 1 <= k <= 64.
+ * 1 <= k <= 64; T and N below 2^22, T N / 8 below 2^32 - 512.
  */
 tile_gemm_status_t tile_gemm_run_combine(tile_gemm_t h, const void* Z, const int32_t* places,
                                          const float* weights, void* Y, int64_t T, int64_t N, int64_t k,

@@ -52,6 +52,7 @@ def fp8(E=None, **kw):
     (dict(M=-1), SHAPE), (dict(M=1 << 22), SHAPE), (dict(N=1 << 22), SHAPE), (dict(K=1 << 22), SHAPE),
     (dict(K=264), SHAPE),
     (dict(M=(1 << 22) - 16, N=(1 << 22) - 16, K=16), SHAPE),  # too many tiles
+    (dict(M=(1 << 22) - 16, N=(1 << 18) + 64, K=16), SHAPE),   # (of 16 x 32)
     (dict(a_stride=256), STRIDE), (dict(a_stride=1 << 22), STRIDE), (dict(a_stride=280), MISALIGNED),
     (dict(b_stride=256), STRIDE), (dict(b_stride=280), MISALIGNED),
     (dict(c_stride=196), STRIDE), (dict(c_stride=202), MISALIGNED),
@@ -136,6 +137,7 @@ COMMON = [
     (dict(scale=float("nan")), SHAPE), (dict(scale=float("inf")), SHAPE), (dict(options=None), NULL),
     (dict(E=0), SHAPE), (dict(E=1024), OK), (dict(E=1025), SHAPE), (dict(k=0), SHAPE), (dict(k=32), OK),
     (dict(k=33), SHAPE), (dict(T=-1), SHAPE), (dict(T=1 << 31), SHAPE), (dict(ld=63), STRIDE),
+    (dict(T=1 << 25), SHAPE),
     (dict(T=0, logits=None, ids=None, weights=None, dlogits=None), OK),
     (dict(logits=None), NULL), (dict(ids=None), NULL), (dict(weights=None), NULL),
     (dict(logits=A0 + 2), MISALIGNED), (dict(logits=A0 + 2, logits_type=1), OK), (dict(ids=IDS + 2), MISALIGNED),
@@ -208,6 +210,7 @@ def combine(**kw):
     (dict(z_rows=0, Z=None), OK), (dict(z_rows=-1), SHAPE),
     (dict(T=0, places=None, Y=None, weights=None), OK), (dict(N=0, Z=None, Y=None), OK),
     (dict(k=0), SHAPE), (dict(k=64), OK), (dict(k=65), SHAPE), (dict(T=1 << 22), SHAPE), (dict(N=1 << 22), SHAPE),
+    (dict(T=(1 << 22) - 1, N=8200), SHAPE),  # threads of one launch
     (dict(Z=None), NULL), (dict(places=None), NULL), (dict(Y=None), NULL),
     (dict(ldz=196), STRIDE), (dict(ldy=196), STRIDE), (dict(ldz=204), MISALIGNED), (dict(ldy=204), MISALIGNED),
     (dict(Z=A0 + 2), MISALIGNED), (dict(places=IDS + 2), MISALIGNED),

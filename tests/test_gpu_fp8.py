@@ -1,6 +1,8 @@
 """The E4M3 products with block scales, for one weight and for rows sorted by
 expert, and the quantization, against plain 64-bit references."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -299,6 +301,56 @@ def test_experts_bad_offsets(g):
     assert bool(got.isfinite().all())
 
 
+def test_experts_zigzag_offsets(g):
+    """Every other expert claims all rows: far more row tiles than the output
+    has. Any expert's result or none in a row, nothing outside of C."""
+    M, N, K, E = 300, 72, 144, 200
+    a, _, _, _ = operands(M, N, K)
+    one, sa = torch.full((E, N, K), 1.0).to(bh.FP8).cuda(), to_row_scales(torch.ones(M, 2))
+    whole, c = out_like(M, N, torch.float32)
+    off = torch.tensor(([0, M] * E)[:E + 1], dtype=torch.int32, device="cuda")
+    g.fp8_experts(a.cuda(), one, c, sa, torch.ones(E, 1, 2, device="cuda"), off)
+    want = a.double().sum(1, keepdim=True).expand(M, N)
+    got = c.cpu().double()
+    near = (got - want).abs() <= bh.TAU * a.double().abs().sum(1, keepdim=True)
+    assert bool((near | got.isnan()).all()) and untouched(whole, c)
+
+
+def test_single_rows_and_blocks_of_any_stride(g):
+    """The stride of a single row, or of a single block's scales, is not looked at."""
+    for M, N, K in ((1, 300, 128), (70, 128, 112), (300, 100, 16), (1, 28690, 16)):
+        a, sa, b, sb = operands(M, N, K)
+        want, err = bh.product(a, sa, b, sb, fp32=True)
+        s = tg.Fp8Strides(a_stride=-5 if M == 1 else K, b_stride=K, c_stride=-9 if M == 1 else N,
+                          a_scale_stride=-(1 << 40), b_scale_stride=-3 if N <= 128 else 1)
+        ad, bd, sad, sbd, c = (a.cuda(), b.cuda(), sa.t().contiguous().cuda(), sb.cuda(),
+                               torch.full((M, N), NAN, device="cuda"))
+        status = tg.load_library().tile_gemm_run_fp8(
+            g.handle, ad.data_ptr(), bd.data_ptr(), c.data_ptr(), M, N, K, ctypes.byref(s), sad.data_ptr(),
+            sbd.data_ptr(), 0, None, 0, torch.cuda.current_stream().cuda_stream)
+        assert status == 0, tg.last_error_detail()
+        bh.close(c, want, err, False, f"{M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("config", [0, 1, 2])
+def test_far_rows(g, config, dtype):
+    """Rows of C as far apart as they may be: a tile of 256 of them spans 4 GiB."""
+    shape = smallest_shapes(0).get((config, dtype))
+    if shape is None:
+        assert (config, dtype) == (0, torch.float32)
+        return
+    M, N, K = shape
+    print(f"[fp8 far {config}: {M}x{N}x{K} {dtype}]", flush=True)
+    a, b, sa, sb = (integers(1, M, K), integers(2, N, K), powers(3, M, bh.blocks(K)),
+                    powers(4, bh.blocks(N), bh.blocks(K)))
+    want = wide(a, sa, 1).double() @ wide(b, sb, 128).double().T
+    c = torch.empty(M, (1 << 22) - 8, dtype=dtype, device="cuda")[:, :N]
+    c.fill_(NAN)
+    g.fp8(a.cuda(), b.cuda(), c, to_row_scales(sa), sb.cuda())
+    assert torch.equal(c.double(), want.to(dtype).double())
+
+
 def test_expert_matrices_past_4_gib(g):
     """The last experts' matrices and scales, 4 GiB and more behind the first's."""
     E, N, K = 40, 8192, 16384
@@ -394,6 +446,27 @@ def test_quantize_gathered(g):
     q, s = q.cpu(), s.cpu()
     assert torch.equal(q[on], want_q.view(torch.uint8)[rows[on].long()]) and torch.equal(s[on], want_s[rows[on].long()])
     assert bool((q[~on] == 0x55).all()) and bool((s[~on] == -5.0).all())
+
+
+@pytest.mark.parametrize("form", ["ROWS", "BLOCKS"])
+def test_quantize_many_rows(g, form):
+    """More rows than the workgroups a grid has along a second axis of 65535."""
+    M = 8500003 // 8 if form == "ROWS" else (1 << 22) - 5
+    x = (torch.arange(M, device="cuda") % 251 + 1).bfloat16()[:, None].expand(M, 16).contiguous()
+    q = torch.zeros(M, 16, dtype=torch.uint8, device="cuda")
+    if form == "ROWS":
+        s = bh.row_scales(M, 16, "cuda")
+        g.quantize(x, q, s)
+        assert bool((q == 0x7e).all())  # 448
+        # (the nearest fp32 value; a division of tensors on the GPU may be a product by 1 / 448)
+        assert torch.equal(s[:, 0], (x[:, 0].double() / 448).float())
+    else:
+        s = torch.zeros(bh.blocks(M), 1, device="cuda")
+        g.quantize(x, q, s, form=tg.Quant.BLOCKS)
+        top = torch.nn.functional.pad(x[:, 0].float(), (0, -M % 128)).view(-1, 128).amax(1)
+        assert torch.equal(s[:, 0], (top.double() / 448).float())
+        back = q.view(bh.FP8).float() * s.repeat_interleave(128, 0)[:M]
+        assert bool(((back - x.float()).abs() <= x.float() / 16 * 1.0001).all())
 
 
 @pytest.mark.parametrize("gate", ["SILU", "GELU", "GELU_TANH", "RELU", "SIGMOID"])

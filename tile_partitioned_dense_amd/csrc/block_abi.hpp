@@ -12,6 +12,7 @@ namespace {
 constexpr int64_t kMax22 = (int64_t)1 << 22;
 constexpr int64_t kPlaceRound = 1024;       // entries a workgroup places at a time
 constexpr int64_t kPlaceMaxChunks = 128;    // workgroups of a call
+constexpr int64_t kMaxRouteT = (int64_t)1 << 25;  // up to 64 threads each, a launch has less than 2^32
 constexpr int64_t kMaxRouteK = 32, kMaxCombineK = 64, kMaxGroups = 64;
 
 tile_gemm_status_t check_dtype(int dtype) {
@@ -54,9 +55,9 @@ tile_gemm_status_t check_fp8(const void* A, const void* B, const void* C, int64_
   if (act < TILE_GEMM_ACT_NONE || act > TILE_GEMM_ACT_SILU)
     return fail(TILE_GEMM_ERR_EPILOGUE, "act: %d is not available for the E4M3 product", act);
   if (M == 0 || N == 0) return TILE_GEMM_OK;
-  // the kernels number tiles (16 x 64 at the smallest, and a part of one for
+  // the kernels number tiles (16 x 32 at the smallest, and a part of one for
   // each expert) in 32 bits
-  if ((tg::ceil_div(M, 16) + (experts > 0 ? experts : 0)) * tg::ceil_div(N, 64) >= kMaxDim)
+  if ((tg::ceil_div(M, 16) + (experts > 0 ? experts : 0)) * tg::ceil_div(N, 32) >= kMaxDim)
     return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: M=%lld N=%lld, too many tiles for one call", (long long)M,
                 (long long)N);
   const int64_t kb = tg::ceil_div(K, tg::kScaleBlock), nb = tg::ceil_div(N, tg::kScaleBlock);
@@ -131,7 +132,7 @@ tile_gemm_status_t check_route_common(int64_t T, int64_t E, int64_t k, int64_t l
     return fail(TILE_GEMM_ERR_DTYPE, "logits_type: unknown value %d", (int)o->logits_type);
   if (!(o->scale > -INFINITY && o->scale < INFINITY))
     return fail(TILE_GEMM_ERR_BAD_SHAPE, "scale: %g, must be finite", (double)o->scale);
-  TG_TRY(check_range("T", T, 0, kMaxDim));
+  TG_TRY(check_range("T", T, 0, kMaxRouteT));
   TG_TRY(check_range("E", E, 1, tg::kBlockMaxGroups + 1));
   TG_TRY(check_range("k", k, 1, kMaxRouteK + 1));
   return check_stride("logit_stride", ld, E, kMaxDim, T);
@@ -224,8 +225,8 @@ tile_gemm_status_t check_combine(const void* Z, const int32_t* places, const flo
   TG_TRY(check_range("k", k, 1, kMaxCombineK + 1));
   TG_TRY(check_range("z_rows", z_rows, 0, kMaxDim));
   if (T == 0 || N == 0) return TILE_GEMM_OK;
-  // (256 threads of 8 columns each)
-  if (T * tg::ceil_div(N, 8) >= kMaxDim * 256)
+  // (threads of 8 columns each, in workgroups of 256: a launch has less than 2^32)
+  if (T * tg::ceil_div(N, 8) > 2 * kMaxDim - 512)
     return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: T=%lld N=%lld, too many values for one call", (long long)T,
                 (long long)N);
   Arg a[4];
@@ -306,7 +307,7 @@ tile_gemm_status_t tile_gemm_plan_fp8(int64_t M, int64_t N, int64_t K, int64_t E
   TG_TRY(check_range("N", N, 0, kMax22));
   TG_TRY(check_range("K", K, 0, kMax22));
   TG_TRY(check_range("E", E, 0, tg::kBlockMaxGroups + 1));
-  if ((tg::ceil_div(M, 16) + E) * tg::ceil_div(N, 64) >= kMaxDim)
+  if ((tg::ceil_div(M, 16) + E) * tg::ceil_div(N, 32) >= kMaxDim)
     return fail(TILE_GEMM_ERR_BAD_SHAPE, "shape: too many tiles");
   if (cu_count <= 0) return fail(TILE_GEMM_ERR_DEVICE, "cu_count: %d", cu_count);
   fill_plan(E ? tg::make_plan_experts(M, N, K, E, fp32, cu_count) : tg::make_plan_block(M, N, K, fp32, cu_count), out);

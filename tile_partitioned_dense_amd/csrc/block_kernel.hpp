@@ -90,7 +90,8 @@ __device__ __forceinline__ float lds_load_f32(uint32_t addr) {
 }
 
 // Experts: the row tiles before each expert into LDS at pre0 (groups + 1
-// values); the tiles there are.
+// values); the tiles there are. Ascending offsets give at most M / BM + groups
+// row tiles, the number that is checked to fit 32 bits: the rest is cut off.
 template <int BM>
 __device__ __forceinline__ int expert_tiles(const BlockArgs& p, uint32_t pre0, int wave, int lane) {
   if (wave == 0) {
@@ -115,7 +116,8 @@ __device__ __forceinline__ int expert_tiles(const BlockArgs& p, uint32_t pre0, i
     if (lane == 0) lds_store_i32(pre0 + 4u * p.groups, base);
   }
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(lds_load_i32(pre0 + 4u * p.groups)) * p.map.tiles_n;
+  const int most = (p.M + BM - 1) / BM + p.groups;
+  return __builtin_amdgcn_readfirstlane(min(lds_load_i32(pre0 + 4u * p.groups), most)) * p.map.tiles_n;
 }
 
 // The tile of index wg: of the output, or (experts) of one expert's rows, 8 row
@@ -162,6 +164,7 @@ __device__ __forceinline__ BlockTile block_tile(const BlockArgs& p, uint32_t pre
 
 template <int BM, int BN, int WM, int WN, int KS, int SB, int NST, bool EXPERTS, bool OUT_BF16>
 __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockArgs p) {
+  static_assert(NST >= 2, "a stage is read behind the loads of the next");
   constexpr int NW = WM * WN * KS;
   constexpr int WTM = BM / WM, WTN = BN / WN;
   constexpr int FM = WTM / 16, FN = WTN / 16;

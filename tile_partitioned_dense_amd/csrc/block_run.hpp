@@ -37,11 +37,11 @@ tile_gemm_status_t run_fp8(tile_gemm_t h, const void* A, const void* B, void* C,
   a.M = (int32_t)M;
   a.N = (int32_t)N;
   a.K = (int32_t)K;
-  // (the stride of a single row is any: the kernels form offsets of a tile's other rows from it)
+  // (the stride of a single row or block is any: the kernels form offsets of a tile's other ones from it)
   a.lda = M > 1 ? s->a_stride : K;
   a.ldb = N > 1 ? s->b_stride : K;
-  a.ldc = s->c_stride;
-  a.lsa = s->a_scale_stride;
+  a.ldc = M > 1 ? s->c_stride : N;
+  a.lsa = K > tg::kScaleBlock ? s->a_scale_stride : M;
   a.lsb = N > tg::kScaleBlock ? s->b_scale_stride : 0;
   a.map = p.map;
   a.bias = bias;

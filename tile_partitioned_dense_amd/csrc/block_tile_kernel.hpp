@@ -108,6 +108,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
   const uint32_t pre0 = lds0 + RING;
   const int n_tiles = EXPERTS ? expert_tiles<BM>(p, pre0, wave, lane) : p.map.tiles_m * p.map.tiles_n;
   if ((int)blockIdx.x >= n_tiles) return;
+  const bool far = p.ldc * ESZ * BM > 0x7fffffffll;  // a tile of C spans more than a resource
 
   // the tile whose loads are issued
   int m0, n0, m_end;
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
 
     // the next tile's first loads, then this one's store, from registers
     const int row0_c = m0, col0_c = n0, end_c = m_end;
-    const bool edge = n0 + BN > N;
+    const bool edge = n0 + BN > N || far;
     if (p.bias || p.act != kActNone) finish(acc, p, n0 + wn * WTN + 4 * lg);
     wg += gridDim.x;
     if (wg < n_tiles) {
