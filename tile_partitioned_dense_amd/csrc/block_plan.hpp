@@ -18,24 +18,25 @@ struct BlockConfig {
   bool tile;
   // Microseconds of a launch, for bf16 and for fp32 outputs: c0 + rounds (a +
   // stages b), with b going to b2 as a round's tiles come to fill the chip (two
-  // tiles a compute unit where occ is 2). Fitted to 207 shapes of 1 to 4000 rows,
+  // tiles a compute unit where occ is 2). Fitted to 267 shapes of 1 to 6100 rows,
   // 48 to 28672 columns and K of 128 to 8192: the configuration it picks takes
-  // 1.8% longer than the fastest on average (9% or less on 95 of 100).
+  // 1.9% longer than the fastest on average (8% or less on 95 of 100).
   float cost[2][4];
 };
-constexpr int kNumBlockConfigs = 11;
+constexpr int kNumBlockConfigs = 12;
 constexpr BlockConfig kBlockConfigs[kNumBlockConfigs] = {
-    {256, 256, 2, 4, 1, 128, 2, 1, true, {{0.00f, 8.34f, 1.01f, 1.87f}, {}}},   // 0: 8 waves of 128x64 (bf16 outputs)
-    {256, 128, 4, 2, 1, 128, 2, 1, true, {{1.16f, 4.73f, 0.70f, 1.12f}, {0.00f, 7.61f, 0.98f, 1.59f}}},   // 1: 8 waves of 64x64
-    {128, 128, 2, 2, 1, 128, 2, 2, true, {{0.65f, 4.58f, 0.62f, 1.16f}, {0.00f, 6.36f, 0.94f, 1.91f}}},   // 2: 4 waves of 64x64
-    {16, 128, 1, 4, 2, 256, 3, 1, false, {{2.57f, 1.61f, 0.67f, 0.75f}, {2.58f, 1.72f, 0.80f, 0.88f}}},   // 3
-    {32, 128, 1, 4, 2, 256, 3, 1, false, {{2.50f, 1.97f, 0.76f, 0.86f}, {2.49f, 2.39f, 1.00f, 1.11f}}},   // 4
-    {64, 128, 1, 4, 2, 256, 3, 1, false, {{2.50f, 3.03f, 1.06f, 1.24f}, {2.33f, 3.39f, 1.45f, 1.63f}}},   // 5
-    {16, 64, 1, 2, 4, 512, 3, 1, false, {{2.52f, 1.63f, 0.66f, 0.74f}, {2.56f, 1.67f, 0.81f, 0.90f}}},    // 6
-    {32, 64, 1, 2, 4, 512, 3, 1, false, {{2.64f, 2.02f, 0.82f, 0.95f}, {2.55f, 2.40f, 1.06f, 1.18f}}},    // 7
-    {64, 64, 2, 2, 4, 512, 2, 1, false, {{2.99f, 2.35f, 1.04f, 1.29f}, {2.90f, 2.71f, 1.42f, 1.60f}}},    // 8
-    {16, 32, 1, 1, 8, 1024, 3, 1, false, {{2.62f, 1.70f, 0.79f, 0.90f}, {2.69f, 1.64f, 0.94f, 1.08f}}},   // 9
-    {32, 32, 1, 1, 8, 1024, 2, 1, false, {{2.78f, 1.74f, 0.97f, 1.22f}, {2.78f, 1.95f, 1.20f, 1.39f}}},   // 10
+    {256, 256, 2, 4, 1, 128, 2, 1, true, {{0.83f, 7.80f, 1.01f, 1.83f}, {}}},  // 0: 8 waves of 128x64 (bf16 outputs)
+    {192, 256, 2, 4, 1, 128, 2, 1, true, {{0.94f, 5.56f, 0.91f, 1.45f}, {0.00f, 8.25f, 1.67f, 2.56f}}},  // 1: 8 waves of 96x64
+    {256, 128, 4, 2, 1, 128, 2, 1, true, {{1.57f, 3.94f, 0.71f, 1.09f}, {0.00f, 6.79f, 1.05f, 1.75f}}},  // 2: 8 waves of 64x64
+    {128, 128, 2, 2, 1, 128, 2, 2, true, {{0.89f, 3.95f, 0.63f, 1.07f}, {0.00f, 5.77f, 0.96f, 1.80f}}},  // 3: 4 waves of 64x64
+    {16, 128, 1, 4, 2, 256, 3, 1, false, {{2.57f, 1.63f, 0.68f, 0.71f}, {2.62f, 1.74f, 0.81f, 0.84f}}},  // 4
+    {32, 128, 1, 4, 2, 256, 3, 1, false, {{2.55f, 1.99f, 0.77f, 0.81f}, {2.48f, 2.41f, 1.01f, 1.06f}}},  // 5
+    {64, 128, 1, 4, 2, 256, 3, 1, false, {{2.57f, 3.03f, 1.07f, 1.16f}, {2.41f, 3.37f, 1.46f, 1.55f}}},  // 6
+    {16, 64, 1, 2, 4, 512, 3, 1, false, {{2.58f, 1.64f, 0.67f, 0.72f}, {2.57f, 1.69f, 0.82f, 0.87f}}},  // 7
+    {32, 64, 1, 2, 4, 512, 3, 1, false, {{2.67f, 2.05f, 0.83f, 0.90f}, {2.56f, 2.43f, 1.06f, 1.13f}}},  // 8
+    {64, 64, 2, 2, 4, 512, 2, 1, false, {{3.08f, 2.33f, 1.04f, 1.18f}, {2.97f, 2.69f, 1.42f, 1.54f}}},  // 9
+    {16, 32, 1, 1, 8, 1024, 3, 1, false, {{2.60f, 1.72f, 0.80f, 0.88f}, {2.67f, 1.66f, 0.95f, 1.05f}}},  // 10
+    {32, 32, 1, 1, 8, 1024, 2, 1, false, {{2.80f, 1.79f, 0.98f, 1.11f}, {2.81f, 1.98f, 1.20f, 1.32f}}},  // 11
 };
 
 inline int block_lds_bytes(const BlockConfig& c) {

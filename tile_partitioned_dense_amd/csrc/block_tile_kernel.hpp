@@ -68,6 +68,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     return n;
   }();
 
+  constexpr bool LAST = FM * FN < 32;     // an odd last stage by itself (below)
   constexpr int STORES = WIDE ? FM * FN : FM * (FN / 2);  // of a tile, per wave
   constexpr int ESZ = WIDE ? 4 : 2;       // bytes of an output
   static_assert(FN % 2 == 0 && NU1 + STORES <= 63, "pairs of blocks; the counter");
@@ -185,10 +186,12 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
         static_for<0, NU1>([&](auto u_c) { load(std::integral_constant<int, ST>{}, s + 2, decltype(u_c)::value); });
       };
 
-      for (int s = 0; s < nst; s += 2) {
+      int s = 0;
+      for (; LAST ? s + 1 < nst : s < nst; s += 2) {
         idle(std::integral_constant<int, 0>{}, s);
         idle(std::integral_constant<int, 1>{}, s + 1);
       }
+      if (LAST && s < nst) idle(std::integral_constant<int, 0>{}, s);
       wait_vmcnt<0>();
       block_barrier();
       wg += gridDim.x;
@@ -288,12 +291,15 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
         __builtin_amdgcn_sched_barrier(0);
       });
     };
-    // (two at a time, so that the buffers are fixed; with an odd number the last
-    // one is of zeros: a way out in between kept a copy of the accumulators)
-    for (int s = 0; s < nst; s += 2) {
+    // (two at a time, so that the buffers are fixed. An odd last one is done by
+    // itself, 3 to 7% on 33 and 11 of them; on the largest tile that kept a copy
+    // of the accumulators, and one of zeros makes the number even)
+    int s = 0;
+    for (; LAST ? s + 1 < nst : s < nst; s += 2) {
       step(std::integral_constant<int, 0>{}, s);
       step(std::integral_constant<int, 1>{}, s + 1);
     }
+    if (LAST && s < nst) step(std::integral_constant<int, 0>{}, s);
     add(std::integral_constant<int, FM * FN - 2>{});
     add(std::integral_constant<int, FM * FN - 1>{});
     wait_vmcnt<0>();  // (zeros past the last stage)

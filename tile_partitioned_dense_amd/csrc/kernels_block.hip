@@ -11,7 +11,7 @@ namespace tg {
 template <int CFG, bool EXPERTS, bool OB>
 const void* block_fn() {
   constexpr BlockConfig c = kBlockConfigs[CFG];
-  if constexpr (!OB && c.bm * c.bn / (c.wm * c.wn) > 64 * 64) return nullptr;  // (not planned for fp32)
+  if constexpr (!OB && c.bm * c.bn / (c.wm * c.wn) > 96 * 64) return nullptr;  // (not planned for fp32)
   else if constexpr (c.tile)
     return reinterpret_cast<const void*>(&block_tile_kernel<c.bm, c.bn, c.wm, c.wn, EXPERTS, !OB>);
   else return reinterpret_cast<const void*>(
