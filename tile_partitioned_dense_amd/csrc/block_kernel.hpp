@@ -1,6 +1,29 @@
 // block_kernel.hpp -- E4M3 products with float32 scales for blocks of 128.
 //
 //   C[i][j] = sum_b sA[b][i] sB[j / 128][b] * sum_{k in block b} A[i][k] B[j][k]
+//
+// The inner sum is one matrix instruction's (16 x 16 x 128); its fp32 result is
+// scaled and added to the accumulators by an FMA an element: 2 K / 128 VALU
+// operations a value of C against 2 K products, which fit beside the matrix
+// instructions of another wave.
+//
+// This kernel is for outputs of few rows or columns: such a call is bound by
+// reading B once. Tiles of 16, 32 or 64 rows and 32 to 128 columns; the waves of
+// a workgroup share K as well (KS of them, two to eight) where the tile is too
+// small for eight waves, each taking every KS-th block, and the first adds the
+// others' sums through LDS in a fixed order. Operands, the blocks' scales among
+// them, arrive by direct loads to LDS, NST - 1 stages of 64 to 96 KB of both
+// ahead: with 256 units 16 MB and more are under way, what the memory's latency
+// times its rate asks for. Chunks of 16 bytes are kept at positions XORed with
+// their row, so that the 16 rows of a fragment read come from all banks. Rows
+// and chunks past an operand's end are sent past their resource's and arrive
+// as zeros; no load or store depends on a branch.
+//
+// Measured: 16 x 28672 x 8192 36 us (6.5 TB/s; the launch and the first loads
+// are 5 of them); 24 tokens of 8 of 64 experts, 4096 x 2048 each, 76 us (7.1
+// TB/s of the 8 there are). Not faster: tiles cut so that 256 instead
+// of 224 units have one (the memory is as busy with either); the sc0 and sc1
+// cache hints instead of nt.
 #pragma once
 
 #include "mx_kernel.hpp"  // first: the HIP runtime headers plan.hpp relies on under hipcc

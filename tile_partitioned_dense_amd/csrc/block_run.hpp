@@ -146,6 +146,8 @@ tile_gemm_status_t tile_gemm_run_route_backward(tile_gemm_t h, const void* logit
   a.dweights = dweights;
   a.dlogits = dlogits;
   a.ldd = dlogit_stride;
+  a.wide = a.wide && (uintptr_t)dlogits % 16 == 0 &&
+           dlogit_stride * (options->logits_type == TILE_GEMM_LOGITS_BF16 ? 2 : 4) % 16 == 0;
   return hip_status(tg::launch_route_backward(a, options->logits_type == TILE_GEMM_LOGITS_BF16,
                                               static_cast<hipStream_t>(stream)));
 }

@@ -1,6 +1,30 @@
 // block_tile_kernel.hpp -- E4M3 products with block scales for outputs of many
 // rows and columns (the operands, formula, scales and owned tiles of
 // block_kernel.hpp).
+//
+// One persistent workgroup a compute unit (two of the 128 x 128 ones) takes
+// tiles of one XCD's run, 256 x 256 where the output fills the chip with them.
+// Two stages of 128 bytes of K are in LDS (131 KB). A stage is one pass over the
+// wave's blocks, row by row: a matrix instruction, the fragment reads that later
+// ones need, a part of the loads of the stage after next and the scaling of the
+// sum formed two instructions ago, pinned in this order (left to itself the
+// compiler moves them together and spills). One barrier a stage, before the last
+// two rows of blocks: these are worked column by column, so that B of the next
+// stage takes the place of each column as its last use is through and the loads
+// go out over half a stage. Sums leave from registers behind the next tile's
+// first loads.
+//
+// Bound by power (the clock falls to 1.9 to 2.0 GHz; the bare instructions do
+// 3.9 PFLOP/s under load, the bf16 ones 2.1) and by the loads' path into LDS (10
+// to 11 TB/s): without loads it is 18 to 20% faster, without the FMAs 10%,
+// without fragment reads 9%. Measured: 8192 x 7168 x 8192
+// to bf16 420 us (2.29 PFLOP/s; the library's product with one scale 388);
+// 16396 rows of 16 experts, 7168 x 2048, 274 us; to fp32 8192 x 7168 x 8192
+// 755 us (1.27 PFLOP/s, bf16 instructions; the library's bf16 8192^3 reaches
+// 1.45). Not faster: a second barrier that frees B early (7% slower), three
+// stages of a 256 x 128 tile, loads over 8, 12, 20 and 24 instead of 16
+// instructions, wave priorities, waves of 64 x 128 (9% slower), runs of 4 and 16
+// row tiles, smaller tiles for the last round.
 #pragma once
 
 #include "block_kernel.hpp"
@@ -35,7 +59,8 @@ __device__ __forceinline__ void finish(floatx4 (&acc)[FM][FN], const BlockArgs& 
   }
 }
 
-// WIDE: an fp32 output, its products on bf16 instructions (widen_e4m3).
+// WIDE: an fp32 output, its products on bf16 instructions (widen_e4m3). The
+// conversions are 2% of its time.
 template <int BM, int BN, int WM, int WN, bool EXPERTS, bool WIDE>
 __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p) {
   constexpr int NW = WM * WN;

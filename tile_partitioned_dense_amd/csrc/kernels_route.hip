@@ -15,37 +15,7 @@ __device__ __forceinline__ float load_value(const void* p, int64_t i) {
   else return static_cast<const float*>(p)[i];
 }
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int m) { return __shfl_xor(v, m, 64); }
-
-// Scores of a wave's token in 64 bits; expert lane + 64 i in s[i]. In 32 bits
-// neighbouring scores would round to equal ones and the choice hang on them.
-template <int PL>
-__device__ __forceinline__ void scores_of(const float (&l)[PL], int E, int lane, bool sigmoid, double (&s)[PL]) {
-  if (sigmoid) {
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-    return;
-  }
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < PL; ++i) m = fmaxf(m, l[i]);
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) m = fmaxf(m, __shfl_xor(m, d, 64));
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    // (an infinite largest logit: those experts share the weight; no finite
-    // logit at all: every score is 0)
-    s[i] = l[i] == m ? (m == -INFINITY ? 0.0 : 1.0) : exp((double)l[i] - (double)m);
-    sum += s[i];
-  }
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) sum += shfl_xor_f64(sum, d);
-#pragma unroll
-  for (int i = 0; i < PL; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
-}
-
-// --- choice
+// --- scores and choice
 // L lanes work on a token, lane l of them on the experts l PL .. l PL + PL - 1, so
 // that the lowest lane and then the lowest slot is the lowest index. Measured on
 // 8191 tokens of 256 experts, 8 of them (sigmoid, bias, 8 groups), with scores in
@@ -165,20 +135,11 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-template <int L, int PL, bool BF16>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
-  constexpr int TPW = 64 / L, TPG = 256 / L;  // tokens of a wave and of the workgroup
-  __shared__ int32_t chosen[TPG][kRouteMaxK];
-  extern __shared__ double groups_lds[];      // with groups: E values and `groups` of them a token
-  const int lane = threadIdx.x & 63, sub = lane % L, q = lane / L;
-  const int slot = threadIdx.x / L;
-  const int64_t t = (int64_t)blockIdx.x * TPG + slot;
-  const bool live = t < p.T;  // (no barrier below: a wave works alone)
-  const int e0 = sub * PL;
-  // (no branch around a load: each would be waited for by itself; experts and
-  // tokens past the last read the last one's)
-  float l[PL], bias[PL];
-  const int64_t row = (live ? t : p.T - 1) * p.ld;
+// Logits of the experts e0 .. e0 + PL - 1; -inf for a NaN (an expert that is not
+// there) and past the last. No branch around a load: each would be waited for by
+// itself; experts past the last read the last one's.
+template <int PL, bool BF16>
+__device__ __forceinline__ void load_logits(const RouteArgs& p, int64_t row, int e0, float (&l)[PL]) {
   constexpr int V = BF16 ? 8 : 4;  // logits of 16 bytes
   if (PL % V == 0 && p.wide && e0 + PL <= p.E) {
     if constexpr (PL % V == 0) {
@@ -197,6 +158,61 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
 #pragma unroll
     for (int i = 0; i < PL; ++i) l[i] = load_value<BF16>(p.logits, row + min(e0 + i, p.E - 1));
   }
+#pragma unroll
+  for (int i = 0; i < PL; ++i) l[i] = e0 + i < p.E && l[i] == l[i] ? l[i] : -INFINITY;
+}
+
+// e^(x - m), m the largest logit: an infinite one's experts share the weight,
+// and with no finite logit at all every score is 0.
+__device__ __forceinline__ double score_part(float x, float m) {
+  return x == m ? (m == -INFINITY ? 0.0 : 1.0) : exp((double)x - (double)m);
+}
+__device__ __forceinline__ double sigmoid64(float x) { return 1.0 / (1.0 + exp(-(double)x)); }
+
+// Scores of a token's experts in 64 bits (in 32 neighbouring ones would round to
+// equal ones and the choice hang on them), with the largest logit m and one over
+// the sum of their parts.
+template <int L, int PL>
+__device__ __forceinline__ void scores_of(const float (&l)[PL], bool sigmoid, double (&s)[PL], float& m, double& inv) {
+  m = -INFINITY;
+  inv = 0.0;
+  double part = 0.0;
+  if (sigmoid) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) s[i] = sigmoid64(l[i]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < PL; ++i) m = fmaxf(m, l[i]);
+  m = max_token<L>(m);
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    s[i] = score_part(l[i], m);
+    part += s[i];
+  }
+  const double sum = sum_token<L>(part);
+  inv = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+  for (int i = 0; i < PL; ++i) s[i] *= inv;
+}
+// The same of one logit.
+__device__ __forceinline__ double score_of(float x, bool sigmoid, float m, double inv) {
+  x = x == x ? x : -INFINITY;
+  return sigmoid ? sigmoid64(x) : score_part(x, m) * inv;
+}
+
+template <int L, int PL, bool BF16>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
+  constexpr int TPW = 64 / L, TPG = 256 / L;  // tokens of a wave and of the workgroup
+  __shared__ int32_t chosen[TPG][kRouteMaxK];
+  extern __shared__ double groups_lds[];      // with groups: E values and `groups` of them a token
+  const int lane = threadIdx.x & 63, sub = lane % L, q = lane / L;
+  const int slot = threadIdx.x / L;
+  const int64_t t = (int64_t)blockIdx.x * TPG + slot;
+  const bool live = t < p.T;  // (no barrier below: a wave works alone)
+  const int e0 = sub * PL;
+  float l[PL], bias[PL];
+  const int64_t row = (live ? t : p.T - 1) * p.ld;
   if (!p.bias) {
 #pragma unroll
     for (int i = 0; i < PL; ++i) bias[i] = 0.0f;
@@ -213,34 +229,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
 #pragma unroll
     for (int i = 0; i < PL; ++i) bias[i] = p.bias[min(e0 + i, p.E - 1)];
   }
-#pragma unroll
-  for (int i = 0; i < PL; ++i)  // (NaN: an expert that is not there)
-    l[i] = e0 + i < p.E && l[i] == l[i] ? l[i] : -INFINITY;
-  // the score of a logit: 1 / (1 + e^-l), or e^(l - m) / sum (an infinite largest
-  // logit: those experts share the weight; no finite logit at all: every score
-  // is 0)
-  float m = 0.0f;
-  double sum = 1.0;
-  auto part = [&](float x) { return x == m ? (m == -INFINITY ? 0.0 : 1.0) : exp((double)x - (double)m); };
+  load_logits<PL, BF16>(p, row, e0, l);
+  float m;
+  double inv;
   double s[PL];
-  if (p.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-  } else {
-    m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) m = fmaxf(m, l[i]);
-    m = max_token<L>(m);
-    sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      s[i] = part(l[i]);
-      sum += s[i];
-    }
-    sum = sum_token<L>(sum);
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
-  }
+  scores_of<L, PL>(l, p.sigmoid, s, m, inv);
 #pragma unroll
   for (int i = 0; i < PL; ++i) {  // values from here on
     s[i] += (double)bias[i];
@@ -392,9 +385,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
     w[r] = 0.0;
     if (j < p.k) {
       id[r] = chosen[slot][j];
-      float x = load_value<BF16>(p.logits, row + id[r]);
-      x = x == x ? x : -INFINITY;
-      w[r] = p.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : sum > 0.0 ? part(x) / sum : 0.0;
+      const float x = load_value<BF16>(p.logits, row + id[r]);
+      w[r] = score_of(x, p.sigmoid, m, inv);
     }
     total += w[r];
   }
@@ -413,62 +405,97 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p) {
   }
 }
 
-template <int PL, bool BF16>
+// With x the scores, d = scale dweights (renormalised: (d - sum x d / sum x) / sum
+// x over the chosen ones) and g an expert's d, or 0:
+//   dlogits = g x (1 - x)  (sigmoid),  x (g - sum x d)  (softmax; the sum is 0
+//   where the weights are renormalised)
+// The lanes of a token as above; BACK_US.
+template <int L, int PL, bool BF16>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteArgs p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = (int)blockIdx.x * 4 + wave;
-  if (t >= p.T) return;
+  constexpr int TPG = 256 / L, PER = (kRouteMaxK + L - 1) / L;
+  __shared__ __attribute__((aligned(16))) double chosen[TPG][kRouteMaxK][2];  // d, and the id's bits
+  const int sub = threadIdx.x % L, slot = threadIdx.x / L;
+  const int64_t t = (int64_t)blockIdx.x * TPG + slot;
+  const bool live = t < p.T;  // (no barrier below: a wave works alone)
+  const int64_t tok = live ? t : p.T - 1;
+  const int e0 = sub * PL;
+  // places sub, sub + L, ..: ids and gradients; then the logits
+  int id[PER];
+  double d[PER], x[PER];
+#pragma unroll
+  for (int r = 0; r < PER; ++r) {
+    const int j = min(sub + r * L, p.k - 1);
+    id[r] = p.ids[tok * p.k + j];
+    d[r] = (double)p.dweights[tok * p.k + j] * (double)p.scale;
+    if (sub + r * L >= p.k || (uint32_t)id[r] >= (uint32_t)p.E) id[r] = -1;
+  }
   float l[PL];
+  const int64_t row = tok * p.ld;
+  load_logits<PL, BF16>(p, row, e0, l);
+  float at[PER];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = load_value<BF16>(p.logits, (int64_t)t * p.ld + min(e, p.E - 1));
-    if (e >= p.E || !(l[i] == l[i])) l[i] = -INFINITY;  // (NaN: an expert that is not there)
-  }
+  for (int r = 0; r < PER; ++r) at[r] = load_value<BF16>(p.logits, row + max(id[r], 0));
+  float m;
+  double inv;
   double s[PL];
-  scores_of<PL>(l, p.E, lane, p.sigmoid, s);
-  int id = -1;
-  double d = 0.0;
-  if (lane < p.k) {
-    id = p.ids[(int64_t)t * p.k + lane];
-    if ((uint32_t)id >= (uint32_t)p.E) id = -1;
-    else d = (double)p.dweights[(int64_t)t * p.k + lane] * (double)p.scale;
-  }
-  // the chosen scores, and with renormalised weights the gradient through their sum
+  scores_of<L, PL>(l, p.sigmoid, s, m, inv);
   double total = 0.0, dot = 0.0;
-  for (int j = 0; j < p.k; ++j) {
-    const int e = __shfl(id, j, 64);
-    if (e < 0) continue;
-    double x = 0.0;
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (i == (e >> 6)) x = s[i];
-    x = __shfl(x, e & 63, 64);
-    total += x;
-    dot += x * __shfl(d, j, 64);
+  for (int r = 0; r < PER; ++r) {
+    x[r] = 0.0;
+    if (id[r] < 0) d[r] = 0.0;
+    else x[r] = score_of(at[r], p.sigmoid, m, inv);
+    total += x[r];
+    dot += x[r] * d[r];
   }
+  dot = sum_token<L>(dot);
   if (p.renorm) {
-    d = total > 0.0 ? (d - dot / total) / total : 0.0;
-    dot = 0.0;  // (of the new gradients and the scores: their mean is taken out)
+    total = sum_token<L>(total);
+#pragma unroll
+    for (int r = 0; r < PER; ++r) d[r] = total > 0.0 ? (d[r] - dot / total) / total : 0.0;
+    dot = 0.0;
   }
+#pragma unroll
+  for (int r = 0; r < PER; ++r)
+    if (sub + r * L < p.k) {
+      chosen[slot][sub + r * L][0] = d[r];
+      chosen[slot][sub + r * L][1] = __builtin_bit_cast(double, (int64_t)id[r]);
+    }
+  wave_lds_sync();
   double g[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) g[i] = 0.0;
-  for (int j = 0; j < p.k; ++j) {
-    const int e = __shfl(id, j, 64);
-    const double x = __shfl(d, j, 64);
-    if (e < 0) continue;
+  for (int j = 0; j < p.k; ++j) {  // (in the order of j: an id that comes twice counts twice)
+    const double v = chosen[slot][j][0];
+    const int e = (int)__builtin_bit_cast(int64_t, chosen[slot][j][1]) - e0;
 #pragma unroll
     for (int i = 0; i < PL; ++i)
-      if (e == lane + 64 * i) g[i] += x;
+      if (e == i) g[i] += v;
   }
+  float out[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = lane + 64 * i;
-    if (e >= p.E) continue;
-    const double r = p.sigmoid ? g[i] * s[i] * (1.0 - s[i]) : s[i] * (g[i] - dot);
-    if constexpr (BF16) static_cast<uint16_t*>(p.dlogits)[(int64_t)t * p.ldd + e] = f32_to_bf16((float)r);
-    else static_cast<float*>(p.dlogits)[(int64_t)t * p.ldd + e] = (float)r;
+  for (int i = 0; i < PL; ++i) out[i] = (float)(p.sigmoid ? g[i] * s[i] * (1.0 - s[i]) : s[i] * (g[i] - dot));
+  if (!live) return;
+  constexpr int V = BF16 ? 8 : 4;
+  char* const o = static_cast<char*>(p.dlogits) + (t * p.ldd + e0) * (BF16 ? 2 : 4);
+  if (PL % V == 0 && p.wide && e0 + PL <= p.E) {
+    if constexpr (PL % V == 0) {
+#pragma unroll
+      for (int i = 0; i < PL; i += V) {
+        if constexpr (BF16)
+          *reinterpret_cast<uint4*>(o + 2 * i) =
+              make_uint4(pack_bf16x2(out[i], out[i + 1]), pack_bf16x2(out[i + 2], out[i + 3]),
+                         pack_bf16x2(out[i + 4], out[i + 5]), pack_bf16x2(out[i + 6], out[i + 7]));
+        else *reinterpret_cast<float4*>(o + 4 * i) = make_float4(out[i], out[i + 1], out[i + 2], out[i + 3]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+      if (e0 + i < p.E) {
+        if constexpr (BF16) reinterpret_cast<uint16_t*>(o)[i] = f32_to_bf16(out[i]);
+        else reinterpret_cast<float*>(o)[i] = out[i];
+      }
   }
 }
 
@@ -646,18 +673,17 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs p) {
 // The kernel for E experts and the tokens of a workgroup.
 template <bool BF16>
 const void* route_of(int E, bool backward, int* tokens) {
-#define TG_ROUTE(PL)                                                                                          \
-  {                                                                                                           \
-    constexpr int L = PL > 4 ? 64 : PL > 2 ? 32 : 16;                                                                      \
-    *tokens = backward ? 4 : 256 / L;                                                                         \
-    return backward ? reinterpret_cast<const void*>(&route_backward_kernel<PL, BF16>)                         \
-                    : reinterpret_cast<const void*>(&route_kernel<L, PL * 64 / L, BF16>);                     \
+#define TG_ROUTE(L, PL)                                                                 \
+  {                                                                                     \
+    *tokens = 256 / L;                                                                  \
+    return backward ? reinterpret_cast<const void*>(&route_backward_kernel<L, PL, BF16>) \
+                    : reinterpret_cast<const void*>(&route_kernel<L, PL, BF16>);        \
   }
-  if (E <= 64) TG_ROUTE(1);
-  if (E <= 128) TG_ROUTE(2);
-  if (E <= 256) TG_ROUTE(4);
-  if (E <= 512) TG_ROUTE(8);
-  TG_ROUTE(16);
+  if (E <= 64) TG_ROUTE(16, 4);
+  if (E <= 128) TG_ROUTE(16, 8);
+  if (E <= 256) TG_ROUTE(32, 8);
+  if (E <= 512) TG_ROUTE(64, 8);
+  TG_ROUTE(64, 16);
 #undef TG_ROUTE
 }
 
