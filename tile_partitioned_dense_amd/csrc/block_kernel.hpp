@@ -208,10 +208,21 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
   static_assert((NST - 1) * NDMA <= 63, "loads in flight fit the counter");
   constexpr int RING = NST * STAGE;
   constexpr int LDS_EXTRA = EXPERTS ? (kBlockMaxGroups + 4) * 4 : 0;
-  static_assert(RING + LDS_EXTRA <= 160 * 1024, "LDS");
+  // the store's LDS: partial sums, then a strip of 16 rows a wave; beside the
+  // ring where that fits, and the next tile's first stages are loaded during the
+  // store (AHEAD_US)
+  constexpr int WT = WM * WN;
+  constexpr int PART = (KS - 1) * WT * FM * FN * 1024;
+  constexpr int OPF = WTN * 4 + 16;
+  constexpr int EPI = PART + WT * 16 * OPF;
+  static_assert(EPI <= RING, "partial sums and strips fit the ring");
+  constexpr bool AHEAD = RING + (kBlockMaxGroups + 4) * 4 + EPI <= 160 * 1024;
+  constexpr int LDS = RING + LDS_EXTRA + (AHEAD ? EPI : 0);
+  static_assert(LDS <= 160 * 1024, "LDS");
 
-  __shared__ __attribute__((aligned(1024))) uint4 smem[(RING + LDS_EXTRA) / 16];
+  __shared__ __attribute__((aligned(1024))) uint4 smem[LDS / 16];
   const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+  const uint32_t epi0 = lds0 + (AHEAD ? RING + LDS_EXTRA : 0);
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -251,58 +262,70 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
 
   const uint32_t pre0 = lds0 + RING;
   const int n_tiles = EXPERTS ? expert_tiles<BM>(p, pre0, wave, lane) : p.map.tiles_m * p.map.tiles_n;
-  for (int wg = blockIdx.x; wg < n_tiles; wg += gridDim.x) {
-    const BlockTile at = block_tile<BM, BN, EXPERTS>(p, pre0, wg, n_tiles);
-    const int m0 = at.m0, n0 = at.n0, m_end = at.m_end;
-    const uint8_t* Bp = at.B;
-    const float* sBp = at.sB;
-    const uint8_t* a_panel = p.A + (int64_t)m0 * p.lda;
-    const uint8_t* b_panel = Bp + (int64_t)n0 * p.ldb;
-    const int64_t a_bytes = (int64_t)(p.M - 1 - m0) * p.lda + K;
-    const int64_t b_bytes = (int64_t)(N - 1 - n0) * p.ldb + K;
+  // the tile whose loads are issued
+  int m0, n0, m_end;
+  const uint8_t *a_panel, *b_panel;
+  const float* sb_row;
+  int64_t a_bytes, b_bytes, sa_left, sb_left;
+  auto take = [&](const BlockTile& at) {
+    m0 = at.m0;
+    n0 = at.n0;
+    m_end = at.m_end;
+    a_panel = p.A + (int64_t)m0 * p.lda;
+    b_panel = at.B + (int64_t)n0 * p.ldb;
+    a_bytes = (int64_t)(p.M - 1 - m0) * p.lda + K;
+    b_bytes = (int64_t)(N - 1 - n0) * p.ldb + K;
     const int nb0 = n0 / kScaleBlock;
-    const int64_t sb_left = ((int64_t)((N - 1) / kScaleBlock - nb0) * p.lsb + nkb) * 4;
-    const int64_t sa_left = ((int64_t)(nkb - 1) * p.lsa + (p.M - m0)) * 4;
-
-    auto issue = [&](int s) {
-      const uint32_t st = lds0 + (uint32_t)((s % NST) * STAGE);
-      const int64_t kbyte = (int64_t)s * SB;
-      const i32x4 rsA = panel_rsrc(a_panel + kbyte, a_bytes - kbyte);
-      const i32x4 rsB = panel_rsrc(b_panel + kbyte, b_bytes - kbyte);
-      const int left = kch - s * CPR;  // whole chunks of this stage's rows
+    sb_row = at.sB + (int64_t)nb0 * p.lsb;
+    sb_left = ((int64_t)((N - 1) / kScaleBlock - nb0) * p.lsb + nkb) * 4;
+    sa_left = ((int64_t)(nkb - 1) * p.lsa + (p.M - m0)) * 4;
+  };
+  auto issue = [&](int s) {
+    const uint32_t st = lds0 + (uint32_t)((s % NST) * STAGE);
+    const int64_t kbyte = (int64_t)s * SB;
+    const i32x4 rsA = panel_rsrc(a_panel + kbyte, a_bytes - kbyte);
+    const i32x4 rsB = panel_rsrc(b_panel + kbyte, b_bytes - kbyte);
+    const int left = kch - s * CPR;  // whole chunks of this stage's rows
 #pragma unroll
-      for (int t = 0; t < A_PER; ++t) {
-        const int u = wave + NW * t < A_DMA ? wave + NW * t : A_DMA - 1;
-        dma16(st + 1024 * u, rsA, chA[t] < left ? voA[t] : kDmaPast, 0u);
-      }
-      if (p.once) {
+    for (int t = 0; t < A_PER; ++t) {
+      const int u = wave + NW * t < A_DMA ? wave + NW * t : A_DMA - 1;
+      dma16(st + 1024 * u, rsA, chA[t] < left ? voA[t] : kDmaPast, 0u);
+    }
+    if (p.once) {
 #pragma unroll
-        for (int t = 0; t < B_PER; ++t)
-          dma16_once(st + A_BYTES + 1024 * (wave + NW * t), rsB, chB[t] < left ? voB[t] : kDmaPast);
+      for (int t = 0; t < B_PER; ++t)
+        dma16_once(st + A_BYTES + 1024 * (wave + NW * t), rsB, chB[t] < left ? voB[t] : kDmaPast);
+    } else {
+#pragma unroll
+      for (int t = 0; t < B_PER; ++t)
+        dma16(st + A_BYTES + 1024 * (wave + NW * t), rsB, chB[t] < left ? voB[t] : kDmaPast, 0u);
+    }
+    const int kb = s * KBS;
+#pragma unroll
+    for (int t = 0; t < S_PER; ++t) {
+      const int u = wave + NW * t < S_DMA ? wave + NW * t : S_DMA - 1;
+      const uint32_t dst = st + A_BYTES + B_BYTES + 256 * u;
+      if (u < S_DMA - 1) {
+        const int b = kb + u / (SROW / 64), r0 = 64 * (u % (SROW / 64));
+        const int64_t off = ((int64_t)b * p.lsa + r0) * 4;
+        dma4(dst, make_rsrc(reinterpret_cast<const char*>(p.sA + m0) + off, sa_left - off), 4u * lane, 0u);
       } else {
-#pragma unroll
-        for (int t = 0; t < B_PER; ++t)
-          dma16(st + A_BYTES + 1024 * (wave + NW * t), rsB, chB[t] < left ? voB[t] : kDmaPast, 0u);
+        // lane 2 j + i: block kb + j of the tile's i-th 128 rows of B
+        const int i = lane & 1, j = lane >> 1;
+        const bool ok = j < KBS && kb + j < nkb && (BN > kScaleBlock || i == 0);
+        const int64_t off = ((int64_t)kb) * 4;
+        dma4(dst, panel_rsrc(reinterpret_cast<const char*>(sb_row) + off, sb_left - off),
+             ok ? (uint32_t)(i * (int)p.lsb + j) * 4u : kDmaPast, 0u);
       }
-      const int kb = s * KBS;
-#pragma unroll
-      for (int t = 0; t < S_PER; ++t) {
-        const int u = wave + NW * t < S_DMA ? wave + NW * t : S_DMA - 1;
-        const uint32_t dst = st + A_BYTES + B_BYTES + 256 * u;
-        if (u < S_DMA - 1) {
-          const int b = kb + u / (SROW / 64), r0 = 64 * (u % (SROW / 64));
-          const int64_t off = ((int64_t)b * p.lsa + r0) * 4;
-          dma4(dst, make_rsrc(reinterpret_cast<const char*>(p.sA + m0) + off, sa_left - off), 4u * lane, 0u);
-        } else {
-          // lane 2 j + i: block kb + j of the tile's i-th 128 rows of B
-          const int i = lane & 1, j = lane >> 1;
-          const bool ok = j < KBS && kb + j < nkb && (BN > kScaleBlock || i == 0);
-          const int64_t off = ((int64_t)kb) * 4;
-          dma4(dst, panel_rsrc(reinterpret_cast<const char*>(sBp + (int64_t)nb0 * p.lsb) + off, sb_left - off),
-               ok ? (uint32_t)(i * (int)p.lsb + j) * 4u : kDmaPast, 0u);
-        }
-      }
-    };
+    }
+  };
+  if ((int)blockIdx.x >= n_tiles) return;
+  take(block_tile<BM, BN, EXPERTS>(p, pre0, blockIdx.x, n_tiles));
+  for (int s = 0; s < NST - 1 && s < nst; ++s) issue(s);
+  for (int wg = blockIdx.x; wg < n_tiles; wg += gridDim.x) {
+    // (found while this one's first stages arrive)
+    const bool more = wg + (int)gridDim.x < n_tiles;
+    const BlockTile after = block_tile<BM, BN, EXPERTS>(p, pre0, more ? wg + (int)gridDim.x : wg, n_tiles);
     auto frag = [&](uint32_t row_base, int kb, int blk) -> i32x8 {
       const uint32_t b = row_base + (uint32_t)(blk * 16 * SB);
       const uint4 x = __builtin_bit_cast(uint4, lds_read16(b + (uint32_t)(((8 * kb + lg) ^ sw) << 4)));
@@ -316,13 +339,12 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{};
 
-    wait_vmcnt<0>();  // the previous tile's stores are not counted with this one's loads
-    for (int s = 0; s < NST - 1 && s < nst; ++s) issue(s);
     for (int s = 0; s < nst; ++s) {
       // stage s has landed: the stages issued after it are those up to s + NST - 2
-      const int after = min(nst - 1, s + NST - 2) - s;
+      // (and the stores of the tile before, which only make this wait longer)
+      const int behind = min(nst - 1, s + NST - 2) - s;
       static_for<0, NST - 1>([&](auto a_c) {
-        if (after == decltype(a_c)::value) wait_vmcnt<decltype(a_c)::value * NDMA>();
+        if (behind == decltype(a_c)::value) wait_vmcnt<decltype(a_c)::value * NDMA>();
       });
       wait_lgkmcnt0();
       block_barrier();
@@ -369,15 +391,18 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
     }
 
     // store: waves that share K pass their sums through LDS in a fixed order;
-    // then 16-row strips staged as fp32 in the free ring
+    // then 16-row strips staged as fp32
     wait_lgkmcnt0();
-    block_barrier();
-    constexpr int WT = WM * WN;
-    constexpr int PART = (KS - 1) * WT * FM * FN * 1024;
+    block_barrier();  // the ring is free
+    const int row0 = m0, col0 = n0, end = m_end;
+    auto next = [&] {
+      take(after);
+      for (int s = 0; s < NST - 1 && s < nst; ++s) issue(s);
+    };
+    if (AHEAD && more) next();
     if constexpr (KS > 1) {
-      static_assert(PART + WT * 16 * (WTN * 4 + 16) <= RING, "partial sums and strips fit the ring");
       if (ks > 0) {
-        const uint32_t at = lds0 + (uint32_t)((((ks - 1) * WT + wave % WT) * FM * FN) * 1024 + lane * 16);
+        const uint32_t at = epi0 + (uint32_t)((((ks - 1) * WT + wave % WT) * FM * FN) * 1024 + lane * 16);
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -388,7 +413,7 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
       if (ks == 0) {
 #pragma unroll
         for (int h = 1; h < KS; ++h) {
-          const uint32_t at = lds0 + (uint32_t)((((h - 1) * WT + wave) * FM * FN) * 1024 + lane * 16);
+          const uint32_t at = epi0 + (uint32_t)((((h - 1) * WT + wave) * FM * FN) * 1024 + lane * 16);
 #pragma unroll
           for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -401,20 +426,23 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
       }
     }
     if (KS == 1 || ks == 0) {
-      constexpr int OPF = WTN * 4 + 16;
-      const uint32_t stf = lds0 + (uint32_t)(PART + (wave % WT) * 16 * OPF);
-      const EpiOut eo{p.C, p.ldc, m_end, N, p.bias, p.act, nullptr, 0};
+      const uint32_t stf = epi0 + (uint32_t)(PART + (wave % WT) * 16 * OPF);
+      const EpiOut eo{p.C, p.ldc, end, N, p.bias, p.act, nullptr, 0};
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) lds_store_f4(stf + (uint32_t)(l16 * OPF + (16 * j + 4 * lg) * 4), acc[i][j]);
         wait_lgkmcnt0();
-        store_staged_fused<OUT_BF16, false>(stf, OPF, 16, WTN, m0 + wm * WTM + 16 * i, n0 + wn * WTN, lane, 64, eo);
+        store_staged_fused<OUT_BF16, false>(stf, OPF, 16, WTN, row0 + wm * WTM + 16 * i, col0 + wn * WTN, lane, 64, eo);
         wait_lgkmcnt0();
       }
     }
-    wait_lgkmcnt0();
-    block_barrier();
+    if (!AHEAD && more) {
+      wait_vmcnt<0>();
+      wait_lgkmcnt0();
+      block_barrier();
+      next();
+    }
   }
 }
 
