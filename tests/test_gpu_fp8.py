@@ -134,6 +134,46 @@ def test_every_tile(g, config, dtype):
         assert untouched(whole, c)
 
 
+@pytest.mark.parametrize("K", [0, 16, 128, 272, 528, 800, 1056])
+@pytest.mark.parametrize("M", [5, 20])
+def test_rounds_of_few_rows(g, M, K):
+    """Three rounds of tiles and more, of one stage, of a few, of none: stages
+    of the tiles behind are loaded while a tile is in use."""
+    N = 98354
+    print(f"[fp8 rounds {M}x{N}x{K}]", flush=True)
+    a, b, sa, sb = (integers(1, M, K), integers(2, N, K), powers(3, M, bh.blocks(K)),
+                    powers(4, bh.blocks(N), bh.blocks(K)))
+    want = wide(a, sa, 1).double() @ wide(b, sb, 128).double().T if K else torch.zeros(M, N, device="cuda").double()
+    for dtype in (torch.bfloat16, torch.float32):
+        whole, c = out_like(M, N, dtype)
+        g.fp8(a.cuda(), b.cuda(), c, to_row_scales(sa), sb.cuda())
+        assert torch.equal(c.double(), want.to(dtype).double())
+        assert untouched(whole, c)
+
+
+@pytest.mark.parametrize("K", [0, 16, 272, 528, 800])
+@pytest.mark.parametrize("rows", [3, 20, 40])
+def test_rounds_of_experts(g, rows, K):
+    """The same with 40 experts of about `rows` rows, every third one with none."""
+    E, N = 40, 4098
+    sizes = [0 if e % 3 == 1 else rows + e % 5 - 2 for e in range(E)]
+    off = torch.tensor([0] + sizes).cumsum(0)
+    M = int(off[-1]) + 3
+    print(f"[experts rounds {M}x{N}x{K}]", flush=True)
+    a, b, sa, sb = (integers(1, M, K), integers(2, E, N, K), powers(3, M, bh.blocks(K)),
+                    powers(4, E, bh.blocks(N), bh.blocks(K)))
+    for dtype in (torch.bfloat16, torch.float32):
+        whole, c = out_like(M, N, dtype)
+        g.fp8_experts(a.cuda(), b.cuda(), c, to_row_scales(sa), sb.cuda(), off.int().cuda())
+        for e in range(E):
+            lo, hi = int(off[e]), int(off[e + 1])
+            if hi > lo:
+                want = (wide(a[lo:hi], sa[lo:hi], 1).double() @ wide(b[e], sb[e], 128).double().T if K
+                        else torch.zeros(hi - lo, N, device="cuda").double())
+                assert torch.equal(c[lo:hi].double(), want.to(dtype).double()), e
+        assert untouched(whole, c[:int(off[-1])])
+
+
 @pytest.mark.parametrize("config", range(N_CONFIGS))
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 def test_every_tile_of_experts(g, config, dtype):

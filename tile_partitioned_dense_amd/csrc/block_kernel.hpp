@@ -112,11 +112,22 @@ __device__ __forceinline__ float lds_load_f32(uint32_t addr) {
   return *(const __attribute__((address_space(3))) float*)(uintptr_t)addr;
 }
 
-// Experts: the row tiles before each expert into LDS at pre0 (groups + 1
-// values); the tiles there are. Ascending offsets give at most M / BM + groups
-// row tiles, the number that is checked to fit 32 bits: the rest is cut off.
+// Experts, in LDS: the row tiles before each expert, and each one's first row cut
+// to [0, M] (groups + 1 values of both).
+constexpr int kExpertLds = 2 * (kBlockMaxGroups + 4) * 4;
+struct ExpertTables {
+  uint32_t pre, row;  // addresses
+  int last;           // expert of the last tile asked for
+};
+
+// Fills the tables at `at`; the tiles there are. Ascending offsets give at most
+// M / BM + groups row tiles, the number that is checked to fit 32 bits: the rest
+// is cut off.
 template <int BM>
-__device__ __forceinline__ int expert_tiles(const BlockArgs& p, uint32_t pre0, int wave, int lane) {
+__device__ __forceinline__ int expert_tiles(const BlockArgs& p, uint32_t at, int wave, int lane, ExpertTables& tab) {
+  tab.pre = at;
+  tab.row = at + kExpertLds / 2;
+  tab.last = 0;
   if (wave == 0) {
     int base = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 64) {
@@ -124,8 +135,10 @@ __device__ __forceinline__ int expert_tiles(const BlockArgs& p, uint32_t pre0, i
       int t = 0;
       if (g < p.groups) {
         const int lo = min(max(p.offsets[g], 0), p.M);
-        const int hi = min(max(p.offsets[g + 1], lo), p.M);
-        t = (hi - lo + BM - 1) / BM;
+        const int hi = min(max(p.offsets[g + 1], 0), p.M);
+        t = (max(hi - lo, 0) + BM - 1) / BM;
+        lds_store_i32(tab.row + 4u * g, lo);
+        if (g == p.groups - 1) lds_store_i32(tab.row + 4u * g + 4u, hi);
       }
       int incl = t;
 #pragma unroll
@@ -133,20 +146,20 @@ __device__ __forceinline__ int expert_tiles(const BlockArgs& p, uint32_t pre0, i
         const int up = __shfl_up(incl, d, 64);
         if (lane >= d) incl += up;
       }
-      if (g < p.groups) lds_store_i32(pre0 + 4u * g, base + incl - t);
+      if (g < p.groups) lds_store_i32(tab.pre + 4u * g, base + incl - t);
       base += __shfl(incl, 63, 64);
     }
-    if (lane == 0) lds_store_i32(pre0 + 4u * p.groups, base);
+    if (lane == 0) lds_store_i32(tab.pre + 4u * p.groups, base);
   }
   __syncthreads();
   const int most = (p.M + BM - 1) / BM + p.groups;
-  return __builtin_amdgcn_readfirstlane(min(lds_load_i32(pre0 + 4u * p.groups), most)) * p.map.tiles_n;
+  return __builtin_amdgcn_readfirstlane(min(lds_load_i32(tab.pre + 4u * p.groups), most)) * p.map.tiles_n;
 }
 
 // The tile of index wg: of the output, or (experts) of one expert's rows, 8 row
 // tiles of it at a time before the next columns; consecutive tiles on one XCD.
 template <int BM, int BN, bool EXPERTS>
-__device__ __forceinline__ BlockTile block_tile(const BlockArgs& p, uint32_t pre0, int wg, int n_tiles) {
+__device__ __forceinline__ BlockTile block_tile(const BlockArgs& p, ExpertTables& tab, int wg, int n_tiles) {
   BlockTile at;
   at.B = p.B;
   at.sB = p.sB;
@@ -154,18 +167,23 @@ __device__ __forceinline__ BlockTile block_tile(const BlockArgs& p, uint32_t pre
     const int q = n_tiles / kXcds, r = n_tiles % kXcds, x = wg % kXcds;
     const int t = x * q + min(x, r) + wg / kXcds;
     const int row_tile = t / p.map.tiles_n;
-    // the last expert whose first row tile is not past this one
-    int lo = 0, hi = p.groups - 1;
+    // the last expert whose first row tile is not past this one: mostly that of
+    // the tile before or the next
+    int lo = tab.last, hi = min(lo + 1, p.groups - 1);
+    if (lds_load_i32(tab.pre + 4u * lo) > row_tile || lds_load_i32(tab.pre + 4u * hi + 4u) <= row_tile) {
+      lo = 0;
+      hi = p.groups - 1;
+    }
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (lds_load_i32(pre0 + 4u * mid) <= row_tile) lo = mid;
+      if (lds_load_i32(tab.pre + 4u * mid) <= row_tile) lo = mid;
       else hi = mid - 1;
     }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int first = __builtin_amdgcn_readfirstlane(lds_load_i32(pre0 + 4u * e));
-    const int next = __builtin_amdgcn_readfirstlane(lds_load_i32(pre0 + 4u * e + 4u));
-    const int e_lo = min(max(p.offsets[e], 0), p.M);
-    at.m_end = min(max(p.offsets[e + 1], e_lo), p.M);
+    const int e = tab.last = __builtin_amdgcn_readfirstlane(lo);
+    const int first = __builtin_amdgcn_readfirstlane(lds_load_i32(tab.pre + 4u * e));
+    const int next = __builtin_amdgcn_readfirstlane(lds_load_i32(tab.pre + 4u * e + 4u));
+    const int e_lo = __builtin_amdgcn_readfirstlane(lds_load_i32(tab.row + 4u * e));
+    at.m_end = __builtin_amdgcn_readfirstlane(lds_load_i32(tab.row + 4u * e + 4u));
     const int local = t - first * p.map.tiles_n;
     const int per = 8 * p.map.tiles_n;
     const int grp = local / per;
@@ -207,7 +225,7 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
   constexpr int NDMA = A_PER + B_PER + S_PER;
   static_assert((NST - 1) * NDMA <= 63, "loads in flight fit the counter");
   constexpr int RING = NST * STAGE;
-  constexpr int LDS_EXTRA = EXPERTS ? (kBlockMaxGroups + 4) * 4 : 0;
+  constexpr int LDS_EXTRA = EXPERTS ? kExpertLds : 0;
   // the store's LDS: partial sums, then a strip of 16 rows a wave; beside the
   // ring where that fits, and the next tile's first stages are loaded during the
   // store (AHEAD_US)
@@ -216,7 +234,7 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
   constexpr int OPF = WTN * 4 + 16;
   constexpr int EPI = PART + WT * 16 * OPF;
   static_assert(EPI <= RING, "partial sums and strips fit the ring");
-  constexpr bool AHEAD = RING + (kBlockMaxGroups + 4) * 4 + EPI <= 160 * 1024;
+  constexpr bool AHEAD = RING + kExpertLds + EPI <= 160 * 1024;
   constexpr int LDS = RING + LDS_EXTRA + (AHEAD ? EPI : 0);
   static_assert(LDS <= 160 * 1024, "LDS");
 
@@ -260,28 +278,37 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
   const uint32_t scA = lds0 + A_BYTES + B_BYTES + (uint32_t)((wm * WTM + l16) * 4);
   const uint32_t scB = lds0 + A_BYTES + B_BYTES + (uint32_t)((S_DMA - 1) * 256);
 
-  const uint32_t pre0 = lds0 + RING;
-  const int n_tiles = EXPERTS ? expert_tiles<BM>(p, pre0, wave, lane) : p.map.tiles_m * p.map.tiles_n;
+  ExpertTables tab{};
+  const int n_tiles = EXPERTS ? expert_tiles<BM>(p, lds0 + RING, wave, lane, tab) : p.map.tiles_m * p.map.tiles_n;
   // the tile whose loads are issued
-  int m0, n0, m_end;
+  int m0;
   const uint8_t *a_panel, *b_panel;
   const float* sb_row;
   int64_t a_bytes, b_bytes, sa_left, sb_left;
+  // where the tiles in use, with stages loaded and next to be loaded go, the
+  // oldest first (of single stages, with NST - 1 of them ahead, that is NST + 1)
+  constexpr int QUEUE = AHEAD ? NST + 1 : 1;
+  struct Place {
+    int m0, n0, m_end;
+  } under_way[QUEUE] = {};
+  int n_under_way = 0;
   auto take = [&](const BlockTile& at) {
     m0 = at.m0;
-    n0 = at.n0;
-    m_end = at.m_end;
     a_panel = p.A + (int64_t)m0 * p.lda;
-    b_panel = at.B + (int64_t)n0 * p.ldb;
+    b_panel = at.B + (int64_t)at.n0 * p.ldb;
     a_bytes = (int64_t)(p.M - 1 - m0) * p.lda + K;
-    b_bytes = (int64_t)(N - 1 - n0) * p.ldb + K;
-    const int nb0 = n0 / kScaleBlock;
+    b_bytes = (int64_t)(N - 1 - at.n0) * p.ldb + K;
+    const int nb0 = at.n0 / kScaleBlock;
     sb_row = at.sB + (int64_t)nb0 * p.lsb;
     sb_left = ((int64_t)((N - 1) / kScaleBlock - nb0) * p.lsb + nkb) * 4;
     sa_left = ((int64_t)(nkb - 1) * p.lsa + (p.M - m0)) * 4;
+#pragma unroll
+    for (int i = 0; i < QUEUE; ++i)
+      if (i == n_under_way) under_way[i] = {at.m0, at.n0, at.m_end};
+    ++n_under_way;
   };
-  auto issue = [&](int s) {
-    const uint32_t st = lds0 + (uint32_t)((s % NST) * STAGE);
+  auto issue = [&](int s, int buf) {
+    const uint32_t st = lds0 + (uint32_t)(buf * STAGE);
     const int64_t kbyte = (int64_t)s * SB;
     const i32x4 rsA = panel_rsrc(a_panel + kbyte, a_bytes - kbyte);
     const i32x4 rsB = panel_rsrc(b_panel + kbyte, b_bytes - kbyte);
@@ -320,12 +347,34 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
     }
   };
   if ((int)blockIdx.x >= n_tiles) return;
-  take(block_tile<BM, BN, EXPERTS>(p, pre0, blockIdx.x, n_tiles));
-  for (int s = 0; s < NST - 1 && s < nst; ++s) issue(s);
+  // The stages of all this workgroup's tiles go through the ring one after the
+  // other, NST - 1 of them ahead (without AHEAD, those of a tile).
+  int wg_next = blockIdx.x;                 // of the tile behind the one whose stages are loaded
+  int s_next = nst > 0 ? 0 : -1, buf_next = 0;  // the next stage to load (-1: none), its place
+  int ahead = 0;                            // stages loaded and not used yet
+  take(block_tile<BM, BN, EXPERTS>(p, tab, blockIdx.x, n_tiles));
+  auto tile_behind = [&] {
+    wg_next += gridDim.x;
+    return block_tile<BM, BN, EXPERTS>(p, tab, wg_next < n_tiles ? wg_next : (int)blockIdx.x, n_tiles);
+  };
+  BlockTile behind = tile_behind();
+  auto issue_next = [&] {
+    if (s_next < 0) return;
+    issue(s_next, buf_next);
+    buf_next = buf_next + 1 == NST ? 0 : buf_next + 1;
+    ++ahead;
+    if (++s_next == nst) {
+      s_next = -1;
+      if (AHEAD && wg_next < n_tiles) {
+        s_next = 0;
+        take(behind);
+        behind = tile_behind();  // (found while loads are under way)
+      }
+    }
+  };
+  int buf = 0;  // of the stage in use
+  for (int i = 0; i < NST - 1; ++i) issue_next();
   for (int wg = blockIdx.x; wg < n_tiles; wg += gridDim.x) {
-    // (found while this one's first stages arrive)
-    const bool more = wg + (int)gridDim.x < n_tiles;
-    const BlockTile after = block_tile<BM, BN, EXPERTS>(p, pre0, more ? wg + (int)gridDim.x : wg, n_tiles);
     auto frag = [&](uint32_t row_base, int kb, int blk) -> i32x8 {
       const uint32_t b = row_base + (uint32_t)(blk * 16 * SB);
       const uint4 x = __builtin_bit_cast(uint4, lds_read16(b + (uint32_t)(((8 * kb + lg) ^ sw) << 4)));
@@ -340,16 +389,17 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
       for (int j = 0; j < FN; ++j) acc[i][j] = floatx4{};
 
     for (int s = 0; s < nst; ++s) {
-      // stage s has landed: the stages issued after it are those up to s + NST - 2
-      // (and the stores of the tile before, which only make this wait longer)
-      const int behind = min(nst - 1, s + NST - 2) - s;
+      // stage s has landed: `ahead` - 1 were issued after it (and the stores of the
+      // tile before, which only make this wait longer)
+      --ahead;
       static_for<0, NST - 1>([&](auto a_c) {
-        if (behind == decltype(a_c)::value) wait_vmcnt<decltype(a_c)::value * NDMA>();
+        if (ahead == decltype(a_c)::value) wait_vmcnt<decltype(a_c)::value * NDMA>();
       });
       wait_lgkmcnt0();
       block_barrier();
-      if (s + NST - 1 < nst) issue(s + NST - 1);
-      const uint32_t so = (uint32_t)((s % NST) * STAGE);
+      issue_next();
+      const uint32_t so = (uint32_t)(buf * STAGE);
+      buf = buf + 1 == NST ? 0 : buf + 1;
       static_for<0, KBS / KS>([&](auto q_c) {
         const int kb = ks + KS * decltype(q_c)::value;
         if (KBS == 1 || s * KBS + kb < nkb) {
@@ -394,12 +444,10 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
     // then 16-row strips staged as fp32
     wait_lgkmcnt0();
     block_barrier();  // the ring is free
-    const int row0 = m0, col0 = n0, end = m_end;
-    auto next = [&] {
-      take(after);
-      for (int s = 0; s < NST - 1 && s < nst; ++s) issue(s);
-    };
-    if (AHEAD && more) next();
+    const int row0 = under_way[0].m0, col0 = under_way[0].n0, end = under_way[0].m_end;
+#pragma unroll
+    for (int i = 0; i + 1 < QUEUE; ++i) under_way[i] = under_way[i + 1];
+    --n_under_way;
     if constexpr (KS > 1) {
       if (ks > 0) {
         const uint32_t at = epi0 + (uint32_t)((((ks - 1) * WT + wave % WT) * FM * FN) * 1024 + lane * 16);
@@ -437,11 +485,15 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
         wait_lgkmcnt0();
       }
     }
-    if (!AHEAD && more) {
+    if (wg + (int)gridDim.x >= n_tiles) break;
+    if (!AHEAD || nst == 0) {
       wait_vmcnt<0>();
       wait_lgkmcnt0();
       block_barrier();
-      next();
+      take(behind);
+      behind = tile_behind();
+      s_next = nst > 0 ? 0 : -1;
+      for (int i = 0; i < NST - 1; ++i) issue_next();
     }
   }
 }

@@ -76,7 +76,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
   static_assert(S_DMA <= NW, "a scale load each at most");
   constexpr int STAGE = A_BYTES + B_BYTES + S_DMA * 256;
   constexpr int RING = 2 * STAGE;
-  constexpr int LDS_EXTRA = EXPERTS ? (kBlockMaxGroups + 4) * 4 : 0;
+  constexpr int LDS_EXTRA = EXPERTS ? kExpertLds : 0;
   static_assert(RING + LDS_EXTRA <= 160 * 1024, "LDS");
   constexpr int NU = A_PER + B_PER + 1;   // a wave's loads of a stage
   // MFMA n of a stage: row by row of blocks, the last two rows together, column
@@ -131,8 +131,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
   const uint32_t scA = lds0 + A_BYTES + B_BYTES + (uint32_t)((wm * WTM + l16) * 4);
   const uint32_t scB = lds0 + A_BYTES + B_BYTES + (uint32_t)((S_DMA - 1) * 256 + ((wn * WTN) / kScaleBlock) * 4);
 
-  const uint32_t pre0 = lds0 + RING;
-  const int n_tiles = EXPERTS ? expert_tiles<BM>(p, pre0, wave, lane) : p.map.tiles_m * p.map.tiles_n;
+  ExpertTables tab{};
+  const int n_tiles = EXPERTS ? expert_tiles<BM>(p, lds0 + RING, wave, lane, tab) : p.map.tiles_m * p.map.tiles_n;
   if ((int)blockIdx.x >= n_tiles) return;
   const bool far = p.ldc * ESZ * BM > 0x7fffffffll;  // a tile of C spans more than a resource
 
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
   const char* s_base;
   int64_t s_bytes;
   auto take = [&](int wg) {
-    const BlockTile at = block_tile<BM, BN, EXPERTS>(p, pre0, wg, n_tiles);
+    const BlockTile at = block_tile<BM, BN, EXPERTS>(p, tab, wg, n_tiles);
     m0 = at.m0;
     n0 = at.n0;
     m_end = at.m_end;
