@@ -51,7 +51,7 @@ void plans() {
                       "plan: tiles", p.tiles, p.grid);
               // rows of a tile from its first, as far apart as they may be
               require((int64_t)(p.bm > p.bn ? p.bm : p.bn) * (k22 - 1) < k31, "plan: 32-bit offsets", p.bm, p.bn);
-              require(p.lds_bytes + (E ? 2 * (tg::kBlockMaxGroups + 4) * 4 : 0) <= 160 * 1024, "plan: LDS", p.lds_bytes);
+              require(p.lds_bytes + (E ? tg::kExpertLds : 0) <= 160 * 1024, "plan: LDS", p.lds_bytes);
             }
 }
 

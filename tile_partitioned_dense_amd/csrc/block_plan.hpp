@@ -8,6 +8,7 @@ namespace tg {
 
 constexpr int kScaleBlock = 128;      // values of K that share a scale (and rows of B)
 constexpr int kBlockMaxGroups = 1024;  // experts of one call
+constexpr int kExpertLds = 2 * (kBlockMaxGroups + 4) * 4;  // bytes of their tables in LDS
 
 // Compiled configurations: tiles of bm x bn, wm x wn waves on it times ks that
 // share every stage's K, stages of sb bytes of K per row. `tile`: those of
@@ -18,30 +19,33 @@ struct BlockConfig {
   bool tile;
   // Microseconds of a launch, for bf16 and for fp32 outputs: c0 + rounds (a +
   // stages b), with b going to b2 as a round's tiles come to fill the chip (two
-  // tiles a compute unit where occ is 2). Fitted to 267 shapes of 1 to 6100 rows,
-  // 48 to 28672 columns and K of 128 to 8192: the configuration it picks takes
-  // 1.9% longer than the fastest on average (8% or less on 95 of 100).
+  // tiles a compute unit where occ is 2). Fitted to 315 shapes of 1 to 6100 rows,
+  // 48 to 131072 columns and K of 128 to 8192: the configuration it picks takes
+  // 1.6% longer than the fastest on average (8% or less on 95 of 100).
   float cost[2][4];
 };
-constexpr int kNumBlockConfigs = 12;
+constexpr int kNumBlockConfigs = 11;
 constexpr BlockConfig kBlockConfigs[kNumBlockConfigs] = {
-    {256, 256, 2, 4, 1, 128, 2, 1, true, {{0.83f, 7.80f, 1.01f, 1.83f}, {}}},  // 0: 8 waves of 128x64 (bf16 outputs)
-    {192, 256, 2, 4, 1, 128, 2, 1, true, {{0.94f, 5.56f, 0.91f, 1.45f}, {0.00f, 8.25f, 1.67f, 2.56f}}},  // 1: 8 waves of 96x64
-    {256, 128, 4, 2, 1, 128, 2, 1, true, {{1.57f, 3.94f, 0.71f, 1.09f}, {0.00f, 6.79f, 1.05f, 1.75f}}},  // 2: 8 waves of 64x64
-    {128, 128, 2, 2, 1, 128, 2, 2, true, {{0.89f, 3.95f, 0.63f, 1.07f}, {0.00f, 5.77f, 0.96f, 1.80f}}},  // 3: 4 waves of 64x64
-    {16, 128, 1, 4, 2, 256, 3, 1, false, {{2.57f, 1.63f, 0.68f, 0.71f}, {2.62f, 1.74f, 0.81f, 0.84f}}},  // 4
-    {32, 128, 1, 4, 2, 256, 3, 1, false, {{2.55f, 1.99f, 0.77f, 0.81f}, {2.48f, 2.41f, 1.01f, 1.06f}}},  // 5
-    {64, 128, 1, 4, 2, 256, 3, 1, false, {{2.57f, 3.03f, 1.07f, 1.16f}, {2.41f, 3.37f, 1.46f, 1.55f}}},  // 6
-    {16, 64, 1, 2, 4, 512, 3, 1, false, {{2.58f, 1.64f, 0.67f, 0.72f}, {2.57f, 1.69f, 0.82f, 0.87f}}},  // 7
-    {32, 64, 1, 2, 4, 512, 3, 1, false, {{2.67f, 2.05f, 0.83f, 0.90f}, {2.56f, 2.43f, 1.06f, 1.13f}}},  // 8
-    {64, 64, 2, 2, 4, 512, 2, 1, false, {{3.08f, 2.33f, 1.04f, 1.18f}, {2.97f, 2.69f, 1.42f, 1.54f}}},  // 9
-    {16, 32, 1, 1, 8, 1024, 3, 1, false, {{2.60f, 1.72f, 0.80f, 0.88f}, {2.67f, 1.66f, 0.95f, 1.05f}}},  // 10
-    {32, 32, 1, 1, 8, 1024, 2, 1, false, {{2.80f, 1.79f, 0.98f, 1.11f}, {2.81f, 1.98f, 1.20f, 1.32f}}},  // 11
+    {256, 256, 2, 4, 1, 128, 2, 1, true, {{1.39f, 6.55f, 1.05f, 1.74f}, {}}},  // 0: 8 waves of 128x64 (bf16 outputs)
+    {192, 256, 2, 4, 1, 128, 2, 1, true, {{0.61f, 5.40f, 0.94f, 1.42f}, {0.00f, 7.35f, 1.77f, 2.36f}}},  // 1: 8 waves of 96x64
+    {256, 128, 4, 2, 1, 128, 2, 1, true, {{2.68f, 2.66f, 0.72f, 1.07f}, {0.83f, 5.36f, 1.13f, 1.64f}}},  // 2: 8 waves of 64x64
+    {128, 128, 2, 2, 1, 128, 2, 2, true, {{1.11f, 3.87f, 0.63f, 1.11f}, {0.00f, 5.64f, 0.96f, 1.74f}}},  // 3: 4 waves of 64x64
+    {16, 128, 1, 4, 2, 256, 3, 1, false, {{2.84f, 1.42f, 0.68f, 0.72f}, {2.89f, 1.55f, 0.80f, 0.84f}}},  // 4
+    {32, 128, 1, 4, 2, 256, 3, 1, false, {{2.87f, 1.90f, 0.79f, 0.85f}, {2.86f, 2.06f, 1.02f, 1.08f}}},  // 5
+    {16, 64, 1, 2, 4, 512, 3, 1, false, {{2.93f, 1.52f, 0.66f, 0.70f}, {2.92f, 1.58f, 0.80f, 0.83f}}},  // 6
+    {32, 64, 1, 2, 4, 512, 3, 1, false, {{2.88f, 1.99f, 0.76f, 0.85f}, {2.78f, 2.20f, 1.02f, 1.12f}}},  // 7
+    {64, 64, 2, 2, 4, 512, 2, 1, false, {{3.63f, 2.38f, 1.28f, 1.44f}, {3.53f, 2.97f, 1.39f, 1.53f}}},  // 8
+    {16, 32, 1, 1, 8, 1024, 3, 1, false, {{2.77f, 1.65f, 0.78f, 0.86f}, {2.72f, 1.70f, 0.89f, 0.98f}}},  // 9
+    {32, 32, 1, 1, 8, 1024, 2, 1, false, {{3.00f, 1.89f, 1.00f, 1.14f}, {2.88f, 2.05f, 1.23f, 1.36f}}},  // 10
 };
 
+// The ring of stages, and the store's own part where it fits beside it and the
+// experts' tables (block_kernel.hpp).
 inline int block_lds_bytes(const BlockConfig& c) {
   const int rows = (c.bm + 63) / 64 * 64;  // of scales
-  return c.stages * ((c.bm + c.bn) * c.sb + rows * (c.sb / kScaleBlock) * 4 + 256);
+  const int ring = c.stages * ((c.bm + c.bn) * c.sb + rows * (c.sb / kScaleBlock) * 4 + 256);
+  const int store = (c.ks - 1) * c.bm * c.bn * 4 + c.wm * c.wn * 16 * (c.bn / c.wn * 4 + 16);
+  return ring + (!c.tile && ring + kExpertLds + store <= 160 * 1024 ? store : 0);
 }
 
 inline Plan plan_block_for(int config, int64_t M, int64_t N, int cu_count) {
