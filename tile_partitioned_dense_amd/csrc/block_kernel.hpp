@@ -348,15 +348,14 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
   if ((int)blockIdx.x >= n_tiles) return;
   // The stages of all this workgroup's tiles go through the ring one after the
   // other, NST - 1 of them ahead (without AHEAD, those of a tile).
-  int wg_next = blockIdx.x;                 // of the tile behind the one whose stages are loaded
+  int wg_next = blockIdx.x;                 // of the tile whose stages are loaded
   int s_next = nst > 0 ? 0 : -1, buf_next = 0;  // the next stage to load (-1: none), its place
   int ahead = 0;                            // stages loaded and not used yet
   take(block_tile<BM, BN, EXPERTS>(p, tab, blockIdx.x, n_tiles));
   auto tile_behind = [&] {
     wg_next += gridDim.x;
-    return block_tile<BM, BN, EXPERTS>(p, tab, wg_next < n_tiles ? wg_next : (int)blockIdx.x, n_tiles);
+    return block_tile<BM, BN, EXPERTS>(p, tab, wg_next, n_tiles);
   };
-  BlockTile behind = tile_behind();
   auto issue_next = [&] {
     if (s_next < 0) return;
     issue(s_next, buf_next);
@@ -364,10 +363,9 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
     ++ahead;
     if (++s_next == nst) {
       s_next = -1;
-      if (AHEAD && wg_next < n_tiles) {
+      if (AHEAD && wg_next + (int)gridDim.x < n_tiles) {  // (loads are under way)
         s_next = 0;
-        take(behind);
-        behind = tile_behind();  // (found while loads are under way)
+        take(tile_behind());
       }
     }
   };
@@ -489,8 +487,7 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
       wait_vmcnt<0>();
       wait_lgkmcnt0();
       block_barrier();
-      take(behind);
-      behind = tile_behind();
+      take(tile_behind());
       s_next = nst > 0 ? 0 : -1;
       for (int i = 0; i < NST - 1; ++i) issue_next();
     }
