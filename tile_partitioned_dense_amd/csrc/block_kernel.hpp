@@ -12,18 +12,18 @@
 // a workgroup share K as well (KS of them, two to eight) where the tile is too
 // small for eight waves, each taking every KS-th block, and the first adds the
 // others' sums through LDS in a fixed order. Operands, the blocks' scales among
-// them, arrive by direct loads to LDS, NST - 1 stages of 64 to 96 KB of both
-// ahead: with 256 units 16 MB and more are under way, what the memory's latency
+// them, arrive by direct loads to LDS, NST - 1 stages of 36 to 64 KB
+// ahead: with 256 units about 16 MB are under way, what the memory's latency
 // times its rate asks for. Chunks of 16 bytes are kept at positions XORed with
 // their row, so that the 16 rows of a fragment read come from all banks. Rows
 // and chunks past an operand's end are sent past their resource's and arrive
 // as zeros; no load or store depends on a branch.
 //
 // Measured: 16 x 28672 x 8192 36 us (6.5 TB/s; the launch and the first loads
-// are 5 of them); 64 experts of 4096 x 2048 with 3 rows each 81 us (6.7 TB/s;
-// one read of many large pieces reaches 7.1). Not faster: tiles cut so that 256 instead
-// of 224 units have one (the memory is as busy with either); the sc0 and sc1
-// cache hints instead of nt.
+// are 5 of them); 64 experts of 4096 x 2048 with 3 rows each 80 us (6.8 TB/s;
+// one read of many large pieces reaches 7.1). Not faster: tiles cut so that 256
+// instead of 224 units have one (the memory is as busy with either); the sc0 and
+// sc1 cache hints instead of nt.
 #pragma once
 
 #include "mx_kernel.hpp"  // first: the HIP runtime headers plan.hpp relies on under hipcc
