@@ -82,7 +82,7 @@ def test_product(g, M, N, K, dtype):
     assert untouched(whole, c)
 
 
-N_CONFIGS = 11  # compiled tiles
+N_CONFIGS = 15  # compiled tiles
 
 
 def smallest_shapes(experts):

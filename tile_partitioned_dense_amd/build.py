@@ -29,7 +29,7 @@ ARCH = "gfx950"
 N_TILE_CONFIGS = 29
 N_SKINNY_CONFIGS = 6
 N_MX_CONFIGS = 8
-N_BLOCK_CONFIGS = 11
+N_BLOCK_CONFIGS = 15
 N_TRAIN_KERNELS = 114  # kernels_train.hip: products with the stores of train_epilogue.hpp
 
 COMMON_FLAGS = [

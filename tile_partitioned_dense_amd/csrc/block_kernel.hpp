@@ -8,16 +8,17 @@
 // instructions of another wave.
 //
 // This kernel is for outputs of few rows or columns: such a call is bound by
-// reading B once. Tiles of 16, 32 or 64 rows and 32 to 128 columns; the waves of
-// a workgroup share K as well (KS of them, two to eight) where the tile is too
-// small for eight waves, each taking every KS-th block, and the first adds the
-// others' sums through LDS in a fixed order. Operands, the blocks' scales among
-// them, arrive by direct loads to LDS, NST - 1 stages of 36 to 64 KB
-// ahead: with 256 units about 16 MB are under way, what the memory's latency
-// times its rate asks for. Chunks of 16 bytes are kept at positions XORed with
-// their row, so that the 16 rows of a fragment read come from all banks. Rows
-// and chunks past an operand's end are sent past their resource's and arrive
-// as zeros; no load or store depends on a branch.
+// reading B once, or by its operands' way into LDS (55 to 60 GB/s a compute
+// unit) where a few hundred rows read B again. Tiles of 16 to 96 rows and 32 to
+// 128 columns; the waves of a workgroup share K as well (KS of them, two to
+// eight) where the tile is too small for eight waves, each taking every KS-th
+// block, and the first adds the others' sums through LDS in a fixed order.
+// Operands, the blocks' scales among them, arrive by direct loads to LDS, NST - 1
+// stages of 36 to 64 KB ahead: with 256 units about 16 MB are under way, what the
+// memory's latency times its rate asks for. Chunks of 16 bytes are kept at
+// positions XORed with their row, so that the 16 rows of a fragment read come
+// from all banks. Rows and chunks past an operand's end are sent past their
+// resource's and arrive as zeros; no load or store depends on a branch.
 //
 // Measured: 16 x 28672 x 8192 36 us (6.5 TB/s; the launch and the first loads
 // are 5 of them); 64 experts of 4096 x 2048 with 3 rows each 80 us (6.8 TB/s;
@@ -401,26 +402,31 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
         const int kb = ks + KS * decltype(q_c)::value;
         if (KBS == 1 || s * KBS + kb < nkb) {
           const float sb = lds_load_f32(scB + so + (uint32_t)(8 * kb + (BN > kScaleBlock ? 4 * ((wn * WTN) / kScaleBlock) : 0)));
-          i32x8 bq[FN];
+          i32x8 bq[FN], aq[FM];
           bf16x32 bw[OUT_BF16 ? 1 : FN];
-#pragma unroll
-          for (int j = 0; j < FN; ++j) {
-            bq[j] = frag(rowB + so, kb, j);
-            if constexpr (!OUT_BF16) widen_e4m3(bq[j], bw[j]);
-          }
           float sc[FM];
+          // (all of them under way before the first is waited for: 64 x 128 tiles of
+          // 200 x 8000 x 8192 48.6 to 39.0 us)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) bq[j] = frag(rowB + so, kb, j);
+#pragma unroll
+          for (int i = 0; i < FM; ++i) aq[i] = frag(rowA + so, kb, i);
 #pragma unroll
           for (int i = 0; i < FM; ++i) sc[i] = lds_load_f32(scA + so + (uint32_t)(kb * SROW * 4 + i * 64)) * sb;
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (!OUT_BF16) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) widen_e4m3(bq[j], bw[j]);
+          }
 #pragma unroll
           for (int i = 0; i < FM; ++i) {
-            const i32x8 a = frag(rowA + so, kb, i);
             floatx4 d[FN];
             if constexpr (OUT_BF16) {
 #pragma unroll
-              for (int j = 0; j < FN; ++j) d[j] = mma_fp8(a, bq[j]);
+              for (int j = 0; j < FN; ++j) d[j] = mma_fp8(aq[i], bq[j]);
             } else {
               bf16x32 aw;
-              widen_e4m3(a, aw);
+              widen_e4m3(aq[i], aw);
 #pragma unroll
               for (int j = 0; j < FN; ++j) d[j] = floatx4{};
 #pragma unroll

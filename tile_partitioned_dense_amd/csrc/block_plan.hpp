@@ -19,24 +19,28 @@ struct BlockConfig {
   bool tile;
   // Microseconds of a launch, for bf16 and for fp32 outputs: c0 + rounds (a +
   // stages b), with b going to b2 as a round's tiles come to fill the chip (two
-  // tiles a compute unit where occ is 2). Fitted to 315 shapes of 1 to 6100 rows,
+  // tiles a compute unit where occ is 2). Fitted to 411 shapes of 1 to 6100 rows,
   // 48 to 131072 columns and K of 128 to 8192: the configuration it picks takes
-  // 1.6% longer than the fastest on average (8% or less on 95 of 100).
+  // 0.6% longer than the fastest on average (4% or less on 95 of 100).
   float cost[2][4];
 };
-constexpr int kNumBlockConfigs = 11;
+constexpr int kNumBlockConfigs = 15;
 constexpr BlockConfig kBlockConfigs[kNumBlockConfigs] = {
-    {256, 256, 2, 4, 1, 128, 2, 1, true, {{1.39f, 6.55f, 1.05f, 1.74f}, {}}},  // 0: 8 waves of 128x64 (bf16 outputs)
-    {192, 256, 2, 4, 1, 128, 2, 1, true, {{0.61f, 5.40f, 0.94f, 1.42f}, {0.00f, 7.35f, 1.77f, 2.36f}}},  // 1: 8 waves of 96x64
-    {256, 128, 4, 2, 1, 128, 2, 1, true, {{2.68f, 2.66f, 0.72f, 1.07f}, {0.83f, 5.36f, 1.13f, 1.64f}}},  // 2: 8 waves of 64x64
-    {128, 128, 2, 2, 1, 128, 2, 2, true, {{1.11f, 3.87f, 0.63f, 1.11f}, {0.00f, 5.64f, 0.96f, 1.74f}}},  // 3: 4 waves of 64x64
-    {16, 128, 1, 4, 2, 256, 3, 1, false, {{2.84f, 1.42f, 0.68f, 0.72f}, {2.89f, 1.55f, 0.80f, 0.84f}}},  // 4
-    {32, 128, 1, 4, 2, 256, 3, 1, false, {{2.87f, 1.90f, 0.79f, 0.85f}, {2.86f, 2.06f, 1.02f, 1.08f}}},  // 5
-    {16, 64, 1, 2, 4, 512, 3, 1, false, {{2.93f, 1.52f, 0.66f, 0.70f}, {2.92f, 1.58f, 0.80f, 0.83f}}},  // 6
-    {32, 64, 1, 2, 4, 512, 3, 1, false, {{2.88f, 1.99f, 0.76f, 0.85f}, {2.78f, 2.20f, 1.02f, 1.12f}}},  // 7
-    {64, 64, 2, 2, 4, 512, 2, 1, false, {{3.63f, 2.38f, 1.28f, 1.44f}, {3.53f, 2.97f, 1.39f, 1.53f}}},  // 8
-    {16, 32, 1, 1, 8, 1024, 3, 1, false, {{2.77f, 1.65f, 0.78f, 0.86f}, {2.72f, 1.70f, 0.89f, 0.98f}}},  // 9
-    {32, 32, 1, 1, 8, 1024, 2, 1, false, {{3.00f, 1.89f, 1.00f, 1.14f}, {2.88f, 2.05f, 1.23f, 1.36f}}},  // 10
+    {256, 256, 2, 4, 1, 128, 2, 1, true, {{1.53f, 6.30f, 1.09f, 1.75f}, {}}},  // 0: 8 waves of 128x64 (bf16 outputs)
+    {192, 256, 2, 4, 1, 128, 2, 1, true, {{0.54f, 5.31f, 0.98f, 1.43f}, {0.00f, 7.61f, 1.74f, 2.35f}}},  // 1: 8 waves of 96x64
+    {256, 128, 4, 2, 1, 128, 2, 1, true, {{2.72f, 2.39f, 0.76f, 1.10f}, {0.73f, 5.36f, 1.09f, 1.63f}}},  // 2: 8 waves of 64x64
+    {128, 128, 2, 2, 1, 128, 2, 2, true, {{0.76f, 3.93f, 0.68f, 1.10f}, {0.00f, 5.53f, 0.98f, 1.73f}}},  // 3: 4 waves of 64x64
+    {16, 128, 1, 4, 2, 256, 3, 1, false, {{2.42f, 1.43f, 0.66f, 0.71f}, {2.42f, 1.57f, 0.81f, 0.86f}}},  // 4
+    {32, 128, 1, 4, 2, 256, 3, 1, false, {{2.49f, 1.84f, 0.74f, 0.81f}, {2.47f, 2.02f, 0.97f, 1.05f}}},  // 5
+    {64, 128, 2, 2, 2, 256, 3, 1, false, {{2.26f, 2.55f, 0.88f, 1.00f}, {1.98f, 3.27f, 1.32f, 1.46f}}},  // 6
+    {96, 128, 2, 2, 2, 256, 2, 1, false, {{2.20f, 3.05f, 1.10f, 1.25f}, {1.86f, 4.01f, 1.64f, 1.78f}}},  // 7
+    {96, 64, 2, 2, 2, 256, 3, 1, false, {{2.39f, 2.47f, 0.77f, 0.81f}, {2.39f, 2.78f, 1.16f, 1.21f}}},  // 8
+    {16, 64, 1, 2, 4, 512, 3, 1, false, {{2.43f, 1.51f, 0.67f, 0.70f}, {2.45f, 1.55f, 0.86f, 0.89f}}},  // 9
+    {32, 64, 1, 2, 4, 512, 3, 1, false, {{2.47f, 1.95f, 0.77f, 0.86f}, {2.40f, 2.35f, 1.00f, 1.11f}}},  // 10
+    {48, 64, 1, 2, 4, 512, 2, 1, false, {{2.40f, 2.26f, 0.97f, 1.10f}, {2.33f, 2.76f, 1.21f, 1.34f}}},  // 11
+    {64, 64, 2, 2, 4, 512, 2, 1, false, {{2.98f, 2.47f, 1.11f, 1.27f}, {2.92f, 2.98f, 1.40f, 1.55f}}},  // 12
+    {16, 32, 1, 1, 8, 1024, 3, 1, false, {{2.36f, 1.66f, 0.79f, 0.88f}, {2.24f, 1.69f, 0.92f, 1.02f}}},  // 13
+    {32, 32, 1, 1, 8, 1024, 2, 1, false, {{2.57f, 1.82f, 1.00f, 1.18f}, {2.49f, 2.07f, 1.20f, 1.36f}}},  // 14
 };
 
 // The ring of stages, and the store's own part where it fits beside it and the
