@@ -248,3 +248,32 @@ def test_plan_refusals():
     p = binding.Plan()
     assert lib().tile_gemm_plan_fp8(8, 8, 16, 0, 5, 256, ctypes.byref(p)) == DTYPE
     assert lib().tile_gemm_plan_fp8(8, 8, 16, 0, 1, 256, None) == NULL
+
+
+def host_operands():
+    torch = pytest.importorskip("torch")
+    u8, i32 = torch.uint8, torch.int32
+    z = torch.zeros
+    a, sa = z(8, 256, dtype=u8), z(2, 8).t()
+    return {
+        "fp8": (a, z(64, 256, dtype=u8), z(8, 64), sa, z(1, 2)),
+        "fp8_experts": (a, z(3, 64, 256, dtype=u8), z(8, 64), sa, z(3, 1, 2), z(4, dtype=i32)),
+        "quantize": (z(8, 256, dtype=torch.bfloat16), a, sa),
+        "route": (z(8, 16), z(8, 2, dtype=i32), z(8, 2)),
+        "route_backward": (z(8, 16), z(8, 2, dtype=i32), z(8, 2), z(8, 16)),
+        "place": (z(8, 2, dtype=i32), z(17, dtype=i32), z(16, dtype=i32), z(8, 2, dtype=i32)),
+        "combine": (z(16, 64, dtype=torch.bfloat16), z(8, 2, dtype=i32), z(8, 2), z(8, 64)),
+    }
+
+
+@pytest.mark.parametrize("name", ["fp8", "fp8_experts", "quantize", "route", "route_backward", "place", "combine"])
+def test_host_tensors_are_refused(name):
+    """A tensor in host memory never reaches the library."""
+    call = getattr(tg, "tile_gemm_run_" + name)
+    with pytest.raises(ValueError, match="must be on the GPU"):
+        call(None, *host_operands()[name])
+    for i in range(len(host_operands()[name])):  # nor does anything but a tensor
+        bad = list(host_operands()[name])
+        bad[i] = 12345
+        with pytest.raises((TypeError, AttributeError)):
+            call(None, *bad)

@@ -592,6 +592,18 @@ def test_binding_refusals(g):
                        ((a, b.t(), c, s, sb), ValueError)):
         with pytest.raises(error):
             g.fp8(*bad)
+    be, sbe, off = b.view(1, *b.shape), sb.view(1, *sb.shape), torch.tensor([0, 20], dtype=torch.int32).cuda()
+    g.fp8_experts(a, be, c, s, sbe, off)
+    for call, good in ((g.fp8, (a, b, c, s, sb)), (g.fp8_experts, (a, be, c, s, sbe, off))):
+        for i, t in enumerate(good):  # one of them in host memory, or of another type
+            with pytest.raises(ValueError):
+                call(*good[:i], t.cpu(), *good[i + 1:])
+            with pytest.raises(TypeError):
+                call(*good[:i], t.to(torch.float64), *good[i + 1:])
+    for bad, error in (((a, be[:, :, :256], c, s, sbe, off), ValueError), ((a, be, c, s, sbe[:, :1], off), ValueError),
+                       ((a, be, c, s, sbe, off[:1]), ValueError), ((a, b, c, s, sb, off), ValueError)):
+        with pytest.raises(error):
+            g.fp8_experts(*bad)
     with pytest.raises(tg.TileGemmError):  # K not a multiple of 16
         g.fp8(a[:, :264], b[:, :264], c, s, sb)
     x, q = torch.empty(20, 272, dtype=torch.bfloat16, device="cuda"), torch.empty(20, 272, dtype=bh.FP8, device="cuda")

@@ -802,6 +802,18 @@ def tile_gemm_check_xent_backward(A, B, target, lse, dloss, dA, dB, M, N, K, str
 # (as above, one look at each tensor's shape and strides; these calls are often
 # a microsecond or two of GPU work)
 
+# torch's tensor class, types and current device and stream, looked up once
+_torch_names = None
+
+
+def _names():
+    global _torch_names
+    import torch
+    _torch_names = (torch.Tensor, torch.float8_e4m3fn, torch.uint8, torch.bfloat16, torch.float32, torch.int32,
+                    torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    return _torch_names
+
+
 def _bad(name, t, what):
     raise ValueError(f"{name} must have {what}, got shape {tuple(t.shape)} strides {tuple(t.stride())}")
 
@@ -869,21 +881,45 @@ def tile_gemm_run_fp8(h, A, Bt, C, a_scale, b_scale, bias=None, act=Act.NONE, st
     (M x K) and Bt (N x K; float8_e4m3fn or uint8 codes) and float32 scales:
     a_scale (M, ceil(K / 128)) with rows next to each other (stride(0) == 1),
     b_scale (ceil(N / 128), ceil(K / 128)), one for each 128 x 128 block."""
-    (M, K), a = _e4m3("A", A, 2)
-    (N, K2), b = _e4m3("Bt", Bt, 2)
-    if K2 != K:
-        raise ValueError(f"shapes do not chain: A{tuple(A.shape)} Bt{tuple(Bt.shape)}")
-    dt, ldc = _result_rows("C", C, M, N)
-    kb = (K + 127) // 128
-    s = _fp8_strides(a[0] if M > 1 else K, b[0] if N > 1 else K, ldc, _row_scales("a_scale", a_scale, M, kb),
-                     _block_scales("b_scale", b_scale, (), (N + 127) // 128, kb)[0], 0, 0)
+    tensor, f8, u8, bf16, f32, _, device, raw_stream = _torch_names or _names()
+    # plain tensors of the expected form in one look; anything else step by step
+    if (type(A) is tensor and type(Bt) is tensor and type(C) is tensor and type(a_scale) is tensor
+            and type(b_scale) is tensor and A.dim() == 2 and Bt.dim() == 2 and C.dim() == 2 and a_scale.dim() == 2
+            and b_scale.dim() == 2):
+        (M, K), (N, K2), (ta, tb, tc) = A.shape, Bt.shape, (A.dtype, Bt.dtype, C.dtype)
+        kb, nb = (K + 127) // 128, (N + 127) // 128
+        (a, a1), (b, b1), (c, c1), (x1, x), (y, y1) = (A.stride(), Bt.stride(), C.stride(), a_scale.stride(),
+                                                       b_scale.stride())
+        plain = (K == K2 and a1 == b1 == c1 == x1 == y1 == 1 and (ta is f8 or ta is u8) and (tb is f8 or tb is u8)
+                 and (tc is bf16 or tc is f32) and a_scale.dtype is f32 and b_scale.dtype is f32
+                 and C.shape == (M, N) and a_scale.shape == (M, kb) and b_scale.shape == (nb, kb))
+    else:
+        plain = False
+    if plain:
+        dt = 1 if tc is bf16 else 0
+        s = _fp8_strides(a if M > 1 else K, b if N > 1 else K, c if M > 1 else (N + 7) // 8 * 8,
+                         x if kb > 1 else max(M, 1), y if nb > 1 else kb, 0, 0)
+    else:
+        (M, K), a = _e4m3("A", A, 2)
+        (N, K2), b = _e4m3("Bt", Bt, 2)
+        if K2 != K:
+            raise ValueError(f"shapes do not chain: A{tuple(A.shape)} Bt{tuple(Bt.shape)}")
+        dt, ldc = _result_rows("C", C, M, N)
+        kb = (K + 127) // 128
+        s = _fp8_strides(a[0] if M > 1 else K, b[0] if N > 1 else K, ldc, _row_scales("a_scale", a_scale, M, kb),
+                         _block_scales("b_scale", b_scale, (), (N + 127) // 128, kb)[0], 0, 0)
     p_bias = None
     if bias is not None:
         _check_bias(bias, N)
         p_bias = bias.data_ptr() if _is_tensor(bias) else bias
-    dev = _current_device(("A", "Bt", "C", "a_scale", "b_scale", "bias"),
-                          (A, Bt, C, a_scale, b_scale, bias if _is_tensor(bias) else None))
-    raw, _ = _launch_stream(stream, dev)
+    dev = A.get_device()
+    if (p_bias is not None or stream is not None or dev < 0 or Bt.get_device() != dev or C.get_device() != dev
+            or a_scale.get_device() != dev or b_scale.get_device() != dev or device() != dev):
+        dev = _current_device(("A", "Bt", "C", "a_scale", "b_scale", "bias"),
+                              (A, Bt, C, a_scale, b_scale, bias if _is_tensor(bias) else None))
+        raw, _ = _launch_stream(stream, dev)
+    else:
+        raw = raw_stream(dev)
     st = (_lib or load_library()).tile_gemm_run_fp8(h, A.data_ptr(), Bt.data_ptr(), C.data_ptr(), M, N, K,
                                                     s, a_scale.data_ptr(), b_scale.data_ptr(), dt,
                                                     p_bias, act, raw)
@@ -895,19 +931,44 @@ def tile_gemm_run_fp8_experts(h, A, Bt, C, a_scale, b_scale, offsets, stream=Non
     those rows of A times expert e's matrix. Bt (E, N, K), b_scale
     (E, ceil(N / 128), ceil(K / 128)), offsets E + 1 int32 values; A and a_scale
     as for tile_gemm_run_fp8."""
-    import torch
-    (M, K), a = _e4m3("A", A, 2)
-    (E, N, K2), b = _e4m3("Bt", Bt, 3)
-    if K2 != K:
-        raise ValueError(f"shapes do not chain: A{tuple(A.shape)} Bt{tuple(Bt.shape)}")
-    dt, ldc = _result_rows("C", C, M, N)
-    kb = (K + 127) // 128
-    lsb, esb = _block_scales("b_scale", b_scale, (E,), (N + 127) // 128, kb)
-    s = _fp8_strides(a[0] if M > 1 else K, b[1] if N > 1 else K, ldc, _row_scales("a_scale", a_scale, M, kb), lsb,
-                     b[0] if E > 1 else N * K, esb if E > 1 else 0)
-    _vector("offsets", offsets, E + 1, (torch.int32,))
-    dev = _current_device(("A", "Bt", "C", "a_scale", "b_scale", "offsets"), (A, Bt, C, a_scale, b_scale, offsets))
-    raw, _ = _launch_stream(stream, dev)
+    tensor, f8, u8, bf16, f32, i32, device, raw_stream = _torch_names or _names()
+    # (as in tile_gemm_run_fp8)
+    if (type(A) is tensor and type(Bt) is tensor and type(C) is tensor and type(a_scale) is tensor
+            and type(b_scale) is tensor and A.dim() == 2 and Bt.dim() == 3 and C.dim() == 2 and a_scale.dim() == 2
+            and b_scale.dim() == 3):
+        (M, K), (E, N, K2), (ta, tb, tc) = A.shape, Bt.shape, (A.dtype, Bt.dtype, C.dtype)
+        kb, nb = (K + 127) // 128, (N + 127) // 128
+        (a, a1), (be, b, b1), (c, c1), (x1, x), (ye, y, y1) = (A.stride(), Bt.stride(), C.stride(), a_scale.stride(),
+                                                               b_scale.stride())
+        plain = (K == K2 and a1 == b1 == c1 == x1 == y1 == 1 and (ta is f8 or ta is u8) and (tb is f8 or tb is u8)
+                 and (tc is bf16 or tc is f32) and a_scale.dtype is f32 and b_scale.dtype is f32
+                 and C.shape == (M, N) and a_scale.shape == (M, kb) and b_scale.shape == (E, nb, kb))
+    else:
+        plain = False
+    if plain:
+        dt = 1 if tc is bf16 else 0
+        s = _fp8_strides(a if M > 1 else K, b if N > 1 else K, c if M > 1 else (N + 7) // 8 * 8,
+                         x if kb > 1 else max(M, 1), y if nb > 1 else kb, be if E > 1 else N * K,
+                         ye if E > 1 else 0)
+    else:
+        (M, K), a = _e4m3("A", A, 2)
+        (E, N, K2), b = _e4m3("Bt", Bt, 3)
+        if K2 != K:
+            raise ValueError(f"shapes do not chain: A{tuple(A.shape)} Bt{tuple(Bt.shape)}")
+        dt, ldc = _result_rows("C", C, M, N)
+        kb = (K + 127) // 128
+        lsb, esb = _block_scales("b_scale", b_scale, (E,), (N + 127) // 128, kb)
+        s = _fp8_strides(a[0] if M > 1 else K, b[1] if N > 1 else K, ldc, _row_scales("a_scale", a_scale, M, kb), lsb,
+                         b[0] if E > 1 else N * K, esb if E > 1 else 0)
+    _vector("offsets", offsets, E + 1, (i32,))
+    dev = A.get_device()
+    if (stream is not None or dev < 0 or Bt.get_device() != dev or C.get_device() != dev
+            or a_scale.get_device() != dev or b_scale.get_device() != dev or offsets.get_device() != dev
+            or device() != dev):
+        dev = _current_device(("A", "Bt", "C", "a_scale", "b_scale", "offsets"), (A, Bt, C, a_scale, b_scale, offsets))
+        raw, _ = _launch_stream(stream, dev)
+    else:
+        raw = raw_stream(dev)
     st = (_lib or load_library()).tile_gemm_run_fp8_experts(h, A.data_ptr(), Bt.data_ptr(), C.data_ptr(), M, N, K, E,
                                                             offsets.data_ptr(), s, a_scale.data_ptr(),
                                                             b_scale.data_ptr(), dt, raw)
