@@ -819,8 +819,7 @@ def _bad(name, t, what):
 
 
 def _typed(name, t, dtype):
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, (_torch_names or _names())[0]):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -828,11 +827,12 @@ def _typed(name, t, dtype):
 
 def _e4m3(name, t, dims):
     """Shape and row stride of a tensor of E4M3 codes (float8_e4m3fn, or their bytes as uint8)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    tensor, f8, u8 = (_torch_names or _names())[:3]
+    if not isinstance(t, tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype is not torch.float8_e4m3fn and t.dtype is not torch.uint8:
-        raise TypeError(f"{name} must be float8_e4m3fn (or uint8 codes), got {t.dtype}")
+    dtype = t.dtype
+    if dtype is not f8 and dtype is not u8:
+        raise TypeError(f"{name} must be float8_e4m3fn (or uint8 codes), got {dtype}")
     s, d = t.shape, t.stride()
     if len(s) != dims or (d[-1] != 1 and s[-1] > 1):
         _bad(name, t, f"{dims} dimensions, the last of stride 1")
@@ -842,8 +842,7 @@ def _e4m3(name, t, dims):
 def _row_scales(name, t, M, kb):
     """The stride between blocks of K of the scales of M rows, (M, blocks of K)
     with rows next to each other."""
-    import torch
-    _typed(name, t, torch.float32)
+    _typed(name, t, (_torch_names or _names())[4])
     s, d = t.shape, t.stride()
     if len(s) != 2 or s[0] != M or s[1] != kb or (d[0] != 1 and M > 1):
         _bad(name, t, f"shape ({M}, {kb}) and a row stride of 1")
@@ -852,8 +851,7 @@ def _row_scales(name, t, M, kb):
 
 def _block_scales(name, t, lead, nb, kb):
     """The strides of the scales of blocks of 128 x 128, (*lead, blocks of rows, blocks of K)."""
-    import torch
-    _typed(name, t, torch.float32)
+    _typed(name, t, (_torch_names or _names())[4])
     s, d = t.shape, t.stride()
     if s != (*lead, nb, kb) or (d[-1] != 1 and kb > 1):
         _bad(name, t, f"shape {(*lead, nb, kb)} and a last stride of 1")
@@ -981,7 +979,7 @@ def tile_gemm_run_quantize(h, X, Q, scale, form=Quant.ROWS, gate=None, rows=None
     ceil(K / 128)) with rows next to each other; with `gate`, Q is made of
     act(first half of X's columns) * (second half). form=Quant.BLOCKS: scale
     (ceil(M / 128), ceil(K / 128)). `rows`: M int32 row numbers of X."""
-    import torch
+    _, _, _, bf16, _, i32, device, raw_stream = _torch_names or _names()
     (M, K), q = _e4m3("Q", Q, 2)
     blocks = form == 2  # Quant.BLOCKS
     if gate is not None:
@@ -990,11 +988,11 @@ def tile_gemm_run_quantize(h, X, Q, scale, form=Quant.ROWS, gate=None, rows=None
         form = 1  # Quant.GATED_ROWS
     elif form == 1:
         raise ValueError("form=Quant.GATED_ROWS needs a gate")
-    _typed("X", X, torch.bfloat16)
+    _typed("X", X, bf16)
     x_rows = M
     p_rows = None
     if rows is not None:
-        _vector("rows", rows, M, (torch.int32,))
+        _vector("rows", rows, M, (i32,))
         p_rows = rows.data_ptr()
         if X.dim() == 2:
             x_rows = X.shape[0]
@@ -1004,8 +1002,13 @@ def tile_gemm_run_quantize(h, X, Q, scale, form=Quant.ROWS, gate=None, rows=None
         lds = _block_scales("scale", scale, (), (M + 127) // 128, kb)[0]
     else:
         lds = _row_scales("scale", scale, M, kb)
-    dev = _current_device(("X", "Q", "scale", "rows"), (X, Q, scale, rows))
-    raw, _ = _launch_stream(stream, dev)
+    dev = X.get_device()
+    if (stream is not None or dev < 0 or Q.get_device() != dev or scale.get_device() != dev
+            or (rows is not None and rows.get_device() != dev) or device() != dev):
+        dev = _current_device(("X", "Q", "scale", "rows"), (X, Q, scale, rows))
+        raw, _ = _launch_stream(stream, dev)
+    else:
+        raw = raw_stream(dev)
     st = (_lib or load_library()).tile_gemm_run_quantize(h, X.data_ptr(), Q.data_ptr(), scale.data_ptr(), M, K, ldx,
                                                          q[0] if M > 1 else K, lds, form, 0 if gate is None else gate,
                                                          p_rows, x_rows, raw)
@@ -1014,21 +1017,25 @@ def tile_gemm_run_quantize(h, X, Q, scale, form=Quant.ROWS, gate=None, rows=None
 
 def _logits(name, t, T):
     """Experts, type (bfloat16 or not) and row stride of a router's logits of T tokens."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    names = _torch_names or _names()
+    if not isinstance(t, names[0]):
         raise TypeError(f"{name} must be a torch tensor")
-    bf16 = t.dtype is torch.bfloat16
-    if not bf16 and t.dtype is not torch.float32:
-        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    s, d = t.shape, t.stride()
-    if len(s) != 2 or s[0] != T or (d[1] != 1 and s[1] > 1):
+    dtype = t.dtype
+    bf16 = dtype is names[3]
+    if not bf16 and dtype is not names[4]:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    if t.dim() != 2:
         _bad(name, t, f"a row for each of the {T} tokens and a column stride of 1")
-    return s[1], bf16, d[0] if T > 1 else s[1]
+    (rows, E), (ld, one) = t.shape, t.stride()
+    if rows != T or (one != 1 and E > 1):
+        _bad(name, t, f"a row for each of the {T} tokens and a column stride of 1")
+    return E, bf16, ld if T > 1 else E
 
 
 def _per_place(name, t, T, k, dtype):
     """Checks a contiguous (T, k) tensor; its shape."""
-    _typed(name, t, dtype)
+    if type(t) is not (_torch_names or _names())[0] or t.dtype is not dtype:
+        _typed(name, t, dtype)
     s = t.shape
     if len(s) != 2 or (T is not None and (s[0] != T or s[1] != k)) or not t.is_contiguous():
         _bad(name, t, "contiguous values for each token's experts" if T is None else f"shape ({T}, {k}), contiguous")
@@ -1041,16 +1048,21 @@ def tile_gemm_run_route(h, logits, ids, weights, score=Score.SOFTMAX, bias=None,
     and weights (T, k) float32, from logits (T, E) float32 or bfloat16. `bias`
     (E float32 values) is added to the scores for the choice only; with groups
     only experts of the top_groups best of `groups` runs of experts are chosen."""
-    import torch
-    T, k = _per_place("ids", ids, None, None, torch.int32)
+    _, _, _, _, f32, i32, device, raw_stream = _torch_names or _names()
+    T, k = _per_place("ids", ids, None, None, i32)
     E, bf16, ld = _logits("logits", logits, T)
-    _per_place("weights", weights, T, k, torch.float32)
+    _per_place("weights", weights, T, k, f32)
     p_bias = None
     if bias is not None:
-        _vector("bias", bias, E, (torch.float32,))
+        _vector("bias", bias, E, (f32,))
         p_bias = bias.data_ptr()
-    dev = _current_device(("logits", "ids", "weights", "bias"), (logits, ids, weights, bias))
-    raw, _ = _launch_stream(stream, dev)
+    dev = logits.get_device()
+    if (stream is not None or dev < 0 or ids.get_device() != dev or weights.get_device() != dev
+            or (bias is not None and bias.get_device() != dev) or device() != dev):
+        dev = _current_device(("logits", "ids", "weights", "bias"), (logits, ids, weights, bias))
+        raw, _ = _launch_stream(stream, dev)
+    else:
+        raw = raw_stream(dev)
     o = RouteOptions(score, bf16, groups, top_groups, group_top, renormalize, scale)
     st = (_lib or load_library()).tile_gemm_run_route(h, logits.data_ptr(), p_bias, ids.data_ptr(),
                                                       weights.data_ptr(), T, E, k, ld, ctypes.byref(o), raw)
@@ -1061,17 +1073,22 @@ def tile_gemm_run_route_backward(h, logits, ids, dweights, dlogits, score=Score.
                                  stream=None, check: bool = True):
     """Enqueue the gradient of tile_gemm_run_route's weights: dlogits (T, E, of
     the logits' type) from dweights (T, k) float32 and the ids chosen."""
-    import torch
-    T, k = _per_place("ids", ids, None, None, torch.int32)
+    _, _, _, _, f32, i32, device, raw_stream = _torch_names or _names()
+    T, k = _per_place("ids", ids, None, None, i32)
     E, bf16, ld = _logits("logits", logits, T)
     dE, dbf16, ldd = _logits("dlogits", dlogits, T)
     if dE != E:
         _bad("dlogits", dlogits, f"shape ({T}, {E})")
     if dbf16 != bf16:
         raise TypeError(f"dlogits must be of the logits' type {logits.dtype}, got {dlogits.dtype}")
-    _per_place("dweights", dweights, T, k, torch.float32)
-    dev = _current_device(("logits", "ids", "dweights", "dlogits"), (logits, ids, dweights, dlogits))
-    raw, _ = _launch_stream(stream, dev)
+    _per_place("dweights", dweights, T, k, f32)
+    dev = logits.get_device()
+    if (stream is not None or dev < 0 or ids.get_device() != dev or dweights.get_device() != dev
+            or dlogits.get_device() != dev or device() != dev):
+        dev = _current_device(("logits", "ids", "dweights", "dlogits"), (logits, ids, dweights, dlogits))
+        raw, _ = _launch_stream(stream, dev)
+    else:
+        raw = raw_stream(dev)
     o = RouteOptions(score, bf16, 1, 1, 1, renormalize, scale)
     st = (_lib or load_library()).tile_gemm_run_route_backward(h, logits.data_ptr(), ids.data_ptr(),
                                                                dweights.data_ptr(), dlogits.data_ptr(), T, E, k, ld,
@@ -1092,21 +1109,28 @@ def tile_gemm_run_place(h, ids, offsets, rows=None, places=None, first=0, worksp
     E experts from number `first` on), rows (T k) and places (T, k), either of
     which may be left out, from ids (T, k) int32. Without `workspace` one is
     allocated for the call where it needs one."""
-    import torch
-    T, k = _per_place("ids", ids, None, None, torch.int32)
-    _typed("offsets", offsets, torch.int32)
+    _, _, _, _, _, i32, device, raw_stream = _torch_names or _names()
+    T, k = _per_place("ids", ids, None, None, i32)
+    _typed("offsets", offsets, i32)
     E = offsets.numel() - 1
     if E < 1 or offsets.dim() != 1 or not offsets.is_contiguous():
         _bad("offsets", offsets, "one dimension of at least 2 contiguous values")
     p_rows = p_places = p_ws = None
     if rows is not None:
-        _vector("rows", rows, T * k, (torch.int32,))
+        _vector("rows", rows, T * k, (i32,))
         p_rows = rows.data_ptr()
     if places is not None:
-        _per_place("places", places, T, k, torch.int32)
+        _per_place("places", places, T, k, i32)
         p_places = places.data_ptr()
-    dev = _current_device(("ids", "offsets", "rows", "places", "workspace"), (ids, offsets, rows, places, workspace))
-    raw, other = _launch_stream(stream, dev)
+    dev = ids.get_device()
+    if (stream is not None or workspace is not None or dev < 0 or offsets.get_device() != dev
+            or (rows is not None and rows.get_device() != dev)
+            or (places is not None and places.get_device() != dev) or device() != dev):
+        dev = _current_device(("ids", "offsets", "rows", "places", "workspace"),
+                              (ids, offsets, rows, places, workspace))
+        raw, other = _launch_stream(stream, dev)
+    else:
+        raw, other = raw_stream(dev), None
     lib = _lib or load_library()
     nbytes = 0
     if workspace is not None:
@@ -1130,17 +1154,30 @@ def tile_gemm_run_combine(h, Z, places, weights, Y, stream=None, check: bool = T
     """Enqueue Y[t] := sum_j weights[t, j] Z[places[t, j]] (Z bf16, Y bf16 or
     float32; places (T, k) int32, those outside Z's rows left out; weights
     (T, k) float32 or None for ones)."""
-    import torch
-    T, k = _per_place("places", places, None, None, torch.int32)
-    z_rows, N = _matrix("Z", Z, None, None)
-    ldz = _rows_of("Z", Z, z_rows, N)
-    dt, ldy = _result_rows("Y", Y, T, N)
+    tensor, _, _, bf16, f32, i32, device, raw_stream = _torch_names or _names()
+    if type(places) is tensor and type(Z) is tensor and type(Y) is tensor and places.dim() == Z.dim() == Y.dim() == 2:
+        (T, k), (z_rows, N), (ldz, z1), (ldy, y1), ty = places.shape, Z.shape, Z.stride(), Y.stride(), Y.dtype
+        plain = (z1 == y1 == 1 and places.dtype is i32 and places.is_contiguous() and Z.dtype is bf16
+                 and (ty is bf16 or ty is f32) and Y.shape == (T, N) and z_rows > 1 and T > 1)
+        dt = 1 if ty is bf16 else 0
+    else:
+        plain = False
+    if not plain:
+        T, k = _per_place("places", places, None, None, i32)
+        z_rows, N = _matrix("Z", Z, None, None)
+        ldz = _rows_of("Z", Z, z_rows, N)
+        dt, ldy = _result_rows("Y", Y, T, N)
     p_weights = None
     if weights is not None:
-        _per_place("weights", weights, T, k, torch.float32)
+        _per_place("weights", weights, T, k, f32)
         p_weights = weights.data_ptr()
-    dev = _current_device(("Z", "places", "weights", "Y"), (Z, places, weights, Y))
-    raw, _ = _launch_stream(stream, dev)
+    dev = Z.get_device()
+    if (stream is not None or dev < 0 or places.get_device() != dev or Y.get_device() != dev
+            or (weights is not None and weights.get_device() != dev) or device() != dev):
+        dev = _current_device(("Z", "places", "weights", "Y"), (Z, places, weights, Y))
+        raw, _ = _launch_stream(stream, dev)
+    else:
+        raw = raw_stream(dev)
     st = (_lib or load_library()).tile_gemm_run_combine(h, Z.data_ptr(), places.data_ptr(), p_weights, Y.data_ptr(), T,
                                                         N, k, z_rows, ldz, ldy, dt, raw)
     return _result(st, check) if st else Status.OK
