@@ -151,6 +151,32 @@ def test_rounds_of_few_rows(g, M, K):
         assert untouched(whole, c)
 
 
+@pytest.mark.parametrize("K", [0, 16, 144, 272, 400])
+@pytest.mark.parametrize("M,N", [(2300, 15400), (1100, 28690), (6100, 4104), (1100, 15400), (6100, 8200)])
+def test_rounds_of_large_tiles(g, M, N, K):
+    """Two rounds of the large tiles and more, of one stage to four: the last
+    stages of a tile load the first of the next. Once with one weight, once with
+    experts of which one has a row, one none, and none ends with a tile."""
+    print(f"[fp8 rounds of tiles {M}x{N}x{K}]", flush=True)
+    off = [0, M // 3, M // 3, M // 3 + 1, M - M // 7, M - 2]
+    a, b, sa, sb = (integers(1, M, K), integers(2, 5, N, K), powers(3, M, bh.blocks(K)),
+                    powers(4, 5, bh.blocks(N), bh.blocks(K)))
+    ad, sad, bd, sbd = a.cuda(), to_row_scales(sa), b.cuda(), sb.cuda()
+    x = wide(a, sa, 1) if K else torch.zeros(M, 1, device="cuda")
+    for dtype in (torch.bfloat16, torch.float32):
+        for experts in (False, True):
+            whole, c = out_like(M, N, dtype)
+            if experts:
+                g.fp8_experts(ad, bd, c, sad, sbd, torch.tensor(off, dtype=torch.int32).cuda())
+            else:
+                g.fp8(ad, bd[0], c, sad, sbd[0])
+            for e, (lo, hi) in enumerate(zip(off, off[1:]) if experts else [(0, M)]):
+                y = wide(b[e], sb[e], 128) if K else torch.zeros(N, 1, device="cuda")
+                # (sums of at most 400 products of up to 9 * 16, in steps of 1 / 16: exact in fp32)
+                assert torch.equal(c[lo:hi], (x[lo:hi] @ y.T.contiguous()).to(dtype)), (dtype, e)
+            assert untouched(whole, c[:M - 2] if experts else c)
+
+
 @pytest.mark.parametrize("K", [0, 16, 272, 528, 800])
 @pytest.mark.parametrize("rows", [3, 20, 40])
 def test_rounds_of_experts(g, rows, K):

@@ -11,23 +11,27 @@
 // compiler moves them together and spills). One barrier a stage, before the last
 // two rows of blocks: these are worked column by column, so that B of the next
 // stage takes the place of each column as its last use is through and the loads
-// go out over half a stage. Sums leave from registers behind the next tile's
-// first loads.
+// go out over half a stage. A tile's last two stages load the next one's first
+// (16396 rows of 16 experts, 7168 x 2048: 273 to 268 us; 8192 of 64, 4096 x 1024:
+// 76.9 to 74.6), while its sums leave from registers.
 //
 // Bound by power (the clock falls to 1.9 to 2.0 GHz; the bare instructions do
 // 3.9 PFLOP/s under load, the bf16 ones 2.1) and by the loads' path into LDS (10
 // to 11 TB/s): without loads it is 18 to 20% faster, without the FMAs 10%,
-// without fragment reads 9%. Measured: 8192 x 7168 x 8192
-// to bf16 420 us (2.29 PFLOP/s; the library's product with one scale 388);
-// 16396 rows of 16 experts, 7168 x 2048, 274 us; to fp32 8192 x 7168 x 8192
-// 755 us (1.27 PFLOP/s, bf16 instructions; the library's bf16 8192^3 reaches
-// 1.45). Not faster: a second barrier that frees B early (7% slower), three
+// without fragment reads 9%. Measured: 8192 x 7168 x 8192 to bf16 420 us (2.29
+// PFLOP/s; the library's product with one scale 388); 16396 rows of 16 experts,
+// 7168 x 2048, 268 us; to fp32 8192 x 7168 x 8192 755 us (1.27 PFLOP/s, bf16
+// instructions; the library's bf16 8192^3 reaches 1.45). Not faster: a second barrier that frees B early (7% slower), three
 // stages of a 256 x 128 tile, loads over 8, 12, 20 and 24 instead of 16
 // instructions, wave priorities, waves of 64 x 128 (9% slower), runs of 4 and 16
 // row tiles, smaller tiles for the last round.
 #pragma once
 
 #include "block_kernel.hpp"
+
+// The kernel's lambdas: one that is not inlined holds its captures, the operands'
+// addresses among them, in memory (the 128 x 128 tile took nine times as long).
+#define TG_INLINE __attribute__((always_inline))
 
 namespace tg {
 
@@ -136,48 +140,46 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
   if ((int)blockIdx.x >= n_tiles) return;
   const bool far = p.ldc * ESZ * BM > 0x7fffffffll;  // a tile of C spans more than a resource
 
-  // the tile whose loads are issued
-  int m0, n0, m_end;
-  const uint8_t *a_panel, *b_panel;
-  int64_t a_bytes, b_bytes;
+  // the tile whose loads are issued: its operands, and the stages' number from
+  // its first (`past`: the stages of the tile before, when its last ones load this
+  // one's first)
+  struct Source {
+    const uint8_t *a_panel, *b_panel;
+    const char* s_base;
+    int64_t a_bytes, b_bytes, s_bytes;
+  } src;
+  int past = 0;
   // this wave's scales: 64 rows of A, or (one wave) the tile's blocks of B
   // (lane i < BN / 128); the other waves repeat the last of these
   const int su = wave < S_DMA ? wave : S_DMA - 1;
   const bool sA_wave = su < S_DMA - 1;
   const int64_t s_step = sA_wave ? p.lsa * 4 : 4;
   const uint32_t voS = sA_wave ? 4u * lane : lane < BN / kScaleBlock ? (uint32_t)(lane * (int)p.lsb) * 4u : kDmaPast;
-  const char* s_base;
-  int64_t s_bytes;
-  auto take = [&](int wg) {
-    const BlockTile at = block_tile<BM, BN, EXPERTS>(p, tab, wg, n_tiles);
-    m0 = at.m0;
-    n0 = at.n0;
-    m_end = at.m_end;
-    a_panel = p.A + (int64_t)m0 * p.lda;
-    b_panel = at.B + (int64_t)n0 * p.ldb;
-    a_bytes = (int64_t)(p.M - 1 - m0) * p.lda + K;
-    b_bytes = (int64_t)(N - 1 - n0) * p.ldb + K;
-    const int nb0 = n0 / kScaleBlock;
-    s_base = sA_wave ? reinterpret_cast<const char*>(p.sA + m0 + 64 * su)
-                     : reinterpret_cast<const char*>(at.sB + (int64_t)nb0 * p.lsb);
-    s_bytes = sA_wave ? ((int64_t)(nst - 1) * p.lsa + (p.M - m0 - 64 * su)) * 4
-                      : ((int64_t)((N - 1) / kScaleBlock - nb0) * p.lsb + nst) * 4;
+  auto source = [&](const BlockTile& at) TG_INLINE {
+    const int nb0 = at.n0 / kScaleBlock;
+    return Source{p.A + (int64_t)at.m0 * p.lda, at.B + (int64_t)at.n0 * p.ldb,
+                  sA_wave ? reinterpret_cast<const char*>(p.sA + at.m0 + 64 * su)
+                          : reinterpret_cast<const char*>(at.sB + (int64_t)nb0 * p.lsb),
+                  (int64_t)(p.M - 1 - at.m0) * p.lda + K, (int64_t)(N - 1 - at.n0) * p.ldb + K,
+                  sA_wave ? ((int64_t)(nst - 1) * p.lsa + (p.M - at.m0 - 64 * su)) * 4
+                          : ((int64_t)((N - 1) / kScaleBlock - nb0) * p.lsb + nst) * 4};
   };
   // load n of stage s into buffer ST = s % 2: A's, B's, then the scales. Chunks
   // past K are sent to an offset past their resource's end (2 GiB at most),
   // where they arrive as zeros.
-  auto load = [&](auto st_c, int s, int n) {
+  auto load = [&](auto st_c, int s_all, int n) TG_INLINE {
+    const int s = s_all - past;
     constexpr uint32_t st = (uint32_t)(decltype(st_c)::value * STAGE);
     const bool in = chunk * 16 < K - s * RB;
     if (n < A_PER)
-      dma16(ldsw + st + 1024 * NW * n, panel_rsrc(a_panel + (int64_t)s * RB, a_bytes - (int64_t)s * RB),
+      dma16(ldsw + st + 1024 * NW * n, panel_rsrc(src.a_panel + (int64_t)s * RB, src.a_bytes - (int64_t)s * RB),
             (in ? voA : 0x80000000u) + n * stepA, 0u);
     else if (n < A_PER + B_PER)
       dma16(ldsw + st + A_BYTES + 1024 * NW * (n - A_PER),
-            panel_rsrc(b_panel + (int64_t)s * RB, b_bytes - (int64_t)s * RB),
+            panel_rsrc(src.b_panel + (int64_t)s * RB, src.b_bytes - (int64_t)s * RB),
             (in ? voB : 0x80000000u) + (n - A_PER) * stepB, 0u);
     else
-      dma4(lds0 + st + A_BYTES + B_BYTES + 256 * su, panel_rsrc(s_base + s * s_step, s < nst ? s_bytes - s * s_step : 0), voS, 0u);
+      dma4(lds0 + st + A_BYTES + B_BYTES + 256 * su, panel_rsrc(src.s_base + s * s_step, s < nst ? src.s_bytes - s * s_step : 0), voS, 0u);
   };
   auto frag = [&](const uint32_t (&f)[2][2], int st, int blk) -> i32x8 {
     const uint4 x = __builtin_bit_cast(uint4, lds_read16(f[st][0] + (uint32_t)(blk * 16 * RB)));
@@ -185,30 +187,54 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     return i32x8{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
   };
 
-  auto first_loads = [&] {
-    static_for<0, NU>([&](auto u_c) { load(std::integral_constant<int, 0>{}, 0, decltype(u_c)::value); });
-    static_for<0, NU1>([&](auto u_c) { load(std::integral_constant<int, 1>{}, 1, decltype(u_c)::value); });
+  auto first_loads = [&]() TG_INLINE {
+    static_for<0, NU>([&](auto u_c) TG_INLINE { load(std::integral_constant<int, 0>{}, 0, decltype(u_c)::value); });
+    static_for<0, NU1>([&](auto u_c) TG_INLINE { load(std::integral_constant<int, 1>{}, 1, decltype(u_c)::value); });
   };
 
-  take(blockIdx.x);
+  // The last two stages of a tile load the next one's first (`cross`), unless
+  // their number is odd and the buffers would change places. Past the last tile,
+  // and past the last stage without that, zeros arrive, without traffic.
+  const int nst2 = LAST ? nst : (nst + 1) / 2 * 2;
+  const bool cross = nst2 > 0 && nst2 % 2 == 0;
+  BlockTile now = block_tile<BM, BN, EXPERTS>(p, tab, blockIdx.x, n_tiles), next = now;
+  src = source(now);
   first_loads();
   wait_vmcnt<NU1>();
+  block_barrier();
   for (int wg = blockIdx.x; wg < n_tiles;) {
-    // stage 0 has landed (memory operations count down in order: the stores of
-    // the tile before came after the loads)
-    wait_vmcnt<NU1 + STORES>();
-    block_barrier();
+    // (stage 0 has landed)
+    wg += gridDim.x;
+    const int m0 = now.m0, n0 = now.n0, m_end = now.m_end;
+    Source ahead{};
+    if (wg < n_tiles) {
+      next = block_tile<BM, BN, EXPERTS>(p, tab, wg, n_tiles);
+      ahead = source(next);
+    }
+    past = 0;
+    // at the barrier of stage s
+    auto change = [&](int s) TG_INLINE {
+      const bool at = cross && s == nst2 - 2;
+      src.a_panel = at ? ahead.a_panel : src.a_panel;
+      src.b_panel = at ? ahead.b_panel : src.b_panel;
+      src.s_base = at ? ahead.s_base : src.s_base;
+      src.a_bytes = at ? ahead.a_bytes : src.a_bytes;
+      src.b_bytes = at ? ahead.b_bytes : src.b_bytes;
+      src.s_bytes = at ? ahead.s_bytes : src.s_bytes;
+      past = at ? nst2 : past;
+    };
 
     // a wave whose rows are all past the tile's last (an expert's last tile)
     // only takes part in the loads
     if (m0 + wm * WTM >= m_end) {
       // a stage's loads and barrier alone
-      auto idle = [&](auto st_c, int s) {
+      auto idle = [&](auto st_c, int s) TG_INLINE {
         constexpr int ST = decltype(st_c)::value;
-        static_for<NU1, NU>([&](auto u_c) { load(std::integral_constant<int, ST ^ 1>{}, s + 1, decltype(u_c)::value); });
+        static_for<NU1, NU>([&](auto u_c) TG_INLINE { load(std::integral_constant<int, ST ^ 1>{}, s + 1, decltype(u_c)::value); });
         wait_vmcnt<0>();
         block_barrier();
-        static_for<0, NU1>([&](auto u_c) { load(std::integral_constant<int, ST>{}, s + 2, decltype(u_c)::value); });
+        if constexpr (ST == 0) change(s);
+        static_for<0, NU1>([&](auto u_c) TG_INLINE { load(std::integral_constant<int, ST>{}, s + 2, decltype(u_c)::value); });
       };
 
       int s = 0;
@@ -217,14 +243,15 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
         idle(std::integral_constant<int, 1>{}, s + 1);
       }
       if (LAST && s < nst) idle(std::integral_constant<int, 0>{}, s);
-      wait_vmcnt<0>();
-      block_barrier();
-      wg += gridDim.x;
-      if (wg < n_tiles) {
-        take(wg);
-        first_loads();
+      if (!cross) {
+        wait_vmcnt<0>();
+        block_barrier();
+        src = ahead;
+        if (wg < n_tiles) first_loads();
+        wait_vmcnt<NU1>();
+        block_barrier();
       }
-      wait_vmcnt<NU1>();  // (no stores behind these loads)
+      now = next;
       continue;
     }
 
@@ -250,7 +277,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     sb = lds_load_f32(scB);
     sc[0] = sc[1] = raw[1] = 0.0f;
     d[2] = d[3] = floatx4{};
-    auto add = [&](auto m_c) {
+    auto add = [&](auto m_c) TG_INLINE {
       constexpr int m = decltype(m_c)::value, i = mfma_row(m), j = mfma_col(m);
       asm volatile("" : "+v"(d[m % 4]));
 #pragma unroll
@@ -260,9 +287,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
 
     // One stage, in buffer ST. Its last phase and the next stage's first one
     // load stage s + 2; one past the last arrives as zeros, without traffic.
-    auto step = [&](auto st_c, int s) {
+    auto step = [&](auto st_c, int s) TG_INLINE {
       constexpr int ST = decltype(st_c)::value;
-      static_for<0, FM * FN>([&](auto n_c) {
+      static_for<0, FM * FN>([&](auto n_c) TG_INLINE {
         constexpr int n = decltype(n_c)::value;
         constexpr int i = mfma_row(n), j = mfma_col(n);
         constexpr int q = n - PAIR;       // MFMA of the last two rows
@@ -272,6 +299,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
           wait_vmcnt<0>();
           wait_lgkmcnt0();
           block_barrier();
+          if constexpr (ST == 0) change(s);
         }
         if constexpr (WIDE) {
           if constexpr (j == 0) widen_e4m3(a[slot], aw[i & 1]);
@@ -303,7 +331,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
           }
         }
         // loads of stage s + 2 (from the barrier on) and of s + 1 (the rest)
-        static_for<0, NU>([&](auto u_c) {
+        static_for<0, NU>([&](auto u_c) TG_INLINE {
           constexpr int u = decltype(u_c)::value;
           if constexpr (q >= 0 && load_pos(u) == q) load(std::integral_constant<int, ST>{}, s + 2, u);
           if constexpr (q < 0 && load_pos(u) == FM * FN - PAIR + n) load(std::integral_constant<int, ST ^ 1>{}, s + 1, u);
@@ -327,19 +355,18 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     if (LAST && s < nst) step(std::integral_constant<int, 0>{}, s);
     add(std::integral_constant<int, FM * FN - 2>{});
     add(std::integral_constant<int, FM * FN - 1>{});
-    wait_vmcnt<0>();  // (zeros past the last stage)
-    wait_lgkmcnt0();
-    block_barrier();  // the ring is free
+    if (!cross) {
+      wait_vmcnt<0>();  // (zeros past the last stage)
+      wait_lgkmcnt0();
+      block_barrier();  // the ring is free
+      src = ahead;
+      if (wg < n_tiles) first_loads();
+    }
 
-    // the next tile's first loads, then this one's store, from registers
+    // the store, from registers
     const int row0_c = m0, col0_c = n0, end_c = m_end;
     const bool edge = n0 + BN > N || far;
     if (p.bias || p.act != kActNone) finish(acc, p, n0 + wn * WTN + 4 * lg);
-    wg += gridDim.x;
-    if (wg < n_tiles) {
-      take(wg);
-      first_loads();
-    }
     // v_permlane exchanges of the packed blocks j and j + 1 leave a lane 8
     // consecutive columns: of block j + lg / 2, columns 8 (lg % 2) ..
     int row = wm * WTM + l16, col = wn * WTN + (WIDE ? 4 * lg : 16 * (lg >> 1) + 8 * (lg & 1));
@@ -348,9 +375,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     char* const c_tile = static_cast<char*>(p.C) + ((int64_t)row0_c * p.ldc + col0_c) * ESZ;
     const auto rsC = __builtin_amdgcn_make_buffer_rsrc(c_tile, 0, c_bytes > 0x7fffffffll ? 0x7fffffff : (int)c_bytes,
                                                        0x00020000);
-    static_for<0, FM>([&](auto i_c) {
+    static_for<0, FM>([&](auto i_c) TG_INLINE {
       constexpr int i = decltype(i_c)::value;
-      static_for<0, WIDE ? FN : FN / 2>([&](auto h_c) {
+      static_for<0, WIDE ? FN : FN / 2>([&](auto h_c) TG_INLINE {
         constexpr int j = (WIDE ? 1 : 2) * decltype(h_c)::value;
         u32x4v v;
         if constexpr (WIDE) {
@@ -384,8 +411,17 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
         }
       });
     });
-    if (edge) wait_vmcnt<0>();  // (any number of stores)
+    if (!cross) {
+      // (memory operations count down in order: the stores came after the loads)
+      if (edge) wait_vmcnt<0>();  // (any number of stores)
+      wait_vmcnt<NU1 + STORES>();
+      block_barrier();
+    }
+    now = next;
   }
+  wait_vmcnt<0>();  // (zeros on their way into LDS)
 }
 
 }  // namespace tg
+
+#undef TG_INLINE
