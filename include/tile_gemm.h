@@ -361,8 +361,10 @@ tile_gemm_status_t tile_gemm_run_xent_backward(tile_gemm_t h, const void* A, con
  * element written once: results are bit-identical from run to run. fp32 outputs
  * come of bf16 matrix instructions, which add the exact products in fp32; bf16
  * outputs of the E4M3 ones, which cut each run of 8 products at 2^-14 of its
- * largest (1.5e-5 of the result, far below the rounding to bf16). A NaN or
- * infinite scale reaches the rows (or columns) it scales.
+ * largest (1.5e-5 of the result, far below the rounding to bf16). A NaN scale
+ * or value makes the rows (or columns) it belongs to NaN behind every
+ * activation (RELU keeps a NaN here); an infinite scale makes them infinite or
+ * NaN before the activation.
  *
  * Limits: K a multiple of 16; M, N, K and the strides of A, B and C below 2^22; A
  * and B 16-byte aligned with leading dimensions of whole 16 bytes, scales

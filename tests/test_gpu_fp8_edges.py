@@ -1,0 +1,62 @@
+"""E4M3 products and the quantization at the ends of their ranges."""
+
+import pytest
+import torch
+
+import block_helpers as bh
+import tile_partitioned_dense_amd as tg
+
+pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def g():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    with tg.TileGemm(0) as gg:
+        yield gg
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K,many", [(20, 300, 272, False), (2050, 4105, 144, True)])
+@pytest.mark.parametrize("act", ["NONE", "RELU", "SIGMOID", "TANH", "SILU"])
+def test_nan_passes_every_activation(g, M, N, K, many, dtype, act):
+    """A row with a NaN scale, one with a NaN code, one whose block held an
+    infinity when it was quantized, and the columns of a NaN scale are NaN
+    behind any activation, on both kernels; the others are not."""
+    p = tg.tile_gemm_plan_fp8(M, N, K, 0, tg.Dtype(int(dtype is torch.bfloat16)))
+    assert (p.config < 4) == many
+    print(f"[fp8 nan {M}x{N}x{K} {dtype} {act}]", flush=True)
+    x = torch.randn(M, K, generator=gen(M)).bfloat16()
+    x[4, K - 2] = INF
+    q, s = torch.empty(M, K, dtype=torch.uint8, device="cuda"), bh.row_scales(M, K, "cuda")
+    g.quantize(x.cuda(), q, s)
+    b, sb = bh.codes(gen(N), N, K), torch.full((bh.blocks(N), bh.blocks(K)), 1e-3)
+    s[3, 1], sb[1, 0] = NAN, NAN
+    q[M - 1, 0] = 0xff
+    bad = torch.zeros(M, N, dtype=torch.bool)
+    bad[3] = bad[4] = bad[M - 1] = True
+    bad[:, 128:256] = True
+    for bias in (None, torch.randn(N, generator=gen(1)).cuda()):
+        c = torch.zeros(M, (N + 7) // 8 * 8, dtype=dtype, device="cuda")[:, :N]
+        g.fp8(q, b.cuda(), c, s, sb.cuda(), bias=bias, act=tg.Act[act])
+        assert torch.equal(c.isnan().cpu(), bad)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(20, 300, 272), (2050, 4105, 144)])
+def test_infinite_scale_and_relu(g, M, N, K, dtype):
+    """relu of a row with an infinite scale: infinity, or 0 for minus infinity."""
+    a, b = bh.codes(gen(M), M, K), torch.full((N, K), 1.0).to(bh.FP8)
+    s = bh.row_scales(M, K, "cuda")
+    s.fill_(1.0)
+    s[3, 0] = s[7, 0] = INF
+    a[3, :128], a[7, :128] = 2.0, -2.0
+    c = torch.zeros(M, (N + 7) // 8 * 8, dtype=dtype, device="cuda")[:, :N]
+    g.fp8(a.cuda(), b.cuda(), c, s, torch.ones(bh.blocks(N), bh.blocks(K), device="cuda"), act=tg.Act.RELU)
+    assert bool((c[3] == INF).all()) and bool((c[7] == 0).all())

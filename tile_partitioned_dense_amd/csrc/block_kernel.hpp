@@ -484,7 +484,8 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
 #pragma unroll
         for (int j = 0; j < FN; ++j) lds_store_f4(stf + (uint32_t)(l16 * OPF + (16 * j + 4 * lg) * 4), acc[i][j]);
         wait_lgkmcnt0();
-        store_staged_fused<OUT_BF16, false>(stf, OPF, 16, WTN, row0 + wm * WTM + 16 * i, col0 + wn * WTN, lane, 64, eo);
+        store_staged_fused<OUT_BF16, false, kActReluNan>(stf, OPF, 16, WTN, row0 + wm * WTM + 16 * i, col0 + wn * WTN,
+                                                         lane, 64, eo);
         wait_lgkmcnt0();
       }
     }

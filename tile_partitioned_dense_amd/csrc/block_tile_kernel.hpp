@@ -55,7 +55,7 @@ __device__ __forceinline__ void finish_act(floatx4 (&acc)[FM][FN], const BlockAr
 template <int FM, int FN>
 __device__ __forceinline__ void finish(floatx4 (&acc)[FM][FN], const BlockArgs& p, int col) {
   switch (p.act) {
-    case kActRelu: finish_act<FM, FN, kActRelu>(acc, p, col); break;
+    case kActRelu: finish_act<FM, FN, kActReluNan>(acc, p, col); break;
     case kActSigmoid: finish_act<FM, FN, kActSigmoid>(acc, p, col); break;
     case kActTanh: finish_act<FM, FN, kActTanh>(acc, p, col); break;
     case kActSilu: finish_act<FM, FN, kActSilu>(acc, p, col); break;

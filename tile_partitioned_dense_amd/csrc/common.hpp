@@ -13,6 +13,8 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 // Fused-epilogue activations (mirror TILE_GEMM_ACT_* in tile_gemm.h).
 constexpr int kActNone = 0, kActRelu = 1, kActSigmoid = 2, kActTanh = 3, kActSilu = 4,
               kActSwiglu = 5;
+// relu that keeps a NaN, where kActRelu makes it 0
+constexpr int kActReluNan = 6;
 
 // e^x as 2^(x log2 e) on the hardware exponential (v_exp_f32, about 1 ulp):
 // rounding x log2 e adds a relative error of about 2^-24 |x| to the result,
@@ -54,6 +56,7 @@ __device__ __forceinline__ float tanh_hw(float x) {
 template <int ACT>
 __device__ __forceinline__ float act_fn(float x) {
   if constexpr (ACT == kActRelu) return fmaxf(x, 0.0f);
+  else if constexpr (ACT == kActReluNan) return x <= 0.0f ? 0.0f : x;
   else if constexpr (ACT == kActSigmoid) return sigmoid_hw(x);
   else if constexpr (ACT == kActTanh) return tanh_hw(x);
   else if constexpr (ACT == kActSilu) return x * sigmoid_hw(x);
@@ -211,8 +214,9 @@ __device__ __forceinline__ void store_staged_rows(uint32_t src, int pitch, int r
 // as act(x + bias) in fp32, rounded to bf16 (nearest even) for a bf16 output
 // and written once; rows and columns past M and N are masked. The row loop
 // stays rolled (unrolled twice to overlap its LDS reads), so the activation
-// code is emitted a fixed number of times however large the block.
-template <bool OUT_BF16, bool DEBUG>
+// code is emitted a fixed number of times however large the block. RELU: the
+// form that kActRelu asks for.
+template <bool OUT_BF16, bool DEBUG, int RELU = kActRelu>
 __device__ __forceinline__ void store_staged_fused(uint32_t src, int pitch, int rows, int cols,
                                                    int grow0, int gcol0, int tid, int nthr,
                                                    const EpiOut& o) {
@@ -242,7 +246,7 @@ __device__ __forceinline__ void store_staged_fused(uint32_t src, int pitch, int 
   }
   switch (o.act) {
     case kActRelu:
-      store_staged_rows<OUT_BF16, DEBUG, kActRelu>(src, pitch, rows, grow0, tid / cho, rstep, ch, col, full, b, o);
+      store_staged_rows<OUT_BF16, DEBUG, RELU>(src, pitch, rows, grow0, tid / cho, rstep, ch, col, full, b, o);
       break;
     case kActSigmoid:
       store_staged_rows<OUT_BF16, DEBUG, kActSigmoid>(src, pitch, rows, grow0, tid / cho, rstep, ch, col, full, b, o);
