@@ -1,4 +1,5 @@
-"""E4M3 products and the quantization at the ends of their ranges."""
+"""E4M3 products and the quantization at the ends of their ranges: bad values
+behind an activation, gates far out on their tails."""
 
 import pytest
 import torch
@@ -60,3 +61,39 @@ def test_infinite_scale_and_relu(g, M, N, K, dtype):
     c = torch.zeros(M, (N + 7) // 8 * 8, dtype=dtype, device="cuda")[:, :N]
     g.fp8(a.cuda(), b.cuda(), c, s, torch.ones(bh.blocks(N), bh.blocks(K), device="cuda"), act=tg.Act.RELU)
     assert bool((c[3] == INF).all()) and bool((c[7] == 0).all())
+
+
+# (gate, the largest relative error of its value in fp32): the exponential's
+# argument is off by a few of its roundings, 2^-24 of it each -- one for silu and
+# gelu (z^2 / 2 of a bf16 value is exact), six for gelu_tanh -- and by half a step
+# of the hardware's exponential, EVAL at most together with the rest
+TAILS = [("SILU", lambda z: bh.EVAL + 2.0 ** -24 * z.abs()),
+         ("GELU", lambda z: bh.EVAL + 2.0 ** -24 * z * z / 2),
+         ("GELU_TANH", lambda z: bh.EVAL + 6 * 2.0 ** -24 * 1.6 * (z.abs() + 0.045 * z.abs() ** 3)),
+         ("SIGMOID", lambda z: bh.EVAL + 2.0 ** -24 * z.abs())]
+
+
+def gate64(z, gate):
+    if gate == "GELU":
+        return z * 0.5 * torch.special.erfc(-z * 0.5 ** 0.5)
+    if gate == "GELU_TANH":
+        y = 2 * (2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3)
+        return z * torch.sigmoid(y)
+    return torch.sigmoid(z) * (z if gate == "SILU" else 1.0)
+
+
+@pytest.mark.parametrize("gate,bound", TAILS, ids=[t[0] for t in TAILS])
+def test_scales_of_gates_on_their_tails(g, gate, bound):
+    """A block whose gates all lie at one value, from 9 down to -9: its scale is
+    that value's, to the precision of fp32, however small it is."""
+    z = torch.arange(-9.0, 9.0, 1 / 16).bfloat16()
+    z = z[(z.double() * (7.0 if gate == "GELU_TANH" else 1.0)).abs() <= 45]  # (2^-100 and less counts as that)
+    M, K = len(z), 128
+    x = torch.cat([z[:, None].expand(M, K), torch.ones(M, K)], 1).bfloat16().cuda()
+    q, s = torch.empty(M, K, dtype=bh.FP8, device="cuda"), bh.row_scales(M, K, "cuda")
+    g.quantize(x, q, s, gate=tg.Gate[gate])
+    want = gate64(z.double(), gate).abs().clamp(min=2.0 ** -100) / 448
+    off = (s[:, 0].cpu().double() - want).abs() / want
+    # (two more roundings: of the value and of its division by 448)
+    over = off > bound(z.double()) + 2.0 ** -23
+    assert not bool(over.any()), [(float(z[i]), float(off[i])) for i in over.nonzero()[:8, 0]]

@@ -49,6 +49,34 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float r) {
   return make_uint2(w[0], w[1]);
 }
 
+// act(z) of a bf16 value. gelu is z Q(-z), Q the normal distribution's upper tail,
+// Q(z) = e^(-z^2 / 2) R(z / sqrt 2) / 2 for z >= 0 with R(x) = e^(x^2) erfc(x): a
+// block's scale may hang on values far out on the tail, which have to be right
+// relative to themselves (gate_both's are off by up to 1e-7 of 1, 1.5% of the value
+// at -9). R is a polynomial of degree 7 in t =
+// 1 / (1 + 0.45 x) times t, fitted for the least relative error (3e-7, for x up
+// to 9.5) to 64-bit values; z^2 is exact. 8192 x 3584 34 us, 33 with gate_both's.
+template <int GATE>
+__device__ __forceinline__ float gate_of(float z) {
+  if constexpr (GATE == kGateGelu) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.31819805153394637f, fabsf(z), 1.0f));
+    float r = 0.5f * 0.06631969151f;
+    r = fmaf(r, t, 0.5f * -0.2378895656f);
+    r = fmaf(r, t, 0.5f * 0.2045545914f);
+    r = fmaf(r, t, 0.5f * 0.04441020492f);
+    r = fmaf(r, t, 0.5f * 0.1863791616f);
+    r = fmaf(r, t, 0.5f * 0.2287909009f);
+    r = fmaf(r, t, 0.5f * 0.253518495f);
+    r = fmaf(r, t, 0.5f * 0.2539168146f);
+    const float q = r * (t * __builtin_amdgcn_exp2f(z * z * -0.72134752044448171f));
+    return z * (z < 0.0f ? q : 1.0f - q);
+  } else {
+    float act, slope;
+    gate_both<GATE>(z, act, slope);
+    return act;
+  }
+}
+
 // q = x (448 / a), scale = a / 448, a the block's largest magnitude: one pass, the
 // values held in registers between the maximum and the codes. Bound by memory.
 // 16 lanes hold one block of a row, 8 values each, their maximum by four lane
@@ -94,11 +122,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs p) {
       float y[8];
       unpack8(u[r], y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float a, slope;
-        gate_both<GATE>(x[e], a, slope);
-        x[e] = a * y[e];
-      }
+      for (int e = 0; e < 8; ++e) x[e] = gate_of<GATE>(x[e]) * y[e];
     }
     const uint32_t top = max(max_row16(max_bits(x)), kLeastBits);
     const float t = __builtin_bit_cast(float, top);
