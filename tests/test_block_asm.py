@@ -1,0 +1,43 @@
+"""CPU checks of the compiled gfx950 code of the E4M3 products (no GPU needed)."""
+
+import os
+import re
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "tile_partitioned_dense_amd", "csrc")
+HIPCC = "/opt/rocm/bin/hipcc"
+
+
+def compiled(config, out):
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not available")
+    cmd = [HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-Xclang", "-target-feature", "-Xclang",
+           "-packed-fp32-ops", "-I", os.path.join(ROOT, "include"), "-I", CSRC, f"-DTG_BLOCK_CONFIG={config}", "-S",
+           "--cuda-device-only", os.path.join(CSRC, "kernels_block.hip"), "-o", str(out)]
+    subprocess.run(cmd, check=True, capture_output=True)
+    return out.read_text()
+
+
+@pytest.fixture(scope="module")
+def strips(tmp_path_factory):
+    """Assembly of the 32 x 128 tile, whose waves store two strips each."""
+    return compiled(5, tmp_path_factory.mktemp("asm") / "k.s")
+
+
+def test_strips_are_kept_apart(strips):
+    """A wave stores its results by strips that its lanes pass each other through
+    LDS. Lanes with nothing to store may not run ahead and write the next strip
+    before the others have read theirs: the compiler keeps them together
+    only where it is told to."""
+    kernels = re.findall(r"^_ZN2tg17block_gemm_kernel\S+:.*?s_endpgm", strips, flags=re.S | re.M)
+    assert len(kernels) == 4
+    for k in kernels:
+        events = re.findall(r"ds_write_b128|; wave barrier|s_barrier|global_store", k)
+        assert events.count("; wave barrier") == 4  # before and behind each strip's reads
+        stored = False
+        for e in events:
+            assert not (e == "ds_write_b128" and stored), "a strip is written where the last one may still be read"
+            stored = e == "global_store" or (stored and e == "ds_write_b128")

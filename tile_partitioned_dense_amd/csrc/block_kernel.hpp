@@ -32,6 +32,15 @@
 
 namespace tg {
 
+// A wave's own LDS: what its lanes wrote is read by its other lanes, what they read
+// is written again. The hardware keeps a wave's LDS operations in order, but the
+// compiler sees single lanes: without this it may let the lanes that skip a
+// store write the next strip before the others have read theirs.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 struct BlockArgs {
   const uint8_t* A;   // M x K E4M3, lda bytes between rows
   const uint8_t* B;   // N x K E4M3, ldb bytes between rows (one such matrix per expert)
@@ -483,10 +492,10 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
       for (int i = 0; i < FM; ++i) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) lds_store_f4(stf + (uint32_t)(l16 * OPF + (16 * j + 4 * lg) * 4), acc[i][j]);
-        wait_lgkmcnt0();
+        wave_lds_sync();
         store_staged_fused<OUT_BF16, false, kActReluNan>(stf, OPF, 16, WTN, row0 + wm * WTM + 16 * i, col0 + wn * WTN,
                                                          lane, 64, eo);
-        wait_lgkmcnt0();
+        wave_lds_sync();
       }
     }
     if (wg + (int)gridDim.x >= n_tiles) break;

@@ -129,12 +129,6 @@ __device__ __forceinline__ uint32_t max_token_u32(uint32_t v) {
   return v;
 }
 
-// A wave's own LDS: what its lanes wrote is read by its other lanes.
-__device__ __forceinline__ void wave_lds_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Logits of the experts e0 .. e0 + PL - 1; -inf for a NaN (an expert that is not
 // there) and past the last. No branch around a load: each would be waited for by
 // itself; experts past the last read the last one's.
