@@ -41,3 +41,28 @@ def test_strips_are_kept_apart(strips):
         for e in events:
             assert not (e == "ds_write_b128" and stored), "a strip is written where the last one may still be read"
             stored = e == "global_store" or (stored and e == "ds_write_b128")
+
+
+@pytest.fixture(scope="module", params=[0, 4], ids=["tile", "stream"])
+def asm(request, tmp_path_factory):
+    """Assembly of the 256 x 256 tile and of the 16 x 128 one."""
+    return compiled(request.param, tmp_path_factory.mktemp("asm") / "k.s")
+
+
+def kernels(asm):
+    """{mangled name: {resource: value}} of the kernels' metadata."""
+    found = {}
+    for part in asm.split(".amdgpu_metadata")[1].split("  - .agpr_count:")[1:]:
+        name = re.search(r"\.name:\s+(\S+)", part).group(1)
+        found[name] = {k: int(v) for k, v in re.findall(r"\.(\w+):\s+(\d+)\n", part)}
+    return found
+
+
+def test_experts_kernels_use_no_scratch(asm):
+    """Their call has neither bias nor activation, so nothing of an epilogue may
+    take registers that the sums need."""
+    experts = {n: r for n, r in kernels(asm).items()
+               if re.search(r"block_tile_kernel(ILi\d+E|Li\d+E)+Lb1E|block_gemm_kernel(ILi\d+E|Li\d+E)+Lb1E", n)}
+    assert experts
+    for name, r in experts.items():
+        assert r["private_segment_fixed_size"] == 0 and r["vgpr_spill_count"] == 0, (name, r)

@@ -487,7 +487,7 @@ __global__ __launch_bounds__(WM * WN * KS * 64, 2) void block_gemm_kernel(BlockA
     }
     if (KS == 1 || ks == 0) {
       const uint32_t stf = epi0 + (uint32_t)(PART + (wave % WT) * 16 * OPF);
-      const EpiOut eo{p.C, p.ldc, end, N, p.bias, p.act, nullptr, 0};
+      const EpiOut eo{p.C, p.ldc, end, N, EXPERTS ? nullptr : p.bias, EXPERTS ? kActNone : p.act, nullptr, 0};
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
 #pragma unroll

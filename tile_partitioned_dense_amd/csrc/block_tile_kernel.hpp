@@ -366,7 +366,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     // the store, from registers
     const int row0_c = m0, col0_c = n0, end_c = m_end;
     const bool edge = n0 + BN > N || far;
-    if (p.bias || p.act != kActNone) finish(acc, p, n0 + wn * WTN + 4 * lg);
+    if constexpr (!EXPERTS) {  // (the experts' product has no epilogue: with one it held 192 bytes of scratch a lane)
+      if (p.bias || p.act != kActNone) finish(acc, p, n0 + wn * WTN + 4 * lg);
+    }
     // v_permlane exchanges of the packed blocks j and j + 1 leave a lane 8
     // consecutive columns: of block j + lg / 2, columns 8 (lg % 2) ..
     int row = wm * WTM + l16, col = wn * WTN + (WIDE ? 4 * lg : 16 * (lg >> 1) + 8 * (lg & 1));
