@@ -1,4 +1,5 @@
-"""CPU checks of the compiled gfx950 code of the E4M3 products (no GPU needed)."""
+"""CPU checks of the compiled gfx950 code (no GPU needed): the strips through which
+waves store, and the E4M3 products."""
 
 import os
 import re
@@ -11,42 +12,48 @@ CSRC = os.path.join(ROOT, "tile_partitioned_dense_amd", "csrc")
 HIPCC = "/opt/rocm/bin/hipcc"
 
 
-def compiled(config, out):
+def compiled(source, define, out):
     if not os.path.exists(HIPCC):
         pytest.skip("hipcc not available")
     cmd = [HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-Xclang", "-target-feature", "-Xclang",
-           "-packed-fp32-ops", "-I", os.path.join(ROOT, "include"), "-I", CSRC, f"-DTG_BLOCK_CONFIG={config}", "-S",
-           "--cuda-device-only", os.path.join(CSRC, "kernels_block.hip"), "-o", str(out)]
+           "-packed-fp32-ops", "-I", os.path.join(ROOT, "include"), "-I", CSRC, f"-D{define}", "-S",
+           "--cuda-device-only", os.path.join(CSRC, source), "-o", str(out)]
     subprocess.run(cmd, check=True, capture_output=True)
     return out.read_text()
 
 
-@pytest.fixture(scope="module")
-def strips(tmp_path_factory):
-    """Assembly of the 32 x 128 tile, whose waves store two strips each."""
-    return compiled(5, tmp_path_factory.mktemp("asm") / "k.s")
+def check_strips(asm, barriers):
+    kernels = re.findall(r"^_Z\S+:.*?s_endpgm", asm, flags=re.S | re.M)
+    assert kernels
+    for k in kernels:
+        events = re.findall(r"ds_write_b128|ds_write_b64|; wave barrier|s_barrier|global_store", k)
+        assert events.count("; wave barrier") >= barriers and events.count("global_store")
+        stored = False
+        for e in events:
+            write = e.startswith("ds_write")
+            assert not (write and stored), "a strip is written where the last one may still be read"
+            stored = e == "global_store" or (stored and write)
 
 
-def test_strips_are_kept_apart(strips):
+@pytest.mark.parametrize("source,define", [
+    ("kernels_block.hip", "TG_BLOCK_CONFIG=5"),    # E4M3, 32 x 128: two strips a wave
+    ("kernels_train.hip", "TG_TRAIN_KERNEL=9"),    # stores of the gated block and of the loss
+    ("kernels_train.hip", "TG_TRAIN_KERNEL=52"),
+    ("kernels_train.hip", "TG_TRAIN_KERNEL=107"),
+    ("kernels_mx.hip", "TG_MX_CONFIG=6"),
+])
+def test_strips_are_kept_apart(source, define, tmp_path):
     """A wave stores its results by strips that its lanes pass each other through
     LDS. Lanes with nothing to store may not run ahead and write the next strip
     before the others have read theirs: the compiler keeps them together
     only where it is told to."""
-    kernels = re.findall(r"^_ZN2tg17block_gemm_kernel\S+:.*?s_endpgm", strips, flags=re.S | re.M)
-    assert len(kernels) == 4
-    for k in kernels:
-        events = re.findall(r"ds_write_b128|; wave barrier|s_barrier|global_store", k)
-        assert events.count("; wave barrier") == 4  # before and behind each strip's reads
-        stored = False
-        for e in events:
-            assert not (e == "ds_write_b128" and stored), "a strip is written where the last one may still be read"
-            stored = e == "global_store" or (stored and e == "ds_write_b128")
+    check_strips(compiled(source, define, tmp_path / "k.s"), 4)  # before and behind each strip's reads
 
 
 @pytest.fixture(scope="module", params=[0, 4], ids=["tile", "stream"])
 def asm(request, tmp_path_factory):
     """Assembly of the 256 x 256 tile and of the 16 x 128 one."""
-    return compiled(request.param, tmp_path_factory.mktemp("asm") / "k.s")
+    return compiled("kernels_block.hip", f"TG_BLOCK_CONFIG={request.param}", tmp_path_factory.mktemp("asm") / "k.s")
 
 
 def kernels(asm):

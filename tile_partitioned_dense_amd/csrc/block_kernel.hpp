@@ -32,15 +32,6 @@
 
 namespace tg {
 
-// A wave's own LDS: what its lanes wrote is read by its other lanes, what they read
-// is written again. The hardware keeps a wave's LDS operations in order, but the
-// compiler sees single lanes: without this it may let the lanes that skip a
-// store write the next strip before the others have read theirs.
-__device__ __forceinline__ void wave_lds_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 struct BlockArgs {
   const uint8_t* A;   // M x K E4M3, lda bytes between rows
   const uint8_t* B;   // N x K E4M3, ldb bytes between rows (one such matrix per expert)

@@ -133,6 +133,15 @@ __device__ __forceinline__ uint32_t pack_halves(uint32_t x, uint32_t y, bool hi_
   return hi_half ? ((x >> 16) | (y & 0xffff0000u)) : ((x & 0xffffu) | (y << 16));
 }
 
+// A wave's own LDS: what its lanes wrote is read by its other lanes, what they read
+// is written again. The hardware keeps a wave's LDS operations in order, but the
+// compiler sees single lanes: without this it may let the lanes that skip a
+// store write the next strip before the others have read theirs.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Destination and epilogue of store_staged_fused.
 struct EpiOut {
   void* C;

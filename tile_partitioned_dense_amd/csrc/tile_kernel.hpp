@@ -180,8 +180,11 @@ __device__ __forceinline__ void wait_vmcnt() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
+// (It stands before and behind the strips through which a wave passes its
+// results between its lanes, so it keeps them together: wave_lds_sync.)
 __device__ __forceinline__ void wait_lgkmcnt0() {
   __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));
+  __builtin_amdgcn_wave_barrier();
 }
 __device__ __forceinline__ void block_barrier() {
   asm volatile("" ::: "memory");

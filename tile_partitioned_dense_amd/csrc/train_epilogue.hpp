@@ -318,6 +318,7 @@ template <int ROWS, int COLS, class ColOf>
 __device__ __forceinline__ void store_both(uint32_t strip, int lane, int grow0, const TrainArgs& p,
                                            ColOf col_of) {
   constexpr int PITCH = COLS * 2 + 16;
+  wave_lds_sync();
   if (p.Z) {
     constexpr int CH = COLS / 8;
 #pragma unroll
@@ -388,6 +389,7 @@ __device__ __forceinline__ void store_both(uint32_t strip, int lane, int grow0, 
       }
     }
   }
+  wave_lds_sync();
 }
 
 // Gated stores: every 16-column block of the tile is 8 gate columns and the
@@ -559,6 +561,7 @@ __device__ __forceinline__ void glu_store(floatx4 (&acc)[FM][FN], uint32_t strip
           lds_store_f4(a, v);
       }
     });
+    wave_lds_sync();
 #pragma unroll
     for (int c0 = 0; c0 < 16 * CH; c0 += 64) {
       const int c = c0 + lane;
@@ -571,6 +574,7 @@ __device__ __forceinline__ void glu_store(floatx4 (&acc)[FM][FN], uint32_t strip
       if (row < p.M && col < F)
         *reinterpret_cast<u32x4s*>(static_cast<char*>(p.C) + ((int64_t)row * p.ldc + col) * ESZ) = v;
     }
+    wave_lds_sync();
   });
 }
 
