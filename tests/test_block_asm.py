@@ -73,3 +73,21 @@ def test_experts_kernels_use_no_scratch(asm):
     assert experts
     for name, r in experts.items():
         assert r["private_segment_fixed_size"] == 0 and r["vgpr_spill_count"] == 0, (name, r)
+
+
+# M0 may be set from any scalar register; an asm block without instructions pins a value
+ALLOWED = re.compile(r"^(s_mov_b32 m0, (s\d+|vcc_lo|vcc_hi)|"
+                     r"buffer_load_dword(x4)? v\d+, s\[\d+:\d+\], (0|s\d+|vcc_lo|vcc_hi) offen( nt)? lds)$")
+
+
+def test_inline_asm_only_sets_m0_and_loads(asm):
+    """The compiler does not see what such a block writes: it may set M0
+    (declared) and issue a load into LDS, with the cache hint nt, and nothing else."""
+    lines = [line.split(";")[0].strip() for b in re.findall(r";;#ASMSTART\n(.*?);;#ASMEND", asm, flags=re.S)
+             for line in b.splitlines()]
+    lines = [line for line in lines if line]
+    assert any("lds" in line for line in lines)
+    for line in lines:
+        assert ALLOWED.match(line), f"unexpected instruction in inline asm: {line}"
+    outside = re.sub(r";;#ASMSTART\n.*?;;#ASMEND", "", asm, flags=re.S)
+    assert not re.search(r"^\s*s_\w+\s+m0\b", outside, flags=re.M)
