@@ -361,7 +361,10 @@ tile_gemm_status_t tile_gemm_run_xent_backward(tile_gemm_t h, const void* A, con
  * element written once: results are bit-identical from run to run. fp32 outputs
  * come of bf16 matrix instructions, which add the exact products in fp32; bf16
  * outputs of the E4M3 ones, which cut each run of 8 products at 2^-14 of its
- * largest (1.5e-5 of the result, far below the rounding to bf16). A NaN scale
+ * largest (1.5e-5 of the results in the 2-norm, a hundredth of their rounding to
+ * bf16; where products cancel to less than 1% of their usual sum, more than it).
+ * A row's scale times a block's is formed in fp32 and has to be a number of
+ * fp32: past its range it is infinite, below 2^-126 it loses bits. A NaN scale
  * or value makes the rows (or columns) it belongs to NaN behind every
  * activation (RELU keeps a NaN here); an infinite scale makes them infinite or
  * NaN before the activation.

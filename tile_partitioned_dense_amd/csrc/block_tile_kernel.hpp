@@ -20,7 +20,7 @@
 // to 11 TB/s): without loads it is 18 to 20% faster, without the FMAs 10%,
 // without fragment reads 9%. Measured: 8192 x 7168 x 8192 to bf16 420 us (2.29
 // PFLOP/s; the library's product with one scale 388); 16396 rows of 16 experts,
-// 7168 x 2048, 268 us; to fp32 8192 x 7168 x 8192 755 us (1.27 PFLOP/s, bf16
+// 7168 x 2048, 264 us; to fp32 8192 x 7168 x 8192 755 us (1.27 PFLOP/s, bf16
 // instructions; the library's bf16 8192^3 reaches 1.45). Not faster: a second barrier that frees B early (7% slower), three
 // stages of a 256 x 128 tile, loads over 8, 12, 20 and 24 instead of 16
 // instructions, wave priorities, waves of 64 x 128 (9% slower), runs of 4 and 16
@@ -366,7 +366,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void block_tile_kernel(BlockArgs p
     // the store, from registers
     const int row0_c = m0, col0_c = n0, end_c = m_end;
     const bool edge = n0 + BN > N || far;
-    if constexpr (!EXPERTS) {  // (the experts' product has no epilogue: with one it held 192 bytes of scratch a lane)
+    // (The experts' product has no epilogue. On the 256 x 256 tile it spills 143
+    // registers, 192 bytes of scratch a lane, 9 MB of writes beside 117 for 8192 x
+    // 7168; the experts' form takes the same time with and without.)
+    if constexpr (!EXPERTS) {
       if (p.bias || p.act != kActNone) finish(acc, p, n0 + wn * WTN + 4 * lg);
     }
     // v_permlane exchanges of the packed blocks j and j + 1 leave a lane 8
