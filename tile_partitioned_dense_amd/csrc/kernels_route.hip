@@ -162,6 +162,11 @@ __device__ __forceinline__ double score_part(float x, float m) {
   return x == m ? (m == -INFINITY ? 0.0 : 1.0) : exp((double)x - (double)m);
 }
 __device__ __forceinline__ double sigmoid64(float x) { return 1.0 / (1.0 + exp(-(double)x)); }
+// s (1 - s) from the exponential, in which 1 - s does not round away as s comes near 1.
+__device__ __forceinline__ double sigmoid_slope64(float x) {
+  const double t = exp(-fabs((double)x));
+  return t / ((1.0 + t) * (1.0 + t));
+}
 
 // Scores of a token's experts in 64 bits (in 32 neighbouring ones would round to
 // equal ones and the choice hang on them), with the largest logit m and one over
@@ -433,10 +438,15 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteArgs p) {
   float at[PER];
 #pragma unroll
   for (int r = 0; r < PER; ++r) at[r] = load_value<BF16>(p.logits, row + max(id[r], 0));
-  float m;
-  double inv;
-  double s[PL];
-  scores_of<L, PL>(l, p.sigmoid, s, m, inv);
+  float m = 0.0f;
+  double inv = 0.0;
+  double s[PL];  // scores, of sigmoid their slopes
+  if (p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) s[i] = sigmoid_slope64(l[i]);
+  } else {
+    scores_of<L, PL>(l, false, s, m, inv);
+  }
   double total = 0.0, dot = 0.0;
 #pragma unroll
   for (int r = 0; r < PER; ++r) {
@@ -472,7 +482,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteArgs p) {
   }
   float out[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) out[i] = (float)(p.sigmoid ? g[i] * s[i] * (1.0 - s[i]) : s[i] * (g[i] - dot));
+  for (int i = 0; i < PL; ++i) out[i] = (float)(p.sigmoid ? g[i] * s[i] : s[i] * (g[i] - dot));
   if (!live) return;
   constexpr int V = BF16 ? 8 : 4;
   char* const o = static_cast<char*>(p.dlogits) + (t * p.ldd + e0) * (BF16 ? 2 : 4);
