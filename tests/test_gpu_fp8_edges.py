@@ -97,3 +97,42 @@ def test_scales_of_gates_on_their_tails(g, gate, bound):
     # (two more roundings: of the value and of its division by 448)
     over = off > bound(z.double()) + 2.0 ** -23
     assert not bool(over.any()), [(float(z[i]), float(off[i])) for i in over.nonzero()[:8, 0]]
+
+
+# -------------------------------------------------------------- the longest axes
+
+def small(seed, *shape):
+    """Codes of -1, 0 and 1: sums of 2^22 products are exact in fp32."""
+    r = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-1, 2, shape, generator=r, device="cuda").float().to(bh.FP8)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [((1 << 22) - 1, 5, 16), (3, (1 << 22) - 13, 16), (200, (1 << 18) - 3, 16),
+                                   (5, 40, (1 << 22) - 16), (300, 520, (1 << 20) - 112)])
+def test_longest_axes(g, M, N, K, dtype):
+    print(f"[fp8 longest {M}x{N}x{K} {dtype}]", flush=True)
+    a, b = small(1, M, K), small(2, N, K)
+    sa, sb = torch.ones(bh.blocks(K), M, device="cuda").t(), torch.ones(bh.blocks(N), bh.blocks(K), device="cuda")
+    sa[M - 1], sb[bh.blocks(N) - 1] = 2.0, 4.0
+    want = a.float() @ b.float().T.contiguous()
+    want[M - 1] *= 2
+    want[:, (N - 1) // 128 * 128:] *= 4
+    c = torch.full((M, (N + 7) // 8 * 8), NAN, dtype=dtype, device="cuda")
+    g.fp8(a, b, c[:, :N], sa, sb)
+    assert torch.equal(c[:, :N], want.to(dtype)) and bool(c[:, N:].isnan().all())
+    c.fill_(NAN)
+    cut = M // 3
+    off = torch.tensor([0, cut, cut, M], dtype=torch.int32, device="cuda")
+    g.fp8_experts(a, b.float().mul(-1).to(bh.FP8).expand(3, N, K).contiguous(), c[:, :N], sa,
+                  sb.expand(3, *sb.shape).contiguous(), off)
+    assert torch.equal(c[:, :N], (-want).to(dtype)) and bool(c[:, N:].isnan().all())
+
+
+def test_quantize_longest_rows(g):
+    K = (1 << 22) - 16
+    x = (torch.arange(K, device="cuda") // 128 % 61 + 1).bfloat16().view(1, K).repeat(2, 1)
+    q, s = torch.zeros(2, K, dtype=torch.uint8, device="cuda"), bh.row_scales(2, K, "cuda")
+    g.quantize(x, q, s)
+    assert bool((q == 0x7e).all())
+    assert torch.equal(s, (x[:, ::128].double() / 448).float())
