@@ -456,9 +456,11 @@ tile_gemm_status_t tile_gemm_run_quantize(tile_gemm_t h, const void* X, void* Q,
  *   weights = scale * s[ids], with `renormalize` divided by the sum of s[ids]
  *     (0 where that is 0)
  * Scores, values and sums are held in 64 bits, so that the order of close ones
- * is that of the formula. A NaN logit counts as -inf (score 0), a NaN value as
- * -inf; experts at -inf are chosen last. Softmax: logits of +inf share the
- * weight; a token without a finite logit has scores 0.
+ * is that of the formula; what 64 bits do not tell apart (sigmoid scores of
+ * logits past 37, softmax ones of logits 745 below the largest) is equal. A NaN
+ * logit counts as -inf (score 0), a NaN value as -inf; experts at -inf are chosen
+ * last. Softmax: logits of +inf share the weight; a token without a finite logit
+ * has scores 0.
  * 1 <= E <= 1024, groups <= 64 a divisor of E, k <= 32 and at most the experts
  * of top_groups groups; T below 2^25, the strides below 2^31.
  */
@@ -483,7 +485,8 @@ tile_gemm_status_t tile_gemm_run_route(tile_gemm_t h, const void* logits, const 
  * none, nor has the bias): dlogits, T x E, of the logits' type. score, scale,
  * renormalize and logits_type are read of the options. An id outside [0, E)
  * (a place that was masked) counts for nothing; one that a token names twice
- * counts twice.
+ * counts twice. Formed in 64 bits and rounded once; softmax gradients are sums
+ * that may cancel, to a few 2^-53 of their largest term.
  */
 tile_gemm_status_t tile_gemm_run_route_backward(tile_gemm_t h, const void* logits, const int32_t* ids,
                                                 const float* dweights, void* dlogits, int64_t T,
