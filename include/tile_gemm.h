@@ -418,9 +418,9 @@ tile_gemm_status_t tile_gemm_run_fp8_experts(tile_gemm_t h, const void* A, const
  *   ROWS: blocks of 128 values of a row. X is M x K, block b of row i has
  *     scale[b * scale_stride + i].
  *   GATED_ROWS: the same of x = act(g) * u, with g the first K columns of X
- *     (M x 2 K) and u the last K, formed in fp32 (to a few of its steps
- *     relative to the value, on the gates' tails too): the second half of a gated
- *     block whose first half was a product onto a merged gate+up weight.
+ *     (M x 2 K) and u the last K, formed in fp32 (to within 2^-15 of the value
+ *     far out on the gates' tails too): the second half of a gated block whose
+ *     first half was a product onto a merged gate+up weight.
  *   BLOCKS: blocks of 128 x 128 values. X is M x K, the block of rows 128 r ..
  *     and columns 128 b .. has scale[r * scale_stride + b].
  * With `rows` (M int32 values, not with BLOCKS) row i of Q is made of row
